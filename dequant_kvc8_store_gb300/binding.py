@@ -27,6 +27,12 @@ DEV_BAD_BLOCK_ID = 1
 DEV_POS_BEYOND_TABLE = 2
 DEV_OUT_ROW_RANGE = 3
 DEV_BAD_LENGTH = 4
+DEV_TIMEOUT = 5
+
+ROPE_PLAIN = 0
+ROPE_LINEAR = 1
+ROPE_BASE = 2
+ROPE_BY_PARTS = 3
 
 HEADER = os.path.join(_build.INCLUDE, "kvc8.h")
 
@@ -46,6 +52,34 @@ class Geom(ctypes.Structure):
 
     def __repr__(self):
         return "Geom(" + ", ".join(f"{n}={getattr(self, n)}" for n, _ in self._fields_) + ")"
+
+
+class RopeStruct(ctypes.Structure):
+    """kvc8_rope."""
+    _fields_ = [("rotary_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32),
+                ("attention_factor", ctypes.c_float), ("norm_eps", ctypes.c_float),
+                ("freqs", ctypes.c_void_p), ("q_norm_weight", ctypes.c_void_p),
+                ("k_norm_weight", ctypes.c_void_p), ("positions", ctypes.c_void_p)]
+
+
+class Rope:
+    """kvc8_rope with its device arrays: tensors, integer addresses or None,
+    held here for as long as the calls may use them."""
+
+    def __init__(self, rotary_dim, freqs, interleaved=0, attention_factor=1.0, norm_eps=1e-6,
+                 q_norm_weight=None, k_norm_weight=None, positions=None):
+        self.freqs, self.positions = freqs, positions
+        self.q_norm_weight, self.k_norm_weight = q_norm_weight, k_norm_weight
+        self.struct = RopeStruct(int(rotary_dim), int(interleaved), float(attention_factor),
+                                 float(norm_eps), _p(freqs), _p(q_norm_weight), _p(k_norm_weight),
+                                 _p(positions))
+
+
+class RopeScaling(ctypes.Structure):
+    """kvc8_rope_scaling."""
+    _fields_ = [("kind", ctypes.c_int32), ("base", ctypes.c_double), ("factor", ctypes.c_double),
+                ("original_positions", ctypes.c_double), ("low", ctypes.c_double),
+                ("high", ctypes.c_double)]
 
 
 _lock = threading.Lock()
@@ -99,6 +133,25 @@ def configure(lib: ctypes.CDLL) -> ctypes.CDLL:
     lib.kvc8_append_gather_planned.argtypes = [G, i64, P, P, i64, i64, P, P, P, P, P, P, P, P, P,
                                                i64, i64, i64, P, sz, P, P]
     lib.kvc8_append_gather_planned.restype = ctypes.c_int
+    R = ctypes.POINTER(RopeStruct)
+    lib.kvc8_rope_frequencies.argtypes = [ctypes.POINTER(RopeScaling), i32,
+                                          ctypes.POINTER(ctypes.c_uint64),
+                                          ctypes.POINTER(ctypes.c_float)]
+    lib.kvc8_rope_frequencies.restype = ctypes.c_int
+    lib.kvc8_rope_store.argtypes = [G, R, i64, i32, P, i64, i64, P, i64, i64, P, P, i64, i64, P, P,
+                                    P, P, P, P, P, P, P]
+    lib.kvc8_rope_store.restype = ctypes.c_int
+    lib.kvc8_rope_store_bf16.argtypes = [G, R, i64, i32, P, i64, i64, P, i64, i64, P, P, i64, i64,
+                                         P, P, P, P, P, P, P]
+    lib.kvc8_rope_store_bf16.restype = ctypes.c_int
+    lib.kvc8_qk_norm_rope.argtypes = [R, i64, i32, i32, P, i64, i64, P, i64, i64, i32, P, i64, i64,
+                                      P, i64, i64, P]
+    lib.kvc8_qk_norm_rope.restype = ctypes.c_int
+    lib.kvc8_shared_prefix_workspace_bytes.argtypes = [G, i32, i32]
+    lib.kvc8_shared_prefix_workspace_bytes.restype = sz
+    lib.kvc8_shared_prefix_attention.argtypes = [G, i32, P, i64, i64, P, P, P, P, P, i32, P, P, P,
+                                                 ctypes.c_float, P, i64, i64, P, sz, P, P]
+    lib.kvc8_shared_prefix_attention.restype = ctypes.c_int
     return lib
 
 
@@ -298,6 +351,78 @@ def kvc8_paged_decode_attention(g: Geom, num_q_heads, query, q_seq_stride, q_hea
         int(out_head_stride), _p(workspace), int(workspace_bytes), _p(dev_error),
         _stream(stream))
     _ok(st, "kvc8_paged_decode_attention")
+
+
+def kvc8_rope_frequencies(scaling: RopeScaling, rotary_dim: int):
+    """(freqs, attention_factor): the fixed-point frequencies as a numpy uint64
+    array, to be copied to the device once (as int64 bits), and the factor."""
+    import numpy as np
+    n = int(rotary_dim)
+    freqs = np.zeros(max(n // 2, 1), np.uint64)
+    factor = ctypes.c_float(0.0)
+    st = load().kvc8_rope_frequencies(ctypes.byref(scaling), n,
+                                      freqs.ctypes.data_as(ctypes.POINTER(ctypes.c_uint64)),
+                                      ctypes.byref(factor))
+    _ok(st, "kvc8_rope_frequencies")
+    return freqs[: n // 2], float(factor.value)
+
+
+def kvc8_rope_store(g: Geom, rope: Rope, num_tokens, num_q_heads, query, q_tok_stride,
+                    q_head_stride, q_out, qo_tok_stride, qo_head_stride, key_states, value_states,
+                    x_tok_stride, x_head_stride, key_cache, value_cache, key_scale, value_scale,
+                    block_table, cu_q_lens, context_kv_lens, dev_error=None, stream=None) -> None:
+    st = load().kvc8_rope_store(
+        ctypes.byref(g), ctypes.byref(rope.struct), int(num_tokens), int(num_q_heads), _p(query),
+        int(q_tok_stride), int(q_head_stride), _p(q_out), int(qo_tok_stride), int(qo_head_stride),
+        _p(key_states), _p(value_states), int(x_tok_stride), int(x_head_stride), _p(key_cache),
+        _p(value_cache), _p(key_scale), _p(value_scale), _p(block_table), _p(cu_q_lens),
+        _p(context_kv_lens), _p(dev_error), _stream(stream))
+    _ok(st, "kvc8_rope_store")
+
+
+def kvc8_rope_store_bf16(g: Geom, rope: Rope, num_tokens, num_q_heads, query, q_tok_stride,
+                         q_head_stride, q_out, qo_tok_stride, qo_head_stride, key_states,
+                         value_states, x_tok_stride, x_head_stride, key_cache, value_cache,
+                         block_table, cu_q_lens, context_kv_lens, dev_error=None,
+                         stream=None) -> None:
+    st = load().kvc8_rope_store_bf16(
+        ctypes.byref(g), ctypes.byref(rope.struct), int(num_tokens), int(num_q_heads), _p(query),
+        int(q_tok_stride), int(q_head_stride), _p(q_out), int(qo_tok_stride), int(qo_head_stride),
+        _p(key_states), _p(value_states), int(x_tok_stride), int(x_head_stride), _p(key_cache),
+        _p(value_cache), _p(block_table), _p(cu_q_lens), _p(context_kv_lens), _p(dev_error),
+        _stream(stream))
+    _ok(st, "kvc8_rope_store_bf16")
+
+
+def kvc8_qk_norm_rope(rope: Rope, num_tokens, head_dim, num_q_heads, query, q_tok_stride,
+                      q_head_stride, q_out, qo_tok_stride, qo_head_stride, kv_heads, key,
+                      k_tok_stride, k_head_stride, k_out, ko_tok_stride, ko_head_stride,
+                      stream=None) -> None:
+    st = load().kvc8_qk_norm_rope(
+        ctypes.byref(rope.struct), int(num_tokens), int(head_dim), int(num_q_heads), _p(query),
+        int(q_tok_stride), int(q_head_stride), _p(q_out), int(qo_tok_stride), int(qo_head_stride),
+        int(kv_heads), _p(key), int(k_tok_stride), int(k_head_stride), _p(k_out),
+        int(ko_tok_stride), int(ko_head_stride), _stream(stream))
+    _ok(st, "kvc8_qk_norm_rope")
+
+
+def kvc8_shared_prefix_workspace_bytes(g: Geom, num_q_heads: int, max_prefix_blocks: int) -> int:
+    return int(load().kvc8_shared_prefix_workspace_bytes(ctypes.byref(g), int(num_q_heads),
+                                                         int(max_prefix_blocks)))
+
+
+def kvc8_shared_prefix_attention(g: Geom, num_q_heads, query, q_seq_stride, q_head_stride,
+                                 key_cache, value_cache, key_scale, value_scale, prefix_table,
+                                 max_prefix_blocks, prefix_length, block_table, context_lengths,
+                                 softmax_scale, out, out_seq_stride, out_head_stride, workspace,
+                                 workspace_bytes, dev_error=None, stream=None) -> None:
+    st = load().kvc8_shared_prefix_attention(
+        ctypes.byref(g), int(num_q_heads), _p(query), int(q_seq_stride), int(q_head_stride),
+        _p(key_cache), _p(value_cache), _p(key_scale), _p(value_scale), _p(prefix_table),
+        int(max_prefix_blocks), _p(prefix_length), _p(block_table), _p(context_lengths),
+        float(softmax_scale), _p(out), int(out_seq_stride), int(out_head_stride), _p(workspace),
+        int(workspace_bytes), _p(dev_error), _stream(stream))
+    _ok(st, "kvc8_shared_prefix_attention")
 
 
 def kvc8_get_error(dev_error, reset: bool = False, stream=None) -> int:

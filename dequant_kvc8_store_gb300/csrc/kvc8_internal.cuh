@@ -277,6 +277,52 @@ struct AttnArgs {
 
 constexpr int kAttnChunk = 2048;  // positions per split of a sequence
 
+// Rotation and norm of query and key rows on their way into the pages or into
+// contiguous rows (kvc8_rope.cu).
+enum RopeSink { kSinkDynamic = 0, kSinkChannel = 1, kSinkBlock = 2, kSinkBf16 = 3, kSinkRows = 4 };
+
+struct RopeArgs {
+    kvc8_geom g;  // kSinkRows: kv_heads and head_dim only
+    int64_t num_tokens;
+    int32_t q_heads;
+    int32_t rotary_dim;
+    int32_t interleaved;
+    float factor;  // multiplies cos and sin
+    float eps;
+    const uint64_t *freqs;
+    const uint16_t *q_weight;  // bf16 [D] or NULL
+    const uint16_t *k_weight;
+    const int32_t *positions;  // or NULL
+    const uint16_t *q;
+    int64_t q_tok_stride, q_head_stride;
+    uint16_t *q_out;
+    int64_t qo_tok_stride, qo_head_stride;
+    const uint16_t *k;  // new keys; values in the same strides (not in kSinkRows)
+    const uint16_t *v;
+    int64_t x_tok_stride, x_head_stride;
+    uint16_t *k_out;  // kSinkRows
+    int64_t ko_tok_stride, ko_head_stride;
+    void *k_cache;  // int8 or bf16 pages
+    void *v_cache;
+    float *k_scale;  // mode 0: written; modes 1 and 2: read
+    float *v_scale;
+    const int32_t *block_table;
+    const int32_t *cu_q_lens;
+    const int32_t *context_kv_lens;
+    int32_t *dev_error;
+};
+
+// Decode attention over a shared prefix and each sequence's own pages (kvc8_prefix.cu).
+struct PrefixArgs {
+    AttnArgs own;  // the sequences' own positions, the query and the output
+    const int32_t *prefix_table;
+    int32_t max_prefix_blocks;
+    const int32_t *prefix_length;
+};
+size_t shared_prefix_workspace_bytes(const kvc8_geom &g, int group, int32_t max_prefix_blocks);
+cudaError_t launch_shared_prefix(const PrefixArgs &a, void *workspace, cudaStream_t stream);
+cudaError_t launch_rope(const RopeArgs &a, RopeSink sink, cudaStream_t stream);
+
 // Workspace of the attention: the split plan, then the partials.
 size_t attention_workspace_bytes(const kvc8_geom &g, int group);
 cudaError_t launch_attention(AttnArgs a, void *workspace, cudaStream_t stream);

@@ -78,7 +78,8 @@ enum {
     KVC8_DEV_BAD_BLOCK_ID = 1,     /* block_table entry outside [0, num_blocks) */
     KVC8_DEV_POS_BEYOND_TABLE = 2, /* position >= max_blocks_per_seq * block_size */
     KVC8_DEV_OUT_ROW_RANGE = 3,    /* gather output row outside [0, out_rows) */
-    KVC8_DEV_BAD_LENGTH = 4        /* negative length or decreasing cu_q_lens */
+    KVC8_DEV_BAD_LENGTH = 4,       /* negative length or decreasing cu_q_lens */
+    KVC8_DEV_TIMEOUT = 5           /* a bounded wait inside a kernel ran out: outputs are not valid */
 };
 
 /* Geometry of one paged cache and one batch.  quant_mode: 0 = dynamic scale
@@ -395,6 +396,172 @@ kvc8_status kvc8_gather_bf16(const kvc8_geom *g, const void *key_cache,
                              int64_t out_head_stride, void *workspace,
                              size_t workspace_bytes, int32_t *dev_error,
                              cudaStream_t stream);
+
+/*
+ * Rotary positions and per-head norms (kvc8_rope_store, kvc8_rope_store_bf16,
+ * kvc8_qk_norm_rope).  Of a head's D channels, the first R = rotary_dim are
+ * rotated in pairs, the others pass.  Pair i (0 <= i < R / 2) is channels
+ * (i, i + R/2) in the half layout and (2i, 2i + 1) in the interleaved one.  With
+ * y the row after its norm (or the row itself) and phi = pos * f_i:
+ *   y'_a = m (y_a cos phi - y_b sin phi),  y'_b = m (y_b cos phi + y_a sin phi)
+ * and, where a norm weight w is given,
+ *   y_d = x_d / sqrt(mean_d(x_d^2) + eps) * w_d      over all D channels.
+ * Everything is computed in fp32 from the bf16 inputs and rounded once, to bf16
+ * or to the page's codes.  The products may be fused, so the last bit of an
+ * fp32 intermediate is not specified.
+ *
+ * The frequencies f_i are kept as fractions of a turn: freqs[i] =
+ * round(f_i / (2 pi) * 2^64).  The phase pos * freqs[i] is then an integer
+ * product modulo 2^64, exact at any position, where an fp32 angle would have
+ * lost 2^-24 of its size and a table would end.
+ */
+typedef struct kvc8_rope {
+    int32_t rotary_dim;        /* R: a multiple of 16, 0..D (0: no rotation) */
+    int32_t interleaved;       /* 0: half layout, 1: interleaved pairs */
+    float attention_factor;    /* m, multiplies cos and sin (1 unless the scaling asks) */
+    float norm_eps;            /* eps >= 0, used where a norm weight is given */
+    const uint64_t *freqs;     /* device [R/2], 8-byte aligned; NULL only when R = 0 */
+    const void *q_norm_weight; /* device bf16 [D], 16-byte aligned, or NULL: no norm */
+    const void *k_norm_weight; /* the same for the keys */
+    const int32_t *positions;  /* device [num_tokens], any int32 value, or NULL: see the calls */
+} kvc8_rope;
+
+/* How kvc8_rope_frequencies stretches the frequencies base^(-2i/R). */
+enum {
+    KVC8_ROPE_PLAIN = 0,    /* unchanged */
+    KVC8_ROPE_LINEAR = 1,   /* divided by factor (positions interpolated) */
+    KVC8_ROPE_BASE = 2,     /* base * factor^(R/(R-2)): the slowest pair is slowed by factor */
+    KVC8_ROPE_BY_PARTS = 3  /* by each pair's turns r over original_positions: divided by
+                               factor where r <= low, kept where r >= high, in between the
+                               linear blend f/factor (1-g) + f g, g = (r-low)/(high-low) */
+};
+
+typedef struct kvc8_rope_scaling {
+    int32_t kind;
+    double base;               /* > 0 */
+    double factor;             /* > 0; not used by KVC8_ROPE_PLAIN */
+    double original_positions; /* BY_PARTS: > 0 */
+    double low, high;          /* BY_PARTS: turns, low < high */
+} kvc8_rope_scaling;
+
+/*
+ * kvc8_rope_frequencies -- host function: the R/2 fixed-point frequencies of a
+ * scaling, for kvc8_rope.freqs (the caller copies them to the device once).
+ * *attention_factor, if not NULL, receives 0.1 ln(factor) + 1 for
+ * KVC8_ROPE_BY_PARTS with factor > 1 and 1 otherwise.  freqs and
+ * attention_factor are host pointers; rotary_dim is even and >= 0.
+ */
+kvc8_status kvc8_rope_frequencies(const kvc8_rope_scaling *scaling, int32_t rotary_dim,
+                                  uint64_t *freqs, float *attention_factor);
+
+/*
+ * kvc8_rope_store -- kvc8_store with the rotation (and the per-head norm) of the
+ * new keys on the way into the pages, and the same for the queries of the same
+ * tokens, in one launch.  Keys are quantised from their fp32 rotated values
+ * (one rounding); values are quantised as kvc8_store quantises them, with the
+ * same codes and scales.  Slots, scale modes, cu_q_lens, skipped tokens and the
+ * error word are those of kvc8_store; a token that is skipped has its q_out
+ * rows left unwritten too.  Inputs are finite.
+ *
+ *   r               the rotation; positions NULL: a token's position is the slot
+ *                   position context_kv_lens[b] + i, else positions[token]
+ *                   (e.g. behind a shared prefix whose pages are elsewhere)
+ *   num_q_heads     >= 0; 0: no queries, query and q_out are not used
+ *   query           bf16 [N][num_q_heads][D], element strides (q_tok_stride,
+ *                   q_head_stride, 1)
+ *   q_out           bf16 [N][num_q_heads][D], strides (qo_tok_stride,
+ *                   qo_head_stride, 1); may be `query` itself with its strides
+ *   the rest        as in kvc8_store
+ * All four query strides are multiples of 8, both bases 16-byte aligned.
+ */
+kvc8_status kvc8_rope_store(const kvc8_geom *g, const kvc8_rope *r, int64_t num_tokens,
+                            int32_t num_q_heads, const void *query, int64_t q_tok_stride,
+                            int64_t q_head_stride, void *q_out, int64_t qo_tok_stride,
+                            int64_t qo_head_stride, const void *key_states,
+                            const void *value_states, int64_t x_tok_stride,
+                            int64_t x_head_stride, int8_t *key_cache, int8_t *value_cache,
+                            float *key_scale, float *value_scale, const int32_t *block_table,
+                            const int32_t *cu_q_lens, const int32_t *context_kv_lens,
+                            int32_t *dev_error, cudaStream_t stream);
+
+/*
+ * kvc8_rope_store_bf16 -- the same over kvc8_store_bf16's pages: rotated keys
+ * rounded once to bf16, values copied bit for bit; g->quant_mode is ignored.
+ */
+kvc8_status kvc8_rope_store_bf16(const kvc8_geom *g, const kvc8_rope *r, int64_t num_tokens,
+                                 int32_t num_q_heads, const void *query, int64_t q_tok_stride,
+                                 int64_t q_head_stride, void *q_out, int64_t qo_tok_stride,
+                                 int64_t qo_head_stride, const void *key_states,
+                                 const void *value_states, int64_t x_tok_stride,
+                                 int64_t x_head_stride, void *key_cache, void *value_cache,
+                                 const int32_t *block_table, const int32_t *cu_q_lens,
+                                 const int32_t *context_kv_lens, int32_t *dev_error,
+                                 cudaStream_t stream);
+
+/*
+ * kvc8_qk_norm_rope -- the norm and rotation alone, for queries and keys that
+ * stay in contiguous rows (a prompt whose attention runs before or without the
+ * cache).  r->positions is required when r->rotary_dim > 0.  head_dim is a
+ * multiple of 16, 16..256; num_q_heads and kv_heads >= 0 (0: that side is not
+ * used).  Strides are in elements, multiples of 8, bases 16-byte aligned; each
+ * output may be its input itself with the same strides.
+ */
+kvc8_status kvc8_qk_norm_rope(const kvc8_rope *r, int64_t num_tokens, int32_t head_dim,
+                              int32_t num_q_heads, const void *query, int64_t q_tok_stride,
+                              int64_t q_head_stride, void *q_out, int64_t qo_tok_stride,
+                              int64_t qo_head_stride, int32_t kv_heads, const void *key,
+                              int64_t k_tok_stride, int64_t k_head_stride, void *k_out,
+                              int64_t ko_tok_stride, int64_t ko_head_stride,
+                              cudaStream_t stream);
+
+/* Bytes of device workspace kvc8_shared_prefix_attention needs for this
+ * geometry, number of query heads and size of the prefix table.  Host function;
+ * 0 for arguments that the call refuses. */
+size_t kvc8_shared_prefix_workspace_bytes(const kvc8_geom *g, int32_t num_q_heads,
+                                          int32_t max_prefix_blocks);
+
+/*
+ * kvc8_shared_prefix_attention -- kvc8_paged_decode_attention for a batch whose
+ * sequences all start with the same positions: the prefix is kept once in the
+ * pool and read once for all of them.  Query head j of sequence b attends over
+ * the P = *prefix_length positions of prefix_table and then over its own
+ * context_lengths[b] positions of block_table[b], in one softmax:
+ *   out[b][j] = (sum_{p < P} w_p V[p] + sum_{p < len_b} u_p V_b[p]) / (sum w + sum u)
+ *   w_p = exp(softmax_scale <q, K[p]>),  u_p = exp(softmax_scale <q, K_b[p]>)
+ * with K, V the values that the pages stand for, fp32(code) * scale.  Rounded to
+ * bf16 on the way to the tensor cores: the weights (with a row's or block's
+ * value scale multiplied in) and, with per-channel scales, the query (with the
+ * key scale multiplied in); products are accumulated in fp32, the output is
+ * rounded to bf16.  A query with no position at all gives zeros.  P, the lengths and
+ * the tables are read on the device, so a captured graph may be replayed with
+ * other values.
+ *
+ *   prefix_table      int32 [max_prefix_blocks], physical blocks of the prefix
+ *   max_prefix_blocks >= 1; P is at most max_prefix_blocks * block_size
+ *   prefix_length     device int32 [1], >= 0 (0: no prefix)
+ *   workspace         >= kvc8_shared_prefix_workspace_bytes bytes, 256-byte
+ *                     aligned; calls that overlap on the GPU need separate
+ *                     workspaces
+ *   the rest          as in kvc8_paged_decode_attention; context_lengths may be 0
+ * Supported: what kvc8_paged_decode_attention supports (head_dim 64 or 128,
+ * block_size a multiple of 16, at most 8 query heads per kv head).  Positions of
+ * blocks outside the pool are reported through dev_error and left out; a
+ * negative length counts as 0 and one beyond its table as the table's size, both
+ * reported.
+ */
+kvc8_status kvc8_shared_prefix_attention(const kvc8_geom *g, int32_t num_q_heads,
+                                         const void *query, int64_t q_seq_stride,
+                                         int64_t q_head_stride, const int8_t *key_cache,
+                                         const int8_t *value_cache, const float *key_scale,
+                                         const float *value_scale, const int32_t *prefix_table,
+                                         int32_t max_prefix_blocks,
+                                         const int32_t *prefix_length,
+                                         const int32_t *block_table,
+                                         const int32_t *context_lengths, float softmax_scale,
+                                         void *out, int64_t out_seq_stride,
+                                         int64_t out_head_stride, void *workspace,
+                                         size_t workspace_bytes, int32_t *dev_error,
+                                         cudaStream_t stream);
 
 /* Largest num_seqs that kvc8_dequant_gather_noalloc accepts. */
 #define KVC8_NOALLOC_MAX_SEQS 4096

@@ -318,14 +318,20 @@ struct PrefixArgs {
     const int32_t *prefix_table;
     int32_t max_prefix_blocks;
     const int32_t *prefix_length;
+    float *part_o;  // [slots * rows of a tile][D] unnormalised partial outputs of the prefix
+    float *part_m;  // running maxima (log2 domain)
+    float *part_l;  // running sums
 };
 size_t shared_prefix_workspace_bytes(const kvc8_geom &g, int group, int32_t max_prefix_blocks);
-cudaError_t launch_shared_prefix(const PrefixArgs &a, void *workspace, cudaStream_t stream);
+cudaError_t launch_shared_prefix(PrefixArgs a, void *workspace, cudaStream_t stream);
 cudaError_t launch_rope(const RopeArgs &a, RopeSink sink, cudaStream_t stream);
 
 // Workspace of the attention: the split plan, then the partials.
 size_t attention_workspace_bytes(const kvc8_geom &g, int group);
 cudaError_t launch_attention(AttnArgs a, void *workspace, cudaStream_t stream);
+// The plan and the attention kernel alone, each split leaving a partial; sets
+// a.plan and the partials' places in the workspace (attention_workspace_bytes).
+cudaError_t launch_attention_parts(AttnArgs &a, void *workspace, cudaStream_t stream);
 
 cudaError_t launch_store(const StoreArgs &a, cudaStream_t stream);
 cudaError_t launch_store_bf16(const StoreBf16Args &a, cudaStream_t stream);

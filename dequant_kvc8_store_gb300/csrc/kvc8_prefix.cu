@@ -1,146 +1,811 @@
 // kvc8_prefix.cu -- decode attention of a batch whose sequences share a prefix:
 // query head j of sequence b attends over the prefix's positions and then over
 // its own, in one softmax.
-//   out[b][j] = (sum_p w_p V[p] + sum_p u_p V_b[p]) / (sum_p w_p + sum_p u_p)
-//   w_p = exp(scale <q, K[p]>), u_p = exp(scale <q, K_b[p]>)
-// with K, V = fp32(code) * scale; no position at all gives zeros.
+//   out[b][j] = (sum_p w_p V'[p] + sum_p u_p V'_b[p]) / (sum_p w_p + sum_p u_p)
+//   w_p = exp(scale <q, K'[p]>), u_p = exp(scale <q, K'_b[p]>)
+// with K', V' = bf16(fp32(code) * scale); no position at all gives zeros.
 //
-// One CTA per (sequence, kv head) walks its prefix and own positions 128 at a
-// time with an online softmax: a thread per position for the scores, a thread
-// per channel for the weighted sum.
+// The sequences' own positions are the decode attention's splits
+// (kvc8_attention.cu), each left as a partial (m, l, O).  The prefix is one
+// matrix product for all sequences: a kv head's R = sequences * group query rows
+// against P positions, 4 R P D flops for 2 P D bytes of codes, so for R above
+// about 150 rows the tensor cores and not HBM bound it.
+//
+// prefix_kernel: a CTA holds NT tiles of 128 query rows and walks positions 128 at
+// a time.  S = Q K'^T and O += P V' are tcgen05.mma (M = 128, bf16, fp32 in tensor
+// memory); P replaces S in tensor memory and is the second product's A operand.
+// Warps by role:
+//   softmax     4 per tile, one thread per query row: S from tensor memory, online
+//               softmax, P back; the running maximum moves only when it grows by
+//               more than 2^8, so O is seldom rescaled
+//   dequantise  codes from global memory a tile ahead in registers, K' and V' as bf16
+//               into a two-stage ring in the 128-byte swizzle (K' K-major, V' as the
+//               MN-major B operand of the same rows)
+//   mma         one thread issues both products; with two tiles one's products run
+//               while the other's softmax does
+// The (tile, 128 positions) units are cut evenly over the CTAs (one per SM): CTA i
+// takes units [i U / C, (i + 1) U / C) and leaves one partial per tile it touches, in
+// slot tile + i, which no other pair has.  merge_kernel joins a row's partials.
+//
+// Every wait has a limit, after which the kernel reports KVC8_DEV_TIMEOUT and leaves.
 #include "kvc8_internal.cuh"
 
 namespace kvc8 {
 namespace {
 
-constexpr int kTile = 128;
-constexpr int kMaxGroup = 8;
+constexpr int kRows = 128;      // query rows of a tile
+constexpr int kCols = 128;      // positions of a step
+constexpr int kStages = 2;      // steps of K' and of V' in shared memory
+constexpr int kMaskSlots = 4;   // steps whose valid counts are kept
+constexpr int kMaxCtas = 152;   // SMs of a GB300
+constexpr float kLazy = 8.0f;   // log2 of the growth that makes the maximum move
+constexpr long long kWaitCycles = 4000000000ll;  // about two seconds
+constexpr int kMergeThreads = 256;
 
-template <int MODE, int D>
-__global__ void __launch_bounds__(kTile) prefix_kernel(const PrefixArgs p) {
-    const AttnArgs &a = p.own;
-    const int H = a.g.kv_heads, bs = a.g.block_size, G = a.group;
-    const int b = blockIdx.x / H, h = blockIdx.x - b * H;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    __shared__ float q_s[kMaxGroup][D];
-    __shared__ float w_s[kMaxGroup][kTile];
-    __shared__ int64_t row_s[kTile];  // cache row of each position, -1: left out
-    __shared__ float sv_s[kTile];
-    __shared__ float red[4][kMaxGroup];
-    for (int i = tid; i < G * D; i += kTile) {
-        const int j = i / D, d = i - j * D;
-        q_s[j][d] = __uint_as_float((uint32_t)a.q[(int64_t)b * a.q_seq_stride +
-                                                  (int64_t)(h * G + j) * a.q_head_stride + d] << 16);
-    }
-    __syncthreads();
-    float acc[kMaxGroup], m[kMaxGroup], l[kMaxGroup];
-#pragma unroll
-    for (int j = 0; j < kMaxGroup; ++j) {
-        acc[j] = l[j] = 0.0f;
-        m[j] = -INFINITY;
-    }
-    for (int part = 0; part < 2; ++part) {
-        const int32_t *table = part == 0 ? p.prefix_table
-                                         : a.block_table + (int64_t)b * a.g.max_blocks_per_seq;
-        const int64_t cap = (int64_t)(part == 0 ? p.max_prefix_blocks : a.g.max_blocks_per_seq) * bs;
-        int64_t len = part == 0 ? p.prefix_length[0] : a.context_lengths[b];
-        if (tid == 0 && h == 0) {
-            if (len < 0) report(a.dev_error, KVC8_DEV_BAD_LENGTH);
-            if (len > cap) report(a.dev_error, KVC8_DEV_POS_BEYOND_TABLE);
+// ---- PTX ------------------------------------------------------------------------
+
+__device__ __forceinline__ uint32_t smem_u32(const void *p) {
+    return (uint32_t)__cvta_generic_to_shared(p);
+}
+__device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count) {
+    asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
+}
+__device__ __forceinline__ void mbar_arrive(uint32_t bar) {
+    asm volatile("mbarrier.arrive.release.cta.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+__device__ __forceinline__ void fence_async() {
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
+__device__ __forceinline__ void tc_fence_before() {
+    asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+}
+__device__ __forceinline__ void tc_fence_after() {
+    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+}
+__device__ __forceinline__ void tc_commit(uint32_t bar) {
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
+                 : "memory");
+}
+// D[tmem] (+)= A[smem] B[smem]
+__device__ __forceinline__ void tc_mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                          uint32_t acc) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(acc)
+        : "memory");
+}
+// D[tmem] (+)= A[tmem] B[smem]
+__device__ __forceinline__ void tc_mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
+                                          uint32_t acc) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"(acc)
+        : "memory");
+}
+// 32 columns of this thread's row of tensor memory.
+__device__ __forceinline__ void tc_ld32(float (&r)[32], uint32_t addr) {
+    uint32_t *u = reinterpret_cast<uint32_t *>(r);
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]), "=r"(u[4]), "=r"(u[5]), "=r"(u[6]),
+          "=r"(u[7]), "=r"(u[8]), "=r"(u[9]), "=r"(u[10]), "=r"(u[11]), "=r"(u[12]), "=r"(u[13]),
+          "=r"(u[14]), "=r"(u[15]), "=r"(u[16]), "=r"(u[17]), "=r"(u[18]), "=r"(u[19]),
+          "=r"(u[20]), "=r"(u[21]), "=r"(u[22]), "=r"(u[23]), "=r"(u[24]), "=r"(u[25]),
+          "=r"(u[26]), "=r"(u[27]), "=r"(u[28]), "=r"(u[29]), "=r"(u[30]), "=r"(u[31])
+        : "r"(addr)
+        : "memory");
+}
+__device__ __forceinline__ void tc_st32(uint32_t addr, const float (&r)[32]) {
+    const uint32_t *u = reinterpret_cast<const uint32_t *>(r);
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31};" ::"r"(u[0]),
+        "r"(u[1]), "r"(u[2]), "r"(u[3]), "r"(u[4]), "r"(u[5]), "r"(u[6]), "r"(u[7]), "r"(u[8]),
+        "r"(u[9]), "r"(u[10]), "r"(u[11]), "r"(u[12]), "r"(u[13]), "r"(u[14]), "r"(u[15]),
+        "r"(u[16]), "r"(u[17]), "r"(u[18]), "r"(u[19]), "r"(u[20]), "r"(u[21]), "r"(u[22]),
+        "r"(u[23]), "r"(u[24]), "r"(u[25]), "r"(u[26]), "r"(u[27]), "r"(u[28]), "r"(u[29]),
+        "r"(u[30]), "r"(u[31]), "r"(addr)
+        : "memory");
+}
+__device__ __forceinline__ void tc_st16(uint32_t addr, const uint32_t (&u)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15};" ::"r"(u[0]),
+        "r"(u[1]), "r"(u[2]), "r"(u[3]), "r"(u[4]), "r"(u[5]), "r"(u[6]), "r"(u[7]), "r"(u[8]),
+        "r"(u[9]), "r"(u[10]), "r"(u[11]), "r"(u[12]), "r"(u[13]), "r"(u[14]), "r"(u[15]), "r"(addr)
+        : "memory");
+}
+__device__ __forceinline__ void tc_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+__device__ __forceinline__ float ex2(float x) {  // 2^x, -inf gives 0
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+// Shared-memory operand: 128-byte swizzle, 8 rows of 128 bytes 1 KB apart (sbo),
+// 64-channel blocks of an MN-major operand lbo apart.
+__device__ __forceinline__ uint64_t operand_desc(uint32_t addr, uint32_t lbo) {
+    return (uint64_t)((addr & 0x3FFFFu) >> 4) | ((uint64_t)(lbo >> 4) << 16) | ((uint64_t)(1024u >> 4) << 32) |
+           (1ull << 46) | (2ull << 61);
+}
+// M = 128, bf16 operands, fp32 accumulators; b_mn: B is MN-major.
+constexpr uint32_t instr_desc(int n, bool b_mn) {
+    return (1u << 4) | (1u << 7) | (1u << 10) | ((b_mn ? 1u : 0u) << 16) | ((uint32_t)(n >> 3) << 17) |
+           ((uint32_t)(kRows >> 4) << 24);
+}
+
+// ---- the work's split -------------------------------------------------------------
+
+struct PrefixWork {
+    int64_t units;  // tiles * steps
+    int32_t steps;  // of 128 positions
+    int32_t tiles_per_head;
+    int32_t len;
+};
+
+__device__ __forceinline__ PrefixWork prefix_work(const PrefixArgs &p, int rows_per_tile) {
+    const kvc8_geom &g = p.own.g;
+    PrefixWork w;
+    const int64_t cap = (int64_t)p.max_prefix_blocks * g.block_size;
+    w.len = (int32_t)max((int64_t)0, min((int64_t)__ldg(p.prefix_length), cap));
+    w.steps = (w.len + kCols - 1) / kCols;
+    const int64_t rows = (int64_t)g.num_seqs * p.own.group;
+    w.tiles_per_head = (int32_t)((rows + rows_per_tile - 1) / rows_per_tile);
+    w.units = (int64_t)w.tiles_per_head * g.kv_heads * w.steps;
+    return w;
+}
+
+// ---- the kernel ---------------------------------------------------------------------
+
+template <int D, int NT>
+struct Layout {
+    static constexpr int kDequantWarps = NT == 1 ? 8 : 4;
+    static constexpr int kSoftmaxWarps = 4 * NT;
+    static constexpr int kWarps = kSoftmaxWarps + kDequantWarps + 1;
+    static constexpr int kTileBytes = kRows * D * 2;  // Q tile, K' or V' stage
+    static constexpr int kQ = 0;
+    static constexpr int kK = NT * kTileBytes;
+    static constexpr int kV = kK + kStages * kTileBytes;
+    static constexpr int kEnd = kV + kStages * kTileBytes;
+    // more than half of an SM's shared memory, so that a CTA has the SM's tensor
+    // memory to itself
+    static constexpr int kBytes = (kEnd > 120 * 1024 ? kEnd : 120 * 1024) + 1024;
+    static constexpr int kTmemCols = NT * (kCols + D) > 256 ? 512 : 256;
+};
+
+struct Barriers {
+    uint64_t k_full[kStages], k_free[kStages], v_full[kStages], v_free[kStages];
+    uint64_t q_full[2], s_full[2], p_full[2], o_full[2], drained;
+    uint32_t tmem;
+    int32_t stop;
+    uint2 valid[kMaskSlots];  // 8 bytes: valid positions of each group of 16
+};
+
+template <int MODE, int D, int NT>
+struct Prefix {
+    using L = Layout<D, NT>;
+    const PrefixArgs &p;
+    Barriers &bar;
+    const uint32_t base;  // shared memory, 1 KB aligned
+    const PrefixWork w;
+    const int64_t u0, u1;
+    const int lane;
+
+    // false: the limit ran out here or elsewhere in the CTA
+    __device__ __forceinline__ bool wait(uint64_t &b, uint32_t parity) const {
+        const uint32_t at = smem_u32(&b);
+        if (mbar_try(at, parity)) return true;
+        const long long t0 = clock64();
+        while (!mbar_try(at, parity)) {
+            if (*static_cast<volatile int32_t *>(&bar.stop) != 0) return false;
+            if (clock64() - t0 > kWaitCycles) {
+                *static_cast<volatile int32_t *>(&bar.stop) = 1;
+                report(p.own.dev_error, KVC8_DEV_TIMEOUT);
+                return false;
+            }
         }
-        len = min(len, cap);
-        for (int64_t p0 = 0; p0 < len; p0 += kTile) {
-            const int64_t pos = p0 + tid;
-            float s[kMaxGroup];
+        return true;
+    }
+
+    // The same for a whole warp, which leaves it converged.
+    __device__ __forceinline__ bool wait_warp(uint64_t &b, uint32_t parity) const {
+        return __all_sync(0xFFFFFFFFu, wait(b, parity));
+    }
+
+    // ---- dequantise ------------------------------------------------------------
+    static constexpr int kRpw = kCols / L::kDequantWarps;  // positions of a warp
+    static constexpr int kLpr = D / 16;                    // lanes of a position
+    static constexpr int kRpi = 32 / kLpr;                 // positions of one load
+    static constexpr int kLoads = kRpw / kRpi;
+    static constexpr int kGroups = kRpw / 16;  // a group of 16 positions lies in one block
+
+    struct Codes {
+        uint4 c[kLoads];
+        float s;  // modes 0 and 2: the scale of position `lane` of the warp
+    };
+    struct Where {
+        int64_t row[kGroups];  // cache row of each group's first position
+        int64_t blk[kGroups];  // block * heads + head
+        int valid[kGroups];
+    };
+
+    __device__ __forceinline__ Where find(int h, int step, int dw) const {
+        Where x;
+        const kvc8_geom &g = p.own.g;
 #pragma unroll
-            for (int j = 0; j < kMaxGroup; ++j) s[j] = -INFINITY;
-            int64_t row = -1;
-            float sv = 0.0f;
-            if (pos < len) {
-                const int64_t lb = pos / bs;
-                const int32_t blk = table[lb];
-                if (blk < 0 || blk >= a.g.num_blocks) {
-                    report(a.dev_error, KVC8_DEV_BAD_BLOCK_ID);
-                } else {
-                    row = ((int64_t)blk * H + h) * bs + (pos - lb * bs);
-                    const int64_t at = MODE == 0 ? row : (int64_t)blk * H + h;
-                    const float sk = MODE == 1 ? 1.0f : a.k_scale[at];
-                    sv = MODE == 1 ? 1.0f : a.v_scale[at];
-                    float dot[kMaxGroup];
+        for (int i = 0; i < kGroups; ++i) {
+            const int pos = step * kCols + dw * kRpw + 16 * i;
+            x.valid[i] = 0;
+            x.row[i] = x.blk[i] = 0;
+            if (pos < w.len) {
+                const uint32_t lb = (uint32_t)pos / (uint32_t)g.block_size;
+                const int32_t blk = ld_nc_s32(p.prefix_table + lb);
+                if (blk >= 0 && blk < g.num_blocks) {
+                    x.blk[i] = (int64_t)blk * g.kv_heads + h;
+                    x.row[i] = x.blk[i] * g.block_size + (pos - (int)(lb * (uint32_t)g.block_size));
+                    x.valid[i] = min(16, w.len - pos);
+                } else if (lane == 0) {
+                    report(p.own.dev_error, KVC8_DEV_BAD_BLOCK_ID);
+                }
+            }
+        }
+        return x;
+    }
+
+    __device__ __forceinline__ void load(const Where &x, const int8_t *cache, const float *scale,
+                                         Codes &c) const {
 #pragma unroll
-                    for (int j = 0; j < kMaxGroup; ++j) dot[j] = 0.0f;
-                    for (int d = 0; d < D; ++d) {
-                        const float k = (float)a.k_cache[row * D + d] *
-                                        (MODE == 1 ? a.k_scale[h * D + d] : sk);
+        for (int i = 0; i < kLoads; ++i) {
+            const int grp = i * kRpi / 16, at = i * kRpi % 16 + lane / kLpr;
+            c.c[i] = make_uint4(0u, 0u, 0u, 0u);
+            if (at < x.valid[grp])
+                c.c[i] = __ldg(reinterpret_cast<const uint4 *>(cache + (x.row[grp] + at) * D) + lane % kLpr);
+        }
+        c.s = 0.0f;
+        if (MODE != 1) {
+            const int grp = kGroups == 1 ? 0 : lane >> 4;
+            const int64_t row = kGroups == 1 || grp == 0 ? x.row[0] : x.row[kGroups - 1];
+            const int64_t blk = kGroups == 1 || grp == 0 ? x.blk[0] : x.blk[kGroups - 1];
+            const int valid = kGroups == 1 || grp == 0 ? x.valid[0] : x.valid[kGroups - 1];
+            if (lane < kRpw && (lane & 15) < valid)
+                c.s = ld_nc_f32(scale + (MODE == 0 ? row + (lane & 15) : blk));
+        }
+    }
+
+    // bf16(fl(fp32(code) * s)) of a position's 16 codes, as the gather rounds them
+    __device__ __forceinline__ static void expand(const uint4 &c, const float *s, uint32_t (&o)[8]) {
+        const uint32_t wd[4] = {c.x, c.y, c.z, c.w};
 #pragma unroll
-                        for (int j = 0; j < kMaxGroup; ++j)
-                            if (j < G) dot[j] += q_s[j][d] * k;
+        for (int i = 0; i < 8; ++i) {
+            const uint32_t wb = wd[i >> 1] ^ 0x80808080u;
+            const int e = 2 * (i & 1);
+            float2 x = make_float2(__uint_as_float(__byte_perm(wb, 0x4B000000u, 0x7440 + e)),
+                                   __uint_as_float(__byte_perm(wb, 0x4B000000u, 0x7441 + e)));
+            x = __fadd2_rn(x, make_float2(-8388736.0f, -8388736.0f));
+            x = __fmul2_rn(x, MODE == 1 ? make_float2(s[2 * i], s[2 * i + 1]) : make_float2(s[0], s[0]));
+            o[i] = pack_bf16(x.x, x.y);
+        }
+    }
+
+    __device__ __forceinline__ void store(const Codes &c, const float *chan, uint32_t tile, int dw) const {
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) {
+            const int r = i * kRpi + lane / kLpr;  // position of the warp
+            float row_s = 0.0f;
+            if (MODE != 1) row_s = __shfl_sync(0xFFFFFFFFu, c.s, r);
+            uint32_t o[8];
+            expand(c.c[i], MODE == 1 ? chan : &row_s, o);
+            const int row = dw * kRpw + r, c8 = lane % kLpr;
+            // 16-byte chunk n of a 128-byte row lies at n ^ (row mod 8); the lanes of the
+            // second 64 channels write their two chunks in the other order, so that the
+            // eight lanes of a row hit different banks
+            const int n = (c8 & 3) * 2, swap = c8 >> 2, x = row & 7;
+            const uint32_t at = tile + (uint32_t)(c8 >> 2) * (kCols * 128) + (uint32_t)row * 128;
+            const uint32_t a0 = at + (uint32_t)(((n + swap) ^ x) << 4), a1 = at + (uint32_t)(((n + 1 - swap) ^ x) << 4);
+            asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(a0), "r"(swap ? o[4] : o[0]),
+                         "r"(swap ? o[5] : o[1]), "r"(swap ? o[6] : o[2]), "r"(swap ? o[7] : o[3])
+                         : "memory");
+            asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(a1), "r"(swap ? o[0] : o[4]),
+                         "r"(swap ? o[1] : o[5]), "r"(swap ? o[2] : o[6]), "r"(swap ? o[3] : o[7])
+                         : "memory");
+        }
+    }
+
+    __device__ void dequantise(int dw) const {
+        const AttnArgs &a = p.own;
+        int tile = (int)(u0 / w.steps), step = (int)(u0 - (int64_t)tile * w.steps);
+        int h = tile / w.tiles_per_head, h_scale = -1;
+        float kch[16], vch[16];  // mode 1: this lane's channels
+        Where x = find(h, step, dw);
+        Codes k, v;
+        load(x, a.k_cache, a.k_scale, k);
+        load(x, a.v_cache, a.v_scale, v);
+        int n = 0;
+        for (int64_t u = u0; u < u1; ++u, ++n) {
+            if (MODE == 1 && h != h_scale) {
+                h_scale = h;
+                const int64_t at = (int64_t)h * D + (lane % kLpr) * 16;
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    kch[i] = ld_nc_f32(a.k_scale + at + i);
+                    vch[i] = ld_nc_f32(a.v_scale + at + i);
+                }
+            }
+            const int st = n % kStages;
+            const uint32_t par = (uint32_t)(n / kStages) & 1u;
+            if (!wait_warp(bar.k_free[st], par ^ 1u)) return;
+            store(k, kch, base + L::kK + st * L::kTileBytes, dw);
+            if (lane == 0) {
+                uint8_t *vc = reinterpret_cast<uint8_t *>(&bar.valid[n % kMaskSlots]) + dw * kGroups;
+#pragma unroll
+                for (int i = 0; i < kGroups; ++i) vc[i] = (uint8_t)x.valid[i];
+            }
+            fence_async();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&bar.k_full[st]));
+            if (u + 1 < u1) {  // the next step's codes
+                if (++step == w.steps) {
+                    step = 0;
+                    ++tile;
+                    h = tile / w.tiles_per_head;
+                }
+                x = find(h, step, dw);
+                load(x, a.k_cache, a.k_scale, k);
+            }
+            if (!wait_warp(bar.v_free[st], par ^ 1u)) return;
+            store(v, vch, base + L::kV + st * L::kTileBytes, dw);
+            fence_async();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&bar.v_full[st]));
+            if (u + 1 < u1) load(x, a.v_cache, a.v_scale, v);
+        }
+    }
+
+    // ---- products (one thread) --------------------------------------------------
+    __device__ __forceinline__ void qk(int x, int st, uint32_t tmem) const {
+        const uint32_t q = base + L::kQ + x * L::kTileBytes, k = base + L::kK + st * L::kTileBytes;
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i) {
+            const uint32_t at = (uint32_t)(i / 4) * (kRows * 128) + (uint32_t)(i % 4) * 32;
+            tc_mma_ss(tmem + x * kCols, operand_desc(q + at, 16), operand_desc(k + at, 16),
+                      instr_desc(kCols, false), i > 0);
+        }
+    }
+    __device__ __forceinline__ void pv(int x, int st, uint32_t tmem, bool acc) const {
+        const uint32_t v = base + L::kV + st * L::kTileBytes;
+#pragma unroll
+        for (int i = 0; i < kCols / 16; ++i)
+            tc_mma_ts(tmem + NT * kCols + x * D, tmem + x * kCols + 8 * i,
+                      operand_desc(v + (uint32_t)i * 2048, kCols * 128), instr_desc(D, true),
+                      acc || i > 0);
+    }
+
+    __device__ bool products_loop(uint32_t tmem) const {
+        int n = 0, seg = 0, steps_done = 0;
+        for (int64_t u = u0; u < u1; ++seg) {
+            const int64_t tile = u / w.steps;
+            const int count = (int)(min(u1, (tile + 1) * w.steps) - u);
+            for (int t = -1; t < count; ++t) {
+                const int st = (n + t) & 1;
+                const uint32_t par = (uint32_t)((n + t) / kStages) & 1u;
+                const int st1 = (n + t + 1) % kStages;
+                const uint32_t par1 = (uint32_t)((n + t + 1) / kStages) & 1u;
+                const bool more = t + 1 < count;
+#pragma unroll
+                for (int x = 0; x < NT; ++x) {
+                    if (t >= 0) {
+                        if (!wait(bar.p_full[x], (uint32_t)steps_done & 1u)) return false;
+                        if (x == 0 && !wait(bar.v_full[st], par)) return false;
+                        tc_fence_after();
+                        pv(x, st, tmem, t > 0);
+                        if (x == NT - 1) tc_commit(smem_u32(&bar.v_free[st]));
+                        if (!more) tc_commit(smem_u32(&bar.o_full[x]));
                     }
+                    if (more) {
+                        if (t < 0 && !wait(bar.q_full[x], (uint32_t)seg & 1u)) return false;
+                        if (x == 0 && !wait(bar.k_full[st1], par1)) return false;
+                        tc_fence_after();
+                        qk(x, st1, tmem);
+                        tc_commit(smem_u32(&bar.s_full[x]));
+                        if (x == NT - 1) tc_commit(smem_u32(&bar.k_free[st1]));
+                    }
+                }
+                if (t >= 0) ++steps_done;
+            }
+            n += count;
+            u += count;
+        }
+        return true;
+    }
+
+    __device__ void products(uint32_t tmem) const {
+        products_loop(tmem);
+        // what was issued is done before the tensor memory is freed
+        tc_commit(smem_u32(&bar.drained));
+        const long long t0 = clock64();
+        while (!mbar_try(smem_u32(&bar.drained), 0))
+            if (clock64() - t0 > kWaitCycles) break;
+    }
+
+    // ---- softmax (one thread per query row) -----------------------------------
+    __device__ void softmax(int warp, uint32_t tmem) const {
+        const AttnArgs &a = p.own;
+        const int x = warp >> 2, row = (warp & 3) * 32 + lane;  // tile of the CTA, row of the tile
+        const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+        const uint32_t s_at = tmem + lanes + x * kCols, o_at = tmem + lanes + NT * kCols + x * D;
+        const int64_t rows = (int64_t)a.g.num_seqs * a.group;
+        const float scale = fabsf(a.scale_log2);
+        const uint32_t flip = a.scale_log2 < 0.0f ? 0x80008000u : 0u;  // the sign goes to the query
+        int n = 0;
+        uint32_t seg = 0;
+        for (int64_t u = u0; u < u1; ++seg) {
+            const int64_t tile = u / w.steps;
+            const int count = (int)(min(u1, (tile + 1) * w.steps) - u);
+            const int h = (int)(tile / w.tiles_per_head);
+            const int64_t r0 = (tile - (int64_t)h * w.tiles_per_head) * (NT * kRows) + x * kRows + (warp & 3) * 32;
+            const int64_t r = r0 + lane;
+            const bool busy = r0 < rows;  // uniform in the warp: some row is a query's
+            {   // the query row into the swizzled tile
+                const uint32_t dst = base + L::kQ + x * L::kTileBytes + (uint32_t)row * 128;
+                const uint16_t *q = a.q;
+                if (r < rows) {
+                    const int b = (int)(r / a.group), j = (int)(r - (int64_t)b * a.group);
+                    q += (int64_t)b * a.q_seq_stride + (int64_t)(h * a.group + j) * a.q_head_stride;
+                }
 #pragma unroll
-                    for (int j = 0; j < kMaxGroup; ++j)
-                        if (j < G) s[j] = dot[j] * a.scale_log2;
+                for (int i = 0; i < D / 8; ++i) {
+                    uint4 v = make_uint4(0u, 0u, 0u, 0u);
+                    if (r < rows) v = __ldg(reinterpret_cast<const uint4 *>(q) + i);
+                    const uint32_t at = dst + (uint32_t)(i / 8) * (kRows * 128) + (uint32_t)(((i % 8) ^ (row & 7)) << 4);
+                    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(v.x ^ flip),
+                                 "r"(v.y ^ flip), "r"(v.z ^ flip), "r"(v.w ^ flip)
+                                 : "memory");
+                }
+                fence_async();
+                tc_fence_before();  // the last segment's O is read
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&bar.q_full[x]));
+            }
+            float m = -INFINITY, l = 0.0f;
+            for (int t = 0; t < count; ++t, ++n) {
+                if (!wait_warp(bar.s_full[x], (uint32_t)n & 1u)) return;
+                tc_fence_after();
+                if (busy) step(s_at, o_at, scale, t > 0, bar.valid[n % kMaskSlots], m, l);
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&bar.p_full[x]));
+            }
+            if (!wait_warp(bar.o_full[x], seg & 1u)) return;
+            tc_fence_after();
+            if (busy) {
+                const int64_t slot = (tile + blockIdx.x) * (NT * kRows) + x * kRows + row;
+                float *po = p.part_o + slot * D;
+#pragma unroll
+                for (int c = 0; c < D; c += 32) {
+                    float o[32];
+                    tc_ld32(o, o_at + c);
+                    tc_wait_ld();
+                    if (r < rows) {
+#pragma unroll
+                        for (int i = 0; i < 32; i += 4)
+                            *reinterpret_cast<float4 *>(po + c + i) = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+                    }
+                    __syncwarp();
+                }
+                if (r < rows) {
+                    p.part_m[slot] = m;
+                    p.part_l[slot] = l;
                 }
             }
-            __syncthreads();  // the last round's weights are used up
-            row_s[tid] = row;
-            sv_s[tid] = sv;
+            u += count;
+        }
+    }
+
+    // One step of a row: S -> P, the running maximum m and sum l.
+    __device__ __forceinline__ void step(uint32_t s_at, uint32_t o_at, float scale, bool have_o,
+                                         uint2 valid, float &m, float &l) const {
+        const bool whole = valid.x == 0x10101010u && valid.y == 0x10101010u;
+        auto mask = [&](float (&s)[32], int c) {
+            if (whole) return;
 #pragma unroll
-            for (int j = 0; j < kMaxGroup; ++j) {
-                float x = s[j];
-                for (int o = 16; o > 0; o >>= 1) x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, o));
-                if (lane == 0) red[warp][j] = x;
+            for (int i = 0; i < 32; ++i) {
+                const uint32_t wd = c < 64 ? valid.x : valid.y;
+                const int n = (int)(wd >> (((c % 64) / 16 + i / 16) * 8)) & 0xFF;
+                if (i % 16 >= n) s[i] = -INFINITY;
             }
-            __syncthreads();
-            float f[kMaxGroup];
+        };
+        float top = -INFINITY;
 #pragma unroll
-            for (int j = 0; j < kMaxGroup; ++j) {
-                const float top = fmaxf(fmaxf(red[0][j], red[1][j]), fmaxf(red[2][j], red[3][j]));
-                const float n = fmaxf(m[j], top);
-                f[j] = n == -INFINITY ? 1.0f : exp2f(m[j] - n);
-                m[j] = n;
-                w_s[j][tid] = s[j] == -INFINITY ? 0.0f : exp2f(s[j] - n);
-                acc[j] *= f[j];
-                l[j] *= f[j];
+        for (int c = 0; c < kCols; c += 32) {
+            float s[32];
+            tc_ld32(s, s_at + c);
+            tc_wait_ld();
+            mask(s, c);
+            float t0 = fmaxf(s[0], s[1]), t1 = fmaxf(s[2], s[3]);
+#pragma unroll
+            for (int i = 4; i < 32; i += 4) {
+                t0 = fmaxf(t0, fmaxf(s[i], s[i + 1]));
+                t1 = fmaxf(t1, fmaxf(s[i + 2], s[i + 3]));
             }
-            __syncthreads();
-            const int count = (int)min((int64_t)kTile, len - p0);
-            for (int i = 0; i < count; ++i) {
-                const int64_t r = row_s[i];
-                if (r < 0) continue;
-                const float v = tid < D ? (float)a.v_cache[r * D + tid] * sv_s[i] : 0.0f;
+            top = fmaxf(top, fmaxf(t0, t1));
+        }
+        // scale 0 times -inf is no number: such a row has no position yet
+        const float mx = top == -INFINITY ? -INFINITY : top * scale;
+        const bool moves = mx > m + kLazy || (m == -INFINITY && mx > m);
+        if (__any_sync(0xFFFFFFFFu, moves)) {
+            const float f = moves ? ex2(m - mx) : 1.0f;  // 0 where there was nothing yet
+            if (moves) m = mx;
+            l *= f;
+            if (have_o) {
 #pragma unroll
-                for (int j = 0; j < kMaxGroup; ++j) {
-                    acc[j] += w_s[j][i] * v;
-                    l[j] += w_s[j][i];
+                for (int c = 0; c < D; c += 32) {
+                    float o[32];
+                    tc_ld32(o, o_at + c);
+                    tc_wait_ld();
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) o[i] *= f;
+                    tc_st32(o_at + c, o);
                 }
             }
         }
-    }
-    if (tid < D) {
-        const float sv = MODE == 1 ? a.v_scale[h * D + tid] : 1.0f;
+        const float neg = m == -INFINITY ? 0.0f : -m;
+        float2 sum = make_float2(0.0f, 0.0f);
 #pragma unroll
-        for (int j = 0; j < kMaxGroup; ++j) {
-            if (j >= G) continue;
-            unsigned short o;
-            asm("cvt.rn.bf16.f32 %0, %1;" : "=h"(o) : "f"(l[j] > 0.0f ? acc[j] * sv / l[j] : 0.0f));
-            a.out[(int64_t)b * a.out_seq_stride + (int64_t)(h * G + j) * a.out_head_stride + tid] = o;
+        for (int c = 0; c < kCols; c += 32) {
+            float s[32];
+            tc_ld32(s, s_at + c);
+            tc_wait_ld();
+            mask(s, c);
+            uint32_t o[16];
+#pragma unroll
+            for (int i = 0; i < 32; i += 2) {
+                float2 y = make_float2(s[i], s[i + 1]);
+                if (whole) y = __ffma2_rn(y, make_float2(scale, scale), make_float2(neg, neg));
+                else y = make_float2(y.x == -INFINITY ? y.x : fmaf(y.x, scale, neg), y.y == -INFINITY ? y.y : fmaf(y.y, scale, neg));
+                y = make_float2(ex2(y.x), ex2(y.y));
+                sum = __fadd2_rn(sum, y);
+                o[i / 2] = pack_bf16(y.x, y.y);
+            }
+            tc_st16(s_at + c / 2, o);
+        }
+        l += sum.x + sum.y;
+        tc_wait_st();
+    }
+};
+
+template <int MODE, int D, int NT>
+__global__ void __launch_bounds__(Layout<D, NT>::kWarps * 32, 1) prefix_kernel(const PrefixArgs p) {
+    using L = Layout<D, NT>;
+    extern __shared__ uint8_t dyn[];
+    __shared__ Barriers bar;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    pdl_launch_dependents();
+    const PrefixWork w = prefix_work(p, NT * kRows);
+    if (blockIdx.x == 0 && threadIdx.x == 0) {
+        const int32_t given = __ldg(p.prefix_length);
+        if (given < 0) report(p.own.dev_error, KVC8_DEV_BAD_LENGTH);
+        if (given > w.len && given >= 0) report(p.own.dev_error, KVC8_DEV_POS_BEYOND_TABLE);
+    }
+    const int64_t u0 = w.units * blockIdx.x / gridDim.x, u1 = w.units * (blockIdx.x + 1) / gridDim.x;
+    if (u0 < u1) {
+        if (warp == L::kWarps - 1) {
+            if (lane == 0) {
+                for (int i = 0; i < kStages; ++i) {
+                    mbar_init(smem_u32(&bar.k_full[i]), L::kDequantWarps);
+                    mbar_init(smem_u32(&bar.v_full[i]), L::kDequantWarps);
+                    mbar_init(smem_u32(&bar.k_free[i]), 1);
+                    mbar_init(smem_u32(&bar.v_free[i]), 1);
+                }
+                for (int i = 0; i < 2; ++i) {
+                    mbar_init(smem_u32(&bar.q_full[i]), 4);
+                    mbar_init(smem_u32(&bar.p_full[i]), 4);
+                    mbar_init(smem_u32(&bar.s_full[i]), 1);
+                    mbar_init(smem_u32(&bar.o_full[i]), 1);
+                }
+                mbar_init(smem_u32(&bar.drained), 1);
+                bar.stop = 0;
+                asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+                fence_async();
+            }
+            __syncwarp();
+            asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&bar.tmem)),
+                         "r"((uint32_t)L::kTmemCols)
+                         : "memory");
+            asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+        }
+        tc_fence_before();
+        __syncthreads();
+        tc_fence_after();
+        const uint32_t tmem = bar.tmem;
+        const uint32_t base = (smem_u32(dyn) + 1023u) & ~1023u;
+        const Prefix<MODE, D, NT> k{p, bar, base, w, u0, u1, lane};
+        if (warp < L::kSoftmaxWarps) {
+            k.softmax(warp, tmem);
+        } else if (warp < L::kSoftmaxWarps + L::kDequantWarps) {
+            k.dequantise(warp - L::kSoftmaxWarps);
+        } else if (lane == 0) {
+            k.products(tmem);
+        }
+        __syncwarp();
+        tc_fence_before();
+        __syncthreads();
+        tc_fence_after();
+        if (warp == L::kWarps - 1)
+            asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"((uint32_t)L::kTmemCols)
+                         : "memory");
+    }
+    // the merge waits for this grid and, through this wait, for the own positions' splits
+    pdl_wait_prior_grid();
+}
+
+// Joins a query row's partials: the prefix's segments and its own positions' splits.
+// A warp per query row, the lanes over channels.
+template <int D>
+__global__ void __launch_bounds__(kMergeThreads) merge_kernel(const PrefixArgs p, int rows_per_tile, int ctas) {
+    pdl_wait_prior_grid();
+    const AttnArgs &a = p.own;
+    constexpr int kPer = D / 32;
+    const int H = a.g.kv_heads, G = a.group, B = a.g.num_seqs;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int64_t row = (int64_t)blockIdx.x * (kMergeThreads / 32) + warp;
+    if (row >= (int64_t)B * H * G) return;
+    const int b = (int)(row / (H * G)), hj = (int)(row - (int64_t)b * H * G);
+    const int h = hj / G, j = hj - h * G;
+    const PrefixWork w = prefix_work(p, rows_per_tile);
+    const int64_t r = (int64_t)b * G + j;
+    const int64_t tile = (int64_t)h * w.tiles_per_head + r / rows_per_tile;
+    int parts = 0;
+    int64_t slot0 = 0;  // row of the first segment's partial; segments are a tile's rows apart
+    if (w.steps > 0) {
+        const int64_t first = tile * w.steps, last = first + w.steps - 1;
+        const int64_t c0 = ((first + 1) * ctas - 1) / w.units, c1 = ((last + 1) * ctas - 1) / w.units;
+        parts = (int)(c1 - c0 + 1);
+        slot0 = (tile + c0) * rows_per_tile + r % rows_per_tile;
+    }
+    const int32_t *ts = reinterpret_cast<const int32_t *>(static_cast<const char *>(a.plan) + plan_tile_start_at(B));
+    const int first = ts[b], own = ts[b + 1] - first;
+    const int total = parts + own;
+    auto at = [&](int i) -> int64_t {  // partial i as a row of its array
+        return i < parts ? slot0 + (int64_t)i * rows_per_tile : (((int64_t)first + i - parts) * H + h) * G + j;
+    };
+    float M = -INFINITY;
+    for (int i = lane; i < total; i += 32) M = fmaxf(M, (i < parts ? p.part_m : a.part_m)[at(i)]);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xFFFFFFFFu, M, o));
+    float acc[kPer], lsum = 0.0f;
+#pragma unroll
+    for (int e = 0; e < kPer; ++e) acc[e] = 0.0f;
+    for (int i0 = 0; i0 < total; i0 += 32) {
+        const int i = i0 + lane;
+        float f = 0.0f;
+        if (i < total) {
+            const float m = (i < parts ? p.part_m : a.part_m)[at(i)];
+            f = m == -INFINITY ? 0.0f : exp2f(m - M);
+            lsum += (i < parts ? p.part_l : a.part_l)[at(i)] * f;
+        }
+        const int n = min(32, total - i0);
+        for (int k = 0; k < n; ++k) {
+            const float fk = __shfl_sync(0xFFFFFFFFu, f, k);
+            if (fk == 0.0f) continue;
+            const float *po = (i0 + k < parts ? p.part_o : a.part_o) + at(i0 + k) * D + lane * kPer;
+            if (kPer == 4) {
+                const float4 v = *reinterpret_cast<const float4 *>(po);
+                acc[0] += fk * v.x, acc[1] += fk * v.y, acc[kPer - 2] += fk * v.z, acc[kPer - 1] += fk * v.w;
+            } else {
+                const float2 v = *reinterpret_cast<const float2 *>(po);
+                acc[0] += fk * v.x, acc[1] += fk * v.y;
+            }
         }
     }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) lsum += __shfl_xor_sync(0xFFFFFFFFu, lsum, o);
+    const float inv = lsum > 0.0f ? 1.0f / lsum : 0.0f;
+    uint16_t *dst = a.out + (int64_t)b * a.out_seq_stride + (int64_t)hj * a.out_head_stride + lane * kPer;
+#pragma unroll
+    for (int e = 0; e < kPer; e += 2) {
+        const uint32_t pr = pack_bf16(acc[e] * inv, acc[e + 1] * inv);
+        dst[e] = (uint16_t)(pr & 0xFFFFu);
+        dst[e + 1] = (uint16_t)(pr >> 16);
+    }
+}
+
+// Tiles of 128 query rows that a CTA holds: two when there are more rows than one.
+int tiles_per_cta(int64_t rows) { return rows > kRows ? 2 : 1; }
+
+struct Space {
+    size_t own, o, m, bytes;  // own partials first, then the prefix's O, m and l
+};
+
+Space space(const kvc8_geom &g, int group) {
+    const int64_t rows = (int64_t)g.num_seqs * group;
+    const int64_t per = (int64_t)tiles_per_cta(rows) * kRows;
+    const size_t slots = (size_t)((rows + per - 1) / per * g.kv_heads + kMaxCtas) * (size_t)per;
+    Space s;
+    s.own = attention_workspace_bytes(g, group);
+    s.o = s.own;
+    s.m = s.o + align_up(slots * g.head_dim * sizeof(float), kAlign);
+    s.bytes = s.m + 2 * align_up(slots * sizeof(float), kAlign);
+    return s;
+}
+
+template <typename... A>
+cudaError_t launch_dependent(void (*kern)(A...), int64_t grid, int threads, size_t smem, cudaStream_t stream,
+                             A... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)grid);
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+
+template <int MODE, int D, int NT>
+cudaError_t launch_variant(const PrefixArgs &p, cudaStream_t stream) {
+    using L = Layout<D, NT>;
+    auto kern = prefix_kernel<MODE, D, NT>;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kBytes);
+    if (e != cudaSuccess) return e;
+    const int64_t rows = (int64_t)p.own.g.num_seqs * p.own.group;
+    const int64_t tiles = (rows + NT * kRows - 1) / (NT * kRows) * p.own.g.kv_heads;
+    const int64_t steps = ((int64_t)p.max_prefix_blocks * p.own.g.block_size + kCols - 1) / kCols;
+    int64_t ctas = sm_count() < kMaxCtas ? sm_count() : kMaxCtas;
+    if (tiles * steps < ctas) ctas = tiles * steps;
+    e = launch_dependent(kern, ctas, L::kWarps * 32, (size_t)L::kBytes, stream, p);
+    if (e != cudaSuccess) return e;
+    const int64_t all = rows * p.own.g.kv_heads;
+    const int64_t per = kMergeThreads / 32;
+    return launch_dependent(merge_kernel<D>, (all + per - 1) / per, kMergeThreads, (size_t)0, stream, p,
+                            NT * kRows, (int)ctas);
 }
 
 template <int MODE>
 cudaError_t launch_mode(const PrefixArgs &p, cudaStream_t stream) {
-    const unsigned grid = (unsigned)(p.own.g.num_seqs * p.own.g.kv_heads);
-    if (p.own.g.head_dim == 64) prefix_kernel<MODE, 64><<<grid, kTile, 0, stream>>>(p);
-    else prefix_kernel<MODE, 128><<<grid, kTile, 0, stream>>>(p);
-    return cudaGetLastError();
+    const bool two = tiles_per_cta((int64_t)p.own.g.num_seqs * p.own.group) == 2;
+    if (p.own.g.head_dim == 64)
+        return two ? launch_variant<MODE, 64, 2>(p, stream) : launch_variant<MODE, 64, 1>(p, stream);
+    return two ? launch_variant<MODE, 128, 2>(p, stream) : launch_variant<MODE, 128, 1>(p, stream);
 }
 
 }  // namespace
 
-size_t shared_prefix_workspace_bytes(const kvc8_geom &, int, int32_t) { return kAlign; }
+size_t shared_prefix_workspace_bytes(const kvc8_geom &g, int group, int32_t) { return space(g, group).bytes; }
 
-cudaError_t launch_shared_prefix(const PrefixArgs &p, void *, cudaStream_t stream) {
+cudaError_t launch_shared_prefix(PrefixArgs p, void *workspace, cudaStream_t stream) {
+    const Space s = space(p.own.g, p.own.group);
+    char *ws = static_cast<char *>(workspace);
+    p.part_o = reinterpret_cast<float *>(ws + s.o);
+    p.part_m = reinterpret_cast<float *>(ws + s.m);
+    p.part_l = reinterpret_cast<float *>(ws + s.m + (s.bytes - s.m) / 2);
+    cudaError_t e = launch_attention_parts(p.own, workspace, stream);
+    if (e != cudaSuccess) return e;
     if (p.own.g.quant_mode == 0) return launch_mode<0>(p, stream);
     if (p.own.g.quant_mode == 1) return launch_mode<1>(p, stream);
     return launch_mode<2>(p, stream);

@@ -131,7 +131,19 @@ __device__ __forceinline__ void tc_st16(uint32_t addr, const uint32_t (&u)[16]) 
         "r"(u[9]), "r"(u[10]), "r"(u[11]), "r"(u[12]), "r"(u[13]), "r"(u[14]), "r"(u[15]), "r"(addr)
         : "memory");
 }
-__device__ __forceinline__ void tc_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+// The loads before it are done; r takes part so that nothing reads it earlier.
+__device__ __forceinline__ void tc_wait_ld(float (&r)[32]) {
+    uint32_t *u = reinterpret_cast<uint32_t *>(r);
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(u[0]), "+r"(u[1]), "+r"(u[2]), "+r"(u[3]), "+r"(u[4]), "+r"(u[5]), "+r"(u[6]),
+                   "+r"(u[7]), "+r"(u[8]), "+r"(u[9]), "+r"(u[10]), "+r"(u[11]), "+r"(u[12]),
+                   "+r"(u[13]), "+r"(u[14]), "+r"(u[15]), "+r"(u[16]), "+r"(u[17]), "+r"(u[18]),
+                   "+r"(u[19]), "+r"(u[20]), "+r"(u[21]), "+r"(u[22]), "+r"(u[23]), "+r"(u[24]),
+                   "+r"(u[25]), "+r"(u[26]), "+r"(u[27]), "+r"(u[28]), "+r"(u[29]), "+r"(u[30]),
+                   "+r"(u[31])
+                 :
+                 : "memory");
+}
 __device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 __device__ __forceinline__ float ex2(float x) {  // 2^x, -inf gives 0
@@ -151,9 +163,9 @@ __device__ __forceinline__ uint64_t operand_desc(uint32_t addr, uint32_t lbo) {
     return (uint64_t)((addr & 0x3FFFFu) >> 4) | ((uint64_t)(lbo >> 4) << 16) | ((uint64_t)(1024u >> 4) << 32) |
            (1ull << 46) | (2ull << 61);
 }
-// M = 128, bf16 operands, fp32 accumulators; b_mn: B is MN-major.
-constexpr uint32_t instr_desc(int n, bool b_mn) {
-    return (1u << 4) | (1u << 7) | (1u << 10) | ((b_mn ? 1u : 0u) << 16) | ((uint32_t)(n >> 3) << 17) |
+// M = 128, both operands bf16 or both fp16, fp32 accumulators; b_mn: B is MN-major.
+constexpr uint32_t instr_desc(int n, bool b_mn, bool bf16) {
+    return (1u << 4) | ((bf16 ? 1u : 0u) << 7) | ((bf16 ? 1u : 0u) << 10) | ((b_mn ? 1u : 0u) << 16) | ((uint32_t)(n >> 3) << 17) |
            ((uint32_t)(kRows >> 4) << 24);
 }
 
@@ -196,12 +208,37 @@ struct Layout {
     static constexpr int kTmemCols = NT * (kCols + D) > 256 ? 512 : 256;
 };
 
+// Two signed codes as bf16 (both are exact): byte c of the word beside 0x43 is 128 +
+// the low seven bits, or with the sign bit alone 128 or 256 (the exponent's lowest bit
+// is the sign's place); their difference is c.
+__device__ __forceinline__ uint32_t codes_bf16(uint32_t w, uint32_t select) {
+    const uint32_t x = __byte_perm(w, 0x43434343u, select);
+    uint32_t r;
+    asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(x & 0xFF7FFF7Fu), "r"(x & 0xFF80FF80u));
+    return r;
+}
+// Two codes as fp16: (c + 128) beside 0x64 is 1024 + c + 128.
+__device__ __forceinline__ uint32_t codes_fp16(uint32_t biased, uint32_t select) {
+    uint32_t r;
+    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(__byte_perm(biased, 0x64646464u, select)), "r"(0x64806480u));
+    return r;
+}
+__device__ __forceinline__ uint32_t pack_fp16(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
 struct Barriers {
     uint64_t k_full[kStages], k_free[kStages], v_full[kStages], v_free[kStages];
     uint64_t q_full[2], s_full[2], p_full[2], o_full[2], drained;
     uint32_t tmem;
     int32_t stop;
     uint2 valid[kMaskSlots];  // 8 bytes: valid positions of each group of 16
+    // modes 0 and 2: each position's (each group of 16's) key scale times the softmax
+    // scale, and value scale
+    alignas(16) float sk[kMaskSlots][kCols];
+    alignas(16) float sv[kMaskSlots][kCols];
 };
 
 template <int MODE, int D, int NT>
@@ -244,7 +281,6 @@ struct Prefix {
 
     struct Codes {
         uint4 c[kLoads];
-        float s;  // modes 0 and 2: the scale of position `lane` of the warp
     };
     struct Where {
         int64_t row[kGroups];  // cache row of each group's first position
@@ -275,8 +311,7 @@ struct Prefix {
         return x;
     }
 
-    __device__ __forceinline__ void load(const Where &x, const int8_t *cache, const float *scale,
-                                         Codes &c) const {
+    __device__ __forceinline__ void load(const Where &x, const int8_t *cache, Codes &c) const {
 #pragma unroll
         for (int i = 0; i < kLoads; ++i) {
             const int grp = i * kRpi / 16, at = i * kRpi % 16 + lane / kLpr;
@@ -284,40 +319,30 @@ struct Prefix {
             if (at < x.valid[grp])
                 c.c[i] = __ldg(reinterpret_cast<const uint4 *>(cache + (x.row[grp] + at) * D) + lane % kLpr);
         }
-        c.s = 0.0f;
-        if (MODE != 1) {
-            const int grp = kGroups == 1 ? 0 : lane >> 4;
-            const int64_t row = kGroups == 1 || grp == 0 ? x.row[0] : x.row[kGroups - 1];
-            const int64_t blk = kGroups == 1 || grp == 0 ? x.blk[0] : x.blk[kGroups - 1];
-            const int valid = kGroups == 1 || grp == 0 ? x.valid[0] : x.valid[kGroups - 1];
-            if (lane < kRpw && (lane & 15) < valid)
-                c.s = ld_nc_f32(scale + (MODE == 0 ? row + (lane & 15) : blk));
-        }
+    }
+    // Modes 0 and 2: the scale of position `lane` of the warp.
+    __device__ __forceinline__ float load_scale(const Where &x, const float *scale) const {
+        const bool second = kGroups == 2 && lane >= 16;
+        const int64_t row = second ? x.row[kGroups - 1] : x.row[0];
+        const int64_t blk = second ? x.blk[kGroups - 1] : x.blk[0];
+        const int valid = second ? x.valid[kGroups - 1] : x.valid[0];
+        return lane < kRpw && (lane & 15) < valid ? ld_nc_f32(scale + (MODE == 0 ? row + (lane & 15) : blk)) : 0.0f;
     }
 
-    // bf16(fl(fp32(code) * s)) of a position's 16 codes, as the gather rounds them
-    __device__ __forceinline__ static void expand(const uint4 &c, const float *s, uint32_t (&o)[8]) {
-        const uint32_t wd[4] = {c.x, c.y, c.z, c.w};
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const uint32_t wb = wd[i >> 1] ^ 0x80808080u;
-            const int e = 2 * (i & 1);
-            float2 x = make_float2(__uint_as_float(__byte_perm(wb, 0x4B000000u, 0x7440 + e)),
-                                   __uint_as_float(__byte_perm(wb, 0x4B000000u, 0x7441 + e)));
-            x = __fadd2_rn(x, make_float2(-8388736.0f, -8388736.0f));
-            x = __fmul2_rn(x, MODE == 1 ? make_float2(s[2 * i], s[2 * i + 1]) : make_float2(s[0], s[0]));
-            o[i] = pack_bf16(x.x, x.y);
-        }
-    }
-
-    __device__ __forceinline__ void store(const Codes &c, const float *chan, uint32_t tile, int dw) const {
+    // Codes into the swizzled tile, exact in bf16 (or fp16): the scales are multiplied in
+    // later, in fp32 (modes 0 and 2), or are in the query and the output (mode 1).
+    template <bool HALF>
+    __device__ __forceinline__ void store(const Codes &c, uint32_t tile, int dw) const {
 #pragma unroll
         for (int i = 0; i < kLoads; ++i) {
             const int r = i * kRpi + lane / kLpr;  // position of the warp
-            float row_s = 0.0f;
-            if (MODE != 1) row_s = __shfl_sync(0xFFFFFFFFu, c.s, r);
+            const uint32_t wd[4] = {c.c[i].x, c.c[i].y, c.c[i].z, c.c[i].w};
             uint32_t o[8];
-            expand(c.c[i], MODE == 1 ? chan : &row_s, o);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const uint32_t sel = (e & 1) ? 0x4342u : 0x4140u;
+                o[e] = HALF ? codes_fp16(wd[e >> 1] ^ 0x80808080u, sel) : codes_bf16(wd[e >> 1], sel);
+            }
             const int row = dw * kRpw + r, c8 = lane % kLpr;
             // 16-byte chunk n of a 128-byte row lies at n ^ (row mod 8); the lanes of the
             // second 64 channels write their two chunks in the other order, so that the
@@ -337,27 +362,31 @@ struct Prefix {
     __device__ void dequantise(int dw) const {
         const AttnArgs &a = p.own;
         int tile = (int)(u0 / w.steps), step = (int)(u0 - (int64_t)tile * w.steps);
-        int h = tile / w.tiles_per_head, h_scale = -1;
-        float kch[16], vch[16];  // mode 1: this lane's channels
-        Where x = find(h, step, dw);
+        Where x = find(tile / w.tiles_per_head, step, dw);
         Codes k, v;
-        load(x, a.k_cache, a.k_scale, k);
-        load(x, a.v_cache, a.v_scale, v);
+        float sk = 0.0f, sv = 0.0f;
+        auto scales = [&]() {
+            if (MODE == 1) return;
+            sk = load_scale(x, a.k_scale) * fabsf(a.scale_log2);
+            sv = load_scale(x, a.v_scale);
+        };
+        load(x, a.k_cache, k);
+        scales();
+        load(x, a.v_cache, v);
         int n = 0;
         for (int64_t u = u0; u < u1; ++u, ++n) {
-            if (MODE == 1 && h != h_scale) {
-                h_scale = h;
-                const int64_t at = (int64_t)h * D + (lane % kLpr) * 16;
-#pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    kch[i] = ld_nc_f32(a.k_scale + at + i);
-                    vch[i] = ld_nc_f32(a.v_scale + at + i);
-                }
-            }
             const int st = n % kStages;
             const uint32_t par = (uint32_t)(n / kStages) & 1u;
             if (!wait_warp(bar.k_free[st], par ^ 1u)) return;
-            store(k, kch, base + L::kK + st * L::kTileBytes, dw);
+            store<MODE == 1>(k, base + L::kK + st * L::kTileBytes, dw);
+            if (MODE == 0 && lane < kRpw) {
+                bar.sk[n % kMaskSlots][dw * kRpw + lane] = sk;
+                bar.sv[n % kMaskSlots][dw * kRpw + lane] = sv;
+            }
+            if (MODE == 2 && lane < kRpw && lane % 16 == 0) {
+                bar.sk[n % kMaskSlots][dw * kGroups + lane / 16] = sk;
+                bar.sv[n % kMaskSlots][dw * kGroups + lane / 16] = sv;
+            }
             if (lane == 0) {
                 uint8_t *vc = reinterpret_cast<uint8_t *>(&bar.valid[n % kMaskSlots]) + dw * kGroups;
 #pragma unroll
@@ -370,17 +399,17 @@ struct Prefix {
                 if (++step == w.steps) {
                     step = 0;
                     ++tile;
-                    h = tile / w.tiles_per_head;
                 }
-                x = find(h, step, dw);
-                load(x, a.k_cache, a.k_scale, k);
+                x = find(tile / w.tiles_per_head, step, dw);
+                load(x, a.k_cache, k);
+                scales();
             }
             if (!wait_warp(bar.v_free[st], par ^ 1u)) return;
-            store(v, vch, base + L::kV + st * L::kTileBytes, dw);
+            store<false>(v, base + L::kV + st * L::kTileBytes, dw);
             fence_async();
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_u32(&bar.v_full[st]));
-            if (u + 1 < u1) load(x, a.v_cache, a.v_scale, v);
+            if (u + 1 < u1) load(x, a.v_cache, v);
         }
     }
 
@@ -391,7 +420,7 @@ struct Prefix {
         for (int i = 0; i < D / 16; ++i) {
             const uint32_t at = (uint32_t)(i / 4) * (kRows * 128) + (uint32_t)(i % 4) * 32;
             tc_mma_ss(tmem + x * kCols, operand_desc(q + at, 16), operand_desc(k + at, 16),
-                      instr_desc(kCols, false), i > 0);
+                      instr_desc(kCols, false, MODE != 1), i > 0);
         }
     }
     __device__ __forceinline__ void pv(int x, int st, uint32_t tmem, bool acc) const {
@@ -399,7 +428,7 @@ struct Prefix {
 #pragma unroll
         for (int i = 0; i < kCols / 16; ++i)
             tc_mma_ts(tmem + NT * kCols + x * D, tmem + x * kCols + 8 * i,
-                      operand_desc(v + (uint32_t)i * 2048, kCols * 128), instr_desc(D, true),
+                      operand_desc(v + (uint32_t)i * 2048, kCols * 128), instr_desc(D, true, true),
                       acc || i > 0);
     }
 
@@ -457,7 +486,6 @@ struct Prefix {
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t s_at = tmem + lanes + x * kCols, o_at = tmem + lanes + NT * kCols + x * D;
         const int64_t rows = (int64_t)a.g.num_seqs * a.group;
-        const float scale = fabsf(a.scale_log2);
         const uint32_t flip = a.scale_log2 < 0.0f ? 0x80008000u : 0u;  // the sign goes to the query
         int n = 0;
         uint32_t seg = 0;
@@ -468,32 +496,17 @@ struct Prefix {
             const int64_t r0 = (tile - (int64_t)h * w.tiles_per_head) * (NT * kRows) + x * kRows + (warp & 3) * 32;
             const int64_t r = r0 + lane;
             const bool busy = r0 < rows;  // uniform in the warp: some row is a query's
-            {   // the query row into the swizzled tile
-                const uint32_t dst = base + L::kQ + x * L::kTileBytes + (uint32_t)row * 128;
-                const uint16_t *q = a.q;
-                if (r < rows) {
-                    const int b = (int)(r / a.group), j = (int)(r - (int64_t)b * a.group);
-                    q += (int64_t)b * a.q_seq_stride + (int64_t)(h * a.group + j) * a.q_head_stride;
-                }
-#pragma unroll
-                for (int i = 0; i < D / 8; ++i) {
-                    uint4 v = make_uint4(0u, 0u, 0u, 0u);
-                    if (r < rows) v = __ldg(reinterpret_cast<const uint4 *>(q) + i);
-                    const uint32_t at = dst + (uint32_t)(i / 8) * (kRows * 128) + (uint32_t)(((i % 8) ^ (row & 7)) << 4);
-                    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(v.x ^ flip),
-                                 "r"(v.y ^ flip), "r"(v.z ^ flip), "r"(v.w ^ flip)
-                                 : "memory");
-                }
-                fence_async();
-                tc_fence_before();  // the last segment's O is read
-                __syncwarp();
-                if (lane == 0) mbar_arrive(smem_u32(&bar.q_full[x]));
-            }
+            float scale = fabsf(a.scale_log2);  // of a score; modes 0 and 2 have it in sk
+            load_query(x, row, r, rows, h, flip, scale);
+            fence_async();
+            tc_fence_before();  // the last segment's O is read
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&bar.q_full[x]));
             float m = -INFINITY, l = 0.0f;
             for (int t = 0; t < count; ++t, ++n) {
                 if (!wait_warp(bar.s_full[x], (uint32_t)n & 1u)) return;
                 tc_fence_after();
-                if (busy) step(s_at, o_at, scale, t > 0, bar.valid[n % kMaskSlots], m, l);
+                if (busy) step(s_at, o_at, scale, t > 0, n % kMaskSlots, m, l);
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(smem_u32(&bar.p_full[x]));
@@ -507,11 +520,17 @@ struct Prefix {
                 for (int c = 0; c < D; c += 32) {
                     float o[32];
                     tc_ld32(o, o_at + c);
-                    tc_wait_ld();
+                    tc_wait_ld(o);
                     if (r < rows) {
 #pragma unroll
-                        for (int i = 0; i < 32; i += 4)
-                            *reinterpret_cast<float4 *>(po + c + i) = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+                        for (int i = 0; i < 32; i += 4) {
+                            float4 y = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+                            if (MODE == 1) {
+                                const float4 sv = __ldg(reinterpret_cast<const float4 *>(a.v_scale + (int64_t)h * D + c + i));
+                                y = make_float4(y.x * sv.x, y.y * sv.y, y.z * sv.z, y.w * sv.w);
+                            }
+                            *reinterpret_cast<float4 *>(po + c + i) = y;
+                        }
                     }
                     __syncwarp();
                 }
@@ -524,37 +543,166 @@ struct Prefix {
         }
     }
 
-    // One step of a row: S -> P, the running maximum m and sum l.
-    __device__ __forceinline__ void step(uint32_t s_at, uint32_t o_at, float scale, bool have_o,
-                                         uint2 valid, float &m, float &l) const {
-        const bool whole = valid.x == 0x10101010u && valid.y == 0x10101010u;
-        auto mask = [&](float (&s)[32], int c) {
-            if (whole) return;
-#pragma unroll
-            for (int i = 0; i < 32; ++i) {
-                const uint32_t wd = c < 64 ? valid.x : valid.y;
-                const int n = (int)(wd >> (((c % 64) / 16 + i / 16) * 8)) & 0xFF;
-                if (i % 16 >= n) s[i] = -INFINITY;
-            }
-        };
-        float top = -INFINITY;
-#pragma unroll
-        for (int c = 0; c < kCols; c += 32) {
-            float s[32];
-            tc_ld32(s, s_at + c);
-            tc_wait_ld();
-            mask(s, c);
-            float t0 = fmaxf(s[0], s[1]), t1 = fmaxf(s[2], s[3]);
-#pragma unroll
-            for (int i = 4; i < 32; i += 4) {
-                t0 = fmaxf(t0, fmaxf(s[i], s[i + 1]));
-                t1 = fmaxf(t1, fmaxf(s[i + 2], s[i + 3]));
-            }
-            top = fmaxf(top, fmaxf(t0, t1));
+    // Query row r of head h into row `row` of tile x.  Modes 0 and 2: the bf16 values.
+    // Mode 1: times the channels' key scales, in fp16 after a power of two that brings
+    // the row's largest to [1, 2) (returned in `scale`): eight times finer than bf16.
+    __device__ __forceinline__ void load_query(int x, int row, int64_t r, int64_t rows, int h, uint32_t flip,
+                                               float &scale) const {
+        const AttnArgs &a = p.own;
+        const uint32_t dst = base + L::kQ + x * L::kTileBytes + (uint32_t)row * 128;
+        const bool live = r < rows;
+        const uint16_t *q = a.q;
+        if (live) {
+            const int b = (int)(r / a.group), j = (int)(r - (int64_t)b * a.group);
+            q += (int64_t)b * a.q_seq_stride + (int64_t)(h * a.group + j) * a.q_head_stride;
         }
-        // scale 0 times -inf is no number: such a row has no position yet
-        const float mx = top == -INFINITY ? -INFINITY : top * scale;
+        const float *ks = a.k_scale + (MODE == 1 ? (int64_t)h * D : 0);
+        auto scaled = [&](uint32_t wd, int d) {
+            const float2 s = __ldg(reinterpret_cast<const float2 *>(ks + d));
+            return make_float2(__uint_as_float(wd << 16) * s.x, __uint_as_float(wd & 0xFFFF0000u) * s.y);
+        };
+        float turn = 1.0f;
+        if (MODE == 1) {
+            float top = 0.0f;
+#pragma unroll 4
+            for (int i = 0; i < D / 8; ++i) {
+                uint4 v = make_uint4(0u, 0u, 0u, 0u);
+                if (live) v = __ldg(reinterpret_cast<const uint4 *>(q) + i);
+                const uint32_t wd[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float2 y = scaled(wd[e], 8 * i + 2 * e);
+                    top = fmaxf(top, fmaxf(fabsf(y.x), fabsf(y.y)));
+                }
+            }
+            const int ex = min(100, max(-100, (int)(__float_as_uint(top) >> 23) - 127));
+            turn = __uint_as_float((uint32_t)(127 - ex) << 23);
+            scale *= __uint_as_float((uint32_t)(127 + ex) << 23);
+        }
+#pragma unroll 4
+        for (int i = 0; i < D / 8; ++i) {
+            uint4 v = make_uint4(0u, 0u, 0u, 0u);
+            if (live) v = __ldg(reinterpret_cast<const uint4 *>(q) + i);
+            uint32_t wd[4] = {v.x ^ flip, v.y ^ flip, v.z ^ flip, v.w ^ flip};
+            if (MODE == 1) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float2 y = scaled(wd[e], 8 * i + 2 * e);
+                    wd[e] = pack_fp16(y.x * turn, y.y * turn);
+                }
+            }
+            const uint32_t at = dst + (uint32_t)(i / 8) * (kRows * 128) + (uint32_t)(((i % 8) ^ (row & 7)) << 4);
+            asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(wd[0]), "r"(wd[1]), "r"(wd[2]),
+                         "r"(wd[3])
+                         : "memory");
+        }
+    }
+
+    // Scores of 32 positions from c on, in the log2 domain but for the factor `scale`
+    // of mode 1; positions that are left out become -inf.
+    __device__ __forceinline__ void scores(float (&s)[32], int c, int slot, bool whole) const {
+#pragma unroll
+        for (int i = 0; i < 32; i += 4) {
+            float4 f = make_float4(1.0f, 1.0f, 1.0f, 1.0f);
+            if (MODE == 0) f = *reinterpret_cast<const float4 *>(&bar.sk[slot][c + i]);
+            if (MODE == 2) f.x = f.y = f.z = f.w = bar.sk[slot][(c + i) / 16];
+            if (MODE != 1) {
+                const float2 y0 = __fmul2_rn(make_float2(s[i], s[i + 1]), make_float2(f.x, f.y));
+                const float2 y1 = __fmul2_rn(make_float2(s[i + 2], s[i + 3]), make_float2(f.z, f.w));
+                s[i] = y0.x, s[i + 1] = y0.y, s[i + 2] = y1.x, s[i + 3] = y1.y;
+            }
+        }
+        if (whole) return;
+        const uint32_t wd = c < 64 ? bar.valid[slot].x : bar.valid[slot].y;
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+            if (i % 16 >= (int)((wd >> (((c % 64) / 16 + i / 16) * 8)) & 0xFF)) s[i] = -INFINITY;
+    }
+
+    __device__ __forceinline__ static float top_of(const float (&s)[32]) {
+        float t0 = fmaxf(s[0], s[1]), t1 = fmaxf(s[2], s[3]);
+#pragma unroll
+        for (int i = 4; i < 32; i += 4) {
+            t0 = fmaxf(t0, fmaxf(s[i], s[i + 1]));
+            t1 = fmaxf(t1, fmaxf(s[i + 2], s[i + 3]));
+        }
+        return fmaxf(t0, t1);
+    }
+
+    // Weights of 32 positions into P's columns, summed up.
+    __device__ __forceinline__ void weights(float (&s)[32], int c, int slot, bool whole, float scale, float neg,
+                                            uint32_t s_at, float2 &sum) const {
+        uint32_t o[16];
+        if (MODE == 1 || !whole) {
+            scores(s, c, slot, whole);
+#pragma unroll
+            for (int i = 0; i < 32; i += 2) {
+                float2 y = make_float2(s[i], s[i + 1]);
+                if (MODE == 1 && !whole) {  // 0 times -inf is no number
+                    y.x = y.x == -INFINITY ? y.x : fmaf(y.x, scale, neg);
+                    y.y = y.y == -INFINITY ? y.y : fmaf(y.y, scale, neg);
+                } else if (MODE == 1) {
+                    y = __ffma2_rn(y, make_float2(scale, scale), make_float2(neg, neg));
+                } else {
+                    y = __fadd2_rn(y, make_float2(neg, neg));
+                }
+                s[i] = y.x, s[i + 1] = y.y;
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 32; i += 4) {
+                float4 f;
+                if (MODE == 0) f = *reinterpret_cast<const float4 *>(&bar.sk[slot][c + i]);
+                else f.x = f.y = f.z = f.w = bar.sk[slot][(c + i) / 16];
+                const float2 y0 = __ffma2_rn(make_float2(s[i], s[i + 1]), make_float2(f.x, f.y), make_float2(neg, neg));
+                const float2 y1 = __ffma2_rn(make_float2(s[i + 2], s[i + 3]), make_float2(f.z, f.w), make_float2(neg, neg));
+                s[i] = y0.x, s[i + 1] = y0.y, s[i + 2] = y1.x, s[i + 3] = y1.y;
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 32; i += 4) {
+            float2 y0 = make_float2(ex2(s[i]), ex2(s[i + 1])), y1 = make_float2(ex2(s[i + 2]), ex2(s[i + 3]));
+            sum = __fadd2_rn(sum, __fadd2_rn(y0, y1));
+            if (MODE != 1) {
+                float4 f;
+                if (MODE == 0) f = *reinterpret_cast<const float4 *>(&bar.sv[slot][c + i]);
+                else f.x = f.y = f.z = f.w = bar.sv[slot][(c + i) / 16];
+                y0 = __fmul2_rn(y0, make_float2(f.x, f.y));
+                y1 = __fmul2_rn(y1, make_float2(f.z, f.w));
+            }
+            o[i / 2] = pack_bf16(y0.x, y0.y);
+            o[i / 2 + 1] = pack_bf16(y1.x, y1.y);
+        }
+        tc_st16(s_at + c / 2, o);
+    }
+
+    // One step of a row: S -> P, the running maximum m and sum l.  S is read twice, 32
+    // columns ahead of the arithmetic (128 registers hold no more).
+    __device__ __forceinline__ void step(uint32_t s_at, uint32_t o_at, float scale, bool have_o, int slot,
+                                         float &m, float &l) const {
+        const bool whole = bar.valid[slot].x == 0x10101010u && bar.valid[slot].y == 0x10101010u;
+        float a[32], b[32];
+        tc_ld32(a, s_at);
+        tc_wait_ld(a);
+        tc_ld32(b, s_at + 32);
+        scores(a, 0, slot, whole);
+        float top = top_of(a);
+        tc_wait_ld(b);
+        tc_ld32(a, s_at + 64);
+        scores(b, 32, slot, whole);
+        top = fmaxf(top, top_of(b));
+        tc_wait_ld(a);
+        tc_ld32(b, s_at + 96);
+        scores(a, 64, slot, whole);
+        top = fmaxf(top, top_of(a));
+        tc_wait_ld(b);
+        tc_ld32(a, s_at);
+        scores(b, 96, slot, whole);
+        top = fmaxf(top, top_of(b));
+        // mode 1: scale 0 times -inf is no number; such a row has no position yet
+        const float mx = MODE != 1 || top == -INFINITY ? top : top * scale;
         const bool moves = mx > m + kLazy || (m == -INFINITY && mx > m);
+        tc_wait_ld(a);
         if (__any_sync(0xFFFFFFFFu, moves)) {
             const float f = moves ? ex2(m - mx) : 1.0f;  // 0 where there was nothing yet
             if (moves) m = mx;
@@ -564,7 +712,7 @@ struct Prefix {
                 for (int c = 0; c < D; c += 32) {
                     float o[32];
                     tc_ld32(o, o_at + c);
-                    tc_wait_ld();
+                    tc_wait_ld(o);
 #pragma unroll
                     for (int i = 0; i < 32; ++i) o[i] *= f;
                     tc_st32(o_at + c, o);
@@ -573,24 +721,16 @@ struct Prefix {
         }
         const float neg = m == -INFINITY ? 0.0f : -m;
         float2 sum = make_float2(0.0f, 0.0f);
-#pragma unroll
-        for (int c = 0; c < kCols; c += 32) {
-            float s[32];
-            tc_ld32(s, s_at + c);
-            tc_wait_ld();
-            mask(s, c);
-            uint32_t o[16];
-#pragma unroll
-            for (int i = 0; i < 32; i += 2) {
-                float2 y = make_float2(s[i], s[i + 1]);
-                if (whole) y = __ffma2_rn(y, make_float2(scale, scale), make_float2(neg, neg));
-                else y = make_float2(y.x == -INFINITY ? y.x : fmaf(y.x, scale, neg), y.y == -INFINITY ? y.y : fmaf(y.y, scale, neg));
-                y = make_float2(ex2(y.x), ex2(y.y));
-                sum = __fadd2_rn(sum, y);
-                o[i / 2] = pack_bf16(y.x, y.y);
-            }
-            tc_st16(s_at + c / 2, o);
-        }
+        tc_ld32(b, s_at + 32);
+        weights(a, 0, slot, whole, scale, neg, s_at, sum);
+        tc_wait_ld(b);
+        tc_ld32(a, s_at + 64);
+        weights(b, 32, slot, whole, scale, neg, s_at, sum);
+        tc_wait_ld(a);
+        tc_ld32(b, s_at + 96);
+        weights(a, 64, slot, whole, scale, neg, s_at, sum);
+        tc_wait_ld(b);
+        weights(b, 96, slot, whole, scale, neg, s_at, sum);
         l += sum.x + sum.y;
         tc_wait_st();
     }

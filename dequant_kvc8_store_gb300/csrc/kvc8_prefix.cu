@@ -21,7 +21,7 @@
 //   dequantise  codes from global memory a tile ahead in registers, K' and V' as bf16
 //               into a two-stage ring in the 128-byte swizzle (K' K-major, V' as the
 //               MN-major B operand of the same rows)
-//   mma         one thread issues both products; with two tiles one's products run
+//   mma         one lane issues both products; with two tiles one's products run
 //               while the other's softmax does
 // The (tile, 128 positions) units are cut evenly over the CTAs (one per SM): CTA i
 // takes units [i U / C, (i + 1) U / C) and leaves one partial per tile it touches, in
@@ -73,26 +73,36 @@ __device__ __forceinline__ void tc_fence_before() {
 __device__ __forceinline__ void tc_fence_after() {
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
 }
-__device__ __forceinline__ void tc_commit(uint32_t bar) {
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
-                 : "memory");
+// The products are issued by one elected lane of a warp that stays converged, so that
+// addresses and descriptors are uniform.
+__device__ __forceinline__ uint32_t elect_lane() {
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void tc_commit(uint32_t bar, uint32_t leader) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %1, 0;\n\t"
+        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar),
+        "r"(leader)
+        : "memory");
 }
 // D[tmem] (+)= A[smem] B[smem]
-__device__ __forceinline__ void tc_mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
-                                          uint32_t acc) {
+__device__ __forceinline__ void tc_mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc,
+                                          uint32_t leader) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"(acc)
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %4, 0;\n\tsetp.ne.u32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(acc), "r"(leader)
         : "memory");
 }
 // D[tmem] (+)= A[tmem] B[smem]
-__device__ __forceinline__ void tc_mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
-                                          uint32_t acc) {
+__device__ __forceinline__ void tc_mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc,
+                                          uint32_t leader) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-        "r"(a), "l"(b), "r"(idesc), "r"(acc)
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %4, 0;\n\tsetp.ne.u32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"(acc), "r"(leader)
         : "memory");
 }
 // 32 columns of this thread's row of tensor memory.
@@ -110,17 +120,16 @@ __device__ __forceinline__ void tc_ld32(float (&r)[32], uint32_t addr) {
         : "r"(addr)
         : "memory");
 }
-__device__ __forceinline__ void tc_st32(uint32_t addr, const float (&r)[32]) {
-    const uint32_t *u = reinterpret_cast<const uint32_t *>(r);
+__device__ __forceinline__ void tc_ld16(float (&r)[16], uint32_t addr) {
+    uint32_t *u = reinterpret_cast<uint32_t *>(r);
     asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], "
-        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31};" ::"r"(u[0]),
-        "r"(u[1]), "r"(u[2]), "r"(u[3]), "r"(u[4]), "r"(u[5]), "r"(u[6]), "r"(u[7]), "r"(u[8]),
-        "r"(u[9]), "r"(u[10]), "r"(u[11]), "r"(u[12]), "r"(u[13]), "r"(u[14]), "r"(u[15]),
-        "r"(u[16]), "r"(u[17]), "r"(u[18]), "r"(u[19]), "r"(u[20]), "r"(u[21]), "r"(u[22]),
-        "r"(u[23]), "r"(u[24]), "r"(u[25]), "r"(u[26]), "r"(u[27]), "r"(u[28]), "r"(u[29]),
-        "r"(u[30]), "r"(u[31]), "r"(addr)
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]), "=r"(u[4]), "=r"(u[5]), "=r"(u[6]),
+          "=r"(u[7]), "=r"(u[8]), "=r"(u[9]), "=r"(u[10]), "=r"(u[11]), "=r"(u[12]), "=r"(u[13]),
+          "=r"(u[14]), "=r"(u[15])
+        : "r"(addr)
         : "memory");
 }
 __device__ __forceinline__ void tc_st16(uint32_t addr, const uint32_t (&u)[16]) {
@@ -144,6 +153,11 @@ __device__ __forceinline__ void tc_wait_ld(float (&r)[32]) {
                  :
                  : "memory");
 }
+// This warpgroup's registers per thread from here on.
+template <int N>
+__device__ __forceinline__ void reg_give() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
+template <int N>
+__device__ __forceinline__ void reg_take() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
 __device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 __device__ __forceinline__ float ex2(float x) {  // 2^x, -inf gives 0
@@ -196,7 +210,14 @@ template <int D, int NT>
 struct Layout {
     static constexpr int kDequantWarps = NT == 1 ? 8 : 4;
     static constexpr int kSoftmaxWarps = 4 * NT;
-    static constexpr int kWarps = kSoftmaxWarps + kDequantWarps + 1;
+    static constexpr int kMmaWarp = kSoftmaxWarps + kDequantWarps;  // three idle warps behind it
+    static constexpr int kThreads = 512;
+    // registers per thread: a softmax thread holds a row's 128 scores
+    static constexpr int kSoftmaxRegs = 184, kDequantRegs = NT == 1 ? 112 : 104, kMmaRegs = 40;
+    static constexpr int kLaunchRegs = 128;
+    static_assert(32 * (kSoftmaxWarps * kSoftmaxRegs + kDequantWarps * kDequantRegs + 4 * kMmaRegs) <=
+                      kThreads * kLaunchRegs,
+                  "the warpgroups' registers are the block's");
     static constexpr int kTileBytes = kRows * D * 2;  // Q tile, K' or V' stage
     static constexpr int kQ = 0;
     static constexpr int kK = NT * kTileBytes;
@@ -413,26 +434,26 @@ struct Prefix {
         }
     }
 
-    // ---- products (one thread) --------------------------------------------------
-    __device__ __forceinline__ void qk(int x, int st, uint32_t tmem) const {
-        const uint32_t q = base + L::kQ + x * L::kTileBytes, k = base + L::kK + st * L::kTileBytes;
+    // ---- products (a warp, one lane issuing) --------------------------------------------------
+    // Descriptors of the first operand block; a later one is (bytes >> 4) further on.
+    __device__ __forceinline__ void qk(int x, int st, uint32_t tmem, uint32_t leader) const {
+        const uint64_t q = operand_desc(base + L::kQ, 16) + (uint64_t)(x * (L::kTileBytes >> 4));
+        const uint64_t k = operand_desc(base + L::kK, 16) + (uint64_t)(st * (L::kTileBytes >> 4));
 #pragma unroll
         for (int i = 0; i < D / 16; ++i) {
-            const uint32_t at = (uint32_t)(i / 4) * (kRows * 128) + (uint32_t)(i % 4) * 32;
-            tc_mma_ss(tmem + x * kCols, operand_desc(q + at, 16), operand_desc(k + at, 16),
-                      instr_desc(kCols, false, MODE != 1), i > 0);
+            const uint64_t at = (uint64_t)(((i / 4) * (kRows * 128) + (i % 4) * 32) >> 4);
+            tc_mma_ss(tmem + x * kCols, q + at, k + at, instr_desc(kCols, false, MODE != 1), i > 0, leader);
         }
     }
-    __device__ __forceinline__ void pv(int x, int st, uint32_t tmem, bool acc) const {
-        const uint32_t v = base + L::kV + st * L::kTileBytes;
+    __device__ __forceinline__ void pv(int x, int st, uint32_t tmem, bool acc, uint32_t leader) const {
+        const uint64_t v = operand_desc(base + L::kV, kCols * 128) + (uint64_t)(st * (L::kTileBytes >> 4));
 #pragma unroll
         for (int i = 0; i < kCols / 16; ++i)
-            tc_mma_ts(tmem + NT * kCols + x * D, tmem + x * kCols + 8 * i,
-                      operand_desc(v + (uint32_t)i * 2048, kCols * 128), instr_desc(D, true, true),
-                      acc || i > 0);
+            tc_mma_ts(tmem + NT * kCols + x * D, tmem + x * kCols + 8 * i, v + (uint64_t)(i * (2048 >> 4)),
+                      instr_desc(D, true, true), acc || i > 0, leader);
     }
 
-    __device__ bool products_loop(uint32_t tmem) const {
+    __device__ bool products_loop(uint32_t tmem, uint32_t leader) const {
         int n = 0, seg = 0, steps_done = 0;
         for (int64_t u = u0; u < u1; ++seg) {
             const int64_t tile = u / w.steps;
@@ -446,20 +467,20 @@ struct Prefix {
 #pragma unroll
                 for (int x = 0; x < NT; ++x) {
                     if (t >= 0) {
-                        if (!wait(bar.p_full[x], (uint32_t)steps_done & 1u)) return false;
-                        if (x == 0 && !wait(bar.v_full[st], par)) return false;
+                        if (!wait_warp(bar.p_full[x], (uint32_t)steps_done & 1u)) return false;
+                        if (x == 0 && !wait_warp(bar.v_full[st], par)) return false;
                         tc_fence_after();
-                        pv(x, st, tmem, t > 0);
-                        if (x == NT - 1) tc_commit(smem_u32(&bar.v_free[st]));
-                        if (!more) tc_commit(smem_u32(&bar.o_full[x]));
+                        pv(x, st, tmem, t > 0, leader);
+                        if (x == NT - 1) tc_commit(smem_u32(&bar.v_free[st]), leader);
+                        if (!more) tc_commit(smem_u32(&bar.o_full[x]), leader);
                     }
                     if (more) {
-                        if (t < 0 && !wait(bar.q_full[x], (uint32_t)seg & 1u)) return false;
-                        if (x == 0 && !wait(bar.k_full[st1], par1)) return false;
+                        if (t < 0 && !wait_warp(bar.q_full[x], (uint32_t)seg & 1u)) return false;
+                        if (x == 0 && !wait_warp(bar.k_full[st1], par1)) return false;
                         tc_fence_after();
-                        qk(x, st1, tmem);
-                        tc_commit(smem_u32(&bar.s_full[x]));
-                        if (x == NT - 1) tc_commit(smem_u32(&bar.k_free[st1]));
+                        qk(x, st1, tmem, leader);
+                        tc_commit(smem_u32(&bar.s_full[x]), leader);
+                        if (x == NT - 1) tc_commit(smem_u32(&bar.k_free[st1]), leader);
                     }
                 }
                 if (t >= 0) ++steps_done;
@@ -471,9 +492,10 @@ struct Prefix {
     }
 
     __device__ void products(uint32_t tmem) const {
-        products_loop(tmem);
+        const uint32_t leader = elect_lane();
+        products_loop(tmem, leader);
         // what was issued is done before the tensor memory is freed
-        tc_commit(smem_u32(&bar.drained));
+        tc_commit(smem_u32(&bar.drained), leader);
         const long long t0 = clock64();
         while (!mbar_try(smem_u32(&bar.drained), 0))
             if (clock64() - t0 > kWaitCycles) break;
@@ -496,7 +518,9 @@ struct Prefix {
             const int64_t r0 = (tile - (int64_t)h * w.tiles_per_head) * (NT * kRows) + x * kRows + (warp & 3) * 32;
             const int64_t r = r0 + lane;
             const bool busy = r0 < rows;  // uniform in the warp: some row is a query's
-            float scale = fabsf(a.scale_log2);  // of a score; modes 0 and 2 have it in sk
+            // of a score; modes 0 and 2 have it in sk.  Never 0: 0 times -inf is no number,
+            // and scores are far too small for 2^-126 to show
+            float scale = fmaxf(fabsf(a.scale_log2), 0x1p-126f);
             load_query(x, row, r, rows, h, flip, scale);
             fence_async();
             tc_fence_before();  // the last segment's O is read
@@ -577,7 +601,7 @@ struct Prefix {
             }
             const int ex = min(100, max(-100, (int)(__float_as_uint(top) >> 23) - 127));
             turn = __uint_as_float((uint32_t)(127 - ex) << 23);
-            scale *= __uint_as_float((uint32_t)(127 + ex) << 23);
+            scale = fmaxf(scale * __uint_as_float((uint32_t)(127 + ex) << 23), 0x1p-126f);
         }
 #pragma unroll 4
         for (int i = 0; i < D / 8; ++i) {
@@ -599,27 +623,25 @@ struct Prefix {
     }
 
     // Scores of 32 positions from c on, in the log2 domain but for the factor `scale`
-    // of mode 1; positions that are left out become -inf.
-    __device__ __forceinline__ void scores(float (&s)[32], int c, int slot, bool whole) const {
+    // of mode 1; positions that are left out become -inf.  Returns the largest.
+    __device__ __forceinline__ float scores(float (&s)[32], int c, int slot, bool whole) const {
+        if (MODE != 1) {
 #pragma unroll
-        for (int i = 0; i < 32; i += 4) {
-            float4 f = make_float4(1.0f, 1.0f, 1.0f, 1.0f);
-            if (MODE == 0) f = *reinterpret_cast<const float4 *>(&bar.sk[slot][c + i]);
-            if (MODE == 2) f.x = f.y = f.z = f.w = bar.sk[slot][(c + i) / 16];
-            if (MODE != 1) {
+            for (int i = 0; i < 32; i += 4) {
+                float4 f;
+                if (MODE == 0) f = *reinterpret_cast<const float4 *>(&bar.sk[slot][c + i]);
+                else f.x = f.y = f.z = f.w = bar.sk[slot][(c + i) / 16];
                 const float2 y0 = __fmul2_rn(make_float2(s[i], s[i + 1]), make_float2(f.x, f.y));
                 const float2 y1 = __fmul2_rn(make_float2(s[i + 2], s[i + 3]), make_float2(f.z, f.w));
                 s[i] = y0.x, s[i + 1] = y0.y, s[i + 2] = y1.x, s[i + 3] = y1.y;
             }
         }
-        if (whole) return;
-        const uint32_t wd = c < 64 ? bar.valid[slot].x : bar.valid[slot].y;
+        if (!whole) {
+            const uint32_t wd = c < 64 ? bar.valid[slot].x : bar.valid[slot].y;
 #pragma unroll
-        for (int i = 0; i < 32; ++i)
-            if (i % 16 >= (int)((wd >> (((c % 64) / 16 + i / 16) * 8)) & 0xFF)) s[i] = -INFINITY;
-    }
-
-    __device__ __forceinline__ static float top_of(const float (&s)[32]) {
+            for (int i = 0; i < 32; ++i)
+                if (i % 16 >= (int)((wd >> (((c % 64) / 16 + i / 16) * 8)) & 0xFF)) s[i] = -INFINITY;
+        }
         float t0 = fmaxf(s[0], s[1]), t1 = fmaxf(s[2], s[3]);
 #pragma unroll
         for (int i = 4; i < 32; i += 4) {
@@ -630,38 +652,22 @@ struct Prefix {
     }
 
     // Weights of 32 positions into P's columns, summed up.
-    __device__ __forceinline__ void weights(float (&s)[32], int c, int slot, bool whole, float scale, float neg,
-                                            uint32_t s_at, float2 &sum) const {
+    __device__ __forceinline__ void weights(float (&s)[32], int c, int slot, float scale, float neg, uint32_t s_at,
+                                            float2 &sum) const {
         uint32_t o[16];
-        if (MODE == 1 || !whole) {
-            scores(s, c, slot, whole);
-#pragma unroll
-            for (int i = 0; i < 32; i += 2) {
-                float2 y = make_float2(s[i], s[i + 1]);
-                if (MODE == 1 && !whole) {  // 0 times -inf is no number
-                    y.x = y.x == -INFINITY ? y.x : fmaf(y.x, scale, neg);
-                    y.y = y.y == -INFINITY ? y.y : fmaf(y.y, scale, neg);
-                } else if (MODE == 1) {
-                    y = __ffma2_rn(y, make_float2(scale, scale), make_float2(neg, neg));
-                } else {
-                    y = __fadd2_rn(y, make_float2(neg, neg));
-                }
-                s[i] = y.x, s[i + 1] = y.y;
-            }
-        } else {
-#pragma unroll
-            for (int i = 0; i < 32; i += 4) {
-                float4 f;
-                if (MODE == 0) f = *reinterpret_cast<const float4 *>(&bar.sk[slot][c + i]);
-                else f.x = f.y = f.z = f.w = bar.sk[slot][(c + i) / 16];
-                const float2 y0 = __ffma2_rn(make_float2(s[i], s[i + 1]), make_float2(f.x, f.y), make_float2(neg, neg));
-                const float2 y1 = __ffma2_rn(make_float2(s[i + 2], s[i + 3]), make_float2(f.z, f.w), make_float2(neg, neg));
-                s[i] = y0.x, s[i + 1] = y0.y, s[i + 2] = y1.x, s[i + 3] = y1.y;
-            }
-        }
 #pragma unroll
         for (int i = 0; i < 32; i += 4) {
-            float2 y0 = make_float2(ex2(s[i]), ex2(s[i + 1])), y1 = make_float2(ex2(s[i + 2]), ex2(s[i + 3]));
+            float2 y0 = make_float2(s[i], s[i + 1]), y1 = make_float2(s[i + 2], s[i + 3]);
+            if (MODE == 1) {
+                const float2 f = make_float2(scale, scale), g = make_float2(neg, neg);
+                y0 = __ffma2_rn(y0, f, g);
+                y1 = __ffma2_rn(y1, f, g);
+            } else {
+                y0 = __fadd2_rn(y0, make_float2(neg, neg));
+                y1 = __fadd2_rn(y1, make_float2(neg, neg));
+            }
+            y0 = make_float2(ex2(y0.x), ex2(y0.y));
+            y1 = make_float2(ex2(y1.x), ex2(y1.y));
             sum = __fadd2_rn(sum, __fadd2_rn(y0, y1));
             if (MODE != 1) {
                 float4 f;
@@ -676,68 +682,54 @@ struct Prefix {
         tc_st16(s_at + c / 2, o);
     }
 
-    // One step of a row: S -> P, the running maximum m and sum l.  S is read twice, 32
-    // columns ahead of the arithmetic (128 registers hold no more).
+    // One step of a row: S -> P, the running maximum m and sum l.
     __device__ __forceinline__ void step(uint32_t s_at, uint32_t o_at, float scale, bool have_o, int slot,
                                          float &m, float &l) const {
         const bool whole = bar.valid[slot].x == 0x10101010u && bar.valid[slot].y == 0x10101010u;
-        float a[32], b[32];
-        tc_ld32(a, s_at);
-        tc_wait_ld(a);
-        tc_ld32(b, s_at + 32);
-        scores(a, 0, slot, whole);
-        float top = top_of(a);
-        tc_wait_ld(b);
-        tc_ld32(a, s_at + 64);
-        scores(b, 32, slot, whole);
-        top = fmaxf(top, top_of(b));
-        tc_wait_ld(a);
-        tc_ld32(b, s_at + 96);
-        scores(a, 64, slot, whole);
-        top = fmaxf(top, top_of(a));
-        tc_wait_ld(b);
-        tc_ld32(a, s_at);
-        scores(b, 96, slot, whole);
-        top = fmaxf(top, top_of(b));
-        // mode 1: scale 0 times -inf is no number; such a row has no position yet
-        const float mx = MODE != 1 || top == -INFINITY ? top : top * scale;
+        float s0[32], s1[32], s2[32], s3[32];
+        tc_ld32(s0, s_at);
+        tc_ld32(s1, s_at + 32);
+        tc_ld32(s2, s_at + 64);
+        tc_ld32(s3, s_at + 96);
+        tc_wait_ld(s0);
+        tc_wait_ld(s1);
+        tc_wait_ld(s2);
+        tc_wait_ld(s3);
+        const float t0 = scores(s0, 0, slot, whole), t1 = scores(s1, 32, slot, whole);
+        const float t2 = scores(s2, 64, slot, whole), t3 = scores(s3, 96, slot, whole);
+        const float top = fmaxf(fmaxf(t0, t1), fmaxf(t2, t3));
+        // mode 1: a scale of 0 times -inf would be no number, so the factor is never 0
+        const float mx = MODE == 1 ? top * scale : top;
         const bool moves = mx > m + kLazy || (m == -INFINITY && mx > m);
-        tc_wait_ld(a);
         if (__any_sync(0xFFFFFFFFu, moves)) {
             const float f = moves ? ex2(m - mx) : 1.0f;  // 0 where there was nothing yet
             if (moves) m = mx;
             l *= f;
             if (have_o) {
 #pragma unroll
-                for (int c = 0; c < D; c += 32) {
-                    float o[32];
-                    tc_ld32(o, o_at + c);
-                    tc_wait_ld(o);
+                for (int c = 0; c < D; c += 16) {
+                    float o[16];
+                    tc_ld16(o, o_at + c);
+                    uint32_t y[16];
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) o[i] *= f;
-                    tc_st32(o_at + c, o);
+                    for (int i = 0; i < 16; ++i) y[i] = __float_as_uint(o[i] * f);
+                    tc_st16(o_at + c, y);
                 }
             }
         }
         const float neg = m == -INFINITY ? 0.0f : -m;
         float2 sum = make_float2(0.0f, 0.0f);
-        tc_ld32(b, s_at + 32);
-        weights(a, 0, slot, whole, scale, neg, s_at, sum);
-        tc_wait_ld(b);
-        tc_ld32(a, s_at + 64);
-        weights(b, 32, slot, whole, scale, neg, s_at, sum);
-        tc_wait_ld(a);
-        tc_ld32(b, s_at + 96);
-        weights(a, 64, slot, whole, scale, neg, s_at, sum);
-        tc_wait_ld(b);
-        weights(b, 96, slot, whole, scale, neg, s_at, sum);
+        weights(s0, 0, slot, scale, neg, s_at, sum);
+        weights(s1, 32, slot, scale, neg, s_at, sum);
+        weights(s2, 64, slot, scale, neg, s_at, sum);
+        weights(s3, 96, slot, scale, neg, s_at, sum);
         l += sum.x + sum.y;
         tc_wait_st();
     }
 };
 
 template <int MODE, int D, int NT>
-__global__ void __launch_bounds__(Layout<D, NT>::kWarps * 32, 1) prefix_kernel(const PrefixArgs p) {
+__global__ void __launch_bounds__(Layout<D, NT>::kThreads, 1) prefix_kernel(const PrefixArgs p) {
     using L = Layout<D, NT>;
     extern __shared__ uint8_t dyn[];
     __shared__ Barriers bar;
@@ -751,7 +743,7 @@ __global__ void __launch_bounds__(Layout<D, NT>::kWarps * 32, 1) prefix_kernel(c
     }
     const int64_t u0 = w.units * blockIdx.x / gridDim.x, u1 = w.units * (blockIdx.x + 1) / gridDim.x;
     if (u0 < u1) {
-        if (warp == L::kWarps - 1) {
+        if (warp == L::kMmaWarp) {
             if (lane == 0) {
                 for (int i = 0; i < kStages; ++i) {
                     mbar_init(smem_u32(&bar.k_full[i]), L::kDequantWarps);
@@ -782,18 +774,21 @@ __global__ void __launch_bounds__(Layout<D, NT>::kWarps * 32, 1) prefix_kernel(c
         const uint32_t tmem = bar.tmem;
         const uint32_t base = (smem_u32(dyn) + 1023u) & ~1023u;
         const Prefix<MODE, D, NT> k{p, bar, base, w, u0, u1, lane};
-        if (warp < L::kSoftmaxWarps) {
-            k.softmax(warp, tmem);
-        } else if (warp < L::kSoftmaxWarps + L::kDequantWarps) {
+        if (warp >= L::kMmaWarp) {
+            reg_give<L::kMmaRegs>();
+            if (warp == L::kMmaWarp) k.products(tmem);
+        } else if (warp >= L::kSoftmaxWarps) {
+            reg_give<L::kDequantRegs>();
             k.dequantise(warp - L::kSoftmaxWarps);
-        } else if (lane == 0) {
-            k.products(tmem);
+        } else {
+            reg_take<L::kSoftmaxRegs>();
+            k.softmax(warp, tmem);
         }
         __syncwarp();
         tc_fence_before();
         __syncthreads();
         tc_fence_after();
-        if (warp == L::kWarps - 1)
+        if (warp == L::kMmaWarp)
             asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"((uint32_t)L::kTmemCols)
                          : "memory");
     }
@@ -847,17 +842,15 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const PrefixArgs p
             lsum += (i < parts ? p.part_l : a.part_l)[at(i)] * f;
         }
         const int n = min(32, total - i0);
+#pragma unroll 8
         for (int k = 0; k < n; ++k) {
             const float fk = __shfl_sync(0xFFFFFFFFu, f, k);
-            if (fk == 0.0f) continue;
             const float *po = (i0 + k < parts ? p.part_o : a.part_o) + at(i0 + k) * D + lane * kPer;
-            if (kPer == 4) {
-                const float4 v = *reinterpret_cast<const float4 *>(po);
-                acc[0] += fk * v.x, acc[1] += fk * v.y, acc[kPer - 2] += fk * v.z, acc[kPer - 1] += fk * v.w;
-            } else {
-                const float2 v = *reinterpret_cast<const float2 *>(po);
-                acc[0] += fk * v.x, acc[1] += fk * v.y;
-            }
+            float v[kPer];
+            if (kPer == 4) *reinterpret_cast<float4 *>(v) = *reinterpret_cast<const float4 *>(po);
+            else *reinterpret_cast<float2 *>(v) = *reinterpret_cast<const float2 *>(po);
+#pragma unroll
+            for (int e = 0; e < kPer; ++e) acc[e] += fk * v[e];
         }
     }
 #pragma unroll
@@ -913,12 +906,17 @@ cudaError_t launch_variant(const PrefixArgs &p, cudaStream_t stream) {
     auto kern = prefix_kernel<MODE, D, NT>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kBytes);
     if (e != cudaSuccess) return e;
+    // a block launched with fewer registers could never hand out the warpgroups' shares
+    cudaFuncAttributes attr;
+    e = cudaFuncGetAttributes(&attr, kern);
+    if (e != cudaSuccess) return e;
+    if (attr.numRegs < L::kLaunchRegs) return cudaErrorInvalidConfiguration;
     const int64_t rows = (int64_t)p.own.g.num_seqs * p.own.group;
     const int64_t tiles = (rows + NT * kRows - 1) / (NT * kRows) * p.own.g.kv_heads;
     const int64_t steps = ((int64_t)p.max_prefix_blocks * p.own.g.block_size + kCols - 1) / kCols;
     int64_t ctas = sm_count() < kMaxCtas ? sm_count() : kMaxCtas;
     if (tiles * steps < ctas) ctas = tiles * steps;
-    e = launch_dependent(kern, ctas, L::kWarps * 32, (size_t)L::kBytes, stream, p);
+    e = launch_dependent(kern, ctas, L::kThreads, (size_t)L::kBytes, stream, p);
     if (e != cudaSuccess) return e;
     const int64_t all = rows * p.own.g.kv_heads;
     const int64_t per = kMergeThreads / 32;

@@ -256,8 +256,7 @@ struct Barriers {
     uint32_t tmem;
     int32_t stop;
     uint2 valid[kMaskSlots];  // 8 bytes: valid positions of each group of 16
-    // modes 0 and 2: each position's (each group of 16's) key scale times the softmax
-    // scale, and value scale
+    // modes 0 and 2: each position's (each group of 16's) key and value scale
     alignas(16) float sk[kMaskSlots][kCols];
     alignas(16) float sv[kMaskSlots][kCols];
 };
@@ -295,11 +294,12 @@ struct Prefix {
 
     // ---- dequantise ------------------------------------------------------------
     static constexpr int kRpw = kCols / L::kDequantWarps;  // positions of a warp
-    static constexpr int kLpr = D / 16;                    // lanes of a position
-    static constexpr int kRpi = 32 / kLpr;                 // positions of one load
-    static constexpr int kLoads = kRpw / kRpi;
     static constexpr int kGroups = kRpw / 16;  // a group of 16 positions lies in one block
+    static constexpr int kHalves = D / 64;     // blocks of 64 channels
+    static constexpr int kLoads = kRpw / 8 * kHalves;
 
+    // Lane l takes codes [16 (l % 4), +16) of a 64-channel block of position l / 4 of
+    // eight: load i is block i % kHalves of positions 8 (i / kHalves) + l / 4.
     struct Codes {
         uint4 c[kLoads];
     };
@@ -308,37 +308,46 @@ struct Prefix {
         int64_t blk[kGroups];  // block * heads + head
         int valid[kGroups];
     };
+    struct Ids {
+        int32_t blk[kGroups], at[kGroups], valid[kGroups];
+    };
 
-    __device__ __forceinline__ Where find(int h, int step, int dw) const {
-        Where x;
-        const kvc8_geom &g = p.own.g;
+    // Block ids of a step's groups, requested a step before they are used.
+    __device__ __forceinline__ Ids find(int step, int dw) const {
+        Ids x;
+        const uint32_t bs = (uint32_t)p.own.g.block_size;
 #pragma unroll
         for (int i = 0; i < kGroups; ++i) {
             const int pos = step * kCols + dw * kRpw + 16 * i;
-            x.valid[i] = 0;
-            x.row[i] = x.blk[i] = 0;
-            if (pos < w.len) {
-                const uint32_t lb = (uint32_t)pos / (uint32_t)g.block_size;
-                const int32_t blk = ld_nc_s32(p.prefix_table + lb);
-                if (blk >= 0 && blk < g.num_blocks) {
-                    x.blk[i] = (int64_t)blk * g.kv_heads + h;
-                    x.row[i] = x.blk[i] * g.block_size + (pos - (int)(lb * (uint32_t)g.block_size));
-                    x.valid[i] = min(16, w.len - pos);
-                } else if (lane == 0) {
-                    report(p.own.dev_error, KVC8_DEV_BAD_BLOCK_ID);
-                }
-            }
+            const uint32_t lb = (uint32_t)pos / bs;
+            x.at[i] = pos - (int)(lb * bs);
+            x.valid[i] = min(16, w.len - pos);
+            x.blk[i] = pos < w.len ? ld_nc_s32(p.prefix_table + lb) : 0;
         }
         return x;
+    }
+    __device__ __forceinline__ Where place(const Ids &x, int h) const {
+        Where o;
+        const kvc8_geom &g = p.own.g;
+#pragma unroll
+        for (int i = 0; i < kGroups; ++i) {
+            const bool in = x.blk[i] >= 0 && x.blk[i] < g.num_blocks;
+            if (!in && lane == 0) report(p.own.dev_error, KVC8_DEV_BAD_BLOCK_ID);
+            o.valid[i] = in ? max(0, x.valid[i]) : 0;
+            o.blk[i] = (int64_t)(in ? x.blk[i] : 0) * g.kv_heads + h;
+            o.row[i] = o.blk[i] * g.block_size + x.at[i];
+        }
+        return o;
     }
 
     __device__ __forceinline__ void load(const Where &x, const int8_t *cache, Codes &c) const {
 #pragma unroll
         for (int i = 0; i < kLoads; ++i) {
-            const int grp = i * kRpi / 16, at = i * kRpi % 16 + lane / kLpr;
+            const int pos = i / kHalves * 8, at = pos % 16 + lane / 4;
             c.c[i] = make_uint4(0u, 0u, 0u, 0u);
-            if (at < x.valid[grp])
-                c.c[i] = __ldg(reinterpret_cast<const uint4 *>(cache + (x.row[grp] + at) * D) + lane % kLpr);
+            if (at < x.valid[pos / 16])
+                c.c[i] = __ldg(reinterpret_cast<const uint4 *>(cache + (x.row[pos / 16] + at) * D + i % kHalves * 64) +
+                               lane % 4);
         }
     }
     // Modes 0 and 2: the scale of position `lane` of the warp.
@@ -350,13 +359,18 @@ struct Prefix {
         return lane < kRpw && (lane & 15) < valid ? ld_nc_f32(scale + (MODE == 0 ? row + (lane & 15) : blk)) : 0.0f;
     }
 
-    // Codes into the swizzled tile, exact in bf16 (or fp16): the scales are multiplied in
+    // Codes into the swizzled tile, exact in fp16 or bf16: the scales are multiplied in
     // later, in fp32 (modes 0 and 2), or are in the query and the output (mode 1).
+    // 16-byte chunk n of a 128-byte row lies at n ^ (row mod 8), and row mod 8 = l / 4:
+    // a lane's two places are the same in every eight rows, and the eight lanes of an
+    // access (two rows) hit different banks.
     template <bool HALF>
     __device__ __forceinline__ void store(const Codes &c, uint32_t tile, int dw) const {
+        const int n = (lane & 3) * 2, x = lane >> 2;
+        const uint32_t at = tile + (uint32_t)(dw * kRpw + x) * 128;
+        const uint32_t a0 = at + (uint32_t)((n ^ x) << 4), a1 = at + (uint32_t)(((n + 1) ^ x) << 4);
 #pragma unroll
         for (int i = 0; i < kLoads; ++i) {
-            const int r = i * kRpi + lane / kLpr;  // position of the warp
             const uint32_t wd[4] = {c.c[i].x, c.c[i].y, c.c[i].z, c.c[i].w};
             uint32_t o[8];
 #pragma unroll
@@ -364,18 +378,12 @@ struct Prefix {
                 const uint32_t sel = (e & 1) ? 0x4342u : 0x4140u;
                 o[e] = HALF ? codes_fp16(wd[e >> 1] ^ 0x80808080u, sel) : codes_bf16(wd[e >> 1], sel);
             }
-            const int row = dw * kRpw + r, c8 = lane % kLpr;
-            // 16-byte chunk n of a 128-byte row lies at n ^ (row mod 8); the lanes of the
-            // second 64 channels write their two chunks in the other order, so that the
-            // eight lanes of a row hit different banks
-            const int n = (c8 & 3) * 2, swap = c8 >> 2, x = row & 7;
-            const uint32_t at = tile + (uint32_t)(c8 >> 2) * (kCols * 128) + (uint32_t)row * 128;
-            const uint32_t a0 = at + (uint32_t)(((n + swap) ^ x) << 4), a1 = at + (uint32_t)(((n + 1 - swap) ^ x) << 4);
-            asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(a0), "r"(swap ? o[4] : o[0]),
-                         "r"(swap ? o[5] : o[1]), "r"(swap ? o[6] : o[2]), "r"(swap ? o[7] : o[3])
+            const uint32_t off = (uint32_t)(i / kHalves * 1024 + i % kHalves * (kCols * 128));
+            asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(a0 + off), "r"(o[0]), "r"(o[1]), "r"(o[2]),
+                         "r"(o[3])
                          : "memory");
-            asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(a1), "r"(swap ? o[0] : o[4]),
-                         "r"(swap ? o[1] : o[5]), "r"(swap ? o[2] : o[6]), "r"(swap ? o[3] : o[7])
+            asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(a1 + off), "r"(o[4]), "r"(o[5]), "r"(o[6]),
+                         "r"(o[7])
                          : "memory");
         }
     }
@@ -383,23 +391,31 @@ struct Prefix {
     __device__ void dequantise(int dw) const {
         const AttnArgs &a = p.own;
         int tile = (int)(u0 / w.steps), step = (int)(u0 - (int64_t)tile * w.steps);
-        Where x = find(tile / w.tiles_per_head, step, dw);
+        Where x = place(find(step, dw), tile / w.tiles_per_head);
         Codes k, v;
         float sk = 0.0f, sv = 0.0f;
         auto scales = [&]() {
             if (MODE == 1) return;
-            sk = load_scale(x, a.k_scale) * fabsf(a.scale_log2);
+            sk = load_scale(x, a.k_scale);
             sv = load_scale(x, a.v_scale);
+        };
+        auto next = [&]() {
+            if (++step == w.steps) {
+                step = 0;
+                ++tile;
+            }
         };
         load(x, a.k_cache, k);
         scales();
         load(x, a.v_cache, v);
+        next();
+        Ids ids = find(step, dw);
         int n = 0;
         for (int64_t u = u0; u < u1; ++u, ++n) {
             const int st = n % kStages;
             const uint32_t par = (uint32_t)(n / kStages) & 1u;
             if (!wait_warp(bar.k_free[st], par ^ 1u)) return;
-            store<MODE == 1>(k, base + L::kK + st * L::kTileBytes, dw);
+            store<true>(k, base + L::kK + st * L::kTileBytes, dw);
             if (MODE == 0 && lane < kRpw) {
                 bar.sk[n % kMaskSlots][dw * kRpw + lane] = sk;
                 bar.sv[n % kMaskSlots][dw * kRpw + lane] = sv;
@@ -416,21 +432,20 @@ struct Prefix {
             fence_async();
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_u32(&bar.k_full[st]));
-            if (u + 1 < u1) {  // the next step's codes
-                if (++step == w.steps) {
-                    step = 0;
-                    ++tile;
-                }
-                x = find(tile / w.tiles_per_head, step, dw);
+            const bool more = u + 1 < u1;
+            if (more) {  // the next step's codes, and the block ids of the one after
+                x = place(ids, tile / w.tiles_per_head);
                 load(x, a.k_cache, k);
                 scales();
+                next();
+                ids = find(step, dw);
             }
             if (!wait_warp(bar.v_free[st], par ^ 1u)) return;
-            store<false>(v, base + L::kV + st * L::kTileBytes, dw);
+            store<MODE == 1>(v, base + L::kV + st * L::kTileBytes, dw);
             fence_async();
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_u32(&bar.v_full[st]));
-            if (u + 1 < u1) load(x, a.v_cache, v);
+            if (more) load(x, a.v_cache, v);
         }
     }
 
@@ -442,7 +457,7 @@ struct Prefix {
 #pragma unroll
         for (int i = 0; i < D / 16; ++i) {
             const uint64_t at = (uint64_t)(((i / 4) * (kRows * 128) + (i % 4) * 32) >> 4);
-            tc_mma_ss(tmem + x * kCols, q + at, k + at, instr_desc(kCols, false, MODE != 1), i > 0, leader);
+            tc_mma_ss(tmem + x * kCols, q + at, k + at, instr_desc(kCols, false, false), i > 0, leader);
         }
     }
     __device__ __forceinline__ void pv(int x, int st, uint32_t tmem, bool acc, uint32_t leader) const {
@@ -450,7 +465,7 @@ struct Prefix {
 #pragma unroll
         for (int i = 0; i < kCols / 16; ++i)
             tc_mma_ts(tmem + NT * kCols + x * D, tmem + x * kCols + 8 * i, v + (uint64_t)(i * (2048 >> 4)),
-                      instr_desc(D, true, true), acc || i > 0, leader);
+                      instr_desc(D, true, MODE != 1), acc || i > 0, leader);
     }
 
     __device__ bool products_loop(uint32_t tmem, uint32_t leader) const {
@@ -508,7 +523,7 @@ struct Prefix {
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t s_at = tmem + lanes + x * kCols, o_at = tmem + lanes + NT * kCols + x * D;
         const int64_t rows = (int64_t)a.g.num_seqs * a.group;
-        const uint32_t flip = a.scale_log2 < 0.0f ? 0x80008000u : 0u;  // the sign goes to the query
+        const bool flip = a.scale_log2 < 0.0f;  // the sign goes to the query
         int n = 0;
         uint32_t seg = 0;
         for (int64_t u = u0; u < u1; ++seg) {
@@ -518,9 +533,9 @@ struct Prefix {
             const int64_t r0 = (tile - (int64_t)h * w.tiles_per_head) * (NT * kRows) + x * kRows + (warp & 3) * 32;
             const int64_t r = r0 + lane;
             const bool busy = r0 < rows;  // uniform in the warp: some row is a query's
-            // of a score; modes 0 and 2 have it in sk.  Never 0: 0 times -inf is no number,
-            // and scores are far too small for 2^-126 to show
-            float scale = fmaxf(fabsf(a.scale_log2), 0x1p-126f);
+            // log2 per unit of score, with the query's power of two; never 0 (0 times -inf is
+            // no number): 2^-126 instead does not show
+            float scale = fabsf(a.scale_log2);
             load_query(x, row, r, rows, h, flip, scale);
             fence_async();
             tc_fence_before();  // the last segment's O is read
@@ -567,10 +582,12 @@ struct Prefix {
         }
     }
 
-    // Query row r of head h into row `row` of tile x.  Modes 0 and 2: the bf16 values.
-    // Mode 1: times the channels' key scales, in fp16 after a power of two that brings
-    // the row's largest to [1, 2) (returned in `scale`): eight times finer than bf16.
-    __device__ __forceinline__ void load_query(int x, int row, int64_t r, int64_t rows, int h, uint32_t flip,
+    // Query row r of head h into row `row` of tile x, in mode 1 times the channels' key
+    // scales: fp16 after a power of two that brings the row's largest value to [1, 2)
+    // and goes into `scale`.  Eleven bits hold a bf16 value whole (mode 1: round the
+    // product eight times finer than bf16); below 2^-14 of the largest they thin out to
+    // 2^-25 of it.
+    __device__ __forceinline__ void load_query(int x, int row, int64_t r, int64_t rows, int h, bool flip,
                                                float &scale) const {
         const AttnArgs &a = p.own;
         const uint32_t dst = base + L::kQ + x * L::kTileBytes + (uint32_t)row * 128;
@@ -581,39 +598,38 @@ struct Prefix {
             q += (int64_t)b * a.q_seq_stride + (int64_t)(h * a.group + j) * a.q_head_stride;
         }
         const float *ks = a.k_scale + (MODE == 1 ? (int64_t)h * D : 0);
-        auto scaled = [&](uint32_t wd, int d) {
-            const float2 s = __ldg(reinterpret_cast<const float2 *>(ks + d));
-            return make_float2(__uint_as_float(wd << 16) * s.x, __uint_as_float(wd & 0xFFFF0000u) * s.y);
-        };
-        float turn = 1.0f;
-        if (MODE == 1) {
-            float top = 0.0f;
-#pragma unroll 4
-            for (int i = 0; i < D / 8; ++i) {
-                uint4 v = make_uint4(0u, 0u, 0u, 0u);
-                if (live) v = __ldg(reinterpret_cast<const uint4 *>(q) + i);
-                const uint32_t wd[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float2 y = scaled(wd[e], 8 * i + 2 * e);
-                    top = fmaxf(top, fmaxf(fabsf(y.x), fabsf(y.y)));
-                }
+        auto value = [&](uint32_t wd, int d) {
+            float2 y = make_float2(__uint_as_float(wd << 16), __uint_as_float(wd & 0xFFFF0000u));
+            if (MODE == 1) {
+                const float2 s = __ldg(reinterpret_cast<const float2 *>(ks + d));
+                y = make_float2(y.x * s.x, y.y * s.y);
             }
-            const int ex = min(100, max(-100, (int)(__float_as_uint(top) >> 23) - 127));
-            turn = __uint_as_float((uint32_t)(127 - ex) << 23);
-            scale = fmaxf(scale * __uint_as_float((uint32_t)(127 + ex) << 23), 0x1p-126f);
-        }
+            return y;
+        };
+        float top = 0.0f;
 #pragma unroll 4
         for (int i = 0; i < D / 8; ++i) {
             uint4 v = make_uint4(0u, 0u, 0u, 0u);
             if (live) v = __ldg(reinterpret_cast<const uint4 *>(q) + i);
-            uint32_t wd[4] = {v.x ^ flip, v.y ^ flip, v.z ^ flip, v.w ^ flip};
-            if (MODE == 1) {
+            const uint32_t wd[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float2 y = scaled(wd[e], 8 * i + 2 * e);
-                    wd[e] = pack_fp16(y.x * turn, y.y * turn);
-                }
+            for (int e = 0; e < 4; ++e) {
+                const float2 y = value(wd[e], 8 * i + 2 * e);
+                top = fmaxf(top, fmaxf(fabsf(y.x), fabsf(y.y)));
+            }
+        }
+        const int ex = min(100, max(-100, (int)(__float_as_uint(top) >> 23) - 127));
+        const float turn = __uint_as_float(((uint32_t)(127 - ex) << 23) | (flip ? 0x80000000u : 0u));
+        scale = fmaxf(scale * __uint_as_float((uint32_t)(127 + ex) << 23), 0x1p-126f);
+#pragma unroll 4
+        for (int i = 0; i < D / 8; ++i) {
+            uint4 v = make_uint4(0u, 0u, 0u, 0u);
+            if (live) v = __ldg(reinterpret_cast<const uint4 *>(q) + i);
+            uint32_t wd[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float2 y = value(wd[e], 8 * i + 2 * e);
+                wd[e] = pack_fp16(y.x * turn, y.y * turn);
             }
             const uint32_t at = dst + (uint32_t)(i / 8) * (kRows * 128) + (uint32_t)(((i % 8) ^ (row & 7)) << 4);
             asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(wd[0]), "r"(wd[1]), "r"(wd[2]),
@@ -622,8 +638,8 @@ struct Prefix {
         }
     }
 
-    // Scores of 32 positions from c on, in the log2 domain but for the factor `scale`
-    // of mode 1; positions that are left out become -inf.  Returns the largest.
+    // Scores of 32 positions from c on but for the factor `scale`, that is, times the
+    // positions' key scales; positions that are left out become -inf.  Returns the largest.
     __device__ __forceinline__ float scores(float (&s)[32], int c, int slot, bool whole) const {
         if (MODE != 1) {
 #pragma unroll
@@ -658,14 +674,8 @@ struct Prefix {
 #pragma unroll
         for (int i = 0; i < 32; i += 4) {
             float2 y0 = make_float2(s[i], s[i + 1]), y1 = make_float2(s[i + 2], s[i + 3]);
-            if (MODE == 1) {
-                const float2 f = make_float2(scale, scale), g = make_float2(neg, neg);
-                y0 = __ffma2_rn(y0, f, g);
-                y1 = __ffma2_rn(y1, f, g);
-            } else {
-                y0 = __fadd2_rn(y0, make_float2(neg, neg));
-                y1 = __fadd2_rn(y1, make_float2(neg, neg));
-            }
+            y0 = __ffma2_rn(y0, make_float2(scale, scale), make_float2(neg, neg));
+            y1 = __ffma2_rn(y1, make_float2(scale, scale), make_float2(neg, neg));
             y0 = make_float2(ex2(y0.x), ex2(y0.y));
             y1 = make_float2(ex2(y1.x), ex2(y1.y));
             sum = __fadd2_rn(sum, __fadd2_rn(y0, y1));
@@ -676,8 +686,10 @@ struct Prefix {
                 y0 = __fmul2_rn(y0, make_float2(f.x, f.y));
                 y1 = __fmul2_rn(y1, make_float2(f.z, f.w));
             }
-            o[i / 2] = pack_bf16(y0.x, y0.y);
-            o[i / 2 + 1] = pack_bf16(y1.x, y1.y);
+            // mode 1 has nothing but weights here, at most 2^8: fp16 holds them eight times
+            // finer.  Times a value scale, whose size is the caller's, they are bf16.
+            o[i / 2] = MODE == 1 ? pack_fp16(y0.x, y0.y) : pack_bf16(y0.x, y0.y);
+            o[i / 2 + 1] = MODE == 1 ? pack_fp16(y1.x, y1.y) : pack_bf16(y1.x, y1.y);
         }
         tc_st16(s_at + c / 2, o);
     }
@@ -698,8 +710,7 @@ struct Prefix {
         const float t0 = scores(s0, 0, slot, whole), t1 = scores(s1, 32, slot, whole);
         const float t2 = scores(s2, 64, slot, whole), t3 = scores(s3, 96, slot, whole);
         const float top = fmaxf(fmaxf(t0, t1), fmaxf(t2, t3));
-        // mode 1: a scale of 0 times -inf would be no number, so the factor is never 0
-        const float mx = MODE == 1 ? top * scale : top;
+        const float mx = top * scale;
         const bool moves = mx > m + kLazy || (m == -INFINITY && mx > m);
         if (__any_sync(0xFFFFFFFFu, moves)) {
             const float f = moves ? ex2(m - mx) : 1.0f;  // 0 where there was nothing yet

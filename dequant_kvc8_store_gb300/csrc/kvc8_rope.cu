@@ -20,8 +20,14 @@
 // interleaved one -- so nothing is exchanged but the row sums and maxima.  A unit of
 // work is a token, or a part of its row sets where there are fewer tokens than
 // warps.  The warp finds its token's slot, computes the R/2 sines and cosines once
-// (a lane R/64 of them, kept in shared memory) and runs through the row sets, the
-// next set's loads in flight.
+// (a lane R/64 of them, handed over in shared memory), folds the norm's weights into
+// them, and then spends on a row little more than unpacking, the sum of squares, four
+// multiply-adds a pair and packing; the next set's loads are in flight meanwhile.
+//
+// Codes without dividing: with r = fl(1/s), every value fl(y/s) can take lies between
+// y r (1 - 2^-21) and y r (1 + 2^-21) (r and the quotient are each within 2^-24 of
+// theirs).  Where both ends round to the same integer, so does the quotient; else (a
+// value within 2^-21 of a half-integer) the group of four is divided.
 #include "kvc8_internal.cuh"
 
 namespace kvc8 {
@@ -83,9 +89,53 @@ __device__ __forceinline__ Slot find_slot(const RopeArgs &a, int64_t t, int lane
     return s;
 }
 
+constexpr float kMagic = 12582912.0f;            // 1.5 * 2^23: adding it rounds to an integer
+constexpr float kRecipLo = 0.99999952316284180f;  // 1 - 2^-21
+constexpr float kRecipHi = 1.00000047683715820f;  // 1 + 2^-21
+
+// The definition: one division, round half to even, clamp; 0 when s == 0.
+__device__ __noinline__ uint32_t codes_divide(float4 y, float4 s) {
+    auto one = [](float a, float b) {
+        const int q = b == 0.0f ? 0 : __float2int_rn(__fdiv_rn(a, b));
+        return (uint32_t)min(127, max(-127, q)) & 0xFFu;
+    };
+    return one(y.x, s.x) | one(y.y, s.y) << 8 | one(y.z, s.z) << 16 | one(y.w, s.w) << 24;
+}
+
+// |x| limited to b, with x's sign.
+__device__ __forceinline__ float limit(float x, float b) {
+    float r;
+    asm("min.xorsign.abs.f32 %0, %1, %2;" : "=f"(r) : "f"(x), "f"(b));
+    return r;
+}
+
+__device__ __forceinline__ bool recip_ok(float s) { return s >= 0x1p-120f && s <= 0x1p+120f; }
+
+// Four codes of y for scales s with reciprocals r (0: divide).  LIMIT: |y / s| may pass
+// 127; it is cut at fl(127 s), whose code is 127.
+template <bool LIMIT>
+__device__ __forceinline__ uint32_t codes4(float2 y0, float2 y1, float4 s, float4 r) {
+    float2 a = y0, b = y1;
+    if (LIMIT) {
+        a = make_float2(limit(y0.x, __fmul_rn(127.0f, s.x)), limit(y0.y, __fmul_rn(127.0f, s.y)));
+        b = make_float2(limit(y1.x, __fmul_rn(127.0f, s.z)), limit(y1.y, __fmul_rn(127.0f, s.w)));
+    }
+    const float2 lo = make_float2(kRecipLo, kRecipLo), hi = make_float2(kRecipHi, kRecipHi);
+    const float2 m2 = make_float2(kMagic, kMagic), n1 = make_float2(-1.0f, -1.0f);
+    const float2 ra = make_float2(r.x, r.y), rb = make_float2(r.z, r.w);
+    const float2 la = __ffma2_rn(a, __fmul2_rn(ra, lo), m2), ha = __ffma2_rn(a, __fmul2_rn(ra, hi), m2);
+    const float2 lb = __ffma2_rn(b, __fmul2_rn(rb, lo), m2), hb = __ffma2_rn(b, __fmul2_rn(rb, hi), m2);
+    float2 da = __ffma2_rn(la, n1, ha), db = __ffma2_rn(lb, n1, hb);  // 0 where the ends agree
+    da = __ffma2_rn(da, da, __fmul2_rn(db, db));
+    if (da.x + da.y != 0.0f || fminf(fminf(r.x, r.y), fminf(r.z, r.w)) == 0.0f)
+        return codes_divide(make_float4(y0.x, y0.y, y1.x, y1.y), s);
+    return __byte_perm(__byte_perm(__float_as_uint(la.x), __float_as_uint(la.y), 0x0040),
+                       __byte_perm(__float_as_uint(lb.x), __float_as_uint(lb.y), 0x0040), 0x5410);
+}
+
 // L lanes per row, 32 / L rows of a set.
 template <int SINK, int L>
-__global__ void __launch_bounds__(kRopeWarps * 32, 6) rope_kernel(const RopeArgs a, int parts) {
+__global__ void __launch_bounds__(kRopeWarps * 32, 5) rope_kernel(const RopeArgs a, int parts) {
     constexpr int RW = 32 / L;
     constexpr bool kPages = SINK != kSinkRows;
     __shared__ __align__(16) float turn_s[kRopeWarps][2][kMaxPairs];  // m cos, m sin
@@ -101,33 +151,31 @@ __global__ void __launch_bounds__(kRopeWarps * 32, 6) rope_kernel(const RopeArgs
     const bool turns = c < R / 16;
     const int d0 = turns && !a.interleaved ? 8 * c : 16 * c;
     const int d1 = turns && !a.interleaved ? R / 2 + 8 * c : 16 * c + 8;
+    const float inv_d = 1.0f / (float)D;
     float *cos_s = turn_s[warp][0], *sin_s = turn_s[warp][1];
 
     const int64_t units = a.num_tokens * parts;
     for (int64_t u = (int64_t)blockIdx.x * kRopeWarps + warp; u < units; u += (int64_t)gridDim.x * kRopeWarps) {
-        const int64_t t = u / parts;
-        const int part = (int)(u - t * parts);
-        const int s0 = part * per, s1 = min(sets, s0 + per);
+        const int64_t t = parts == 1 ? u : u / parts;
+        const int s0 = (int)(u - t * parts) * per, s1 = min(sets, s0 + per);
         if (s0 >= s1) continue;
 
-        auto source = [&](int set, bool &on, int &h, int &kind) -> const uint16_t * {
-            kind = set < sq ? 0 : set < sq + sk ? 1 : 2;
-            h = (set - (kind == 0 ? 0 : kind == 1 ? sq : sq + sk)) * RW + rl;
-            on = on_c && h < (kind == 0 ? a.q_heads : H);
-            return kind == 0 ? a.q + t * a.q_tok_stride + (int64_t)h * a.q_head_stride
-                             : (kind == 1 ? a.k : a.v) + t * a.x_tok_stride + (int64_t)h * a.x_head_stride;
-        };
-        bool on;
-        int h, kind;
-        uint4 x0 = make_uint4(0u, 0u, 0u, 0u), x1 = x0;
-        {
-            const uint16_t *src = source(s0, on, h, kind);
-            if (on) {
+        uint4 x0, x1;  // the rows of the next set
+        const uint16_t *const qt = a.q + t * a.q_tok_stride, *const kt = a.k + t * a.x_tok_stride;
+        const uint16_t *const vt = a.v + t * a.x_tok_stride;
+        auto fetch = [&](int set) {
+            const int kind = set < sq ? 0 : set < sq + sk ? 1 : 2;
+            const int h = (set - (kind == 0 ? 0 : kind == 1 ? sq : sq + sk)) * RW + rl;
+            x0 = x1 = make_uint4(0u, 0u, 0u, 0u);
+            if (on_c && h < (kind == 0 ? a.q_heads : H)) {
+                const uint16_t *src = kind == 0 ? qt + (int64_t)h * a.q_head_stride
+                                                : (kind == 1 ? kt : vt) + (int64_t)h * a.x_head_stride;
                 x0 = ld_stream_16(src + (kind == 2 ? 16 * c : d0));
                 x1 = ld_stream_16(src + (kind == 2 ? 16 * c + 8 : d1));
             }
-        }
-        const Slot slot = find_slot<SINK>(a, t, lane, part == 0);
+        };
+        fetch(s0);
+        const Slot slot = find_slot<SINK>(a, t, lane, s0 == 0);
         if (kPages && slot.row < 0) continue;  // uniform in the warp
         __syncwarp();
         if (s0 < sq + sk) {
@@ -141,122 +189,160 @@ __global__ void __launch_bounds__(kRopeWarps * 32, 6) rope_kernel(const RopeArgs
         }
         __syncwarp();
 
-        for (int set = s0; set < s1; ++set) {
-            const bool cur_on = on;
-            const int cur_h = h, cur_kind = kind;
-            float2 v[8];  // v[0..3]: the first piece, v[4..7]: the second
+        // Queries and keys: row sets [lo, hi) of one kind.  The rotation with the norm's
+        // weights folded in, per channel: out = x * own + partner * other.
+        auto rotate_sets = [&](int lo, int hi, int first, const uint16_t *w, auto &&sink) {
+            if (lo >= hi) return;
+            float2 own[8], other[8];
             {
-                const uint32_t wd[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
+                float2 wt[8];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) v[i] = make_float2(bf16_lo(wd[i]), bf16_hi(wd[i]));
-            }
-            const uint4 raw0 = x0, raw1 = x1;
-            if (set + 1 < s1) {  // the next set's rows
-                const uint16_t *src = source(set + 1, on, h, kind);
-                x0 = x1 = make_uint4(0u, 0u, 0u, 0u);
-                if (on) {
-                    x0 = ld_stream_16(src + (kind == 2 ? 16 * c : d0));
-                    x1 = ld_stream_16(src + (kind == 2 ? 16 * c + 8 : d1));
-                }
-            }
-            const uint16_t *w = cur_kind == 0 ? a.q_weight : cur_kind == 1 ? a.k_weight : nullptr;
-            if (w != nullptr) {
-                float2 sum2 = make_float2(0.0f, 0.0f);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) sum2 = __ffma2_rn(v[i], v[i], sum2);
-                float sum = sum2.x + sum2.y;
-#pragma unroll
-                for (int o = 1; o < L; o <<= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
-                const float inv = __frcp_rn(__fsqrt_rn(sum / (float)D + a.eps));
-                if (on_c) {
+                for (int i = 0; i < 8; ++i) wt[i] = make_float2(1.0f, 1.0f);
+                if (w != nullptr && on_c) {
                     const uint4 w0 = __ldg(reinterpret_cast<const uint4 *>(w + d0));
                     const uint4 w1 = __ldg(reinterpret_cast<const uint4 *>(w + d1));
                     const uint32_t wd[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
 #pragma unroll
+                    for (int i = 0; i < 8; ++i) wt[i] = make_float2(bf16_lo(wd[i]), bf16_hi(wd[i]));
+                }
+                float co[8], si[8];  // pairs 8c .. 8c + 7 in either layout
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    co[i] = 1.0f;
+                    si[i] = 0.0f;
+                }
+                if (turns) {
+#pragma unroll
+                    for (int i = 0; i < 8; i += 4) {
+                        *reinterpret_cast<float4 *>(co + i) = *reinterpret_cast<const float4 *>(cos_s + 8 * c + i);
+                        *reinterpret_cast<float4 *>(si + i) = *reinterpret_cast<const float4 *>(sin_s + 8 * c + i);
+                    }
+                }
+                if (!a.interleaved) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float2 c2 = make_float2(co[2 * i], co[2 * i + 1]), s2 = make_float2(si[2 * i], si[2 * i + 1]);
+                        own[i] = __fmul2_rn(wt[i], c2);
+                        own[4 + i] = __fmul2_rn(wt[4 + i], c2);
+                        other[i] = __fmul2_rn(wt[4 + i], make_float2(-s2.x, -s2.y));
+                        other[4 + i] = __fmul2_rn(wt[i], s2);
+                    }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        own[i] = make_float2(wt[i].x * co[i], wt[i].y * co[i]);
+                        other[i] = make_float2(-wt[i].y * si[i], wt[i].x * si[i]);
+                    }
+                }
+            }
+            for (int set = lo; set < hi; ++set) {
+                float2 v[8];
+                {
+                    const uint32_t wd[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) v[i] = make_float2(bf16_lo(wd[i]), bf16_hi(wd[i]));
+                }
+                if (set + 1 < s1) fetch(set + 1);
+                if (w != nullptr) {
+                    float2 sa = __fmul2_rn(v[0], v[0]), sb = __fmul2_rn(v[1], v[1]);
+#pragma unroll
+                    for (int i = 2; i < 8; i += 2) {
+                        sa = __ffma2_rn(v[i], v[i], sa);
+                        sb = __ffma2_rn(v[i + 1], v[i + 1], sb);
+                    }
+                    sa = __fadd2_rn(sa, sb);
+                    float sum = sa.x + sa.y;
+#pragma unroll
+                    for (int o = 1; o < L; o <<= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+                    const float inv = rsqrtf(fmaf(sum, inv_d, a.eps));
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) v[i] = __fmul2_rn(v[i], make_float2(inv, inv));
+                }
+                float2 y[8];
+                if (!a.interleaved) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        y[i] = __ffma2_rn(v[i], own[i], __fmul2_rn(v[4 + i], other[i]));
+                        y[4 + i] = __ffma2_rn(v[4 + i], own[4 + i], __fmul2_rn(v[i], other[4 + i]));
+                    }
+                } else {
+#pragma unroll
                     for (int i = 0; i < 8; ++i)
-                        v[i] = __fmul2_rn(__fmul2_rn(v[i], make_float2(inv, inv)),
-                                          make_float2(bf16_lo(wd[i]), bf16_hi(wd[i])));
+                        y[i] = __ffma2_rn(v[i], own[i], __fmul2_rn(make_float2(v[i].y, v[i].x), other[i]));
                 }
+                sink((set - first) * RW + rl, y);
             }
-            if (cur_kind != 2 && turns) {
-                // pairs 8c .. 8c + 7 in either layout
-                const float4 *cp = reinterpret_cast<const float4 *>(cos_s + 8 * c);
-                const float4 *sp = reinterpret_cast<const float4 *>(sin_s + 8 * c);
+        };
+        auto pack_row = [&](uint16_t *dst, const float2 (&y)[8]) {
+            *reinterpret_cast<uint4 *>(dst + d0) = make_uint4(pack_bf16(y[0].x, y[0].y), pack_bf16(y[1].x, y[1].y),
+                                                              pack_bf16(y[2].x, y[2].y), pack_bf16(y[3].x, y[3].y));
+            *reinterpret_cast<uint4 *>(dst + d1) = make_uint4(pack_bf16(y[4].x, y[4].y), pack_bf16(y[5].x, y[5].y),
+                                                              pack_bf16(y[6].x, y[6].y), pack_bf16(y[7].x, y[7].y));
+        };
+        // A row of 16 values a lane into the int8 pages: pieces at channels o0 and o1.
+        auto quantise_row = [&](int h, int8_t *cache, float *scl, const float2 (&y)[8], int o0, int o1) {
+            const bool on = on_c && h < H;
+            const int64_t row = slot.row + (int64_t)h * bs;
+            float s_row = 0.0f;
+            if (SINK == kSinkDynamic) {
+                float m = 0.0f;
 #pragma unroll
-                for (int q = 0; q < 2; ++q) {
-                    const float4 co = cp[q], si = sp[q];
-                    if (!a.interleaved) {
+                for (int i = 0; i < 8; ++i) m = fmaxf(m, fmaxf(fabsf(y[i].x), fabsf(y[i].y)));
 #pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            const float2 c2 = e ? make_float2(co.z, co.w) : make_float2(co.x, co.y);
-                            const float2 s2 = e ? make_float2(si.z, si.w) : make_float2(si.x, si.y);
-                            const float2 ya = v[2 * q + e], yb = v[4 + 2 * q + e];
-                            const float2 ns = make_float2(-s2.x, -s2.y);
-                            v[2 * q + e] = __ffma2_rn(ya, c2, __fmul2_rn(yb, ns));
-                            v[4 + 2 * q + e] = __ffma2_rn(yb, c2, __fmul2_rn(ya, s2));
-                        }
-                    } else {
-                        const float cc[4] = {co.x, co.y, co.z, co.w}, ss[4] = {si.x, si.y, si.z, si.w};
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const float2 y = v[4 * q + e];
-                            v[4 * q + e] = make_float2(fmaf(y.x, cc[e], -(y.y * ss[e])), fmaf(y.y, cc[e], y.x * ss[e]));
-                        }
-                    }
-                }
+                for (int o = 1; o < L; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+                s_row = __fdiv_rn(m, 127.0f);
+                if (on && c == 0) scl[row] = s_row;
+            } else if (SINK == kSinkBlock && on) {
+                s_row = ld_nc_f32(scl + (int64_t)slot.blk * H + h);
             }
-            // a value row is held as sixteen neighbours
-            const int o0 = cur_kind == 2 ? 16 * c : d0, o1 = cur_kind == 2 ? 16 * c + 8 : d1;
-            if (cur_kind == 0 || SINK == kSinkRows || SINK == kSinkBf16) {
-                uint16_t *dst;
-                if (cur_kind == 0) dst = a.q_out + t * a.qo_tok_stride + (int64_t)cur_h * a.qo_head_stride;
-                else if (SINK == kSinkRows) dst = a.k_out + t * a.ko_tok_stride + (int64_t)cur_h * a.ko_head_stride;
-                else dst = static_cast<uint16_t *>(cur_kind == 1 ? a.k_cache : a.v_cache) +
-                           (slot.row + (int64_t)cur_h * bs) * D;
-                uint4 y0 = raw0, y1 = raw1;  // values are copied bit for bit
-                if (cur_kind != 2) {
-                    y0 = make_uint4(pack_bf16(v[0].x, v[0].y), pack_bf16(v[1].x, v[1].y), pack_bf16(v[2].x, v[2].y),
-                                    pack_bf16(v[3].x, v[3].y));
-                    y1 = make_uint4(pack_bf16(v[4].x, v[4].y), pack_bf16(v[5].x, v[5].y), pack_bf16(v[6].x, v[6].y),
-                                    pack_bf16(v[7].x, v[7].y));
+            if (!on) return;
+            const float r_row = SINK != kSinkChannel && recip_ok(s_row) ? __frcp_rn(s_row) : 0.0f;
+            uint32_t o[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                float4 s = make_float4(s_row, s_row, s_row, s_row), r = make_float4(r_row, r_row, r_row, r_row);
+                if (SINK == kSinkChannel) {
+                    s = __ldg(reinterpret_cast<const float4 *>(scl + (int64_t)h * D + (q < 2 ? o0 : o1) + 4 * (q & 1)));
+                    r = make_float4(recip_ok(s.x) ? __frcp_rn(s.x) : 0.0f, recip_ok(s.y) ? __frcp_rn(s.y) : 0.0f,
+                                    recip_ok(s.z) ? __frcp_rn(s.z) : 0.0f, recip_ok(s.w) ? __frcp_rn(s.w) : 0.0f);
                 }
-                if (cur_on) {
-                    *reinterpret_cast<uint4 *>(dst + o0) = y0;
-                    *reinterpret_cast<uint4 *>(dst + o1) = y1;
-                }
+                o[q] = codes4<SINK != kSinkDynamic>(y[2 * q], y[2 * q + 1], s, r);
+            }
+            int8_t *dst = cache + row * D;
+            st_8(dst + o0, o[0], o[1]);
+            st_8(dst + o1, o[2], o[3]);
+        };
+
+        rotate_sets(s0, min(s1, sq), 0, a.q_weight, [&](int h, const float2 (&y)[8]) {
+            if (on_c && h < a.q_heads)
+                pack_row(a.q_out + t * a.qo_tok_stride + (int64_t)h * a.qo_head_stride, y);
+        });
+        rotate_sets(max(s0, sq), min(s1, sq + sk), sq, a.k_weight, [&](int h, const float2 (&y)[8]) {
+            if (SINK == kSinkRows) {
+                if (on_c && h < H) pack_row(a.k_out + t * a.ko_tok_stride + (int64_t)h * a.ko_head_stride, y);
+            } else if (SINK == kSinkBf16) {
+                if (on_c && h < H) pack_row(static_cast<uint16_t *>(a.k_cache) + (slot.row + (int64_t)h * bs) * D, y);
             } else {
-                const int64_t cache_row = slot.row + (int64_t)cur_h * bs;
-                int8_t *dst = static_cast<int8_t *>(cur_kind == 1 ? a.k_cache : a.v_cache) + cache_row * D;
-                float *scl = cur_kind == 1 ? a.k_scale : a.v_scale;
-                float s_row = 0.0f;
-                if (SINK == kSinkDynamic) {
-                    float m = 0.0f;
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) m = fmaxf(m, fmaxf(fabsf(v[i].x), fabsf(v[i].y)));
-#pragma unroll
-                    for (int o = 1; o < L; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
-                    s_row = __fdiv_rn(m, 127.0f);
-                    if (cur_on && c == 0) scl[cache_row] = s_row;
-                } else if (SINK == kSinkBlock && cur_on) {
-                    s_row = ld_nc_f32(scl + (int64_t)slot.blk * H + cur_h);
-                }
-                if (cur_on) {
-                    uint32_t o[4];
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        const float y[4] = {v[2 * q].x, v[2 * q].y, v[2 * q + 1].x, v[2 * q + 1].y};
-                        uint32_t pk = 0;
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const int d = (q < 2 ? o0 : o1) + 4 * (q & 1) + e;
-                            const float s = SINK == kSinkChannel ? ld_nc_f32(scl + (int64_t)cur_h * D + d) : s_row;
-                            const int code = s == 0.0f ? 0 : __float2int_rn(__fdiv_rn(y[e], s));
-                            pk |= (uint32_t)(uint8_t)(int8_t)min(127, max(-127, code)) << (8 * e);
-                        }
-                        o[q] = pk;
+                quantise_row(h, static_cast<int8_t *>(a.k_cache), a.k_scale, y, d0, d1);
+            }
+        });
+        if (kPages) {
+            for (int set = max(s0, sq + sk); set < s1; ++set) {
+                const int h = (set - sq - sk) * RW + rl;
+                const uint4 v0 = x0, v1 = x1;
+                if (set + 1 < s1) fetch(set + 1);
+                if (SINK == kSinkBf16) {  // copied bit for bit
+                    if (on_c && h < H) {
+                        uint16_t *dst = static_cast<uint16_t *>(a.v_cache) + (slot.row + (int64_t)h * bs) * D + 16 * c;
+                        *reinterpret_cast<uint4 *>(dst) = v0;
+                        *reinterpret_cast<uint4 *>(dst + 8) = v1;
                     }
-                    st_8(dst + o0, o[0], o[1]);
-                    st_8(dst + o1, o[2], o[3]);
+                } else {
+                    const uint32_t wd[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
+                    float2 y[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) y[i] = make_float2(bf16_lo(wd[i]), bf16_hi(wd[i]));
+                    quantise_row(h, static_cast<int8_t *>(a.v_cache), a.v_scale, y, 16 * c, 16 * c + 8);
                 }
             }
         }

@@ -250,9 +250,7 @@ __device__ __forceinline__ void compute_tile(const AttnArgs &a, int h, const flo
 
 // One work item = (split j of sequence b, kv head h).  Mode 1 is held to four
 // CTAs per SM (its scale-table reads otherwise push it past 128 registers).
-// PARTS: every split leaves a partial, to be joined with others by the caller's
-// merge; a split with no position in the pool leaves (-inf, 0, 0).
-template <int MODE, int D, bool PARTS>
+template <int MODE, int D>
 __global__ void __launch_bounds__(kAttnThreads, MODE == 1 ? 4 : 0)
 attention_kernel(const AttnArgs a) {
     constexpr int KB = D / 4;   // K code bytes per thread per position
@@ -370,11 +368,11 @@ attention_kernel(const AttnArgs a) {
             float L = 0.0f, O = 0.0f;
 #pragma unroll
             for (int w = 0; w < kAttnWarps; ++w) {
-                const float f = PARTS && M == -INFINITY ? 0.0f : exp2f(s_m[w * kMaxGroup + hd] - M);
+                const float f = exp2f(s_m[w * kMaxGroup + hd] - M);
                 L += s_l[w * kMaxGroup + hd] * f;
                 O += s_o[(w * kMaxGroup + hd) * D + d] * f;
             }
-            if (!PARTS && nsplit == 1) {
+            if (nsplit == 1) {
                 a.out[(int64_t)b * a.out_seq_stride + (int64_t)(h * G + hd) * a.out_head_stride + d] =
                     (uint16_t)(pack_bf16(O / L, 0.0f) & 0xFFFFu);
             } else {
@@ -461,9 +459,9 @@ size_t part_elems(const kvc8_geom &g) {
     return (size_t)g.num_seqs * g.kv_heads * splits;  // items
 }
 
-template <int MODE, int D, bool PARTS>
+template <int MODE, int D>
 cudaError_t launch_attention_variant(const AttnArgs &a, cudaStream_t stream) {
-    auto kern = attention_kernel<MODE, D, PARTS>;
+    auto kern = attention_kernel<MODE, D>;
     const size_t smem = sizeof(float) * ((MODE == 1 ? 2 * a.g.kv_heads * (D + 16) : 0) +
                                          kAttnWarps * kMaxGroup * (D + 2));
     static OccupancySlots slots;
@@ -492,15 +490,21 @@ cudaError_t launch_attention_variant(const AttnArgs &a, cudaStream_t stream) {
     return cudaLaunchKernelEx(&cfg, kern, a);
 }
 
-template <int MODE, bool PARTS>
+template <int MODE>
 cudaError_t launch_attention_mode(const AttnArgs &a, cudaStream_t stream) {
-    if (a.g.head_dim == 64) return launch_attention_variant<MODE, 64, PARTS>(a, stream);
-    return launch_attention_variant<MODE, 128, PARTS>(a, stream);
+    if (a.g.head_dim == 64) return launch_attention_variant<MODE, 64>(a, stream);
+    return launch_attention_variant<MODE, 128>(a, stream);
 }
 
-// The split plan and the attention kernel; fills in the plan and the partials.
-template <bool PARTS>
-cudaError_t launch_splits(AttnArgs &a, void *workspace, cudaStream_t stream) {
+}  // namespace
+
+size_t attention_workspace_bytes(const kvc8_geom &g, int group) {
+    const size_t items = part_elems(g);
+    return plan_bytes(g.num_seqs) + align_up(sizeof(float) * items * group * g.head_dim, kAlign) +
+           2 * align_up(sizeof(float) * items * group, kAlign);
+}
+
+cudaError_t launch_attention(AttnArgs a, void *workspace, cudaStream_t stream) {
     // the split plan: the gather's plan with splits of kAttnChunk positions
     kvc8_geom gs = a.g;
     gs.block_size = kAttnChunk;
@@ -518,25 +522,9 @@ cudaError_t launch_splits(AttnArgs &a, void *workspace, cudaStream_t stream) {
     a.part_m = reinterpret_cast<float *>(base);
     base += align_up(sizeof(float) * items * a.group, kAlign);
     a.part_l = reinterpret_cast<float *>(base);
-    if (a.g.quant_mode == 0) return launch_attention_mode<0, PARTS>(a, stream);
-    if (a.g.quant_mode == 1) return launch_attention_mode<1, PARTS>(a, stream);
-    return launch_attention_mode<2, PARTS>(a, stream);
-}
-
-}  // namespace
-
-size_t attention_workspace_bytes(const kvc8_geom &g, int group) {
-    const size_t items = part_elems(g);
-    return plan_bytes(g.num_seqs) + align_up(sizeof(float) * items * group * g.head_dim, kAlign) +
-           2 * align_up(sizeof(float) * items * group, kAlign);
-}
-
-cudaError_t launch_attention_parts(AttnArgs &a, void *workspace, cudaStream_t stream) {
-    return launch_splits<true>(a, workspace, stream);
-}
-
-cudaError_t launch_attention(AttnArgs a, void *workspace, cudaStream_t stream) {
-    const cudaError_t e = launch_splits<false>(a, workspace, stream);
+    if (a.g.quant_mode == 0) e = launch_attention_mode<0>(a, stream);
+    else if (a.g.quant_mode == 1) e = launch_attention_mode<1>(a, stream);
+    else e = launch_attention_mode<2>(a, stream);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(a.g.num_seqs * a.g.kv_heads));

@@ -322,6 +322,10 @@ struct PrefixArgs {
     float *part_m;  // running maxima (log2 domain)
     float *part_l;  // running sums
 };
+// Its own positions (kvc8_prefix_own.cu): plan and splits, each split leaving a partial;
+// sets a.plan and the partials' places in the workspace.
+size_t own_workspace_bytes(const kvc8_geom &g, int group);
+cudaError_t launch_own(AttnArgs &a, void *workspace, cudaStream_t stream);
 size_t shared_prefix_workspace_bytes(const kvc8_geom &g, int group, int32_t max_prefix_blocks);
 cudaError_t launch_shared_prefix(PrefixArgs a, void *workspace, cudaStream_t stream);
 cudaError_t launch_rope(const RopeArgs &a, RopeSink sink, cudaStream_t stream);
@@ -329,9 +333,6 @@ cudaError_t launch_rope(const RopeArgs &a, RopeSink sink, cudaStream_t stream);
 // Workspace of the attention: the split plan, then the partials.
 size_t attention_workspace_bytes(const kvc8_geom &g, int group);
 cudaError_t launch_attention(AttnArgs a, void *workspace, cudaStream_t stream);
-// The plan and the attention kernel alone, each split leaving a partial; sets
-// a.plan and the partials' places in the workspace (attention_workspace_bytes).
-cudaError_t launch_attention_parts(AttnArgs &a, void *workspace, cudaStream_t stream);
 
 cudaError_t launch_store(const StoreArgs &a, cudaStream_t stream);
 cudaError_t launch_store_bf16(const StoreBf16Args &a, cudaStream_t stream);

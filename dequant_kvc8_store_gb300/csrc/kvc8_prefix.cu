@@ -3,10 +3,10 @@
 // its own, in one softmax.
 //   out[b][j] = (sum_p w_p V'[p] + sum_p u_p V'_b[p]) / (sum_p w_p + sum_p u_p)
 //   w_p = exp(scale <q, K'[p]>), u_p = exp(scale <q, K'_b[p]>)
-// with K', V' = bf16(fp32(code) * scale); no position at all gives zeros.
+// with K', V' = fp32(code) * scale; no position at all gives zeros.
 //
-// The sequences' own positions are the decode attention's splits
-// (kvc8_attention.cu), each left as a partial (m, l, O).  The prefix is one
+// The sequences' own positions are kvc8_prefix_own.cu's: splits, each left as a
+// partial (m, l, O).  The prefix is one
 // matrix product for all sequences: a kv head's R = sequences * group query rows
 // against P positions, 4 R P D flops for 2 P D bytes of codes, so for R above
 // about 150 rows the tensor cores and not HBM bound it.
@@ -28,6 +28,7 @@
 // slot tile + i, which no other pair has.  merge_kernel joins a row's partials.
 //
 // Every wait has a limit, after which the kernel reports KVC8_DEV_TIMEOUT and leaves.
+#include "kvc8_codes.cuh"
 #include "kvc8_internal.cuh"
 
 namespace kvc8 {
@@ -160,17 +161,6 @@ template <int N>
 __device__ __forceinline__ void reg_take() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
 __device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-__device__ __forceinline__ float ex2(float x) {  // 2^x, -inf gives 0
-    float r;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-    return r;
-}
-__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
-    uint32_t r;
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-    return r;
-}
-
 // Shared-memory operand: 128-byte swizzle, 8 rows of 128 bytes 1 KB apart (sbo),
 // 64-channel blocks of an MN-major operand lbo apart.
 __device__ __forceinline__ uint64_t operand_desc(uint32_t addr, uint32_t lbo) {
@@ -228,27 +218,6 @@ struct Layout {
     static constexpr int kBytes = (kEnd > 120 * 1024 ? kEnd : 120 * 1024) + 1024;
     static constexpr int kTmemCols = NT * (kCols + D) > 256 ? 512 : 256;
 };
-
-// Two signed codes as bf16 (both are exact): byte c of the word beside 0x43 is 128 +
-// the low seven bits, or with the sign bit alone 128 or 256 (the exponent's lowest bit
-// is the sign's place); their difference is c.
-__device__ __forceinline__ uint32_t codes_bf16(uint32_t w, uint32_t select) {
-    const uint32_t x = __byte_perm(w, 0x43434343u, select);
-    uint32_t r;
-    asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(x & 0xFF7FFF7Fu), "r"(x & 0xFF80FF80u));
-    return r;
-}
-// Two codes as fp16: (c + 128) beside 0x64 is 1024 + c + 128.
-__device__ __forceinline__ uint32_t codes_fp16(uint32_t biased, uint32_t select) {
-    uint32_t r;
-    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(__byte_perm(biased, 0x64646464u, select)), "r"(0x64806480u));
-    return r;
-}
-__device__ __forceinline__ uint32_t pack_fp16(float lo, float hi) {
-    uint32_t r;
-    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-    return r;
-}
 
 struct Barriers {
     uint64_t k_full[kStages], k_free[kStages], v_full[kStages], v_free[kStages];
@@ -618,7 +587,7 @@ struct Prefix {
                 top = fmaxf(top, fmaxf(fabsf(y.x), fabsf(y.y)));
             }
         }
-        const int ex = min(100, max(-100, (int)(__float_as_uint(top) >> 23) - 127));
+        const int ex = power_of(top);
         const float turn = __uint_as_float(((uint32_t)(127 - ex) << 23) | (flip ? 0x80000000u : 0u));
         scale = fmaxf(scale * __uint_as_float((uint32_t)(127 + ex) << 23), 0x1p-126f);
 #pragma unroll 4
@@ -807,66 +776,80 @@ __global__ void __launch_bounds__(Layout<D, NT>::kThreads, 1) prefix_kernel(cons
     pdl_wait_prior_grid();
 }
 
+// a / b for 0 <= a, 0 < b: in 32 bits where that does.
+__device__ __forceinline__ int64_t divide(int64_t a, int64_t b) {
+    if (((a | b) >> 32) == 0) return (int64_t)((uint32_t)a / (uint32_t)b);
+    return a / b;
+}
+
 // Joins a query row's partials: the prefix's segments and its own positions' splits.
-// A warp per query row, the lanes over channels.
+// A warp per query row, the lanes over channels, eight partials' loads in flight.
 template <int D>
 __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const PrefixArgs p, int rows_per_tile, int ctas) {
-    pdl_wait_prior_grid();
     const AttnArgs &a = p.own;
     constexpr int kPer = D / 32;
     const int H = a.g.kv_heads, G = a.group, B = a.g.num_seqs;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int64_t row = (int64_t)blockIdx.x * (kMergeThreads / 32) + warp;
-    if (row >= (int64_t)B * H * G) return;
-    const int b = (int)(row / (H * G)), hj = (int)(row - (int64_t)b * H * G);
-    const int h = hj / G, j = hj - h * G;
+    const int row = blockIdx.x * (kMergeThreads / 32) + warp;  // sequences * query heads < 2^30
+    const bool live = row < B * H * G;
+    const int b = row / (H * G), hj = row - b * (H * G), h = hj / G, j = hj - h * G;
     const PrefixWork w = prefix_work(p, rows_per_tile);
-    const int64_t r = (int64_t)b * G + j;
+    const int r = b * G + j, in_tile = r % rows_per_tile;
     const int64_t tile = (int64_t)h * w.tiles_per_head + r / rows_per_tile;
     int parts = 0;
     int64_t slot0 = 0;  // row of the first segment's partial; segments are a tile's rows apart
     if (w.steps > 0) {
         const int64_t first = tile * w.steps, last = first + w.steps - 1;
-        const int64_t c0 = ((first + 1) * ctas - 1) / w.units, c1 = ((last + 1) * ctas - 1) / w.units;
+        const int64_t c0 = divide((first + 1) * ctas - 1, w.units), c1 = divide((last + 1) * ctas - 1, w.units);
         parts = (int)(c1 - c0 + 1);
-        slot0 = (tile + c0) * rows_per_tile + r % rows_per_tile;
+        slot0 = (tile + c0) * rows_per_tile + in_tile;
     }
-    const int32_t *ts = reinterpret_cast<const int32_t *>(static_cast<const char *>(a.plan) + plan_tile_start_at(B));
-    const int first = ts[b], own = ts[b + 1] - first;
-    const int total = parts + own;
-    auto at = [&](int i) -> int64_t {  // partial i as a row of its array
-        return i < parts ? slot0 + (int64_t)i * rows_per_tile : (((int64_t)first + i - parts) * H + h) * G + j;
-    };
-    float M = -INFINITY;
-    for (int i = lane; i < total; i += 32) M = fmaxf(M, (i < parts ? p.part_m : a.part_m)[at(i)]);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xFFFFFFFFu, M, o));
-    float acc[kPer], lsum = 0.0f;
+    pdl_wait_prior_grid();
+    if (!live) return;
+    float M = -INFINITY, L = 0.0f, acc[kPer];  // L: this lane's share
 #pragma unroll
     for (int e = 0; e < kPer; ++e) acc[e] = 0.0f;
-    for (int i0 = 0; i0 < total; i0 += 32) {
-        const int i = i0 + lane;
-        float f = 0.0f;
-        if (i < total) {
-            const float m = (i < parts ? p.part_m : a.part_m)[at(i)];
-            f = m == -INFINITY ? 0.0f : exp2f(m - M);
-            lsum += (i < parts ? p.part_l : a.part_l)[at(i)] * f;
-        }
-        const int n = min(32, total - i0);
-#pragma unroll 8
-        for (int k = 0; k < n; ++k) {
-            const float fk = __shfl_sync(0xFFFFFFFFu, f, k);
-            const float *po = (i0 + k < parts ? p.part_o : a.part_o) + at(i0 + k) * D + lane * kPer;
-            float v[kPer];
-            if (kPer == 4) *reinterpret_cast<float4 *>(v) = *reinterpret_cast<const float4 *>(po);
-            else *reinterpret_cast<float2 *>(v) = *reinterpret_cast<const float2 *>(po);
+    // count partials, `stride` rows apart
+    auto join = [&](const float *pm, const float *pl, const float *po, int64_t stride, int count) {
+        for (int i0 = 0; i0 < count; i0 += 32) {
+            const bool in = i0 + lane < count;
+            const float m = in ? pm[(i0 + lane) * stride] : -INFINITY, l = in ? pl[(i0 + lane) * stride] : 0.0f;
+            float top = m;
 #pragma unroll
-            for (int e = 0; e < kPer; ++e) acc[e] += fk * v[e];
-        }
-    }
+            for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+            const float n = fmaxf(M, top);
+            if (n == -INFINITY) continue;  // uniform: nothing here has a position
+            const float g = M == -INFINITY ? 0.0f : exp2f(M - n), f = m == -INFINITY ? 0.0f : exp2f(m - n);
+            M = n;
+            L = L * g + l * f;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) lsum += __shfl_xor_sync(0xFFFFFFFFu, lsum, o);
-    const float inv = lsum > 0.0f ? 1.0f / lsum : 0.0f;
+            for (int e = 0; e < kPer; ++e) acc[e] *= g;
+            const int n_in = min(32, count - i0);
+            for (int k0 = 0; k0 < n_in; k0 += 8) {
+                float v[8][kPer];
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {  // past the end: the last one again, with weight 0
+                    const float *src = po + (i0 + min(k0 + k, n_in - 1)) * stride * D + lane * kPer;
+                    if (kPer == 4) *reinterpret_cast<float4 *>(v[k]) = *reinterpret_cast<const float4 *>(src);
+                    else *reinterpret_cast<float2 *>(v[k]) = *reinterpret_cast<const float2 *>(src);
+                }
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    const float fk = __shfl_sync(0xFFFFFFFFu, f, k0 + k);
+#pragma unroll
+                    for (int e = 0; e < kPer; ++e) acc[e] += fk * v[k][e];
+                }
+            }
+        }
+    };
+    const int32_t *ts = reinterpret_cast<const int32_t *>(static_cast<const char *>(a.plan) + plan_tile_start_at(B));
+    const int first = ts[b], own = ts[b + 1] - first;
+    join(p.part_m + slot0, p.part_l + slot0, p.part_o + slot0 * D, rows_per_tile, parts);
+    const int64_t own0 = ((int64_t)first * H + h) * G + j;
+    join(a.part_m + own0, a.part_l + own0, a.part_o + own0 * D, (int64_t)H * G, own);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xFFFFFFFFu, L, o);
+    const float inv = L > 0.0f ? 1.0f / L : 0.0f;
     uint16_t *dst = a.out + (int64_t)b * a.out_seq_stride + (int64_t)hj * a.out_head_stride + lane * kPer;
 #pragma unroll
     for (int e = 0; e < kPer; e += 2) {
@@ -888,7 +871,7 @@ Space space(const kvc8_geom &g, int group) {
     const int64_t per = (int64_t)tiles_per_cta(rows) * kRows;
     const size_t slots = (size_t)((rows + per - 1) / per * g.kv_heads + kMaxCtas) * (size_t)per;
     Space s;
-    s.own = attention_workspace_bytes(g, group);
+    s.own = own_workspace_bytes(g, group);
     s.o = s.own;
     s.m = s.o + align_up(slots * g.head_dim * sizeof(float), kAlign);
     s.bytes = s.m + 2 * align_up(slots * sizeof(float), kAlign);
@@ -915,13 +898,21 @@ template <int MODE, int D, int NT>
 cudaError_t launch_variant(const PrefixArgs &p, cudaStream_t stream) {
     using L = Layout<D, NT>;
     auto kern = prefix_kernel<MODE, D, NT>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kBytes);
+    static std::atomic<uint64_t> prepared{0};  // a bit per device
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
-    // a block launched with fewer registers could never hand out the warpgroups' shares
-    cudaFuncAttributes attr;
-    e = cudaFuncGetAttributes(&attr, kern);
-    if (e != cudaSuccess) return e;
-    if (attr.numRegs < L::kLaunchRegs) return cudaErrorInvalidConfiguration;
+    const uint64_t bit = dev >= 0 && dev < kMaxDevices ? 1ull << dev : 0;
+    if ((prepared.load(std::memory_order_relaxed) & bit) == 0) {
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kBytes);
+        if (e != cudaSuccess) return e;
+        // a block launched with fewer registers could never hand out the warpgroups' shares
+        cudaFuncAttributes attr;
+        e = cudaFuncGetAttributes(&attr, kern);
+        if (e != cudaSuccess) return e;
+        if (attr.numRegs < L::kLaunchRegs) return cudaErrorInvalidConfiguration;
+        prepared.fetch_or(bit, std::memory_order_relaxed);
+    }
     const int64_t rows = (int64_t)p.own.g.num_seqs * p.own.group;
     const int64_t tiles = (rows + NT * kRows - 1) / (NT * kRows) * p.own.g.kv_heads;
     const int64_t steps = ((int64_t)p.max_prefix_blocks * p.own.g.block_size + kCols - 1) / kCols;
@@ -953,7 +944,7 @@ cudaError_t launch_shared_prefix(PrefixArgs p, void *workspace, cudaStream_t str
     p.part_o = reinterpret_cast<float *>(ws + s.o);
     p.part_m = reinterpret_cast<float *>(ws + s.m);
     p.part_l = reinterpret_cast<float *>(ws + s.m + (s.bytes - s.m) / 2);
-    cudaError_t e = launch_attention_parts(p.own, workspace, stream);
+    cudaError_t e = launch_own(p.own, workspace, stream);
     if (e != cudaSuccess) return e;
     if (p.own.g.quant_mode == 0) return launch_mode<0>(p, stream);
     if (p.own.g.quant_mode == 1) return launch_mode<1>(p, stream);

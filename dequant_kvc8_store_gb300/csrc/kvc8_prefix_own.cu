@@ -1,0 +1,346 @@
+// kvc8_prefix_own.cu -- the own positions of the shared-prefix attention: each
+// sequence's queries over its own pages, every split left as a partial (m, l, O) for
+// the merge in kvc8_prefix.cu.
+//
+// The work's split is the decode attention's (kvc8_attention.cu): a sequence's context
+// in splits of kAttnChunk positions, a work item is (split, kv head), a CTA of four
+// warps takes an item, a warp walks sub-tiles of 16 positions with mma.sync.m16n8k16:
+// S^T = K Q^T and O^T += V^T P^T, positions or channels on M, the group's query heads
+// on N, so nothing is padded and codes go from global memory to operands in registers.
+//
+// What differs is what the codes cost.  HBM bounds this part (2 D bytes and four
+// products' worth of work a position), and the issue slots are mostly conversions.  So
+// codes are converted exactly and unscaled: to fp16 by one byte permute and one
+// subtraction a pair (bf16, for values that a row's scale follows, takes two logic
+// operations more).  The scales follow in fp32: a position's key scale and the head's
+// factor multiply the score, its value scale the weight, four products each a sub-tile;
+// per-channel scales are in the fp16 query and in the output.  The running maximum moves
+// only when a score passes it by 2^8, so most sub-tiles reduce and rescale nothing.
+#include "kvc8_codes.cuh"
+#include "kvc8_internal.cuh"
+
+namespace kvc8 {
+namespace {
+
+constexpr int kWarps = 4;
+constexpr int kThreads = kWarps * 32;
+constexpr int kSub = 16;      // positions per warp step
+constexpr int kMaxGroup = 8;  // query heads per kv head (mma N)
+constexpr float kLazy = 8.0f;
+
+template <bool HALF>
+__device__ __forceinline__ void mma(float c[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                    uint32_t b1) {
+    if (HALF)
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, "
+            "{%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+            : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+    else
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, "
+            "{%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+            : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+    uint32_t y;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+
+template <int N>
+__device__ __forceinline__ void load_codes(const void *p, uint32_t *w) {
+    if (N == 8) {
+        asm("ld.global.nc.L1::no_allocate.v2.u32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "l"(p));
+    } else {
+#pragma unroll
+        for (int i = 0; i < N / 16; ++i) {
+            const uint4 x = ld_stream_16(static_cast<const char *>(p) + 16 * i);
+            w[4 * i] = x.x, w[4 * i + 1] = x.y, w[4 * i + 2] = x.z, w[4 * i + 3] = x.w;
+        }
+    }
+}
+
+// Largest b in [0, B) with ts[b] <= tile.
+__device__ __forceinline__ int seq_of_split(const int32_t *ts, int B, int tile) {
+    int lo = 0, hi = B;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (ts[mid] <= tile) lo = mid; else hi = mid;
+    }
+    return lo;
+}
+
+// Query heads gid of an item as mma operands: fp16 (mode 1: times the channels' key
+// scales) after a power of two that brings a head's largest value to [1, 2); returns
+// the factor of head gid's scores, with that power and the softmax scale in it.
+template <int MODE, int D>
+__device__ __forceinline__ float load_query(const AttnArgs &a, int b, int h, int gid, int tig, uint32_t (&qf)[D / 8]) {
+    constexpr int KB = D / 4;
+    float2 v[KB / 2];
+#pragma unroll
+    for (int i = 0; i < KB / 2; ++i) v[i] = make_float2(0.0f, 0.0f);
+    float top = 0.0f;
+    if (gid < a.group) {
+        const uint16_t *qp = a.q + (int64_t)b * a.q_seq_stride + (int64_t)(h * a.group + gid) * a.q_head_stride + tig * KB;
+        const float *ks = a.k_scale + (MODE == 1 ? (int64_t)h * D + tig * KB : 0);
+#pragma unroll
+        for (int i = 0; i < KB / 8; ++i) {
+            const uint4 x = __ldg(reinterpret_cast<const uint4 *>(qp) + i);
+            const uint32_t wd[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                float2 y = make_float2(__uint_as_float(wd[e] << 16), __uint_as_float(wd[e] & 0xFFFF0000u));
+                if (MODE == 1) {
+                    const float2 s = __ldg(reinterpret_cast<const float2 *>(ks + 8 * i + 2 * e));
+                    y = make_float2(y.x * s.x, y.y * s.y);
+                }
+                v[4 * i + e] = y;
+                top = fmaxf(top, fmaxf(fabsf(y.x), fabsf(y.y)));
+            }
+        }
+    }
+    top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
+    top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
+    const int ex = power_of(top);
+    const float turn = __uint_as_float((uint32_t)(127 - ex) << 23);
+#pragma unroll
+    for (int i = 0; i < KB / 2; ++i) qf[i] = pack_fp16(v[i].x * turn, v[i].y * turn);
+    return a.scale_log2 * __uint_as_float((uint32_t)(127 + ex) << 23);
+}
+
+template <int MODE, int D>
+__global__ void __launch_bounds__(kThreads, 4) own_kernel(const AttnArgs a) {
+    constexpr int KB = D / 4;   // K code bytes per thread per position
+    constexpr int VB = D / 8;   // V code bytes per thread per position
+    constexpr int KS = D / 16;  // QK k-steps = PV m-tiles
+    constexpr bool kHalfV = MODE == 1;
+    const int H = a.g.kv_heads, bs = a.g.block_size, B = a.g.num_seqs, MB = a.g.max_blocks_per_seq, G = a.group;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int gid = lane >> 2, tig = lane & 3;
+    __shared__ float s_o[kWarps][kMaxGroup][D];
+    __shared__ float s_m[kWarps][kMaxGroup], s_l[kWarps][kMaxGroup];
+    __shared__ int s_item;
+
+    pdl_launch_dependents();
+    pdl_wait_prior_grid();  // the split plan is complete
+
+    const char *plan = static_cast<const char *>(a.plan);
+    const PlanHeader *hdr = reinterpret_cast<const PlanHeader *>(plan);
+    const int32_t *ts = reinterpret_cast<const int32_t *>(plan + plan_tile_start_at(B));
+    unsigned long long *counter = reinterpret_cast<unsigned long long *>(const_cast<int64_t *>(&hdr->work_counter));
+    const int items = (int)hdr->total_tiles * H;  // < 2^31, checked on the host
+    const int64_t cap = (int64_t)MB * bs;
+
+    int item = blockIdx.x;
+    while (item < items) {
+        int next = 0;
+        if (threadIdx.x == 0) next = (int)min((long long)atomicAdd(counter, 1ull) + gridDim.x, (long long)items);
+        const int tile = (int)((uint32_t)item / (uint32_t)H);
+        const int h = item - tile * H;
+        const int b = seq_of_split(ts, B, tile);
+        const int j = tile - ts[b];
+        const int64_t raw_len = ld_nc_s32(a.context_lengths + b);
+        if (raw_len > cap && j == 0 && h == 0 && threadIdx.x == 0) report(a.dev_error, KVC8_DEV_POS_BEYOND_TABLE);
+        const int64_t len = min(raw_len, cap);
+        const int64_t p_begin = (int64_t)j * a.chunk;
+        const int64_t p_end = min(len, p_begin + a.chunk);
+
+        uint32_t qf[KB / 2];
+        const float factor = load_query<MODE, D>(a, b, h, gid, tig, qf);
+        // the heads of this thread's score columns, 2 tig and 2 tig + 1
+        const float f0 = __shfl_sync(0xFFFFFFFFu, factor, 8 * tig), f1 = __shfl_sync(0xFFFFFFFFu, factor, 8 * tig + 4);
+
+        float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.0f, l1 = 0.0f;
+        float o[KS][4];
+#pragma unroll
+        for (int i = 0; i < KS; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.0f;
+
+        constexpr int64_t kStride = kWarps * kSub;
+        for (int64_t p0 = p_begin + warp * kSub; p0 < p_end; p0 += kStride) {
+            const int64_t lb = (int64_t)((uint32_t)p0 / (uint32_t)bs);
+            const int32_t blk = ld_nc_s32(a.block_table + (int64_t)b * MB + lb);
+            if (blk < 0 || blk >= a.g.num_blocks) {
+                if (lane == 0) report(a.dev_error, KVC8_DEV_BAD_BLOCK_ID);
+                continue;
+            }
+            const int valid = (int)min((int64_t)kSub, p_end - p0);
+            const int64_t row0 = ((int64_t)blk * H + h) * bs + (p0 - lb * bs);
+            uint32_t k0[D / 16], k1[D / 16], v[4][D / 32];
+            const int8_t *kp = a.k_cache + (row0 + gid) * D + tig * KB;
+            load_codes<KB>(kp, k0);
+            load_codes<KB>(kp + 8 * D, k1);
+            const int8_t *vp = a.v_cache + (row0 + 2 * tig) * D + gid * VB;
+            load_codes<VB>(vp, v[0]);
+            load_codes<VB>(vp + D, v[1]);
+            load_codes<VB>(vp + 8 * D, v[2]);
+            load_codes<VB>(vp + 9 * D, v[3]);
+            const bool va = gid < valid, vb = gid + 8 < valid;
+            float ka = 1.0f, kb = 1.0f, sa = 1.0f, sb = 1.0f;  // scales of positions gid and gid + 8
+            if (MODE == 0) {
+                ka = ld_nc_f32(a.k_scale + row0 + gid);
+                kb = ld_nc_f32(a.k_scale + row0 + gid + 8);
+                sa = ld_nc_f32(a.v_scale + row0 + gid);
+                sb = ld_nc_f32(a.v_scale + row0 + gid + 8);
+            } else if (MODE == 2) {
+                ka = kb = ld_nc_f32(a.k_scale + (int64_t)blk * H + h);
+                sa = sb = ld_nc_f32(a.v_scale + (int64_t)blk * H + h);
+            }
+            // S^T = K Q^T
+            float c[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+            for (int kk = 0; kk < KS; ++kk) {
+                const uint32_t wa = k0[kk] ^ 0x80808080u, wb = k1[kk] ^ 0x80808080u;
+                mma<true>(c, codes_fp16(wa, 0x4140u), codes_fp16(wb, 0x4140u), codes_fp16(wa, 0x4342u),
+                          codes_fp16(wb, 0x4342u), qf[2 * kk], qf[2 * kk + 1]);
+            }
+            c[0] = va ? c[0] * (ka * f0) : -INFINITY;
+            c[1] = va ? c[1] * (ka * f1) : -INFINITY;
+            c[2] = vb ? c[2] * (kb * f0) : -INFINITY;
+            c[3] = vb ? c[3] * (kb * f1) : -INFINITY;
+            float x0 = fmaxf(c[0], c[2]), x1 = fmaxf(c[1], c[3]);
+            if (__any_sync(0xFFFFFFFFu, x0 > m0 + kLazy || x1 > m1 + kLazy || m0 == -INFINITY)) {
+                // a column's maximum is that of the lanes with the same tig
+#pragma unroll
+                for (int sh = 4; sh < 32; sh <<= 1) {
+                    x0 = fmaxf(x0, __shfl_xor_sync(0xFFFFFFFFu, x0, sh));
+                    x1 = fmaxf(x1, __shfl_xor_sync(0xFFFFFFFFu, x1, sh));
+                }
+                const float n0 = fmaxf(m0, x0), n1 = fmaxf(m1, x1);  // finite: valid >= 1
+                const float g0 = ex2(m0 - n0), g1 = ex2(m1 - n1);
+                m0 = n0;
+                m1 = n1;
+                l0 *= g0;
+                l1 *= g1;
+#pragma unroll
+                for (int i = 0; i < KS; ++i) {
+                    o[i][0] *= g0, o[i][2] *= g0;
+                    o[i][1] *= g1, o[i][3] *= g1;
+                }
+            }
+            float w[4] = {ex2(c[0] - m0), ex2(c[1] - m1), ex2(c[2] - m0), ex2(c[3] - m1)};
+            l0 += w[0] + w[2];
+            l1 += w[1] + w[3];
+            if (MODE != 1) {  // rows behind the end may hold any scale
+                w[0] = va ? w[0] * sa : 0.0f, w[1] = va ? w[1] * sa : 0.0f;
+                w[2] = vb ? w[2] * sb : 0.0f, w[3] = vb ? w[3] * sb : 0.0f;
+            }
+            const uint32_t pb0 = transpose8x8(kHalfV ? pack_fp16(w[0], w[1]) : pack_bf16(w[0], w[1]));
+            const uint32_t pb1 = transpose8x8(kHalfV ? pack_fp16(w[2], w[3]) : pack_bf16(w[2], w[3]));
+            // O^T += V^T P^T; m-tile i: channels gid * VB + 2i and 2i + 1
+#pragma unroll
+            for (int i = 0; i < KS; ++i) {
+                const int wd = (2 * i) >> 2;
+                const uint32_t lo = (i & 1) ? 0x0602u : 0x0400u, hi = (i & 1) ? 0x0703u : 0x0501u;
+                mma<kHalfV>(o[i], codes_of_two<kHalfV>(v[0][wd], v[1][wd], lo), codes_of_two<kHalfV>(v[0][wd], v[1][wd], hi),
+                            codes_of_two<kHalfV>(v[2][wd], v[3][wd], lo), codes_of_two<kHalfV>(v[2][wd], v[3][wd], hi),
+                            pb0, pb1);
+            }
+        }
+#pragma unroll
+        for (int sh = 4; sh < 32; sh <<= 1) {
+            l0 += __shfl_xor_sync(0xFFFFFFFFu, l0, sh);
+            l1 += __shfl_xor_sync(0xFFFFFFFFu, l1, sh);
+        }
+        float *so0 = &s_o[warp][2 * tig][gid * VB], *so1 = so0 + D;
+#pragma unroll
+        for (int i = 0; i < KS; ++i) {
+            *reinterpret_cast<float2 *>(so0 + 2 * i) = make_float2(o[i][0], o[i][2]);
+            *reinterpret_cast<float2 *>(so1 + 2 * i) = make_float2(o[i][1], o[i][3]);
+        }
+        if (gid == 0) {
+            s_m[warp][2 * tig] = m0;
+            s_m[warp][2 * tig + 1] = m1;
+            s_l[warp][2 * tig] = l0;
+            s_l[warp][2 * tig + 1] = l1;
+        }
+        if (threadIdx.x == 0) s_item = next;
+        __syncthreads();
+        // join the warps; with no position in the pool the partial is (-inf, 0, 0)
+        for (int idx = threadIdx.x; idx < G * D; idx += kThreads) {
+            const int hd = idx / D, d = idx - hd * D;
+            float M = -INFINITY;
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) M = fmaxf(M, s_m[w][hd]);
+            float L = 0.0f, O = 0.0f;
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) {
+                const float f = s_m[w][hd] == -INFINITY ? 0.0f : ex2(s_m[w][hd] - M);
+                L += s_l[w][hd] * f;
+                O += s_o[w][hd][d] * f;
+            }
+            if (MODE == 1) O *= __ldg(a.v_scale + (int64_t)h * D + d);
+            a.part_o[((int64_t)item * G + hd) * D + d] = O;
+            if (d == 0) {
+                a.part_m[(int64_t)item * G + hd] = M;
+                a.part_l[(int64_t)item * G + hd] = L;
+            }
+        }
+        item = s_item;
+        __syncthreads();
+    }
+}
+
+template <int MODE, int D>
+cudaError_t launch_variant(const AttnArgs &a, int64_t max_items, cudaStream_t stream) {
+    auto kern = own_kernel<MODE, D>;
+    static OccupancySlots slots;
+    int occ = 0;
+    cudaError_t e = occupancy(slots, kern, kThreads, 0, &occ);
+    if (e != cudaSuccess) return e;
+    const int64_t cap = (int64_t)sm_count() * occ;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(max_items < cap ? max_items : cap));
+    cfg.blockDim = dim3(kThreads);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, a);
+}
+
+template <int MODE>
+cudaError_t launch_mode(const AttnArgs &a, int64_t max_items, cudaStream_t stream) {
+    if (a.g.head_dim == 64) return launch_variant<MODE, 64>(a, max_items, stream);
+    return launch_variant<MODE, 128>(a, max_items, stream);
+}
+
+int32_t max_splits(const kvc8_geom &g) {
+    return (int32_t)(((int64_t)g.max_blocks_per_seq * g.block_size + kAttnChunk - 1) / kAttnChunk);
+}
+
+}  // namespace
+
+// The split plan, then the partials: O, m, l of each (split, kv head, query head).
+size_t own_workspace_bytes(const kvc8_geom &g, int group) {
+    const size_t rows = (size_t)g.num_seqs * g.kv_heads * max_splits(g) * group;
+    return plan_bytes(g.num_seqs) + align_up(sizeof(float) * rows * g.head_dim, kAlign) +
+           2 * align_up(sizeof(float) * rows, kAlign);
+}
+
+cudaError_t launch_own(AttnArgs &a, void *workspace, cudaStream_t stream) {
+    // the split plan: the gather's plan with splits of kAttnChunk positions
+    kvc8_geom gs = a.g;
+    gs.block_size = kAttnChunk;
+    gs.max_blocks_per_seq = max_splits(a.g);
+    cudaError_t e = launch_plan(gs, a.context_lengths, nullptr, nullptr, workspace, a.dev_error, stream);
+    if (e != cudaSuccess) return e;
+    const int64_t items = (int64_t)a.g.num_seqs * a.g.kv_heads * max_splits(a.g);
+    const size_t rows = (size_t)items * a.group;
+    char *base = static_cast<char *>(workspace) + plan_bytes(a.g.num_seqs);
+    a.plan = workspace;
+    a.chunk = kAttnChunk;
+    a.part_o = reinterpret_cast<float *>(base);
+    base += align_up(sizeof(float) * rows * a.g.head_dim, kAlign);
+    a.part_m = reinterpret_cast<float *>(base);
+    base += align_up(sizeof(float) * rows, kAlign);
+    a.part_l = reinterpret_cast<float *>(base);
+    if (a.g.quant_mode == 0) return launch_mode<0>(a, items, stream);
+    if (a.g.quant_mode == 1) return launch_mode<1>(a, items, stream);
+    return launch_mode<2>(a, items, stream);
+}
+
+}  // namespace kvc8

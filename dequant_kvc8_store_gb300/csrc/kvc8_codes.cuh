@@ -21,6 +21,11 @@ __device__ __forceinline__ uint32_t pack_fp16(float lo, float hi) {
     asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
     return r;
 }
+__device__ __forceinline__ uint32_t mul_fp16(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
 // The power of two at or below x > 0, kept where it and its reciprocal are normal.
 __device__ __forceinline__ int power_of(float x) {
     return min(100, max(-100, (int)(__float_as_uint(x) >> 23) - 127));

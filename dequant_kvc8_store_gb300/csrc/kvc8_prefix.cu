@@ -12,13 +12,13 @@
 // about 150 rows the tensor cores and not HBM bound it.
 //
 // prefix_kernel: a CTA holds NT tiles of 128 query rows and walks positions 128 at
-// a time.  S = Q K'^T and O += P V' are tcgen05.mma (M = 128, bf16, fp32 in tensor
+// a time.  S = Q K'^T and O += P V' are tcgen05.mma (M = 128, fp16, fp32 in tensor
 // memory); P replaces S in tensor memory and is the second product's A operand.
 // Warps by role:
 //   softmax     4 per tile, one thread per query row: S from tensor memory, online
 //               softmax, P back; the running maximum moves only when it grows by
 //               more than 2^8, so O is seldom rescaled
-//   dequantise  codes from global memory a tile ahead in registers, K' and V' as bf16
+//   dequantise  codes from global memory a tile ahead in registers, K' and V' as fp16
 //               into a two-stage ring in the 128-byte swizzle (K' K-major, V' as the
 //               MN-major B operand of the same rows)
 //   mma         one lane issues both products; with two tiles one's products run
@@ -167,9 +167,9 @@ __device__ __forceinline__ uint64_t operand_desc(uint32_t addr, uint32_t lbo) {
     return (uint64_t)((addr & 0x3FFFFu) >> 4) | ((uint64_t)(lbo >> 4) << 16) | ((uint64_t)(1024u >> 4) << 32) |
            (1ull << 46) | (2ull << 61);
 }
-// M = 128, both operands bf16 or both fp16, fp32 accumulators; b_mn: B is MN-major.
-constexpr uint32_t instr_desc(int n, bool b_mn, bool bf16) {
-    return (1u << 4) | ((bf16 ? 1u : 0u) << 7) | ((bf16 ? 1u : 0u) << 10) | ((b_mn ? 1u : 0u) << 16) | ((uint32_t)(n >> 3) << 17) |
+// M = 128, fp16 operands, fp32 accumulators; b_mn: B is MN-major.
+constexpr uint32_t instr_desc(int n, bool b_mn) {
+    return (1u << 4) | ((b_mn ? 1u : 0u) << 16) | ((uint32_t)(n >> 3) << 17) |
            ((uint32_t)(kRows >> 4) << 24);
 }
 
@@ -225,9 +225,11 @@ struct Barriers {
     uint32_t tmem;
     int32_t stop;
     uint2 valid[kMaskSlots];  // 8 bytes: valid positions of each group of 16
-    // modes 0 and 2: each position's (each group of 16's) key and value scale
-    alignas(16) float sk[kMaskSlots][kCols];
-    alignas(16) float sv[kMaskSlots][kCols];
+    // modes 0 and 2: what was taken out of each group of 16's scales, as powers of two:
+    // the keys' 2^e, the values' e and 2^-e
+    alignas(16) float k_pow[kMaskSlots][kCols / 16];
+    alignas(16) float v_exp[kMaskSlots][kCols / 16];
+    alignas(16) float v_inv[kMaskSlots][kCols / 16];
 };
 
 template <int MODE, int D, int NT>
@@ -328,24 +330,36 @@ struct Prefix {
         return lane < kRpw && (lane & 15) < valid ? ld_nc_f32(scale + (MODE == 0 ? row + (lane & 15) : blk)) : 0.0f;
     }
 
-    // Codes into the swizzled tile, exact in fp16 or bf16: the scales are multiplied in
-    // later, in fp32 (modes 0 and 2), or are in the query and the output (mode 1).
+    // fp16 pair (s / 2^e, s / 2^e) of a position's scale, e the exponent of the largest
+    // of its group of 16, so that 127 times it is far inside fp16 whatever the scales' size.
+    __device__ __forceinline__ uint32_t normal_scale(float s, int &e) const {
+        float top = fabsf(s);
+#pragma unroll
+        for (int o = 1; o < 16; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+        e = power_of(top);
+        s *= __uint_as_float((uint32_t)(127 - e) << 23);
+        return pack_fp16(s, s);
+    }
+
+    // Codes times their scale (modes 0 and 2; mode 1 has the scales in the query and the
+    // output) into the swizzled tile, as fp16: the code is exact, the scale and the product
+    // are each rounded to eleven bits, eight times finer than the bf16 rows of the gather.
     // 16-byte chunk n of a 128-byte row lies at n ^ (row mod 8), and row mod 8 = l / 4:
     // a lane's two places are the same in every eight rows, and the eight lanes of an
     // access (two rows) hit different banks.
-    template <bool HALF>
-    __device__ __forceinline__ void store(const Codes &c, uint32_t tile, int dw) const {
+    __device__ __forceinline__ void store(const Codes &c, uint32_t scale, uint32_t tile, int dw) const {
         const int n = (lane & 3) * 2, x = lane >> 2;
         const uint32_t at = tile + (uint32_t)(dw * kRpw + x) * 128;
         const uint32_t a0 = at + (uint32_t)((n ^ x) << 4), a1 = at + (uint32_t)(((n + 1) ^ x) << 4);
 #pragma unroll
         for (int i = 0; i < kLoads; ++i) {
             const uint32_t wd[4] = {c.c[i].x, c.c[i].y, c.c[i].z, c.c[i].w};
+            const uint32_t s = MODE == 1 ? 0u : __shfl_sync(0xFFFFFFFFu, scale, i / kHalves * 8 + x);
             uint32_t o[8];
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                const uint32_t sel = (e & 1) ? 0x4342u : 0x4140u;
-                o[e] = HALF ? codes_fp16(wd[e >> 1] ^ 0x80808080u, sel) : codes_bf16(wd[e >> 1], sel);
+                o[e] = codes_fp16(wd[e >> 1] ^ 0x80808080u, (e & 1) ? 0x4342u : 0x4140u);
+                if (MODE != 1) o[e] = mul_fp16(o[e], s);
             }
             const uint32_t off = (uint32_t)(i / kHalves * 1024 + i % kHalves * (kCols * 128));
             asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(a0 + off), "r"(o[0]), "r"(o[1]), "r"(o[2]),
@@ -384,15 +398,19 @@ struct Prefix {
             const int st = n % kStages;
             const uint32_t par = (uint32_t)(n / kStages) & 1u;
             if (!wait_warp(bar.k_free[st], par ^ 1u)) return;
-            store<true>(k, base + L::kK + st * L::kTileBytes, dw);
-            if (MODE == 0 && lane < kRpw) {
-                bar.sk[n % kMaskSlots][dw * kRpw + lane] = sk;
-                bar.sv[n % kMaskSlots][dw * kRpw + lane] = sv;
+            uint32_t sk_half = 0u, sv_half = 0u;
+            if (MODE != 1) {
+                int ek, ev;
+                sk_half = normal_scale(sk, ek);
+                sv_half = normal_scale(sv, ev);
+                if (lane < kRpw && lane % 16 == 0) {
+                    const int grp = dw * kGroups + lane / 16;
+                    bar.k_pow[n % kMaskSlots][grp] = __uint_as_float((uint32_t)(127 + ek) << 23);
+                    bar.v_exp[n % kMaskSlots][grp] = (float)ev;
+                    bar.v_inv[n % kMaskSlots][grp] = __uint_as_float((uint32_t)(127 - ev) << 23);
+                }
             }
-            if (MODE == 2 && lane < kRpw && lane % 16 == 0) {
-                bar.sk[n % kMaskSlots][dw * kGroups + lane / 16] = sk;
-                bar.sv[n % kMaskSlots][dw * kGroups + lane / 16] = sv;
-            }
+            store(k, sk_half, base + L::kK + st * L::kTileBytes, dw);
             if (lane == 0) {
                 uint8_t *vc = reinterpret_cast<uint8_t *>(&bar.valid[n % kMaskSlots]) + dw * kGroups;
 #pragma unroll
@@ -410,7 +428,7 @@ struct Prefix {
                 ids = find(step, dw);
             }
             if (!wait_warp(bar.v_free[st], par ^ 1u)) return;
-            store<MODE == 1>(v, base + L::kV + st * L::kTileBytes, dw);
+            store(v, sv_half, base + L::kV + st * L::kTileBytes, dw);
             fence_async();
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_u32(&bar.v_full[st]));
@@ -426,7 +444,7 @@ struct Prefix {
 #pragma unroll
         for (int i = 0; i < D / 16; ++i) {
             const uint64_t at = (uint64_t)(((i / 4) * (kRows * 128) + (i % 4) * 32) >> 4);
-            tc_mma_ss(tmem + x * kCols, q + at, k + at, instr_desc(kCols, false, false), i > 0, leader);
+            tc_mma_ss(tmem + x * kCols, q + at, k + at, instr_desc(kCols, false), i > 0, leader);
         }
     }
     __device__ __forceinline__ void pv(int x, int st, uint32_t tmem, bool acc, uint32_t leader) const {
@@ -434,7 +452,7 @@ struct Prefix {
 #pragma unroll
         for (int i = 0; i < kCols / 16; ++i)
             tc_mma_ts(tmem + NT * kCols + x * D, tmem + x * kCols + 8 * i, v + (uint64_t)(i * (2048 >> 4)),
-                      instr_desc(D, true, MODE != 1), acc || i > 0, leader);
+                      instr_desc(D, true), acc || i > 0, leader);
     }
 
     __device__ bool products_loop(uint32_t tmem, uint32_t leader) const {
@@ -502,8 +520,7 @@ struct Prefix {
             const int64_t r0 = (tile - (int64_t)h * w.tiles_per_head) * (NT * kRows) + x * kRows + (warp & 3) * 32;
             const int64_t r = r0 + lane;
             const bool busy = r0 < rows;  // uniform in the warp: some row is a query's
-            // log2 per unit of score, with the query's power of two; never 0 (0 times -inf is
-            // no number): 2^-126 instead does not show
+            // log2 per unit of score, with the query's power of two
             float scale = fabsf(a.scale_log2);
             load_query(x, row, r, rows, h, flip, scale);
             fence_async();
@@ -589,7 +606,7 @@ struct Prefix {
         }
         const int ex = power_of(top);
         const float turn = __uint_as_float(((uint32_t)(127 - ex) << 23) | (flip ? 0x80000000u : 0u));
-        scale = fmaxf(scale * __uint_as_float((uint32_t)(127 + ex) << 23), 0x1p-126f);
+        scale *= __uint_as_float((uint32_t)(127 + ex) << 23);
 #pragma unroll 4
         for (int i = 0; i < D / 8; ++i) {
             uint4 v = make_uint4(0u, 0u, 0u, 0u);
@@ -607,103 +624,102 @@ struct Prefix {
         }
     }
 
-    // Scores of 32 positions from c on but for the factor `scale`, that is, times the
-    // positions' key scales; positions that are left out become -inf.  Returns the largest.
-    __device__ __forceinline__ float scores(float (&s)[32], int c, int slot, bool whole) const {
-        if (MODE != 1) {
+    // Leaves out positions of the 32 from c on that are behind the end or in a bad block.
+    __device__ __forceinline__ void mask(float (&s)[32], int c, int slot) const {
+        const uint32_t wd = c < 64 ? bar.valid[slot].x : bar.valid[slot].y;
 #pragma unroll
-            for (int i = 0; i < 32; i += 4) {
-                float4 f;
-                if (MODE == 0) f = *reinterpret_cast<const float4 *>(&bar.sk[slot][c + i]);
-                else f.x = f.y = f.z = f.w = bar.sk[slot][(c + i) / 16];
-                const float2 y0 = __fmul2_rn(make_float2(s[i], s[i + 1]), make_float2(f.x, f.y));
-                const float2 y1 = __fmul2_rn(make_float2(s[i + 2], s[i + 3]), make_float2(f.z, f.w));
-                s[i] = y0.x, s[i + 1] = y0.y, s[i + 2] = y1.x, s[i + 3] = y1.y;
-            }
-        }
-        if (!whole) {
-            const uint32_t wd = c < 64 ? bar.valid[slot].x : bar.valid[slot].y;
+        for (int i = 0; i < 32; ++i)
+            if (i % 16 >= (int)((wd >> (((c % 64) / 16 + i / 16) * 8)) & 0xFF)) s[i] = -INFINITY;
+    }
+    // Largest of a group of 16.
+    __device__ __forceinline__ static float top16(const float (&s)[32], int i0) {
+        float t0 = fmaxf(s[i0], s[i0 + 1]), t1 = fmaxf(s[i0 + 2], s[i0 + 3]);
 #pragma unroll
-            for (int i = 0; i < 32; ++i)
-                if (i % 16 >= (int)((wd >> (((c % 64) / 16 + i / 16) * 8)) & 0xFF)) s[i] = -INFINITY;
-        }
-        float t0 = fmaxf(s[0], s[1]), t1 = fmaxf(s[2], s[3]);
-#pragma unroll
-        for (int i = 4; i < 32; i += 4) {
-            t0 = fmaxf(t0, fmaxf(s[i], s[i + 1]));
-            t1 = fmaxf(t1, fmaxf(s[i + 2], s[i + 3]));
+        for (int i = 4; i < 16; i += 4) {
+            t0 = fmaxf(t0, fmaxf(s[i0 + i], s[i0 + i + 1]));
+            t1 = fmaxf(t1, fmaxf(s[i0 + i + 2], s[i0 + i + 3]));
         }
         return fmaxf(t0, t1);
     }
-
-    // Weights of 32 positions into P's columns, summed up.
-    __device__ __forceinline__ void weights(float (&s)[32], int c, int slot, float scale, float neg, uint32_t s_at,
-                                            float2 &sum) const {
+    // A group's factor of the scores and shift, read again where they are used (a thread
+    // has no registers to keep sixteen).  The factor is never 0, which times the -inf of a
+    // position left out would be no number; 2^-126 instead does not show.
+    __device__ __forceinline__ float2 factor_shift(int slot, int grp, float scale) const {
+        if (MODE == 1) return make_float2(fmaxf(scale, 0x1p-126f), 0.0f);
+        float f, e;
+        asm volatile("ld.shared.f32 %0, [%1];" : "=f"(f) : "r"(smem_u32(&bar.k_pow[slot][grp])));
+        asm volatile("ld.shared.f32 %0, [%1];" : "=f"(e) : "r"(smem_u32(&bar.v_exp[slot][grp])));
+        return make_float2(fmaxf(scale * f, 0x1p-126f), e);
+    }
+    // Weights of 32 positions from c on into P's columns, each group of 16 with its own
+    // factor and shift; returns their sum.
+    __device__ __forceinline__ void weights(const float (&s)[32], int c, const float *f, const float *g, uint32_t s_at,
+                                            float2 (&sum)[2]) const {
         uint32_t o[16];
 #pragma unroll
-        for (int i = 0; i < 32; i += 4) {
-            float2 y0 = make_float2(s[i], s[i + 1]), y1 = make_float2(s[i + 2], s[i + 3]);
-            y0 = __ffma2_rn(y0, make_float2(scale, scale), make_float2(neg, neg));
-            y1 = __ffma2_rn(y1, make_float2(scale, scale), make_float2(neg, neg));
-            y0 = make_float2(ex2(y0.x), ex2(y0.y));
-            y1 = make_float2(ex2(y1.x), ex2(y1.y));
-            sum = __fadd2_rn(sum, __fadd2_rn(y0, y1));
-            if (MODE != 1) {
-                float4 f;
-                if (MODE == 0) f = *reinterpret_cast<const float4 *>(&bar.sv[slot][c + i]);
-                else f.x = f.y = f.z = f.w = bar.sv[slot][(c + i) / 16];
-                y0 = __fmul2_rn(y0, make_float2(f.x, f.y));
-                y1 = __fmul2_rn(y1, make_float2(f.z, f.w));
-            }
-            // mode 1 has nothing but weights here, at most 2^8: fp16 holds them eight times
-            // finer.  Times a value scale, whose size is the caller's, they are bf16.
-            o[i / 2] = MODE == 1 ? pack_fp16(y0.x, y0.y) : pack_bf16(y0.x, y0.y);
-            o[i / 2 + 1] = MODE == 1 ? pack_fp16(y1.x, y1.y) : pack_bf16(y1.x, y1.y);
+        for (int i = 0; i < 32; i += 2) {
+            float2 y = __ffma2_rn(make_float2(s[i], s[i + 1]), make_float2(f[i / 16], f[i / 16]),
+                                  make_float2(g[i / 16], g[i / 16]));
+            y = make_float2(ex2(y.x), ex2(y.y));
+            sum[i / 16] = i % 16 == 0 ? y : __fadd2_rn(sum[i / 16], y);
+            o[i / 2] = pack_fp16(y.x, y.y);
         }
         tc_st16(s_at + c / 2, o);
     }
 
-    // One step of a row: S -> P, the running maximum m and sum l.
+    // One step of a row: S -> P, the running maximum m and sum l.  A group's weights are
+    // 2^(score + e - m), e the exponent taken out of its value scales, so that the product
+    // with the tile's values is the weight times the value; m bounds score + e, lazily.
+    // fp16 holds such weights (at most 2^8) eight times finer than bf16; what falls below
+    // 2^-24 of the largest is far below that one's own quantisation.
     __device__ __forceinline__ void step(uint32_t s_at, uint32_t o_at, float scale, bool have_o, int slot,
                                          float &m, float &l) const {
         const bool whole = bar.valid[slot].x == 0x10101010u && bar.valid[slot].y == 0x10101010u;
-        float s0[32], s1[32], s2[32], s3[32];
-        tc_ld32(s0, s_at);
-        tc_ld32(s1, s_at + 32);
-        tc_ld32(s2, s_at + 64);
-        tc_ld32(s3, s_at + 96);
-        tc_wait_ld(s0);
-        tc_wait_ld(s1);
-        tc_wait_ld(s2);
-        tc_wait_ld(s3);
-        const float t0 = scores(s0, 0, slot, whole), t1 = scores(s1, 32, slot, whole);
-        const float t2 = scores(s2, 64, slot, whole), t3 = scores(s3, 96, slot, whole);
-        const float top = fmaxf(fmaxf(t0, t1), fmaxf(t2, t3));
-        const float mx = top * scale;
+        float s[4][32];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) tc_ld32(s[q], s_at + 32 * q);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) tc_wait_ld(s[q]);
+        float mx = -INFINITY;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            if (!whole) mask(s[q], 32 * q, slot);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const float2 fe = factor_shift(slot, 2 * q + i, scale);
+                mx = fmaxf(mx, fmaf(top16(s[q], 16 * i), fe.x, fe.y));
+            }
+        }
         const bool moves = mx > m + kLazy || (m == -INFINITY && mx > m);
         if (__any_sync(0xFFFFFFFFu, moves)) {
-            const float f = moves ? ex2(m - mx) : 1.0f;  // 0 where there was nothing yet
+            const float c = moves ? ex2(m - mx) : 1.0f;  // 0 where there was nothing yet
             if (moves) m = mx;
-            l *= f;
+            l *= c;
             if (have_o) {
 #pragma unroll
-                for (int c = 0; c < D; c += 16) {
+                for (int d = 0; d < D; d += 16) {
                     float o[16];
-                    tc_ld16(o, o_at + c);
+                    tc_ld16(o, o_at + d);
                     uint32_t y[16];
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) y[i] = __float_as_uint(o[i] * f);
-                    tc_st16(o_at + c, y);
+                    for (int i = 0; i < 16; ++i) y[i] = __float_as_uint(o[i] * c);
+                    tc_st16(o_at + d, y);
                 }
             }
         }
         const float neg = m == -INFINITY ? 0.0f : -m;
-        float2 sum = make_float2(0.0f, 0.0f);
-        weights(s0, 0, slot, scale, neg, s_at, sum);
-        weights(s1, 32, slot, scale, neg, s_at, sum);
-        weights(s2, 64, slot, scale, neg, s_at, sum);
-        weights(s3, 96, slot, scale, neg, s_at, sum);
-        l += sum.x + sum.y;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const float2 a = factor_shift(slot, 2 * q, scale), b = factor_shift(slot, 2 * q + 1, scale);
+            const float f[2] = {a.x, b.x}, g[2] = {a.y + neg, b.y + neg};
+            float2 sum[2];
+            weights(s[q], 32 * q, f, g, s_at, sum);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const float part = sum[i].x + sum[i].y;
+                l = MODE == 1 ? l + part : fmaf(part, bar.v_inv[slot][2 * q + i], l);
+            }
+        }
         tc_wait_st();
     }
 };

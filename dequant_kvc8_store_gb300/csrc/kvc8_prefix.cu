@@ -65,6 +65,18 @@ __device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
         : "memory");
     return ok != 0;
 }
+// The same without suspending the thread.
+__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
 __device__ __forceinline__ void fence_async() {
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
@@ -438,57 +450,91 @@ struct Prefix {
 
     // ---- products (a warp, one lane issuing) --------------------------------------------------
     // Descriptors of the first operand block; a later one is (bytes >> 4) further on.
-    __device__ __forceinline__ void qk(int x, int st, uint32_t tmem, uint32_t leader) const {
+    // `peek` runs before the last of the eight are issued, while the tensor cores have
+    // work: what it finds ready need not be waited for afterwards.
+    template <typename Peek>
+    __device__ __forceinline__ void qk(int x, int st, uint32_t tmem, uint32_t leader, Peek &&peek) const {
         const uint64_t q = operand_desc(base + L::kQ, 16) + (uint64_t)(x * (L::kTileBytes >> 4));
         const uint64_t k = operand_desc(base + L::kK, 16) + (uint64_t)(st * (L::kTileBytes >> 4));
 #pragma unroll
         for (int i = 0; i < D / 16; ++i) {
+            if (i == D / 16 - 3) peek();
             const uint64_t at = (uint64_t)(((i / 4) * (kRows * 128) + (i % 4) * 32) >> 4);
             tc_mma_ss(tmem + x * kCols, q + at, k + at, instr_desc(kCols, false), i > 0, leader);
         }
     }
-    __device__ __forceinline__ void pv(int x, int st, uint32_t tmem, bool acc, uint32_t leader) const {
+    template <typename Peek>
+    __device__ __forceinline__ void pv(int x, int st, uint32_t tmem, bool acc, uint32_t leader, Peek &&peek) const {
         const uint64_t v = operand_desc(base + L::kV, kCols * 128) + (uint64_t)(st * (L::kTileBytes >> 4));
 #pragma unroll
-        for (int i = 0; i < kCols / 16; ++i)
+        for (int i = 0; i < kCols / 16; ++i) {
+            if (i == kCols / 16 - 3) peek();
             tc_mma_ts(tmem + NT * kCols + x * D, tmem + x * kCols + 8 * i, v + (uint64_t)(i * (2048 >> 4)),
                       instr_desc(D, true), acc || i > 0, leader);
+        }
+    }
+    __device__ __forceinline__ bool ready(uint64_t &b, uint32_t parity) const {
+        return __all_sync(0xFFFFFFFFu, mbar_test(smem_u32(&b), parity));
     }
 
-    __device__ bool products_loop(uint32_t tmem, uint32_t leader) const {
-        int n = 0, seg = 0, steps_done = 0;
-        for (int64_t u = u0; u < u1; ++seg) {
-            const int64_t tile = u / w.steps;
-            const int count = (int)(min(u1, (tile + 1) * w.steps) - u);
-            for (int t = -1; t < count; ++t) {
-                const int st = (n + t) & 1;
-                const uint32_t par = (uint32_t)((n + t) / kStages) & 1u;
-                const int st1 = (n + t + 1) % kStages;
-                const uint32_t par1 = (uint32_t)((n + t + 1) / kStages) & 1u;
-                const bool more = t + 1 < count;
+    // The loop's own quantities come from lane 0, so that the compiler keeps them, and
+    // with them stages, addresses and descriptors, in uniform registers.
+    __device__ __forceinline__ static int uniform(int x) { return __shfl_sync(0xFFFFFFFFu, x, 0); }
+
+    __device__ bool products_loop(uint32_t tmem_any, uint32_t leader) const {
+        const uint32_t tmem = (uint32_t)uniform((int)tmem_any);
+        const int total = uniform((int)(u1 - u0)), steps = uniform(w.steps);
+        int in_tile = uniform((int)(u0 % w.steps));  // step of the tile
+        uint32_t seg = 0;
+        bool first = true, next_p = false, next_v = false;
+        for (int i = 0; i < total; ++i) {
+            const int st = i & 1, st1 = st ^ 1;  // stages of this step and the next
+            const uint32_t par = (uint32_t)(i >> 1) & 1u, par1 = (uint32_t)((i + 1) >> 1) & 1u;
+            const bool more = i + 1 < total && in_tile + 1 < steps;  // the next step is of this tile
+            bool p_in[2] = {false, false}, k_in = false, v_in = false;
+            if (first) {
 #pragma unroll
                 for (int x = 0; x < NT; ++x) {
-                    if (t >= 0) {
-                        if (!wait_warp(bar.p_full[x], (uint32_t)steps_done & 1u)) return false;
-                        if (x == 0 && !wait_warp(bar.v_full[st], par)) return false;
-                        tc_fence_after();
-                        pv(x, st, tmem, t > 0, leader);
-                        if (x == NT - 1) tc_commit(smem_u32(&bar.v_free[st]), leader);
-                        if (!more) tc_commit(smem_u32(&bar.o_full[x]), leader);
-                    }
-                    if (more) {
-                        if (t < 0 && !wait_warp(bar.q_full[x], (uint32_t)seg & 1u)) return false;
-                        if (x == 0 && !wait_warp(bar.k_full[st1], par1)) return false;
-                        tc_fence_after();
-                        qk(x, st1, tmem, leader);
-                        tc_commit(smem_u32(&bar.s_full[x]), leader);
-                        if (x == NT - 1) tc_commit(smem_u32(&bar.k_free[st1]), leader);
-                    }
+                    if (!wait_warp(bar.q_full[x], seg & 1u)) return false;
+                    if (x == 0 && !wait_warp(bar.k_full[st], par)) return false;
+                    tc_fence_after();
+                    qk(x, st, tmem, leader, [] {});
+                    tc_commit(smem_u32(&bar.s_full[x]), leader);
+                    if (x == NT - 1) tc_commit(smem_u32(&bar.k_free[st]), leader);
                 }
-                if (t >= 0) ++steps_done;
+            } else {
+                p_in[0] = next_p;
+                v_in = next_v;
             }
-            n += count;
-            u += count;
+#pragma unroll
+            for (int x = 0; x < NT; ++x) {
+                if (!p_in[x] && !wait_warp(bar.p_full[x], (uint32_t)st)) return false;
+                if (x == 0 && !v_in && !wait_warp(bar.v_full[st], par)) return false;
+                tc_fence_after();
+                pv(x, st, tmem, !first, leader, [&]() {
+                    if (x == 0 && more) k_in = ready(bar.k_full[st1], par1);
+                });
+                if (x == NT - 1) tc_commit(smem_u32(&bar.v_free[st]), leader);
+                if (more) {
+                    if (x == 0 && !k_in && !wait_warp(bar.k_full[st1], par1)) return false;
+                    tc_fence_after();
+                    qk(x, st1, tmem, leader, [&]() {
+                        if (x + 1 < NT) {
+                            p_in[x + 1] = ready(bar.p_full[x + 1], (uint32_t)st);
+                        } else {
+                            next_v = ready(bar.v_full[st1], par1);
+                            next_p = NT > 1 && ready(bar.p_full[0], (uint32_t)st1);
+                        }
+                    });
+                    tc_commit(smem_u32(&bar.s_full[x]), leader);
+                    if (x == NT - 1) tc_commit(smem_u32(&bar.k_free[st1]), leader);
+                } else {
+                    tc_commit(smem_u32(&bar.o_full[x]), leader);
+                }
+            }
+            first = !more;
+            seg += first ? 1 : 0;
+            in_tile = first ? 0 : in_tile + 1;
         }
         return true;
     }
@@ -631,15 +677,17 @@ struct Prefix {
         for (int i = 0; i < 32; ++i)
             if (i % 16 >= (int)((wd >> (((c % 64) / 16 + i / 16) * 8)) & 0xFF)) s[i] = -INFINITY;
     }
+    __device__ __forceinline__ static float max3(float a, float b, float c) {
+        float r;
+        asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+        return r;
+    }
     // Largest of a group of 16.
     __device__ __forceinline__ static float top16(const float (&s)[32], int i0) {
-        float t0 = fmaxf(s[i0], s[i0 + 1]), t1 = fmaxf(s[i0 + 2], s[i0 + 3]);
-#pragma unroll
-        for (int i = 4; i < 16; i += 4) {
-            t0 = fmaxf(t0, fmaxf(s[i0 + i], s[i0 + i + 1]));
-            t1 = fmaxf(t1, fmaxf(s[i0 + i + 2], s[i0 + i + 3]));
-        }
-        return fmaxf(t0, t1);
+        const float t0 = max3(s[i0], s[i0 + 1], s[i0 + 2]), t1 = max3(s[i0 + 3], s[i0 + 4], s[i0 + 5]);
+        const float t2 = max3(s[i0 + 6], s[i0 + 7], s[i0 + 8]), t3 = max3(s[i0 + 9], s[i0 + 10], s[i0 + 11]);
+        const float t4 = max3(s[i0 + 12], s[i0 + 13], s[i0 + 14]);
+        return max3(max3(t0, t1, t2), max3(t3, t4, s[i0 + 15]), -INFINITY);
     }
     // A group's factor of the scores and shift, read again where they are used (a thread
     // has no registers to keep sixteen).  The factor is never 0, which times the -inf of a

@@ -278,11 +278,18 @@ struct Prefix {
     // ---- dequantise ------------------------------------------------------------
     static constexpr int kRpw = kCols / L::kDequantWarps;  // positions of a warp
     static constexpr int kGroups = kRpw / 16;  // a group of 16 positions lies in one block
-    static constexpr int kHalves = D / 64;     // blocks of 64 channels
-    static constexpr int kLoads = kRpw / 8 * kHalves;
+    static constexpr int kRpl = 512 / D;  // positions of one load (whole lines: 512 bytes)
+    static constexpr int kLoads = kRpw / kRpl;
 
-    // Lane l takes codes [16 (l % 4), +16) of a 64-channel block of position l / 4 of
-    // eight: load i is block i % kHalves of positions 8 (i / kHalves) + l / 4.
+    // Of each load a lane takes 16 codes of a 64-channel block.  D = 64: codes 16 (l % 4)
+    // of position l / 4.  D = 128: of every 16 lanes and two positions, lanes 0-3 take the
+    // first block of the first, 4-7 the second of the second, 8-11 the first of the
+    // second, 12-15 the second of the first, so that the eight lanes of a shared-memory
+    // access hold different rows (see store).
+    static __device__ __forceinline__ int row_in(int lane) {
+        return D == 64 ? lane >> 2 : 2 * (lane >> 4) + (((lane >> 2) ^ (lane >> 3)) & 1);
+    }
+    static __device__ __forceinline__ int block_in(int lane) { return D == 64 ? 0 : (lane >> 2) & 1; }
     struct Codes {
         uint4 c[kLoads];
     };
@@ -326,11 +333,10 @@ struct Prefix {
     __device__ __forceinline__ void load(const Where &x, const int8_t *cache, Codes &c) const {
 #pragma unroll
         for (int i = 0; i < kLoads; ++i) {
-            const int pos = i / kHalves * 8, at = pos % 16 + lane / 4;
+            const int pos = i * kRpl, at = pos % 16 + row_in(lane);
             c.c[i] = make_uint4(0u, 0u, 0u, 0u);
             if (at < x.valid[pos / 16])
-                c.c[i] = __ldg(reinterpret_cast<const uint4 *>(cache + (x.row[pos / 16] + at) * D + i % kHalves * 64) +
-                               lane % 4);
+                c.c[i] = ld_stream_16(cache + (x.row[pos / 16] + at) * D + block_in(lane) * 64 + lane % 4 * 16);
         }
     }
     // Modes 0 and 2: the scale of position `lane` of the warp.
@@ -356,29 +362,29 @@ struct Prefix {
     // Codes times their scale (modes 0 and 2; mode 1 has the scales in the query and the
     // output) into the swizzled tile, as fp16: the code is exact, the scale and the product
     // are each rounded to eleven bits, eight times finer than the bf16 rows of the gather.
-    // 16-byte chunk n of a 128-byte row lies at n ^ (row mod 8), and row mod 8 = l / 4:
-    // a lane's two places are the same in every eight rows, and the eight lanes of an
-    // access (two rows) hit different banks.
+    // 16-byte chunk n of a 128-byte row lies at n ^ (row mod 8): a lane's two places repeat
+    // (D = 128: with one bit flipped) from load to load, and the eight lanes of an access,
+    // on two neighbouring rows, hit different banks.
     __device__ __forceinline__ void store(const Codes &c, uint32_t scale, uint32_t tile, int dw) const {
-        const int n = (lane & 3) * 2, x = lane >> 2;
-        const uint32_t at = tile + (uint32_t)(dw * kRpw + x) * 128;
-        const uint32_t a0 = at + (uint32_t)((n ^ x) << 4), a1 = at + (uint32_t)(((n + 1) ^ x) << 4);
+        const int n = (lane & 3) * 2, r = row_in(lane);
+        const uint32_t at = tile + (uint32_t)(dw * kRpw + r) * 128 + (uint32_t)block_in(lane) * (kCols * 128);
+        const uint32_t c0 = (uint32_t)((n ^ r) << 4), c1 = (uint32_t)(((n + 1) ^ r) << 4);
 #pragma unroll
         for (int i = 0; i < kLoads; ++i) {
             const uint32_t wd[4] = {c.c[i].x, c.c[i].y, c.c[i].z, c.c[i].w};
-            const uint32_t s = MODE == 1 ? 0u : __shfl_sync(0xFFFFFFFFu, scale, i / kHalves * 8 + x);
+            const uint32_t s = MODE == 1 ? 0u : __shfl_sync(0xFFFFFFFFu, scale, i * kRpl + r);
             uint32_t o[8];
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 o[e] = codes_fp16(wd[e >> 1] ^ 0x80808080u, (e & 1) ? 0x4342u : 0x4140u);
                 if (MODE != 1) o[e] = mul_fp16(o[e], s);
             }
-            const uint32_t off = (uint32_t)(i / kHalves * 1024 + i % kHalves * (kCols * 128));
-            asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(a0 + off), "r"(o[0]), "r"(o[1]), "r"(o[2]),
-                         "r"(o[3])
+            const uint32_t flip = (uint32_t)(i * kRpl % 8) << 4, row = at + (uint32_t)(i * kRpl * 128);
+            asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(row + (c0 ^ flip)), "r"(o[0]), "r"(o[1]),
+                         "r"(o[2]), "r"(o[3])
                          : "memory");
-            asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(a1 + off), "r"(o[4]), "r"(o[5]), "r"(o[6]),
-                         "r"(o[7])
+            asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(row + (c1 ^ flip)), "r"(o[4]), "r"(o[5]),
+                         "r"(o[6]), "r"(o[7])
                          : "memory");
         }
     }
@@ -638,12 +644,16 @@ struct Prefix {
             }
             return y;
         };
-        float top = 0.0f;
-#pragma unroll 4
+        uint4 v[D / 8];  // the whole row in flight at once
+#pragma unroll
         for (int i = 0; i < D / 8; ++i) {
-            uint4 v = make_uint4(0u, 0u, 0u, 0u);
-            if (live) v = __ldg(reinterpret_cast<const uint4 *>(q) + i);
-            const uint32_t wd[4] = {v.x, v.y, v.z, v.w};
+            v[i] = make_uint4(0u, 0u, 0u, 0u);
+            if (live) v[i] = __ldg(reinterpret_cast<const uint4 *>(q) + i);
+        }
+        float top = 0.0f;
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i) {
+            const uint32_t wd[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 const float2 y = value(wd[e], 8 * i + 2 * e);
@@ -653,11 +663,9 @@ struct Prefix {
         const int ex = power_of(top);
         const float turn = __uint_as_float(((uint32_t)(127 - ex) << 23) | (flip ? 0x80000000u : 0u));
         scale *= __uint_as_float((uint32_t)(127 + ex) << 23);
-#pragma unroll 4
+#pragma unroll
         for (int i = 0; i < D / 8; ++i) {
-            uint4 v = make_uint4(0u, 0u, 0u, 0u);
-            if (live) v = __ldg(reinterpret_cast<const uint4 *>(q) + i);
-            uint32_t wd[4] = {v.x, v.y, v.z, v.w};
+            uint32_t wd[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 const float2 y = value(wd[e], 8 * i + 2 * e);

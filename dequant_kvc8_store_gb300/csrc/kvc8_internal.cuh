@@ -318,7 +318,13 @@ struct PrefixArgs {
     const int32_t *prefix_table;
     int32_t max_prefix_blocks;
     const int32_t *prefix_length;
-    float *part_o;  // [slots * rows of a tile][D] unnormalised partial outputs of the prefix
+    int32_t rows;            // query rows of a kv head: sequences * group
+    int32_t tiles_per_head;  // tiles of query rows
+    int32_t ctas;            // CTAs that share the prefix's work
+    // Unnormalised partial outputs of the prefix, [slots * rows of a tile] rows of D floats:
+    // 32 rows together, eight channels of each in turn ([row / 32][D / 8][32][8]), so
+    // that both a thread per row and a few lanes per row touch whole sectors.
+    float *part_o;
     float *part_m;  // running maxima (log2 domain)
     float *part_l;  // running sums
 };

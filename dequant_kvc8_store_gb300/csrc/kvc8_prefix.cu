@@ -23,9 +23,9 @@
 //               MN-major B operand of the same rows)
 //   mma         one lane issues both products; with two tiles one's products run
 //               while the other's softmax does
-// The (tile, 128 positions) units are cut evenly over the CTAs (one per SM): CTA i
-// takes units [i U / C, (i + 1) U / C) and leaves one partial per tile it touches, in
-// slot tile + i, which no other pair has.  merge_kernel joins a row's partials.
+// The (tile, 128 positions) units are cut evenly over the CTAs (one per SM): each takes
+// its share in a row and leaves one partial per tile it touches; CTA i's of tile t is in
+// slot t + i, which no other pair has.  merge_kernel joins a row's partials.
 //
 // Every wait has a limit, after which the kernel reports KVC8_DEV_TIMEOUT and leaves.
 #include "kvc8_codes.cuh"
@@ -187,22 +187,32 @@ constexpr uint32_t instr_desc(int n, bool b_mn) {
 
 // ---- the work's split -------------------------------------------------------------
 
+// a / b for 0 <= a, 0 < b: in 32 bits where that does.
+__device__ __forceinline__ int64_t divide(int64_t a, int64_t b) {
+    if (((a | b) >> 32) == 0) return (int64_t)((uint32_t)a / (uint32_t)b);
+    return a / b;
+}
+
+// Units (tile, step of 128 positions), numbered tile by tile; every CTA takes `per` in a
+// row, the first `more` one more.
 struct PrefixWork {
-    int64_t units;  // tiles * steps
-    int32_t steps;  // of 128 positions
-    int32_t tiles_per_head;
-    int32_t len;
+    int64_t units, per, more;
+    int32_t steps, len;
+    __device__ __forceinline__ int64_t first_of(int cta) const { return cta * per + min((int64_t)cta, more); }
+    __device__ __forceinline__ int cta_of(int64_t unit) const {
+        const int64_t edge = more * (per + 1);
+        return (int)(unit < edge ? divide(unit, per + 1) : more + divide(unit - edge, per));
+    }
 };
 
-__device__ __forceinline__ PrefixWork prefix_work(const PrefixArgs &p, int rows_per_tile) {
-    const kvc8_geom &g = p.own.g;
+__device__ __forceinline__ PrefixWork prefix_work(const PrefixArgs &p) {
     PrefixWork w;
-    const int64_t cap = (int64_t)p.max_prefix_blocks * g.block_size;
+    const int64_t cap = (int64_t)p.max_prefix_blocks * p.own.g.block_size;
     w.len = (int32_t)max((int64_t)0, min((int64_t)__ldg(p.prefix_length), cap));
-    w.steps = (w.len + kCols - 1) / kCols;
-    const int64_t rows = (int64_t)g.num_seqs * p.own.group;
-    w.tiles_per_head = (int32_t)((rows + rows_per_tile - 1) / rows_per_tile);
-    w.units = (int64_t)w.tiles_per_head * g.kv_heads * w.steps;
+    w.steps = (int32_t)(((uint32_t)w.len + kCols - 1) / kCols);
+    w.units = (int64_t)p.tiles_per_head * p.own.g.kv_heads * w.steps;
+    w.per = divide(w.units, p.ctas);
+    w.more = w.units - w.per * p.ctas;
     return w;
 }
 
@@ -251,7 +261,8 @@ struct Prefix {
     Barriers &bar;
     const uint32_t base;  // shared memory, 1 KB aligned
     const PrefixWork w;
-    const int64_t u0, u1;
+    const int64_t total;     // units of this CTA
+    const int tile0, step0;  // the first one's tile and step
     const int lane;
 
     // false: the limit ran out here or elsewhere in the CTA
@@ -391,8 +402,8 @@ struct Prefix {
 
     __device__ void dequantise(int dw) const {
         const AttnArgs &a = p.own;
-        int tile = (int)(u0 / w.steps), step = (int)(u0 - (int64_t)tile * w.steps);
-        Where x = place(find(step, dw), tile / w.tiles_per_head);
+        int tile = tile0, step = step0;
+        Where x = place(find(step, dw), tile / p.tiles_per_head);
         Codes k, v;
         float sk = 0.0f, sv = 0.0f;
         auto scales = [&]() {
@@ -412,7 +423,7 @@ struct Prefix {
         next();
         Ids ids = find(step, dw);
         int n = 0;
-        for (int64_t u = u0; u < u1; ++u, ++n) {
+        for (int64_t u = 0; u < total; ++u, ++n) {
             const int st = n % kStages;
             const uint32_t par = (uint32_t)(n / kStages) & 1u;
             if (!wait_warp(bar.k_free[st], par ^ 1u)) return;
@@ -437,9 +448,9 @@ struct Prefix {
             fence_async();
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_u32(&bar.k_full[st]));
-            const bool more = u + 1 < u1;
+            const bool more = u + 1 < total;
             if (more) {  // the next step's codes, and the block ids of the one after
-                x = place(ids, tile / w.tiles_per_head);
+                x = place(ids, tile / p.tiles_per_head);
                 load(x, a.k_cache, k);
                 scales();
                 next();
@@ -489,14 +500,14 @@ struct Prefix {
 
     __device__ bool products_loop(uint32_t tmem_any, uint32_t leader) const {
         const uint32_t tmem = (uint32_t)uniform((int)tmem_any);
-        const int total = uniform((int)(u1 - u0)), steps = uniform(w.steps);
-        int in_tile = uniform((int)(u0 % w.steps));  // step of the tile
+        const int units = uniform((int)total), steps = uniform(w.steps);
+        int in_tile = uniform(step0);  // step of the tile
         uint32_t seg = 0;
         bool first = true, next_p = false, next_v = false;
-        for (int i = 0; i < total; ++i) {
+        for (int i = 0; i < units; ++i) {
             const int st = i & 1, st1 = st ^ 1;  // stages of this step and the next
             const uint32_t par = (uint32_t)(i >> 1) & 1u, par1 = (uint32_t)((i + 1) >> 1) & 1u;
-            const bool more = i + 1 < total && in_tile + 1 < steps;  // the next step is of this tile
+            const bool more = i + 1 < units && in_tile + 1 < steps;  // the next step is of this tile
             bool p_in[2] = {false, false}, k_in = false, v_in = false;
             if (first) {
 #pragma unroll
@@ -561,16 +572,16 @@ struct Prefix {
         const int x = warp >> 2, row = (warp & 3) * 32 + lane;  // tile of the CTA, row of the tile
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t s_at = tmem + lanes + x * kCols, o_at = tmem + lanes + NT * kCols + x * D;
-        const int64_t rows = (int64_t)a.g.num_seqs * a.group;
+        const int rows = p.rows;
         const bool flip = a.scale_log2 < 0.0f;  // the sign goes to the query
         int n = 0;
         uint32_t seg = 0;
-        for (int64_t u = u0; u < u1; ++seg) {
-            const int64_t tile = u / w.steps;
-            const int count = (int)(min(u1, (tile + 1) * w.steps) - u);
-            const int h = (int)(tile / w.tiles_per_head);
-            const int64_t r0 = (tile - (int64_t)h * w.tiles_per_head) * (NT * kRows) + x * kRows + (warp & 3) * 32;
-            const int64_t r = r0 + lane;
+        int64_t left = total;
+        for (int tile = tile0; left > 0; ++tile, ++seg) {
+            const int count = (int)min(left, (int64_t)(w.steps - (tile == tile0 ? step0 : 0)));
+            const int h = tile / p.tiles_per_head;
+            const int r0 = (tile - h * p.tiles_per_head) * (NT * kRows) + x * kRows + (warp & 3) * 32;
+            const int r = r0 + lane;
             const bool busy = r0 < rows;  // uniform in the warp: some row is a query's
             // log2 per unit of score, with the query's power of two
             float scale = fabsf(a.scale_log2);
@@ -591,32 +602,27 @@ struct Prefix {
             if (!wait_warp(bar.o_full[x], seg & 1u)) return;
             tc_fence_after();
             if (busy) {
-                const int64_t slot = (tile + blockIdx.x) * (NT * kRows) + x * kRows + row;
-                float *po = p.part_o + slot * D;
+                const int64_t slot = ((int64_t)tile + blockIdx.x) * (NT * kRows) + x * kRows + row;
+                float *po = p.part_o + (slot - lane) * D + lane * 8;  // 32 rows' eighths in turn
 #pragma unroll
                 for (int c = 0; c < D; c += 32) {
                     float o[32];
                     tc_ld32(o, o_at + c);
                     tc_wait_ld(o);
-                    if (r < rows) {
 #pragma unroll
-                        for (int i = 0; i < 32; i += 4) {
-                            float4 y = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
-                            if (MODE == 1) {
-                                const float4 sv = __ldg(reinterpret_cast<const float4 *>(a.v_scale + (int64_t)h * D + c + i));
-                                y = make_float4(y.x * sv.x, y.y * sv.y, y.z * sv.z, y.w * sv.w);
-                            }
-                            *reinterpret_cast<float4 *>(po + c + i) = y;
+                    for (int i = 0; i < 32; i += 4) {
+                        float4 y = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+                        if (MODE == 1) {
+                            const float4 sv = __ldg(reinterpret_cast<const float4 *>(a.v_scale + (int64_t)h * D + c + i));
+                            y = make_float4(y.x * sv.x, y.y * sv.y, y.z * sv.z, y.w * sv.w);
                         }
+                        *reinterpret_cast<float4 *>(po + (c + i) / 8 * 256 + i % 8) = y;
                     }
-                    __syncwarp();
                 }
-                if (r < rows) {
-                    p.part_m[slot] = m;
-                    p.part_l[slot] = l;
-                }
+                p.part_m[slot] = m;
+                p.part_l[slot] = l;
             }
-            u += count;
+            left -= count;
         }
     }
 
@@ -625,14 +631,14 @@ struct Prefix {
     // and goes into `scale`.  Eleven bits hold a bf16 value whole (mode 1: round the
     // product eight times finer than bf16); below 2^-14 of the largest they thin out to
     // 2^-25 of it.
-    __device__ __forceinline__ void load_query(int x, int row, int64_t r, int64_t rows, int h, bool flip,
+    __device__ __forceinline__ void load_query(int x, int row, int r, int rows, int h, bool flip,
                                                float &scale) const {
         const AttnArgs &a = p.own;
         const uint32_t dst = base + L::kQ + x * L::kTileBytes + (uint32_t)row * 128;
         const bool live = r < rows;
         const uint16_t *q = a.q;
         if (live) {
-            const int b = (int)(r / a.group), j = (int)(r - (int64_t)b * a.group);
+            const int b = r / a.group, j = r - b * a.group;
             q += (int64_t)b * a.q_seq_stride + (int64_t)(h * a.group + j) * a.q_head_stride;
         }
         const float *ks = a.k_scale + (MODE == 1 ? (int64_t)h * D : 0);
@@ -787,14 +793,14 @@ __global__ void __launch_bounds__(Layout<D, NT>::kThreads, 1) prefix_kernel(cons
     __shared__ Barriers bar;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     pdl_launch_dependents();
-    const PrefixWork w = prefix_work(p, NT * kRows);
+    const PrefixWork w = prefix_work(p);
     if (blockIdx.x == 0 && threadIdx.x == 0) {
         const int32_t given = __ldg(p.prefix_length);
         if (given < 0) report(p.own.dev_error, KVC8_DEV_BAD_LENGTH);
         if (given > w.len && given >= 0) report(p.own.dev_error, KVC8_DEV_POS_BEYOND_TABLE);
     }
-    const int64_t u0 = w.units * blockIdx.x / gridDim.x, u1 = w.units * (blockIdx.x + 1) / gridDim.x;
-    if (u0 < u1) {
+    const int64_t first = w.first_of(blockIdx.x), total = w.first_of(blockIdx.x + 1) - first;
+    if (total > 0) {
         if (warp == L::kMmaWarp) {
             if (lane == 0) {
                 for (int i = 0; i < kStages; ++i) {
@@ -825,7 +831,8 @@ __global__ void __launch_bounds__(Layout<D, NT>::kThreads, 1) prefix_kernel(cons
         tc_fence_after();
         const uint32_t tmem = bar.tmem;
         const uint32_t base = (smem_u32(dyn) + 1023u) & ~1023u;
-        const Prefix<MODE, D, NT> k{p, bar, base, w, u0, u1, lane};
+        const int tile0 = (int)divide(first, w.steps);
+        const Prefix<MODE, D, NT> k{p, bar, base, w, total, tile0, (int)(first - (int64_t)tile0 * w.steps), lane};
         if (warp >= L::kMmaWarp) {
             reg_give<L::kMmaRegs>();
             if (warp == L::kMmaWarp) k.products(tmem);
@@ -848,86 +855,116 @@ __global__ void __launch_bounds__(Layout<D, NT>::kThreads, 1) prefix_kernel(cons
     pdl_wait_prior_grid();
 }
 
-// a / b for 0 <= a, 0 < b: in 32 bits where that does.
-__device__ __forceinline__ int64_t divide(int64_t a, int64_t b) {
-    if (((a | b) >> 32) == 0) return (int64_t)((uint32_t)a / (uint32_t)b);
-    return a / b;
-}
-
 // Joins a query row's partials: the prefix's segments and its own positions' splits.
-// A warp per query row, the lanes over channels, eight partials' loads in flight.
+// D / 8 lanes per query row, eight channels each, four partials' loads in flight; where
+// rows are few and partials many, `share` warps take a part of them each.
 template <int D>
-__global__ void __launch_bounds__(kMergeThreads) merge_kernel(const PrefixArgs p, int rows_per_tile, int ctas) {
+__global__ void __launch_bounds__(kMergeThreads) merge_kernel(const PrefixArgs p, int rows_per_tile, int share) {
+    constexpr int kLanes = D / 8, kWarpRows = 32 / kLanes;
+    __shared__ float s_acc[kMergeThreads][9], s_top[kMergeThreads], s_sum[kMergeThreads];
     const AttnArgs &a = p.own;
-    constexpr int kPer = D / 32;
     const int H = a.g.kv_heads, G = a.group, B = a.g.num_seqs;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int row = blockIdx.x * (kMergeThreads / 32) + warp;  // sequences * query heads < 2^30
-    const bool live = row < B * H * G;
+    const int lane = threadIdx.x & 31, gl = lane % kLanes;
+    // sequences * query heads < 2^30; rows past the end redo the last one and do not store
+    const int mine = (threadIdx.x >> 5) % share;  // which of the warps that share these rows
+    const int at = (blockIdx.x * (kMergeThreads / 32) + (threadIdx.x >> 5)) / share * kWarpRows + lane / kLanes;
+    const int row = min(at, B * H * G - 1);
     const int b = row / (H * G), hj = row - b * (H * G), h = hj / G, j = hj - h * G;
-    const PrefixWork w = prefix_work(p, rows_per_tile);
-    const int r = b * G + j, in_tile = r % rows_per_tile;
-    const int64_t tile = (int64_t)h * w.tiles_per_head + r / rows_per_tile;
+    const PrefixWork w = prefix_work(p);
+    const int r = b * G + j, tile = h * p.tiles_per_head + r / rows_per_tile;
     int parts = 0;
-    int64_t slot0 = 0;  // row of the first segment's partial; segments are a tile's rows apart
+    int64_t slot = 0;  // row of the first segment's partial; segments are a tile's rows apart
     if (w.steps > 0) {
-        const int64_t first = tile * w.steps, last = first + w.steps - 1;
-        const int64_t c0 = divide((first + 1) * ctas - 1, w.units), c1 = divide((last + 1) * ctas - 1, w.units);
-        parts = (int)(c1 - c0 + 1);
-        slot0 = (tile + c0) * rows_per_tile + in_tile;
+        const int64_t first = (int64_t)tile * w.steps;
+        const int c0 = w.cta_of(first), c1 = w.cta_of(first + w.steps - 1);
+        parts = c1 - c0 + 1;
+        slot = ((int64_t)tile + c0) * rows_per_tile + r % rows_per_tile;
     }
     pdl_wait_prior_grid();
-    if (!live) return;
-    float M = -INFINITY, L = 0.0f, acc[kPer];  // L: this lane's share
+    float M = -INFINITY, L = 0.0f, acc[8];  // L: this lane's share
 #pragma unroll
-    for (int e = 0; e < kPer; ++e) acc[e] = 0.0f;
-    // count partials, `stride` rows apart
-    auto join = [&](const float *pm, const float *pl, const float *po, int64_t stride, int count) {
-        for (int i0 = 0; i0 < count; i0 += 32) {
-            const bool in = i0 + lane < count;
-            const float m = in ? pm[(i0 + lane) * stride] : -INFINITY, l = in ? pl[(i0 + lane) * stride] : 0.0f;
-            float top = m;
+    for (int e = 0; e < 8; ++e) acc[e] = 0.0f;
+    // all partials, `stride` rows apart, of which this warp takes every share-th; o points
+    // to this lane's channels of the first.  The rows of a warp have their own counts: all
+    // stay for the longest.
+    auto join = [&](const float *pm, const float *pl, const float *o, int64_t stride, int all) {
+        const int count = (all - mine + share - 1) / share;  // 0 where all <= mine
+        pm += mine * stride, pl += mine * stride, o += mine * stride * D;
+        stride *= share;
+        const int rounds = (__reduce_max_sync(0xFFFFFFFFu, count) + kLanes - 1) / kLanes;
+        for (int i0 = 0; i0 < rounds * kLanes; i0 += kLanes) {
+            const bool in = i0 + gl < count;
+            const float m = in ? pm[(i0 + gl) * stride] : -INFINITY, l = in ? pl[(i0 + gl) * stride] : 0.0f;
+            float n = m;
 #pragma unroll
-            for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
-            const float n = fmaxf(M, top);
-            if (n == -INFINITY) continue;  // uniform: nothing here has a position
+            for (int s = kLanes / 2; s > 0; s >>= 1) n = fmaxf(n, __shfl_xor_sync(0xFFFFFFFFu, n, s));
+            n = fmaxf(M, n);
+            // no position yet: nothing is added
             const float g = M == -INFINITY ? 0.0f : exp2f(M - n), f = m == -INFINITY ? 0.0f : exp2f(m - n);
             M = n;
             L = L * g + l * f;
 #pragma unroll
-            for (int e = 0; e < kPer; ++e) acc[e] *= g;
-            const int n_in = min(32, count - i0);
-            for (int k0 = 0; k0 < n_in; k0 += 8) {
-                float v[8][kPer];
+            for (int e = 0; e < 8; ++e) acc[e] *= g;
+            const int most = __reduce_max_sync(0xFFFFFFFFu, min(kLanes, count - i0));
+            for (int k0 = 0; k0 < most; k0 += 4) {
+                float4 v[4][2];
 #pragma unroll
-                for (int k = 0; k < 8; ++k) {  // past the end: the last one again, with weight 0
-                    const float *src = po + (i0 + min(k0 + k, n_in - 1)) * stride * D + lane * kPer;
-                    if (kPer == 4) *reinterpret_cast<float4 *>(v[k]) = *reinterpret_cast<const float4 *>(src);
-                    else *reinterpret_cast<float2 *>(v[k]) = *reinterpret_cast<const float2 *>(src);
+                for (int k = 0; k < 4; ++k) {
+                    v[k][0] = v[k][1] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                    if (i0 + k0 + k < count) {
+                        const float4 *src = reinterpret_cast<const float4 *>(o + (i0 + k0 + k) * stride * D);
+                        v[k][0] = src[0];
+                        v[k][1] = src[1];
+                    }
                 }
 #pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    const float fk = __shfl_sync(0xFFFFFFFFu, f, k0 + k);
-#pragma unroll
-                    for (int e = 0; e < kPer; ++e) acc[e] += fk * v[k][e];
+                for (int k = 0; k < 4; ++k) {
+                    const float fk = __shfl_sync(0xFFFFFFFFu, f, k0 + k, kLanes);
+                    acc[0] += fk * v[k][0].x, acc[1] += fk * v[k][0].y, acc[2] += fk * v[k][0].z, acc[3] += fk * v[k][0].w;
+                    acc[4] += fk * v[k][1].x, acc[5] += fk * v[k][1].y, acc[6] += fk * v[k][1].z, acc[7] += fk * v[k][1].w;
                 }
             }
         }
     };
     const int32_t *ts = reinterpret_cast<const int32_t *>(static_cast<const char *>(a.plan) + plan_tile_start_at(B));
     const int first = ts[b], own = ts[b + 1] - first;
-    join(p.part_m + slot0, p.part_l + slot0, p.part_o + slot0 * D, rows_per_tile, parts);
+    join(p.part_m + slot, p.part_l + slot, p.part_o + slot / 32 * 32 * D + gl * 256 + slot % 32 * 8, rows_per_tile, parts);
     const int64_t own0 = ((int64_t)first * H + h) * G + j;
-    join(a.part_m + own0, a.part_l + own0, a.part_o + own0 * D, (int64_t)H * G, own);
+    join(a.part_m + own0, a.part_l + own0, a.part_o + own0 * D + gl * 8, (int64_t)H * G, own);
+    if (share > 1) {  // the same in every warp
+        s_top[threadIdx.x] = M;
+        s_sum[threadIdx.x] = L;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xFFFFFFFFu, L, o);
+        for (int e = 0; e < 8; ++e) s_acc[threadIdx.x][e] = acc[e];
+        __syncthreads();
+        if (mine == 0) {
+            for (int k = 1; k < share; ++k) {
+                const int o = threadIdx.x + 32 * k;
+                const float n = fmaxf(M, s_top[o]);
+                const float g = M == -INFINITY ? 0.0f : exp2f(M - n), f = s_top[o] == -INFINITY ? 0.0f : exp2f(s_top[o] - n);
+                M = n;
+                L = L * g + s_sum[o] * f;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) acc[e] = acc[e] * g + s_acc[o][e] * f;
+            }
+        }
+    }
+#pragma unroll
+    for (int s = kLanes / 2; s > 0; s >>= 1) L += __shfl_xor_sync(0xFFFFFFFFu, L, s);
     const float inv = L > 0.0f ? 1.0f / L : 0.0f;
-    uint16_t *dst = a.out + (int64_t)b * a.out_seq_stride + (int64_t)hj * a.out_head_stride + lane * kPer;
+    if (at != row || mine != 0) return;
+    uint16_t *dst = a.out + (int64_t)b * a.out_seq_stride + (int64_t)hj * a.out_head_stride + gl * 8;
+    uint32_t y[4];
 #pragma unroll
-    for (int e = 0; e < kPer; e += 2) {
-        const uint32_t pr = pack_bf16(acc[e] * inv, acc[e + 1] * inv);
-        dst[e] = (uint16_t)(pr & 0xFFFFu);
-        dst[e + 1] = (uint16_t)(pr >> 16);
+    for (int e = 0; e < 4; ++e) y[e] = pack_bf16(acc[2 * e] * inv, acc[2 * e + 1] * inv);
+    if ((reinterpret_cast<uintptr_t>(dst) & 15) == 0) {
+        *reinterpret_cast<uint4 *>(dst) = make_uint4(y[0], y[1], y[2], y[3]);
+    } else {  // the output may lie on any element
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            dst[2 * e] = (uint16_t)(y[e] & 0xFFFFu);
+            dst[2 * e + 1] = (uint16_t)(y[e] >> 16);
+        }
     }
 }
 
@@ -967,7 +1004,7 @@ cudaError_t launch_dependent(void (*kern)(A...), int64_t grid, int threads, size
 }
 
 template <int MODE, int D, int NT>
-cudaError_t launch_variant(const PrefixArgs &p, cudaStream_t stream) {
+cudaError_t launch_variant(PrefixArgs p, cudaStream_t stream) {
     using L = Layout<D, NT>;
     auto kern = prefix_kernel<MODE, D, NT>;
     static std::atomic<uint64_t> prepared{0};  // a bit per device
@@ -985,17 +1022,22 @@ cudaError_t launch_variant(const PrefixArgs &p, cudaStream_t stream) {
         if (attr.numRegs < L::kLaunchRegs) return cudaErrorInvalidConfiguration;
         prepared.fetch_or(bit, std::memory_order_relaxed);
     }
-    const int64_t rows = (int64_t)p.own.g.num_seqs * p.own.group;
-    const int64_t tiles = (rows + NT * kRows - 1) / (NT * kRows) * p.own.g.kv_heads;
+    p.rows = p.own.g.num_seqs * p.own.group;
+    p.tiles_per_head = (p.rows + NT * kRows - 1) / (NT * kRows);
     const int64_t steps = ((int64_t)p.max_prefix_blocks * p.own.g.block_size + kCols - 1) / kCols;
-    int64_t ctas = sm_count() < kMaxCtas ? sm_count() : kMaxCtas;
-    if (tiles * steps < ctas) ctas = tiles * steps;
-    e = launch_dependent(kern, ctas, L::kThreads, (size_t)L::kBytes, stream, p);
+    const int64_t units = (int64_t)p.tiles_per_head * p.own.g.kv_heads * steps;
+    p.ctas = sm_count() < kMaxCtas ? sm_count() : kMaxCtas;
+    if (units < p.ctas) p.ctas = (int32_t)units;
+    e = launch_dependent(kern, p.ctas, L::kThreads, (size_t)L::kBytes, stream, p);
     if (e != cudaSuccess) return e;
-    const int64_t all = rows * p.own.g.kv_heads;
-    const int64_t per = kMergeThreads / 32;
-    return launch_dependent(merge_kernel<D>, (all + per - 1) / per, kMergeThreads, (size_t)0, stream, p,
-                            NT * kRows, (int)ctas);
+    // Partials a row has of the prefix, about: CTAs per tile.  Up to six a warp (of 644 rows
+    // with 38 partials each the merge took 32 us with one warp per two rows).
+    const int64_t tiles = (int64_t)p.tiles_per_head * p.own.g.kv_heads;
+    int share = 1;
+    while (share < kMergeThreads / 32 && p.ctas > 6 * share * tiles) share *= 2;
+    const int64_t all = (int64_t)p.rows * p.own.g.kv_heads, per = kMergeThreads / (D / 8) / share;
+    return launch_dependent(merge_kernel<D>, (all + per - 1) / per, kMergeThreads, (size_t)0, stream, p, NT * kRows,
+                            share);
 }
 
 template <int MODE>

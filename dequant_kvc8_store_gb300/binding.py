@@ -158,6 +158,8 @@ def configure(lib: ctypes.CDLL) -> ctypes.CDLL:
 def load(build_if_needed: bool = True) -> ctypes.CDLL:
     """Load libkvc8.so (building it with nvcc first if it is missing or stale)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -184,10 +186,26 @@ def _p(x):
     return x.data_ptr()
 
 
+_current_stream = None
+
+
+def _find_current_stream():
+    """torch's current stream as an address.  Asked for on every call, so by the
+    lookup under torch.cuda.current_stream() where torch has it (0.3 us against
+    2.9 us for the Stream object)."""
+    import torch
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    if raw is None:
+        return lambda: torch.cuda.current_stream().cuda_stream
+    return lambda: raw(torch.cuda.current_device())
+
+
 def _stream(stream):
+    global _current_stream
     if stream is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream
+        if _current_stream is None:
+            _current_stream = _find_current_stream()
+        return _current_stream()
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream

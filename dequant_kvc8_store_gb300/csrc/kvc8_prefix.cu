@@ -926,10 +926,10 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const PrefixArgs p
             }
         }
     };
-    const int32_t *ts = reinterpret_cast<const int32_t *>(static_cast<const char *>(a.plan) + plan_tile_start_at(B));
-    const int first = ts[b], own = ts[b + 1] - first;
+    const int64_t len = min((int64_t)ld_nc_s32(a.context_lengths + b), (int64_t)a.g.max_blocks_per_seq * a.g.block_size);
+    const int own = len > 0 ? (int)((len + kAttnChunk - 1) / kAttnChunk) : 0;  // splits of its own positions
     join(p.part_m + slot, p.part_l + slot, p.part_o + slot / 32 * 32 * D + gl * 256 + slot % 32 * 8, rows_per_tile, parts);
-    const int64_t own0 = ((int64_t)first * H + h) * G + j;
+    const int64_t own0 = ((int64_t)b * p.own_splits * H + h) * G + j;
     join(a.part_m + own0, a.part_l + own0, a.part_o + own0 * D + gl * 8, (int64_t)H * G, own);
     if (share > 1) {  // the same in every warp
         s_top[threadIdx.x] = M;
@@ -1058,7 +1058,7 @@ cudaError_t launch_shared_prefix(PrefixArgs p, void *workspace, cudaStream_t str
     p.part_o = reinterpret_cast<float *>(ws + s.o);
     p.part_m = reinterpret_cast<float *>(ws + s.m);
     p.part_l = reinterpret_cast<float *>(ws + s.m + (s.bytes - s.m) / 2);
-    cudaError_t e = launch_own(p.own, workspace, stream);
+    cudaError_t e = launch_own(p, workspace, stream);
     if (e != cudaSuccess) return e;
     if (p.own.g.quant_mode == 0) return launch_mode<0>(p, stream);
     if (p.own.g.quant_mode == 1) return launch_mode<1>(p, stream);

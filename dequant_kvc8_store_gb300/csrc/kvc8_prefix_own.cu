@@ -2,9 +2,10 @@
 // sequence's queries over its own pages, every split left as a partial (m, l, O) for
 // the merge in kvc8_prefix.cu.
 //
-// The work's split is the decode attention's (kvc8_attention.cu): a sequence's context
-// in splits of kAttnChunk positions, a work item is (split, kv head), a CTA of four
-// warps takes an item, a warp walks sub-tiles of 16 positions with mma.sync.m16n8k16:
+// A sequence's context is cut into splits of kAttnChunk positions.  A CTA of four warps
+// takes every `stride`-th split of a (sequence, kv head), so that no plan of the ragged
+// lengths is needed before the launch and the hardware evens out what they differ by; a
+// warp walks sub-tiles of 16 positions with mma.sync.m16n8k16:
 // S^T = K Q^T and O^T += V^T P^T, positions or channels on M, the group's query heads
 // on N, so nothing is padded and codes go from global memory to operands in registers.
 //
@@ -62,16 +63,6 @@ __device__ __forceinline__ void load_codes(const void *p, uint32_t *w) {
     }
 }
 
-// Largest b in [0, B) with ts[b] <= tile.
-__device__ __forceinline__ int seq_of_split(const int32_t *ts, int B, int tile) {
-    int lo = 0, hi = B;
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (ts[mid] <= tile) lo = mid; else hi = mid;
-    }
-    return lo;
-}
-
 // Query heads gid of an item as mma operands: fp16 (mode 1: times the channels' key
 // scales) after a power of two that brings a head's largest value to [1, 2); returns
 // the factor of head gid's scores, with that power and the softmax scale in it.
@@ -111,41 +102,30 @@ __device__ __forceinline__ float load_query(const AttnArgs &a, int b, int h, int
 }
 
 template <int MODE, int D>
-__global__ void __launch_bounds__(kThreads, 4) own_kernel(const AttnArgs a) {
+__global__ void __launch_bounds__(kThreads, 4) own_kernel(const AttnArgs a, int splits, int stride) {
     constexpr int KB = D / 4;   // K code bytes per thread per position
     constexpr int VB = D / 8;   // V code bytes per thread per position
     constexpr int KS = D / 16;  // QK k-steps = PV m-tiles
     constexpr bool kHalfV = MODE == 1;
-    const int H = a.g.kv_heads, bs = a.g.block_size, B = a.g.num_seqs, MB = a.g.max_blocks_per_seq, G = a.group;
+    const int H = a.g.kv_heads, bs = a.g.block_size, MB = a.g.max_blocks_per_seq, G = a.group;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int gid = lane >> 2, tig = lane & 3;
     __shared__ float s_o[kWarps][kMaxGroup][D];
     __shared__ float s_m[kWarps][kMaxGroup], s_l[kWarps][kMaxGroup];
-    __shared__ int s_item;
 
-    pdl_launch_dependents();
-    pdl_wait_prior_grid();  // the split plan is complete
+    pdl_launch_dependents();  // the prefix's kernel needs nothing of this one
+    const int b = blockIdx.x / H, h = blockIdx.x - b * H;
+    const int64_t cap = (int64_t)MB * bs, raw_len = ld_nc_s32(a.context_lengths + b);
+    if (h == 0 && blockIdx.y == 0 && threadIdx.x == 0) {
+        if (raw_len < 0) report(a.dev_error, KVC8_DEV_BAD_LENGTH);
+        if (raw_len > cap) report(a.dev_error, KVC8_DEV_POS_BEYOND_TABLE);
+    }
+    const int64_t len = min(raw_len, cap);
 
-    const char *plan = static_cast<const char *>(a.plan);
-    const PlanHeader *hdr = reinterpret_cast<const PlanHeader *>(plan);
-    const int32_t *ts = reinterpret_cast<const int32_t *>(plan + plan_tile_start_at(B));
-    unsigned long long *counter = reinterpret_cast<unsigned long long *>(const_cast<int64_t *>(&hdr->work_counter));
-    const int items = (int)hdr->total_tiles * H;  // < 2^31, checked on the host
-    const int64_t cap = (int64_t)MB * bs;
-
-    int item = blockIdx.x;
-    while (item < items) {
-        int next = 0;
-        if (threadIdx.x == 0) next = (int)min((long long)atomicAdd(counter, 1ull) + gridDim.x, (long long)items);
-        const int tile = (int)((uint32_t)item / (uint32_t)H);
-        const int h = item - tile * H;
-        const int b = seq_of_split(ts, B, tile);
-        const int j = tile - ts[b];
-        const int64_t raw_len = ld_nc_s32(a.context_lengths + b);
-        if (raw_len > cap && j == 0 && h == 0 && threadIdx.x == 0) report(a.dev_error, KVC8_DEV_POS_BEYOND_TABLE);
-        const int64_t len = min(raw_len, cap);
-        const int64_t p_begin = (int64_t)j * a.chunk;
-        const int64_t p_end = min(len, p_begin + a.chunk);
+    for (int j = blockIdx.y; (int64_t)j * kAttnChunk < len; j += stride) {
+        const int64_t item = ((int64_t)b * splits + j) * H + h;
+        const int64_t p_begin = (int64_t)j * kAttnChunk;
+        const int64_t p_end = min(len, p_begin + kAttnChunk);
 
         uint32_t qf[KB / 2];
         const float factor = load_query<MODE, D>(a, b, h, gid, tig, qf);
@@ -255,7 +235,6 @@ __global__ void __launch_bounds__(kThreads, 4) own_kernel(const AttnArgs a) {
             s_l[warp][2 * tig] = l0;
             s_l[warp][2 * tig + 1] = l1;
         }
-        if (threadIdx.x == 0) s_item = next;
         __syncthreads();
         // join the warps; with no position in the pool the partial is (-inf, 0, 0)
         for (int idx = threadIdx.x; idx < G * D; idx += kThreads) {
@@ -271,76 +250,61 @@ __global__ void __launch_bounds__(kThreads, 4) own_kernel(const AttnArgs a) {
                 O += s_o[w][hd][d] * f;
             }
             if (MODE == 1) O *= __ldg(a.v_scale + (int64_t)h * D + d);
-            a.part_o[((int64_t)item * G + hd) * D + d] = O;
+            a.part_o[(item * G + hd) * D + d] = O;
             if (d == 0) {
-                a.part_m[(int64_t)item * G + hd] = M;
-                a.part_l[(int64_t)item * G + hd] = L;
+                a.part_m[item * G + hd] = M;
+                a.part_l[item * G + hd] = L;
             }
         }
-        item = s_item;
         __syncthreads();
     }
-}
-
-template <int MODE, int D>
-cudaError_t launch_variant(const AttnArgs &a, int64_t max_items, cudaStream_t stream) {
-    auto kern = own_kernel<MODE, D>;
-    static OccupancySlots slots;
-    int occ = 0;
-    cudaError_t e = occupancy(slots, kern, kThreads, 0, &occ);
-    if (e != cudaSuccess) return e;
-    const int64_t cap = (int64_t)sm_count() * occ;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(max_items < cap ? max_items : cap));
-    cfg.blockDim = dim3(kThreads);
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kern, a);
-}
-
-template <int MODE>
-cudaError_t launch_mode(const AttnArgs &a, int64_t max_items, cudaStream_t stream) {
-    if (a.g.head_dim == 64) return launch_variant<MODE, 64>(a, max_items, stream);
-    return launch_variant<MODE, 128>(a, max_items, stream);
 }
 
 int32_t max_splits(const kvc8_geom &g) {
     return (int32_t)(((int64_t)g.max_blocks_per_seq * g.block_size + kAttnChunk - 1) / kAttnChunk);
 }
 
-}  // namespace
+// CTAs of a launch that keep the GPU full and still start and end in no time when the
+// tables have room for many more splits than the sequences use.
+constexpr int64_t kMaxGrid = 8192;
 
-// The split plan, then the partials: O, m, l of each (split, kv head, query head).
-size_t own_workspace_bytes(const kvc8_geom &g, int group) {
-    const size_t rows = (size_t)g.num_seqs * g.kv_heads * max_splits(g) * group;
-    return plan_bytes(g.num_seqs) + align_up(sizeof(float) * rows * g.head_dim, kAlign) +
-           2 * align_up(sizeof(float) * rows, kAlign);
+template <int MODE, int D>
+cudaError_t launch_variant(const AttnArgs &a, cudaStream_t stream) {
+    const int64_t pairs = (int64_t)a.g.num_seqs * a.g.kv_heads;
+    const int splits = max_splits(a.g);
+    int64_t stride = kMaxGrid / pairs;
+    stride = stride < 1 ? 1 : stride > splits ? splits : stride;
+    own_kernel<MODE, D><<<dim3((unsigned)pairs, (unsigned)stride), kThreads, 0, stream>>>(a, splits, (int)stride);
+    return cudaGetLastError();
 }
 
-cudaError_t launch_own(AttnArgs &a, void *workspace, cudaStream_t stream) {
-    // the split plan: the gather's plan with splits of kAttnChunk positions
-    kvc8_geom gs = a.g;
-    gs.block_size = kAttnChunk;
-    gs.max_blocks_per_seq = max_splits(a.g);
-    cudaError_t e = launch_plan(gs, a.context_lengths, nullptr, nullptr, workspace, a.dev_error, stream);
-    if (e != cudaSuccess) return e;
-    const int64_t items = (int64_t)a.g.num_seqs * a.g.kv_heads * max_splits(a.g);
-    const size_t rows = (size_t)items * a.group;
-    char *base = static_cast<char *>(workspace) + plan_bytes(a.g.num_seqs);
-    a.plan = workspace;
-    a.chunk = kAttnChunk;
+template <int MODE>
+cudaError_t launch_mode(const AttnArgs &a, cudaStream_t stream) {
+    if (a.g.head_dim == 64) return launch_variant<MODE, 64>(a, stream);
+    return launch_variant<MODE, 128>(a, stream);
+}
+
+}  // namespace
+
+// The partials: O, m, l of each (sequence, split, kv head, query head).
+size_t own_workspace_bytes(const kvc8_geom &g, int group) {
+    const size_t rows = (size_t)g.num_seqs * g.kv_heads * max_splits(g) * group;
+    return align_up(sizeof(float) * rows * g.head_dim, kAlign) + 2 * align_up(sizeof(float) * rows, kAlign);
+}
+
+cudaError_t launch_own(PrefixArgs &p, void *workspace, cudaStream_t stream) {
+    AttnArgs &a = p.own;
+    const size_t rows = (size_t)a.g.num_seqs * a.g.kv_heads * max_splits(a.g) * a.group;
+    char *base = static_cast<char *>(workspace);
+    p.own_splits = max_splits(a.g);
     a.part_o = reinterpret_cast<float *>(base);
     base += align_up(sizeof(float) * rows * a.g.head_dim, kAlign);
     a.part_m = reinterpret_cast<float *>(base);
     base += align_up(sizeof(float) * rows, kAlign);
     a.part_l = reinterpret_cast<float *>(base);
-    if (a.g.quant_mode == 0) return launch_mode<0>(a, items, stream);
-    if (a.g.quant_mode == 1) return launch_mode<1>(a, items, stream);
-    return launch_mode<2>(a, items, stream);
+    if (a.g.quant_mode == 0) return launch_mode<0>(a, stream);
+    if (a.g.quant_mode == 1) return launch_mode<1>(a, stream);
+    return launch_mode<2>(a, stream);
 }
 
 }  // namespace kvc8

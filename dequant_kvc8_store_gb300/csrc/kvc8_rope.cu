@@ -16,13 +16,14 @@
 // Work: L lanes hold a row (D / 16 rounded up to a power of two), 16 channels
 // each as two pieces of eight, so a warp takes 32 / L rows of one kind (queries,
 // keys or values) of a token at a time.  A lane's two pieces hold whole pairs --
-// channels [8c, 8c+8) and [R/2 + 8c, +8) in the half layout, 16 neighbours in the
-// interleaved one -- so nothing is exchanged but the row sums and maxima.  A unit of
+// channels [8c, 8c+8) and [R/2 + 8c, +8) in the half layout, any eight neighbours in
+// the interleaved one -- so nothing is exchanged but the row sums and maxima.  A unit of
 // work is a token, or a part of its row sets where there are fewer tokens than
 // warps.  The warp finds its token's slot, computes the R/2 sines and cosines once
 // (a lane R/64 of them, handed over in shared memory), folds the norm's weights into
 // them, and then spends on a row little more than unpacking, the sum of squares, four
-// multiply-adds a pair and packing; the next set's loads are in flight meanwhile.
+// multiply-adds a pair and packing.  The rows come through a ring in shared memory,
+// three sets ahead.
 //
 // Codes without dividing: with r = fl(1/s), every value fl(y/s) can take lies between
 // y r (1 - 2^-21) and y r (1 + 2^-21) (r and the quotient are each within 2^-24 of
@@ -34,6 +35,7 @@ namespace kvc8 {
 namespace {
 
 constexpr int kRopeWarps = 4;
+constexpr int kRing = 4;  // row sets per warp in shared memory, one fewer in flight
 constexpr int kMaxPairs = 128;
 
 __device__ __forceinline__ float bf16_lo(uint32_t x) { return __uint_as_float(x << 16); }
@@ -49,44 +51,63 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
 struct Slot {
     int64_t row;  // cache row of (block, head 0, slot); -1: the token is skipped
     int32_t blk;
-    int64_t pos;  // its rotary position
+    int32_t pos;  // its rotary position: as given, or the slot's as an unsigned number
 };
 
+// One token per lane: the warp's next 32 tokens are looked up at once.
 template <int SINK>
-__device__ __forceinline__ Slot find_slot(const RopeArgs &a, int64_t t, int lane, bool report_it) {
+__device__ __forceinline__ Slot find_slot(const RopeArgs &a, int64_t t, bool report_it) {
     Slot s = {0, 0, 0};
     if (SINK != kSinkRows) {
-        const int bs = a.g.block_size, MB = a.g.max_blocks_per_seq;
-        TokenSeq q;
+        const int B = a.g.num_seqs, bs = a.g.block_size, MB = a.g.max_blocks_per_seq;
+        int64_t first = t, next = t + 1;
+        int b = (int)t;
         if (a.cu_q_lens != nullptr) {
-            q = seq_ctx_of_token(a.cu_q_lens, a.context_kv_lens, a.g.num_seqs, t, lane);
-        } else {
-            q = {(int)t, t, t + 1, ld_nc_s32(a.context_kv_lens + t)};
+            // the last sequence whose first new token is at or before t
+            b = 0;
+            for (int step = 1 << (31 - __clz(max(B - 1, 1))); step > 0; step >>= 1)
+                if (b + step < B && (int64_t)ld_nc_s32(a.cu_q_lens + b + step) <= t) b += step;
+            first = ld_nc_s32(a.cu_q_lens + b);
+            next = ld_nc_s32(a.cu_q_lens + b + 1);
         }
-        s.pos = q.ctx + (t - q.first);
+        const int64_t ctx = ld_nc_s32(a.context_kv_lens + b), pos = ctx + (t - first);
         int32_t err = 0;
-        int64_t lb = 0;
-        if (!(q.first <= t && t < q.next) || q.ctx < 0) {
+        if (!(first <= t && t < next) || ctx < 0) {
             err = KVC8_DEV_BAD_LENGTH;
         } else {
             // 0 <= pos < 2^32: a 32-bit division
-            lb = (int64_t)((uint32_t)s.pos / (uint32_t)bs);
+            const int64_t lb = (int64_t)((uint32_t)pos / (uint32_t)bs);
             if (lb >= MB) {
                 err = KVC8_DEV_POS_BEYOND_TABLE;
             } else {
-                s.blk = ld_nc_s32(a.block_table + (int64_t)q.b * MB + lb);
+                s.blk = ld_nc_s32(a.block_table + (int64_t)b * MB + lb);
                 if (s.blk < 0 || s.blk >= a.g.num_blocks) err = KVC8_DEV_BAD_BLOCK_ID;
+                s.row = (int64_t)s.blk * a.g.kv_heads * bs + (pos - lb * bs);
+                s.pos = (int32_t)(uint32_t)pos;
             }
         }
         if (err != 0) {
-            if (report_it && lane == 0) report(a.dev_error, err);
+            if (report_it) report(a.dev_error, err);
             s.row = -1;
             return s;
         }
-        s.row = (int64_t)s.blk * a.g.kv_heads * bs + (s.pos - lb * bs);
     }
     if (a.positions != nullptr) s.pos = ld_nc_s32(a.positions + t);
     return s;
+}
+
+// cp.async: 16 bytes global -> shared, waited for by the thread that asked, which alone
+// reads them.
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+__device__ __forceinline__ uint4 ld_shared16(uint32_t p) {
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(p));
+    return v;
 }
 
 constexpr float kMagic = 12582912.0f;            // 1.5 * 2^23: adding it rounds to an integer
@@ -135,59 +156,129 @@ __device__ __forceinline__ uint32_t codes4(float2 y0, float2 y1, float4 s, float
 
 // L lanes per row, 32 / L rows of a set.
 template <int SINK, int L>
-__global__ void __launch_bounds__(kRopeWarps * 32, 5) rope_kernel(const RopeArgs a, int parts) {
+__global__ void __launch_bounds__(kRopeWarps * 32, 5) rope_kernel(const RopeArgs a, int parts, int per) {
     constexpr int RW = 32 / L;
     constexpr bool kPages = SINK != kSinkRows;
     __shared__ __align__(16) float turn_s[kRopeWarps][2][kMaxPairs];  // m cos, m sin
+    // the two pieces of each lane, apart so that an access covers whole rows of banks
+    __shared__ uint4 ring_s[kRopeWarps][kRing][2][32];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int H = a.g.kv_heads, D = a.g.head_dim, R = a.rotary_dim, bs = a.g.block_size;
     const int sq = (a.q_heads + RW - 1) / RW, sk = (H + RW - 1) / RW;
     const int sets = sq + sk + (kPages ? sk : 0);  // row sets of a token: queries, keys, values
-    const int per = (sets + parts - 1) / parts;
     const int rl = lane / L, c = lane % L;
     const bool on_c = c < D / 16;
-    // This lane's channels.  Half layout: lanes c < R/16 rotate channels 8c and R/2 + 8c
-    // on; the others pass sixteen of the rest.
-    const bool turns = c < R / 16;
-    const int d0 = turns && !a.interleaved ? 8 * c : 16 * c;
-    const int d1 = turns && !a.interleaved ? R / 2 + 8 * c : 16 * c + 8;
+    // This lane's channels, two pieces of eight, neighbouring lanes' side by side so that
+    // every access covers whole sectors.  Half layout: lanes c < R/16 take pairs 8c to
+    // 8c + 7, the others pass channels behind R; interleaved: the halves of the row.
+    const bool half = a.interleaved == 0, turns = half && c < R / 16;
+    const int pass = R + 8 * (c - R / 16);
+    const int d0 = !half || turns ? 8 * c : pass;
+    const int d1 = !half ? D / 2 + 8 * c : turns ? R / 2 + 8 * c : pass + (D - R) / 2;
+    const int v0 = 8 * c, v1 = D / 2 + 8 * c;  // of a value row
     const float inv_d = 1.0f / (float)D;
     float *cos_s = turn_s[warp][0], *sin_s = turn_s[warp][1];
 
-    const int64_t units = a.num_tokens * parts;
-    for (int64_t u = (int64_t)blockIdx.x * kRopeWarps + warp; u < units; u += (int64_t)gridDim.x * kRopeWarps) {
-        const int64_t t = parts == 1 ? u : u / parts;
-        const int s0 = (int)(u - t * parts) * per, s1 = min(sets, s0 + per);
-        if (s0 >= s1) continue;
+    // Units of work (token, part of its row sets): this warp's are u0, u0 + stride, ...
+    const int64_t units = a.num_tokens * parts, stride = (int64_t)gridDim.x * kRopeWarps;
+    const int64_t u0 = (int64_t)blockIdx.x * kRopeWarps + warp;
+    auto token_of = [&](int64_t u) { return parts == 1 ? u : u / parts; };
 
-        uint4 x0, x1;  // the rows of the next set
-        const uint16_t *const qt = a.q + t * a.q_tok_stride, *const kt = a.k + t * a.x_tok_stride;
-        const uint16_t *const vt = a.v + t * a.x_tok_stride;
-        auto fetch = [&](int set) {
-            const int kind = set < sq ? 0 : set < sq + sk ? 1 : 2;
-            const int h = (set - (kind == 0 ? 0 : kind == 1 ? sq : sq + sk)) * RW + rl;
-            x0 = x1 = make_uint4(0u, 0u, 0u, 0u);
-            if (on_c && h < (kind == 0 ? a.q_heads : H)) {
-                const uint16_t *src = kind == 0 ? qt + (int64_t)h * a.q_head_stride
-                                                : (kind == 1 ? kt : vt) + (int64_t)h * a.x_head_stride;
-                x0 = ld_stream_16(src + (kind == 2 ? 16 * c : d0));
-                x1 = ld_stream_16(src + (kind == 2 ? 16 * c + 8 : d1));
+    // The row sets to come, requested kRing - 1 ahead of the one being worked on, over the
+    // ends of kinds, tokens and units alike.  A lane's copies go to its own places, which it
+    // alone reads.
+    const uint32_t ring = (uint32_t)__cvta_generic_to_shared(&ring_s[warp][0][0][lane]);
+    const uint16_t *p0 = nullptr;
+    int64_t p_step = 0, pu = u0;
+    int p_gap = 0;                    // from the first piece to the second
+    int p_left = 0;                   // heads of the kind from this lane's row on
+    int p_set = 0, p_end = 0;         // the next set to request, the end of its unit
+    uint32_t p_slot = 0, r_slot = 0;  // ring places to fill and to read (bytes)
+    constexpr uint32_t kSet = 2 * 32 * 16;
+    auto begin = [&](int64_t t, int set) {  // the set may lie inside a kind
+        const bool q = set < sq, v = set >= sq + sk;
+        const int h = (set - (q ? 0 : v ? sq + sk : sq)) * RW + rl;
+        const int64_t hs = q ? a.q_head_stride : a.x_head_stride;
+        const uint16_t *row = q ? a.q + t * a.q_tok_stride : (v ? a.v : a.k) + t * a.x_tok_stride;
+        p0 = row + h * hs + (v ? v0 : d0);
+        p_gap = v ? v1 - v0 : d1 - d0;
+        p_step = RW * hs;
+        p_left = (q ? a.q_heads : H) - h;
+    };
+    auto pull = [&]() {
+        if (pu < units) {
+            if (on_c && p_left > 0) {
+                cp_async16(ring + p_slot, p0);
+                cp_async16(ring + p_slot + 32 * 16, p0 + p_gap);
             }
-        };
-        fetch(s0);
-        const Slot slot = find_slot<SINK>(a, t, lane, s0 == 0);
-        if (kPages && slot.row < 0) continue;  // uniform in the warp
-        __syncwarp();
+            p0 += p_step;
+            p_left -= RW;
+            if (++p_set == p_end) {  // on to the next unit
+                pu += stride;
+                if (pu < units) {
+                    const int64_t tn = token_of(pu);
+                    p_set = (int)(pu - tn * parts) * per;
+                    p_end = min(sets, p_set + per);
+                    begin(tn, p_set);
+                }
+            } else if (p_set == sq || p_set == sq + sk) {
+                begin(token_of(pu), p_set);
+            }
+        }
+        cp_async_commit();
+        p_slot = (p_slot + kSet) & (kRing * kSet - 1);
+    };
+    uint4 x0, x1;
+    auto take = [&]() {
+        cp_async_wait<kRing - 2>();
+        x0 = ld_shared16(ring + r_slot);
+        x1 = ld_shared16(ring + r_slot + 32 * 16);
+        r_slot = (r_slot + kSet) & (kRing * kSet - 1);
+        pull();
+    };
+
+    if (u0 >= units) return;
+    if (!on_c) {  // no copy lands here: zeros for the row sums and maxima
+#pragma unroll
+        for (int i = 0; i < kRing; ++i) ring_s[warp][i][0][lane] = ring_s[warp][i][1][lane] = make_uint4(0u, 0u, 0u, 0u);
+    }
+    p_set = (int)(u0 - token_of(u0) * parts) * per;
+    p_end = min(sets, p_set + per);
+    begin(token_of(u0), p_set);
+#pragma unroll
+    for (int i = 0; i < kRing - 1; ++i) pull();
+    Slot ahead = {0, 0, 0};
+    int turn = 0;
+    for (int64_t u = u0; u < units; u += stride, ++turn) {
+        if ((turn & 31) == 0) {
+            const int64_t mine = u + lane * stride;
+            if (mine < units) {
+                const int64_t tm = token_of(mine);
+                ahead = find_slot<SINK>(a, tm, mine == tm * parts);
+            }
+        }
+        Slot slot;
+        slot.row = __shfl_sync(0xFFFFFFFFu, ahead.row, turn & 31);
+        slot.blk = __shfl_sync(0xFFFFFFFFu, ahead.blk, turn & 31);
+        slot.pos = __shfl_sync(0xFFFFFFFFu, ahead.pos, turn & 31);
+        const int64_t t = token_of(u);
+        const int s0 = (int)(u - t * parts) * per, s1 = min(sets, s0 + per);
+        if (kPages && slot.row < 0) {  // uniform in the warp: the token is skipped
+            for (int set = s0; set < s1; ++set) take();
+            continue;
+        }
         if (s0 < sq + sk) {
+            __syncwarp();  // the last token's are used up
+            const int64_t pos = a.positions != nullptr ? (int64_t)slot.pos : (int64_t)(uint32_t)slot.pos;
             for (int i = lane; i < R / 2; i += 32) {
-                const uint64_t phase = (uint64_t)slot.pos * __ldg(a.freqs + i);
+                const uint64_t phase = (uint64_t)pos * __ldg(a.freqs + i);
                 float s, co;
                 sincospif((float)(int32_t)(phase >> 32) * 0x1p-31f, &s, &co);
                 cos_s[i] = co * a.factor;
                 sin_s[i] = s * a.factor;
             }
+            __syncwarp();
         }
-        __syncwarp();
 
         // Queries and keys: row sets [lo, hi) of one kind.  The rotation with the norm's
         // weights folded in, per channel: out = x * own + partner * other.
@@ -205,20 +296,17 @@ __global__ void __launch_bounds__(kRopeWarps * 32, 5) rope_kernel(const RopeArgs
 #pragma unroll
                     for (int i = 0; i < 8; ++i) wt[i] = make_float2(bf16_lo(wd[i]), bf16_hi(wd[i]));
                 }
-                float co[8], si[8];  // pairs 8c .. 8c + 7 in either layout
+                float co[8], si[8];  // of this lane's pairs, four to a piece if interleaved
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    co[i] = 1.0f;
-                    si[i] = 0.0f;
+                for (int i = 0; i < 8; i += 4) {
+                    const int pair = half ? 8 * c + i : (i ? d1 : d0) / 2;
+                    const bool in = on_c && (half ? turns : (i ? d1 : d0) < R);
+                    const float4 c4 = in ? *reinterpret_cast<const float4 *>(cos_s + pair) : make_float4(1.0f, 1.0f, 1.0f, 1.0f);
+                    const float4 s4 = in ? *reinterpret_cast<const float4 *>(sin_s + pair) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                    co[i] = c4.x, co[i + 1] = c4.y, co[i + 2] = c4.z, co[i + 3] = c4.w;
+                    si[i] = s4.x, si[i + 1] = s4.y, si[i + 2] = s4.z, si[i + 3] = s4.w;
                 }
-                if (turns) {
-#pragma unroll
-                    for (int i = 0; i < 8; i += 4) {
-                        *reinterpret_cast<float4 *>(co + i) = *reinterpret_cast<const float4 *>(cos_s + 8 * c + i);
-                        *reinterpret_cast<float4 *>(si + i) = *reinterpret_cast<const float4 *>(sin_s + 8 * c + i);
-                    }
-                }
-                if (!a.interleaved) {
+                if (half) {
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const float2 c2 = make_float2(co[2 * i], co[2 * i + 1]), s2 = make_float2(si[2 * i], si[2 * i + 1]);
@@ -237,12 +325,12 @@ __global__ void __launch_bounds__(kRopeWarps * 32, 5) rope_kernel(const RopeArgs
             }
             for (int set = lo; set < hi; ++set) {
                 float2 v[8];
+                take();
                 {
                     const uint32_t wd[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
 #pragma unroll
                     for (int i = 0; i < 8; ++i) v[i] = make_float2(bf16_lo(wd[i]), bf16_hi(wd[i]));
                 }
-                if (set + 1 < s1) fetch(set + 1);
                 if (w != nullptr) {
                     float2 sa = __fmul2_rn(v[0], v[0]), sb = __fmul2_rn(v[1], v[1]);
 #pragma unroll
@@ -259,7 +347,7 @@ __global__ void __launch_bounds__(kRopeWarps * 32, 5) rope_kernel(const RopeArgs
                     for (int i = 0; i < 8; ++i) v[i] = __fmul2_rn(v[i], make_float2(inv, inv));
                 }
                 float2 y[8];
-                if (!a.interleaved) {
+                if (half) {
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         y[i] = __ffma2_rn(v[i], own[i], __fmul2_rn(v[4 + i], other[i]));
@@ -329,20 +417,19 @@ __global__ void __launch_bounds__(kRopeWarps * 32, 5) rope_kernel(const RopeArgs
         if (kPages) {
             for (int set = max(s0, sq + sk); set < s1; ++set) {
                 const int h = (set - sq - sk) * RW + rl;
-                const uint4 v0 = x0, v1 = x1;
-                if (set + 1 < s1) fetch(set + 1);
+                take();
                 if (SINK == kSinkBf16) {  // copied bit for bit
                     if (on_c && h < H) {
-                        uint16_t *dst = static_cast<uint16_t *>(a.v_cache) + (slot.row + (int64_t)h * bs) * D + 16 * c;
-                        *reinterpret_cast<uint4 *>(dst) = v0;
-                        *reinterpret_cast<uint4 *>(dst + 8) = v1;
+                        uint16_t *dst = static_cast<uint16_t *>(a.v_cache) + (slot.row + (int64_t)h * bs) * D;
+                        *reinterpret_cast<uint4 *>(dst + v0) = x0;
+                        *reinterpret_cast<uint4 *>(dst + v1) = x1;
                     }
                 } else {
-                    const uint32_t wd[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
+                    const uint32_t wd[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
                     float2 y[8];
 #pragma unroll
                     for (int i = 0; i < 8; ++i) y[i] = make_float2(bf16_lo(wd[i]), bf16_hi(wd[i]));
-                    quantise_row(h, static_cast<int8_t *>(a.v_cache), a.v_scale, y, 16 * c, 16 * c + 8);
+                    quantise_row(h, static_cast<int8_t *>(a.v_cache), a.v_scale, y, v0, v1);
                 }
             }
         }
@@ -362,8 +449,10 @@ cudaError_t launch_rope_variant(const RopeArgs &a, cudaStream_t stream) {
     // fewer tokens than resident warps: a token's row sets are shared among several
     int64_t parts = cap * kRopeWarps / a.num_tokens;
     parts = parts < 1 ? 1 : parts > sets ? sets : parts;
+    const int64_t per = (sets + parts - 1) / parts;
+    parts = (sets + per - 1) / per;  // no part is empty
     const int64_t need = (a.num_tokens * parts + kRopeWarps - 1) / kRopeWarps;
-    kern<<<(unsigned)(need < cap ? need : cap), kRopeWarps * 32, 0, stream>>>(a, (int)parts);
+    kern<<<(unsigned)(need < cap ? need : cap), kRopeWarps * 32, 0, stream>>>(a, (int)parts, (int)per);
     return cudaGetLastError();
 }
 

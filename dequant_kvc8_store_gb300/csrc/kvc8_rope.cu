@@ -25,10 +25,10 @@
 // multiply-adds a pair and packing.  The rows come through a ring in shared memory,
 // three sets ahead.
 //
-// Codes without dividing: with r = fl(1/s), every value fl(y/s) can take lies between
-// y r (1 - 2^-21) and y r (1 + 2^-21) (r and the quotient are each within 2^-24 of
-// theirs).  Where both ends round to the same integer, so does the quotient; else (a
-// value within 2^-21 of a half-integer) the group of four is divided.
+// Codes without dividing: with r within 2^-23 of 1/s, every value fl(y/s) can take lies
+// between y r (1 - 2^-21) and y r (1 + 2^-21).  Where both ends round to the same integer,
+// so does the quotient; else (a value within 2^-20 of a half-integer, mostly an exact tie of
+// a value row, 2 in 10^4) the lane divides.
 #include "kvc8_internal.cuh"
 
 namespace kvc8 {
@@ -115,12 +115,12 @@ constexpr float kRecipLo = 0.99999952316284180f;  // 1 - 2^-21
 constexpr float kRecipHi = 1.00000047683715820f;  // 1 + 2^-21
 
 // The definition: one division, round half to even, clamp; 0 when s == 0.
-__device__ __noinline__ uint32_t codes_divide(float4 y, float4 s) {
+__device__ __noinline__ uint32_t codes_divide(float2 y0, float2 y1, float4 s) {
     auto one = [](float a, float b) {
         const int q = b == 0.0f ? 0 : __float2int_rn(__fdiv_rn(a, b));
         return (uint32_t)min(127, max(-127, q)) & 0xFFu;
     };
-    return one(y.x, s.x) | one(y.y, s.y) << 8 | one(y.z, s.z) << 16 | one(y.w, s.w) << 24;
+    return one(y0.x, s.x) | one(y0.y, s.y) << 8 | one(y1.x, s.z) << 16 | one(y1.y, s.w) << 24;
 }
 
 // |x| limited to b, with x's sign.
@@ -132,24 +132,41 @@ __device__ __forceinline__ float limit(float x, float b) {
 
 __device__ __forceinline__ bool recip_ok(float s) { return s >= 0x1p-120f && s <= 0x1p+120f; }
 
-// Four codes of y for scales s with reciprocals r (0: divide).  LIMIT: |y / s| may pass
-// 127; it is cut at fl(127 s), whose code is 127.
+// 1/s within 2^-23 of itself (the hardware's approximation), 0 where s has none.
+__device__ __forceinline__ float recip(float s) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(s));
+    return recip_ok(s) ? r : 0.0f;
+}
+
+// fl(m / 127) without dividing, by Markstein's correction of a quotient (IBM Journal of
+// Research and Development 34, 1990): with c = fl(1/127) and q = fl(m c), the remainder
+// m - 127 q is exact in a fused multiply-add, and fl(q + remainder c) is the rounded
+// quotient.  Small m, whose remainder might not be normal, divide.
+__device__ __forceinline__ float over_127(float m) {
+    constexpr float c = 1.0f / 127.0f;
+    if (m < 0x1p-90f) return __fdiv_rn(m, 127.0f);
+    const float q = __fmul_rn(m, c);
+    return __fmaf_rn(__fmaf_rn(-127.0f, q, m), c, q);
+}
+
+// Four codes of y for reciprocals r of their scales s; LIMIT: |y / s| may pass 127 and is
+// cut at fl(127 s), whose code is 127.  `apart` becomes nonzero where the bracket's ends
+// disagree.
 template <bool LIMIT>
-__device__ __forceinline__ uint32_t codes4(float2 y0, float2 y1, float4 s, float4 r) {
-    float2 a = y0, b = y1;
+__device__ __forceinline__ uint32_t codes4(float2 y0, float2 y1, float4 s, float4 r, float2 &apart) {
     if (LIMIT) {
-        a = make_float2(limit(y0.x, __fmul_rn(127.0f, s.x)), limit(y0.y, __fmul_rn(127.0f, s.y)));
-        b = make_float2(limit(y1.x, __fmul_rn(127.0f, s.z)), limit(y1.y, __fmul_rn(127.0f, s.w)));
+        y0 = make_float2(limit(y0.x, __fmul_rn(127.0f, s.x)), limit(y0.y, __fmul_rn(127.0f, s.y)));
+        y1 = make_float2(limit(y1.x, __fmul_rn(127.0f, s.z)), limit(y1.y, __fmul_rn(127.0f, s.w)));
     }
     const float2 lo = make_float2(kRecipLo, kRecipLo), hi = make_float2(kRecipHi, kRecipHi);
     const float2 m2 = make_float2(kMagic, kMagic), n1 = make_float2(-1.0f, -1.0f);
     const float2 ra = make_float2(r.x, r.y), rb = make_float2(r.z, r.w);
-    const float2 la = __ffma2_rn(a, __fmul2_rn(ra, lo), m2), ha = __ffma2_rn(a, __fmul2_rn(ra, hi), m2);
-    const float2 lb = __ffma2_rn(b, __fmul2_rn(rb, lo), m2), hb = __ffma2_rn(b, __fmul2_rn(rb, hi), m2);
-    float2 da = __ffma2_rn(la, n1, ha), db = __ffma2_rn(lb, n1, hb);  // 0 where the ends agree
-    da = __ffma2_rn(da, da, __fmul2_rn(db, db));
-    if (da.x + da.y != 0.0f || fminf(fminf(r.x, r.y), fminf(r.z, r.w)) == 0.0f)
-        return codes_divide(make_float4(y0.x, y0.y, y1.x, y1.y), s);
+    const float2 la = __ffma2_rn(y0, __fmul2_rn(ra, lo), m2), ha = __ffma2_rn(y0, __fmul2_rn(ra, hi), m2);
+    const float2 lb = __ffma2_rn(y1, __fmul2_rn(rb, lo), m2), hb = __ffma2_rn(y1, __fmul2_rn(rb, hi), m2);
+    const float2 da = __ffma2_rn(la, n1, ha), db = __ffma2_rn(lb, n1, hb);  // 0 where the ends agree
+    apart = __ffma2_rn(da, da, apart);
+    apart = __ffma2_rn(db, db, apart);
     return __byte_perm(__byte_perm(__float_as_uint(la.x), __float_as_uint(la.y), 0x0040),
                        __byte_perm(__float_as_uint(lb.x), __float_as_uint(lb.y), 0x0040), 0x5410);
 }
@@ -378,23 +395,39 @@ __global__ void __launch_bounds__(kRopeWarps * 32, 5) rope_kernel(const RopeArgs
                 for (int i = 0; i < 8; ++i) m = fmaxf(m, fmaxf(fabsf(y[i].x), fabsf(y[i].y)));
 #pragma unroll
                 for (int o = 1; o < L; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
-                s_row = __fdiv_rn(m, 127.0f);
+                s_row = over_127(m);
                 if (on && c == 0) scl[row] = s_row;
             } else if (SINK == kSinkBlock && on) {
                 s_row = ld_nc_f32(scl + (int64_t)slot.blk * H + h);
             }
             if (!on) return;
-            const float r_row = SINK != kSinkChannel && recip_ok(s_row) ? __frcp_rn(s_row) : 0.0f;
             uint32_t o[4];
+            float2 apart = make_float2(0.0f, 0.0f);
+            float least = 1.0f;  // 0: some scale has no reciprocal
+            if (SINK == kSinkChannel) {
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                float4 s = make_float4(s_row, s_row, s_row, s_row), r = make_float4(r_row, r_row, r_row, r_row);
-                if (SINK == kSinkChannel) {
-                    s = __ldg(reinterpret_cast<const float4 *>(scl + (int64_t)h * D + (q < 2 ? o0 : o1) + 4 * (q & 1)));
-                    r = make_float4(recip_ok(s.x) ? __frcp_rn(s.x) : 0.0f, recip_ok(s.y) ? __frcp_rn(s.y) : 0.0f,
-                                    recip_ok(s.z) ? __frcp_rn(s.z) : 0.0f, recip_ok(s.w) ? __frcp_rn(s.w) : 0.0f);
+                for (int q = 0; q < 4; ++q) {
+                    const float4 s = __ldg(reinterpret_cast<const float4 *>(scl + h * D + (q < 2 ? o0 : o1) + 4 * (q & 1)));
+                    const float4 r = make_float4(recip(s.x), recip(s.y), recip(s.z), recip(s.w));
+                    least = fminf(fminf(fminf(r.x, r.y), fminf(r.z, r.w)), least);
+                    o[q] = codes4<true>(y[2 * q], y[2 * q + 1], s, r, apart);
                 }
-                o[q] = codes4<SINK != kSinkDynamic>(y[2 * q], y[2 * q + 1], s, r);
+            } else {
+                const float r = recip(s_row);
+                least = r;
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                    o[q] = codes4<SINK != kSinkDynamic>(y[2 * q], y[2 * q + 1], make_float4(s_row, s_row, s_row, s_row),
+                                                        make_float4(r, r, r, r), apart);
+            }
+            if (apart.x + apart.y != 0.0f || least == 0.0f) {
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    float4 s = make_float4(s_row, s_row, s_row, s_row);
+                    if (SINK == kSinkChannel)
+                        s = __ldg(reinterpret_cast<const float4 *>(scl + h * D + (q < 2 ? o0 : o1) + 4 * (q & 1)));
+                    o[q] = codes_divide(y[2 * q], y[2 * q + 1], s);
+                }
             }
             int8_t *dst = cache + row * D;
             st_8(dst + o0, o[0], o[1]);

@@ -761,7 +761,8 @@ static kvc8_status check_prefix_geom(const kvc8_geom *g, int32_t num_q_heads,
         ((int64_t)g->max_blocks_per_seq * g->block_size + kAttnChunk - 1) / kAttnChunk;
     if ((int64_t)g->num_seqs * g->kv_heads * splits > (int64_t)INT32_MAX) return KVC8_ERR_UNSUPPORTED;
     if (max_prefix_blocks < 1) return KVC8_ERR_INVALID_ARG;
-    if ((int64_t)max_prefix_blocks * g->block_size > (int64_t)INT32_MAX ||
+    // (with room for a step's overhang past the end)
+    if ((int64_t)max_prefix_blocks * g->block_size > (int64_t)INT32_MAX - 4096 ||
         (int64_t)g->num_seqs * num_q_heads > (int64_t)INT32_MAX / 2)
         return KVC8_ERR_UNSUPPORTED;
     return KVC8_OK;

@@ -127,6 +127,15 @@ __global__ void __launch_bounds__(kThreads, 4) own_kernel(const AttnArgs a, int 
         const int64_t p_begin = (int64_t)j * kAttnChunk;
         const int64_t p_end = min(len, p_begin + kAttnChunk);
 
+        // The warp's sub-tiles of the split are at most 32: a lane fetches the block id of one.
+        constexpr int kStride = kWarps * kSub;
+        static_assert(kAttnChunk == 32 * kStride, "a lane to a sub-tile");
+        const int start = (int)p_begin + warp * kSub, end = (int)p_end;  // lengths are 32-bit
+        const int count = start < end ? (int)((uint32_t)(end - start + kStride - 1) / kStride) : 0;
+        int32_t ids = 0;
+        if (lane < count)
+            ids = ld_nc_s32(a.block_table + (int64_t)b * MB + (uint32_t)(start + lane * kStride) / (uint32_t)bs);
+
         uint32_t qf[KB / 2];
         const float factor = load_query<MODE, D>(a, b, h, gid, tig, qf);
         // the heads of this thread's score columns, 2 tig and 2 tig + 1
@@ -137,16 +146,15 @@ __global__ void __launch_bounds__(kThreads, 4) own_kernel(const AttnArgs a, int 
 #pragma unroll
         for (int i = 0; i < KS; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.0f;
 
-        constexpr int64_t kStride = kWarps * kSub;
-        for (int64_t p0 = p_begin + warp * kSub; p0 < p_end; p0 += kStride) {
-            const int64_t lb = (int64_t)((uint32_t)p0 / (uint32_t)bs);
-            const int32_t blk = ld_nc_s32(a.block_table + (int64_t)b * MB + lb);
+        for (int i = 0; i < count; ++i) {
+            const int p0 = start + i * kStride;
+            const int32_t blk = __shfl_sync(0xFFFFFFFFu, ids, i);
             if (blk < 0 || blk >= a.g.num_blocks) {
                 if (lane == 0) report(a.dev_error, KVC8_DEV_BAD_BLOCK_ID);
                 continue;
             }
-            const int valid = (int)min((int64_t)kSub, p_end - p0);
-            const int64_t row0 = ((int64_t)blk * H + h) * bs + (p0 - lb * bs);
+            const int valid = min(kSub, end - p0);
+            const int64_t row0 = ((int64_t)blk * H + h) * bs + (int)((uint32_t)p0 % (uint32_t)bs);
             uint32_t k0[D / 16], k1[D / 16], v[4][D / 32];
             const int8_t *kp = a.k_cache + (row0 + gid) * D + tig * KB;
             load_codes<KB>(kp, k0);

@@ -203,6 +203,48 @@ class Bf16Batch:
         return B.kvc8_get_error(self.dev_error, reset=reset)
 
 
+class RotaryAppend:
+    """kvc8_rope_store of a DeviceBatch's new tokens, with num_q_heads seeded N(0, 1)
+    bf16 query heads rotated beside them (q_out bf16 [N][num_q_heads][D])."""
+
+    def __init__(self, d: DeviceBatch, rope: B.Rope, num_q_heads: int, seed: int = 0):
+        self.d, self.rope, self.num_q_heads = d, rope, num_q_heads
+        rng = np.random.default_rng([seed, 78])
+        x = rng.standard_normal((d.w.num_tokens, num_q_heads, d.w.head_dim)).astype(np.float32)
+        self.query = torch.from_numpy(x).to(torch.bfloat16).to(d.device)
+        self.q_out = torch.empty_like(self.query)
+
+    def __call__(self, stream=None):
+        d, q, o, k = self.d, self.query, self.q_out, self.d.k_states
+        B.kvc8_rope_store(d.g, self.rope, k.shape[0], self.num_q_heads, q, q.stride(0), q.stride(1),
+                          o, o.stride(0), o.stride(1), k, d.v_states, k.stride(0), k.stride(1),
+                          d.k_cache, d.v_cache, d.k_scale, d.v_scale, d.block_table, d.cu_q_lens,
+                          d.context_kv_lens, d.dev_error, stream)
+
+
+class SharedPrefixAttention:
+    """kvc8_shared_prefix_attention of a DeviceBatch's sequences (one query each, as
+    in DecodeAttention) behind a prefix of `length` positions in the blocks of
+    `table` (host int32), pages of the same pool."""
+
+    def __init__(self, d: DeviceBatch, group: int, table, length: int, seed: int = 0,
+                 softmax_scale=None):
+        self.at = DecodeAttention(d, group, seed, softmax_scale)
+        self.table = torch.from_numpy(np.asarray(table, np.int32)).to(d.device)
+        self.length = torch.tensor([length], dtype=torch.int32, device=d.device)
+        self.ws_bytes = B.kvc8_shared_prefix_workspace_bytes(d.g, self.at.num_q_heads, len(self.table))
+        self.workspace = torch.empty(self.ws_bytes, dtype=torch.uint8, device=d.device)
+
+    def __call__(self, stream=None):
+        at, d = self.at, self.at.d
+        q, o = at.query, at.out
+        B.kvc8_shared_prefix_attention(d.g, at.num_q_heads, q, q.stride(0), q.stride(1), d.k_cache,
+                                       d.v_cache, d.k_scale, d.v_scale, self.table,
+                                       self.table.shape[0], self.length, d.block_table,
+                                       d.context_lengths, at.scale, o, o.stride(0), o.stride(1),
+                                       self.workspace, self.ws_bytes, d.dev_error, stream)
+
+
 class DecodeAttention:
     """One decode query per sequence (num_q_heads = group * kv_heads, seeded
     N(0, 1) bf16) attending over a DeviceBatch's int8 cache through

@@ -1,6 +1,6 @@
 /*
  * kvc8.h -- C ABI of libkvc8: the int8 ("C8") paged KV-cache store and
- * dequant-gather on NVIDIA GB300 (sm_103a).
+ * dequant-gather on NVIDIA GB300 (sm_103a), with the operators next to them.
  *
  * Source of the operations (web pages, cited by title and section):
  *   [PR379]  mojo_opset pull request #379, "feat: [MLU] add mlu experimental
@@ -528,13 +528,14 @@ size_t kvc8_shared_prefix_workspace_bytes(const kvc8_geom *g, int32_t num_q_head
  * context_lengths[b] positions of block_table[b], in one softmax:
  *   out[b][j] = (sum_{p < P} w_p V[p] + sum_{p < len_b} u_p V_b[p]) / (sum w + sum u)
  *   w_p = exp(softmax_scale <q, K[p]>),  u_p = exp(softmax_scale <q, K_b[p]>)
- * with K, V the values that the pages stand for, fp32(code) * scale.  Rounded to
- * bf16 on the way to the tensor cores: the weights (with a row's or block's
- * value scale multiplied in) and, with per-channel scales, the query (with the
- * key scale multiplied in); products are accumulated in fp32, the output is
- * rounded to bf16.  A query with no position at all gives zeros.  P, the lengths and
- * the tables are read on the device, so a captured graph may be replayed with
- * other values.
+ * with K, V the values that the pages stand for, fp32(code) * scale.  The products
+ * run on the tensor cores with fp32 accumulation; their operands are rounded to
+ * fp16 (the query after a power of two, with per-channel scales times the key
+ * scale; the prefix's rows times their scale; the weights) or, for the weights of
+ * own positions times a row's or block's value scale, to bf16.  Sums and statistics
+ * are fp32, the output is rounded to bf16.  A query with no position at all gives
+ * zeros.  P, the lengths and the tables are read on the device, so a captured graph
+ * may be replayed with other values.  Three launches, no host synchronisation.
  *
  *   prefix_table      int32 [max_prefix_blocks], physical blocks of the prefix
  *   max_prefix_blocks >= 1; P is at most max_prefix_blocks * block_size

@@ -1,12 +1,11 @@
 """Decode attention behind a shared prefix (kvc8_shared_prefix_attention) against
 an fp64 evaluation over fp32(code) * scale.
 
-The kernel rounds each weight (times a row's or block's value scale) to bf16, a
-relative 2^-8 at most, and with per-channel scales the query times the key scale,
-which moves a score by 2^-8 * scale * sum_d |q_d k_d| at most; the rows of a
-sequence's own pages may be rounded to bf16 on the way to the products, which moves
-a score by as much again and each value by 2^-8.  The fp32 accumulation of D
-products moves a score by D * 2^-24 of the same sum.  So with
+The operands of the products are allowed the rounding of bf16 (the kernel rounds most
+of them to fp16, eight times finer): each weight (times a row's or block's value
+scale) moves by a relative 2^-8 at most, the query (times the key scale) and the
+keys move a score by 2^-8 * scale * sum_d |q_d k_d| each, each value moves by 2^-8.  The
+fp32 accumulation of D products moves a score by D * 2^-24 of the same sum.  So with
     delta = scale * max_p sum_d |q_d k_pd| * (2 * 2^-8 + D * 2^-24)
 a weight is off by a relative eps = 2^-8 + expm1(delta), the normalised average of
 values by 2 eps max|V| + 2^-8 max|V|, and the output's rounding adds 2^-8 |out|.

@@ -206,6 +206,26 @@ def test_append_bf16_pages_and_rows_agree(H, D, bs, rot, inter, norm, group, mod
 
 
 @pytest.mark.parametrize("mode", [0, 1, 2])
+def test_no_rotation_and_no_norm_is_the_store(mode):
+    """rotary_dim 0 and no weights: the same pages as kvc8_store, bit for bit, and the queries
+    unchanged."""
+    rng = np.random.default_rng(90 + mode)
+    w = W.make_workload("rope0", q_lens=[130, 0, 7], ctx_before=[5, 3, 60], kv_heads=3, head_dim=96,
+                        block_size=24, num_blocks=30, quant_mode=mode, seed=91, outlier_channels=3)
+    d = DeviceBatch(w)
+    turn = Turn(rng, 96, 0, norm=False)
+    q = bf16_tensor(_rows(rng, w.num_tokens, 5, 96)).cuda()
+    out = torch.zeros_like(q)
+    _append(d, w, turn, q, out)
+    assert d.error_code() == 0
+    want = [x.copy() for x in (w.k_cache, w.v_cache, w.k_scale, w.v_scale)]
+    oracle.store(mode, w.k_states, w.v_states, *want, w.block_table, w.cu_q_lens, w.context_kv_lens)
+    for got, x in zip(d.host_caches(), want):
+        np.testing.assert_array_equal(got, x)
+    assert torch.equal(out, q)
+
+
+@pytest.mark.parametrize("mode", [0, 1, 2])
 def test_decode_form_in_place_and_strided(mode):
     """cu_q_lens NULL, query rotated in place in a wider tensor, keys and values
     views of one packed projection."""

@@ -142,10 +142,10 @@ __device__ __forceinline__ float recip(float s) {
 // fl(m / 127) without dividing, by Markstein's correction of a quotient (IBM Journal of
 // Research and Development 34, 1990): with c = fl(1/127) and q = fl(m c), the remainder
 // m - 127 q is exact in a fused multiply-add, and fl(q + remainder c) is the rounded
-// quotient.  Small m, whose remainder might not be normal, divide.
+// quotient.  Small m, whose remainder might not be normal, and an infinite m divide.
 __device__ __forceinline__ float over_127(float m) {
     constexpr float c = 1.0f / 127.0f;
-    if (m < 0x1p-90f) return __fdiv_rn(m, 127.0f);
+    if (!(m >= 0x1p-90f && m < INFINITY)) return __fdiv_rn(m, 127.0f);
     const float q = __fmul_rn(m, c);
     return __fmaf_rn(__fmaf_rn(-127.0f, q, m), c, q);
 }

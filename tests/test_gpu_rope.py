@@ -336,6 +336,22 @@ def test_zero_rows_tiny_rows_and_zero_scales(mode):
         _check_pool(w, d, turn, pos)
 
 
+def test_a_rotation_past_the_fp32_range():
+    """Finite rows whose rotated values pass the fp32 range: scale infinity and codes 0 by the
+    definition (finite / inf = 0, inf / inf is no number: 0)."""
+    rng = np.random.default_rng(92)
+    w = W.make_workload("ropebig", q_lens=[3], ctx_before=[0], kv_heads=2, head_dim=64,
+                        block_size=16, num_blocks=2, quant_mode=0, seed=93)
+    w.k_states[1] = to_bf16_bits(np.full((2, 64), 2.0 ** 127))
+    d = DeviceBatch(w)
+    _append(d, w, Turn(rng, 64, 64, norm=False, factor=4.0), None, None)
+    assert d.error_code() == 0
+    kc, _, ks, _ = d.host_caches()
+    ids, at, _ = _slots(w)
+    assert np.isinf(ks[ids[1], :, at[1]]).all() and not kc[ids[1], :, at[1]].any()
+    assert np.isfinite(ks[ids[2], :, at[2]]).all() and kc[ids[2], :, at[2]].any()
+
+
 def test_bad_pages_and_lengths_are_skipped_and_reported():
     rng = np.random.default_rng(76)
     H, D = 2, 128

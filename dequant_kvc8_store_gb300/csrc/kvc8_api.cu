@@ -765,6 +765,11 @@ static kvc8_status check_prefix_geom(const kvc8_geom *g, int32_t num_q_heads,
     if ((int64_t)max_prefix_blocks * g->block_size > (int64_t)INT32_MAX - 4096 ||
         (int64_t)g->num_seqs * num_q_heads > (int64_t)INT32_MAX / 2)
         return KVC8_ERR_UNSUPPORTED;
+    // units of 128 query rows and 128 positions are counted in 32 bits
+    const int64_t rows = (int64_t)g->num_seqs * (num_q_heads / g->kv_heads);
+    const int64_t tiles = (rows + 127) / 128 * g->kv_heads;
+    const int64_t steps = ((int64_t)max_prefix_blocks * g->block_size + 127) / 128;
+    if (tiles > (int64_t)INT32_MAX / steps) return KVC8_ERR_UNSUPPORTED;
     return KVC8_OK;
 }
 

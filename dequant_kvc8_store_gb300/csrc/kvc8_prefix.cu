@@ -16,8 +16,8 @@
 // memory); P replaces S in tensor memory and is the second product's A operand.
 // Warps by role:
 //   softmax     4 per tile, one thread per query row: S from tensor memory, online
-//               softmax, P back; the running maximum moves only when it grows by
-//               more than 2^8, so O is seldom rescaled
+//               softmax, P back; the running maximum moves only when the weights
+//               grow by more than 2^8, so O is seldom rescaled
 //   dequantise  codes from global memory a tile ahead in registers, K' and V' as fp16
 //               into a two-stage ring in the 128-byte swizzle (K' K-major, V' as the
 //               MN-major B operand of the same rows)
@@ -39,7 +39,11 @@ constexpr int kCols = 128;      // positions of a step
 constexpr int kStages = 2;      // steps of K' and of V' in shared memory
 constexpr int kMaskSlots = 4;   // steps whose valid counts are kept
 constexpr int kMaxCtas = 152;   // SMs of a GB300
-constexpr float kLazy = 8.0f;   // log2 of the growth that makes the maximum move
+// The weights are 2^(score - m) with m below the largest score by kLift when it is set, and
+// m moves when a score passes it by kLift + kLazy more: the fp16 weights use fp16's range
+// up to 2^15, and one of 2^-21 of the row's largest still has all its eleven bits.
+constexpr float kLazy = 8.0f, kLift = 7.0f;
+constexpr int kLeastValuePower = -60;  // so that the sum of such weights times 2^-e is finite
 constexpr long long kWaitCycles = 4000000000ll;  // about two seconds
 constexpr int kMergeThreads = 256;
 
@@ -361,11 +365,11 @@ struct Prefix {
 
     // fp16 pair (s / 2^e, s / 2^e) of a position's scale, e the exponent of the largest
     // of its group of 16, so that 127 times it is far inside fp16 whatever the scales' size.
-    __device__ __forceinline__ uint32_t normal_scale(float s, int &e) const {
+    __device__ __forceinline__ uint32_t normal_scale(float s, int least, int &e) const {
         float top = fabsf(s);
 #pragma unroll
         for (int o = 1; o < 16; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
-        e = power_of(top);
+        e = max(least, power_of(top));
         s *= __uint_as_float((uint32_t)(127 - e) << 23);
         return pack_fp16(s, s);
     }
@@ -430,8 +434,8 @@ struct Prefix {
             uint32_t sk_half = 0u, sv_half = 0u;
             if (MODE != 1) {
                 int ek, ev;
-                sk_half = normal_scale(sk, ek);
-                sv_half = normal_scale(sv, ev);
+                sk_half = normal_scale(sk, -100, ek);
+                sv_half = normal_scale(sv, kLeastValuePower, ev);
                 if (lane < kRpw && lane % 16 == 0) {
                     const int grp = dw * kGroups + lane / 16;
                     bar.k_pow[n % kMaskSlots][grp] = __uint_as_float((uint32_t)(127 + ek) << 23);
@@ -732,8 +736,8 @@ struct Prefix {
     // One step of a row: S -> P, the running maximum m and sum l.  A group's weights are
     // 2^(score + e - m), e the exponent taken out of its value scales, so that the product
     // with the tile's values is the weight times the value; m bounds score + e, lazily.
-    // fp16 holds such weights (at most 2^8) eight times finer than bf16; what falls below
-    // 2^-24 of the largest is far below that one's own quantisation.
+    // fp16 holds such weights (at most 2^15) eight times finer than bf16, and what falls
+    // below 2^-21 of the largest to 2^-32 of it.
     __device__ __forceinline__ void step(uint32_t s_at, uint32_t o_at, float scale, bool have_o, int slot,
                                          float &m, float &l) const {
         const bool whole = bar.valid[slot].x == 0x10101010u && bar.valid[slot].y == 0x10101010u;
@@ -752,10 +756,10 @@ struct Prefix {
                 mx = fmaxf(mx, fmaf(top16(s[q], 16 * i), fe.x, fe.y));
             }
         }
-        const bool moves = mx > m + kLazy || (m == -INFINITY && mx > m);
+        const bool moves = mx > m + (kLift + kLazy) || (m == -INFINITY && mx > m);
         if (__any_sync(0xFFFFFFFFu, moves)) {
-            const float c = moves ? ex2(m - mx) : 1.0f;  // 0 where there was nothing yet
-            if (moves) m = mx;
+            const float c = moves ? ex2(m - (mx - kLift)) : 1.0f;  // 0 where there was nothing yet
+            if (moves) m = mx - kLift;
             l *= c;
             if (have_o) {
 #pragma unroll

@@ -16,7 +16,7 @@
 // operations more).  The scales follow in fp32: a position's key scale and the head's
 // factor multiply the score, its value scale the weight, four products each a sub-tile;
 // per-channel scales are in the fp16 query and in the output.  The running maximum moves
-// only when a score passes it by 2^8, so most sub-tiles reduce and rescale nothing.
+// only when the weights grow by more than 2^8, so most sub-tiles reduce and rescale nothing.
 #include "kvc8_codes.cuh"
 #include "kvc8_internal.cuh"
 
@@ -27,7 +27,10 @@ constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr int kSub = 16;      // positions per warp step
 constexpr int kMaxGroup = 8;  // query heads per kv head (mma N)
-constexpr float kLazy = 8.0f;
+// The running maximum stays kLift below the largest score when it is set, so that the
+// fp16 weights of mode 1 (at most 2^15) keep their eleven bits down to 2^-21 of a row's
+// largest, and moves when a score passes it by kLift + kLazy.
+constexpr float kLazy = 8.0f, kLift = 7.0f;
 
 template <bool HALF>
 __device__ __forceinline__ void mma(float c[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -188,14 +191,14 @@ __global__ void __launch_bounds__(kThreads, 4) own_kernel(const AttnArgs a, int 
             c[2] = vb ? c[2] * (kb * f0) : -INFINITY;
             c[3] = vb ? c[3] * (kb * f1) : -INFINITY;
             float x0 = fmaxf(c[0], c[2]), x1 = fmaxf(c[1], c[3]);
-            if (__any_sync(0xFFFFFFFFu, x0 > m0 + kLazy || x1 > m1 + kLazy || m0 == -INFINITY)) {
+            if (__any_sync(0xFFFFFFFFu, x0 > m0 + (kLift + kLazy) || x1 > m1 + (kLift + kLazy) || m0 == -INFINITY)) {
                 // a column's maximum is that of the lanes with the same tig
 #pragma unroll
                 for (int sh = 4; sh < 32; sh <<= 1) {
                     x0 = fmaxf(x0, __shfl_xor_sync(0xFFFFFFFFu, x0, sh));
                     x1 = fmaxf(x1, __shfl_xor_sync(0xFFFFFFFFu, x1, sh));
                 }
-                const float n0 = fmaxf(m0, x0), n1 = fmaxf(m1, x1);  // finite: valid >= 1
+                const float n0 = fmaxf(m0, x0 - kLift), n1 = fmaxf(m1, x1 - kLift);  // finite: valid >= 1
                 const float g0 = ex2(m0 - n0), g1 = ex2(m1 - n1);
                 m0 = n0;
                 m1 = n1;

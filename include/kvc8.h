@@ -533,7 +533,10 @@ size_t kvc8_shared_prefix_workspace_bytes(const kvc8_geom *g, int32_t num_q_head
  * fp16 (the query after a power of two, with per-channel scales times the key
  * scale; the prefix's rows times their scale; the weights) or, for the weights of
  * own positions times a row's or block's value scale, to bf16.  Sums and statistics
- * are fp32, the output is rounded to bf16.  A query with no position at all gives
+ * are fp32, the output is rounded to bf16.  fp16 keeps its eleven bits over a range:
+ * of the scales in 16 prefix positions those above 2^-14 of the largest, of a query's
+ * values those above 2^-14 of its largest, of the weights those above 2^-21 of a
+ * row's largest; smaller ones keep 2^-25, 2^-25 and 2^-32 of that largest.  A query with no position at all gives
  * zeros.  P, the lengths and the tables are read on the device, so a captured graph
  * may be replayed with other values.  Three launches, no host synchronisation.
  *
@@ -545,7 +548,8 @@ size_t kvc8_shared_prefix_workspace_bytes(const kvc8_geom *g, int32_t num_q_head
  *                     workspaces
  *   the rest          as in kvc8_paged_decode_attention; context_lengths may be 0
  * Supported: what kvc8_paged_decode_attention supports (head_dim 64 or 128,
- * block_size a multiple of 16, at most 8 query heads per kv head).  Positions of
+ * block_size a multiple of 16, at most 8 query heads per kv head), with fewer than
+ * 2^31 units of 128 queries of a kv head by 128 prefix positions.  Positions of
  * blocks outside the pool are reported through dev_error and left out; a
  * negative length counts as 0 and one beyond its table as the table's size, both
  * reported.

@@ -136,6 +136,11 @@ def test_shared_prefix_refusals():
     assert _prefix(wsb=need - 1) == kv.ERR_WORKSPACE
     assert _prefix(ws=None) == kv.ERR_WORKSPACE and _prefix(ws=FAKE + 16) == kv.ERR_WORKSPACE
     assert _prefix(geom=dict(num_seqs=0), q=None) == kv.OK
+    # 2^21 tiles of rows or more by 1024 steps of positions: not in 32 bits
+    many = dict(num_seqs=1 << 24, max_blocks_per_seq=1)
+    steps = dict(block_size=128, kv_heads=8)
+    assert _prefix(geom=dict(many, **steps), mpb=1 << 10) == uns
+    assert kv.kvc8_shared_prefix_workspace_bytes(kv.Geom(**{**GEOM, **many, **steps}), 32, 1 << 8) > 0
     for hq, mpb in ((30, 8), (32, 0)):
         assert kv.kvc8_shared_prefix_workspace_bytes(g, hq, mpb) == 0
 

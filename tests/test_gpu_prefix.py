@@ -253,6 +253,103 @@ def test_values_of_very_different_scales():
     x.check()
 
 
+@pytest.mark.parametrize("mode", [0, 1, 2])
+@pytest.mark.parametrize("where", ["prefix", "own"])
+def test_many_faint_positions_behind_one_strong(mode, where):
+    """The strong position's value is zero, so that the output is the sum of weights 2^-20.4 of
+    its own: each is still held to bf16's precision."""
+    x = Batch(*((600, [0, 0]) if where == "prefix" else (0, [600, 600])), H=1, G=2, D=64, mode=mode, seed=23)
+    x.ks[:], x.vs[:] = 2.0 ** -7, 2.0 ** -7
+    x.qb[:] = to_bf16_bits(np.ones(64))
+    x.kc[:] = 0
+    x.vc[:] = np.maximum(np.abs(x.vc), 1)
+    first = [x.ptab[0]] if where == "prefix" else list(x.tab[:, 0])
+    x.kc[first, :, 0], x.vc[first, :, 0] = 127, 0
+    x.dev()
+    scale = 20.4 * np.log(2.0) / (64 * 127 * 2.0 ** -7)
+    x.run(scale=scale)
+    assert x.error() == 0
+    got = bf16_f64(bf16_bits(x.out))
+    for b in range(2):
+        table, n = (x.ptab, 600) if where == "prefix" else (x.tab[b], 600)
+        k, v = x.rows(x.kc, x.ks, table, n, 0), x.rows(x.vc, x.vs, table, n, 0)
+        want = attend(x.qb[b], k, v, scale)
+        # all terms are positive: the weights' and the output's 2^-8, the scale's 2^-11 or less,
+        # and 2^-11 for fp32 sums and the strong score (24 bits of 14)
+        assert (np.abs(got[b] - want) <= (2 * BF16 + 2.0 ** -10) * want).all()
+
+
+def test_zero_rows_beside_others():
+    """Rows of zeros are kept with scale 0: alone in their sixteen, among others, everywhere."""
+    x = Batch(500, [40, 0], H=2, G=4, D=128, mode=0, seed=24)
+    for i in [*range(32, 48), 50, 51, 200]:
+        b, at = x.ptab[i // 16], i % 16
+        for cache, s in ((x.kc, x.ks), (x.vc, x.vs)):
+            cache[b, :, at], s[b, :, at] = 0, 0.0
+    x.dev()
+    x.run()
+    assert x.error() == 0
+    x.check()
+    x.vc[:], x.vs[:] = 0, 0.0
+    x.dev()
+    x.run(scale=40.0)  # scores that keep moving the maximum
+    assert x.error() == 0
+    assert not (bf16_bits(x.out) & 0x7FFF).any()
+
+
+def test_more_splits_than_the_grid_takes_at_once():
+    """Thousands of sequences with room for long contexts: a block walks several splits."""
+    rng = np.random.default_rng(25)
+    B, H = 2100, 2
+    x = Batch(40, [1] * B, H=H, G=1, D=64, mode=0, seed=26)
+    x.MB = 400
+    x.tab = rng.integers(0, x.g.num_blocks, (B, x.MB)).astype(np.int32)
+    x.lens = rng.integers(0, 20, B).tolist()
+    x.lens[0], x.lens[1234], x.lens[B - 1] = 6400, 4097, 2049
+    x.g = kv.Geom(B, H, 64, 16, x.g.num_blocks, x.MB, 0)
+    x.dev()
+    x.run()
+    assert x.error() == 0
+    x.check()
+
+
+def test_output_on_any_element():
+    x = Batch(300, [40, 0, 3], H=2, G=4, D=128, seed=27)
+    first = x.run().clone()
+    base = torch.full((x.out.numel() + 9,), 7.0, dtype=torch.bfloat16, device="cuda")
+    for at in (1, 3, 8):
+        base.fill_(7.0)
+        out = base[at:at + x.out.numel()].view(x.out.shape)
+        x.run(out=out)
+        assert torch.equal(out, first)
+        assert (base[:at] == 7).all() and (base[at + x.out.numel():] == 7).all()
+    assert x.error() == 0
+
+
+def test_two_graphs_share_a_workspace():
+    """Replayed in turn on one stream: a call leaves nothing in the workspace that a later one
+    reads."""
+    xs = [Batch(900, [70, 0, 9], H=2, G=8, D=128, bs=32, mode=0, seed=28),
+          Batch(2500, [5, 2100], H=4, G=3, D=64, bs=16, mode=1, seed=29)]
+    ws = torch.full((max(x.d["ws"].numel() for x in xs),), 0xFF, dtype=torch.uint8, device="cuda")
+    graphs = []
+    for x in xs:
+        x.d["ws"] = ws
+        x.run()
+        torch.cuda.synchronize()
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            x.run()
+    for _ in range(3):
+        for x, graph in zip(xs, graphs):
+            x.out.fill_(float("nan"))
+            graph.replay()
+    torch.cuda.synchronize()
+    for x in xs:
+        assert x.error() == 0
+        x.check()
+
+
 def test_strided_query_and_output_rows_beyond_untouched():
     x = Batch(333, [10, 0, 44], H=2, G=4, D=128, bs=16, seed=10)
     hm = x.d["q"].transpose(0, 1).contiguous().transpose(0, 1)

@@ -53,14 +53,15 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
     return y;
 }
 
+// N bytes as 16-byte pieces `gap` apart.
 template <int N>
-__device__ __forceinline__ void load_codes(const void *p, uint32_t *w) {
+__device__ __forceinline__ void load_codes(const void *p, uint32_t *w, int gap = 16) {
     if (N == 8) {
         asm("ld.global.nc.L1::no_allocate.v2.u32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "l"(p));
     } else {
 #pragma unroll
         for (int i = 0; i < N / 16; ++i) {
-            const uint4 x = ld_stream_16(static_cast<const char *>(p) + 16 * i);
+            const uint4 x = ld_stream_16(static_cast<const char *>(p) + gap * i);
             w[4 * i] = x.x, w[4 * i + 1] = x.y, w[4 * i + 2] = x.z, w[4 * i + 3] = x.w;
         }
     }
@@ -77,17 +78,18 @@ __device__ __forceinline__ float load_query(const AttnArgs &a, int b, int h, int
     for (int i = 0; i < KB / 2; ++i) v[i] = make_float2(0.0f, 0.0f);
     float top = 0.0f;
     if (gid < a.group) {
-        const uint16_t *qp = a.q + (int64_t)b * a.q_seq_stride + (int64_t)(h * a.group + gid) * a.q_head_stride + tig * KB;
-        const float *ks = a.k_scale + (MODE == 1 ? (int64_t)h * D + tig * KB : 0);
+        const uint16_t *qp = a.q + (int64_t)b * a.q_seq_stride + (int64_t)(h * a.group + gid) * a.q_head_stride + tig * 16;
+        const float *ks = a.k_scale + (MODE == 1 ? (int64_t)h * D + tig * 16 : 0);
 #pragma unroll
         for (int i = 0; i < KB / 8; ++i) {
-            const uint4 x = __ldg(reinterpret_cast<const uint4 *>(qp) + i);
+            const int at = 64 * (i / 2) + 8 * (i % 2);  // as the codes lie (see the loop)
+            const uint4 x = __ldg(reinterpret_cast<const uint4 *>(qp + at));
             const uint32_t wd[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 float2 y = make_float2(__uint_as_float(wd[e] << 16), __uint_as_float(wd[e] & 0xFFFF0000u));
                 if (MODE == 1) {
-                    const float2 s = __ldg(reinterpret_cast<const float2 *>(ks + 8 * i + 2 * e));
+                    const float2 s = __ldg(reinterpret_cast<const float2 *>(ks + at + 2 * e));
                     y = make_float2(y.x * s.x, y.y * s.y);
                 }
                 v[4 * i + e] = y;
@@ -159,9 +161,10 @@ __global__ void __launch_bounds__(kThreads, 4) own_kernel(const AttnArgs a, int 
             const int valid = min(kSub, end - p0);
             const int64_t row0 = ((int64_t)blk * H + h) * bs + (int)((uint32_t)p0 % (uint32_t)bs);
             uint32_t k0[D / 16], k1[D / 16], v[4][D / 32];
-            const int8_t *kp = a.k_cache + (row0 + gid) * D + tig * KB;
-            load_codes<KB>(kp, k0);
-            load_codes<KB>(kp + 8 * D, k1);
+            // channels 16 tig and on of each 64: a load covers whole sectors
+            const int8_t *kp = a.k_cache + (row0 + gid) * D + tig * 16;
+            load_codes<KB>(kp, k0, 64);
+            load_codes<KB>(kp + 8 * D, k1, 64);
             const int8_t *vp = a.v_cache + (row0 + 2 * tig) * D + gid * VB;
             load_codes<VB>(vp, v[0]);
             load_codes<VB>(vp + D, v[1]);

@@ -4,6 +4,8 @@
 
 #include <cstdint>
 
+#include <cuda_runtime.h>
+
 namespace kvc8 {
 
 __device__ __forceinline__ float ex2(float x) {  // 2^x, -inf gives 0
@@ -56,6 +58,22 @@ template <bool HALF>
 __device__ __forceinline__ uint32_t codes_of_two(uint32_t a, uint32_t b, uint32_t select) {
     const uint32_t x = __byte_perm(a, b, select);
     return HALF ? fp16_of((x & 0x00FF00FFu) ^ 0x64806480u) : bf16_of(x);
+}
+
+// Launch that may start when every block of the kernel before it in the stream has started.
+template <typename... A>
+cudaError_t launch_dependent(void (*kern)(A...), dim3 grid, int threads, size_t smem, cudaStream_t stream, A... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, args...);
 }
 
 }  // namespace kvc8

@@ -321,6 +321,7 @@ struct PrefixArgs {
     int32_t rows;            // query rows of a kv head: sequences * group
     int32_t tiles_per_head;  // tiles of query rows
     int32_t ctas;            // CTAs that share the prefix's work
+    int32_t per_tile;        // CTAs of each tile; 0: the CTAs share all tiles' work evenly
     int32_t own_splits;      // splits of own positions that a sequence has room for
     // Unnormalised partial outputs of the prefix, [slots * rows of a tile] rows of D floats:
     // 32 rows together, eight channels of each in turn ([row / 32][D / 8][32][8]), so
@@ -332,7 +333,8 @@ struct PrefixArgs {
 // Its own positions (kvc8_prefix_own.cu), each split leaving a partial; sets own_splits
 // and the partials' places in the workspace.
 size_t own_workspace_bytes(const kvc8_geom &g, int group);
-cudaError_t launch_own(PrefixArgs &p, void *workspace, cudaStream_t stream);
+void place_own(PrefixArgs &p, void *workspace);  // p.own's partials, p.own_splits
+cudaError_t launch_own(const PrefixArgs &p, cudaStream_t stream);
 size_t shared_prefix_workspace_bytes(const kvc8_geom &g, int group, int32_t max_prefix_blocks);
 cudaError_t launch_shared_prefix(PrefixArgs a, void *workspace, cudaStream_t stream);
 cudaError_t launch_rope(const RopeArgs &a, RopeSink sink, cudaStream_t stream);

@@ -118,7 +118,7 @@ __global__ void __launch_bounds__(kThreads, 4) own_kernel(const AttnArgs a, int 
     __shared__ float s_o[kWarps][kMaxGroup][D];
     __shared__ float s_m[kWarps][kMaxGroup], s_l[kWarps][kMaxGroup];
 
-    pdl_launch_dependents();  // the prefix's kernel needs nothing of this one
+    pdl_launch_dependents();
     const int b = blockIdx.x / H, h = blockIdx.x - b * H;
     const int64_t cap = (int64_t)MB * bs, raw_len = ld_nc_s32(a.context_lengths + b);
     if (h == 0 && blockIdx.y == 0 && threadIdx.x == 0) {
@@ -272,6 +272,8 @@ __global__ void __launch_bounds__(kThreads, 4) own_kernel(const AttnArgs a, int 
         }
         __syncthreads();
     }
+    // The merge waits for this grid and, through one block's wait, for the prefix's kernel.
+    if (blockIdx.x == 0 && blockIdx.y == 0) pdl_wait_prior_grid();
 }
 
 int32_t max_splits(const kvc8_geom &g) {
@@ -288,8 +290,8 @@ cudaError_t launch_variant(const AttnArgs &a, cudaStream_t stream) {
     const int splits = max_splits(a.g);
     int64_t stride = kMaxGrid / pairs;
     stride = stride < 1 ? 1 : stride > splits ? splits : stride;
-    own_kernel<MODE, D><<<dim3((unsigned)pairs, (unsigned)stride), kThreads, 0, stream>>>(a, splits, (int)stride);
-    return cudaGetLastError();
+    return launch_dependent(own_kernel<MODE, D>, dim3((unsigned)pairs, (unsigned)stride), kThreads, (size_t)0, stream, a,
+                            splits, (int)stride);
 }
 
 template <int MODE>
@@ -306,7 +308,7 @@ size_t own_workspace_bytes(const kvc8_geom &g, int group) {
     return align_up(sizeof(float) * rows * g.head_dim, kAlign) + 2 * align_up(sizeof(float) * rows, kAlign);
 }
 
-cudaError_t launch_own(PrefixArgs &p, void *workspace, cudaStream_t stream) {
+void place_own(PrefixArgs &p, void *workspace) {
     AttnArgs &a = p.own;
     const size_t rows = (size_t)a.g.num_seqs * a.g.kv_heads * max_splits(a.g) * a.group;
     char *base = static_cast<char *>(workspace);
@@ -316,6 +318,10 @@ cudaError_t launch_own(PrefixArgs &p, void *workspace, cudaStream_t stream) {
     a.part_m = reinterpret_cast<float *>(base);
     base += align_up(sizeof(float) * rows, kAlign);
     a.part_l = reinterpret_cast<float *>(base);
+}
+
+cudaError_t launch_own(const PrefixArgs &p, cudaStream_t stream) {
+    const AttnArgs &a = p.own;
     if (a.g.quant_mode == 0) return launch_mode<0>(a, stream);
     if (a.g.quant_mode == 1) return launch_mode<1>(a, stream);
     return launch_mode<2>(a, stream);

@@ -313,6 +313,15 @@ struct RopeArgs {
 };
 
 // Decode attention over a shared prefix and each sequence's own pages (kvc8_prefix.cu).
+// One way to cut a prefix's work over CTAs.
+struct PrefixCut {
+    int32_t ctas;      // CTAs that share the prefix's work
+    int32_t per_tile;  // CTAs of each tile; 0: the CTAs share all tiles' work evenly
+    float time;        // of the longest share, in steps times SMs
+    float beside;      // of that on the SMs without a CTA
+};
+constexpr int kPrefixCuts = 8;
+
 struct PrefixArgs {
     AttnArgs own;  // the sequences' own positions, the query and the output
     const int32_t *prefix_table;
@@ -320,8 +329,11 @@ struct PrefixArgs {
     const int32_t *prefix_length;
     int32_t rows;            // query rows of a kv head: sequences * group
     int32_t tiles_per_head;  // tiles of query rows
-    int32_t ctas;            // CTAs that share the prefix's work
-    int32_t per_tile;        // CTAs of each tile; 0: the CTAs share all tiles' work evenly
+    int32_t sms;             // SMs that share everything
+    float own_weight;        // steps of an SM that 64 own positions (of all kv heads) take
+    float own_least;         // the least that the own positions after the prefix take
+    int32_t cuts;            // of those below
+    PrefixCut cut[kPrefixCuts];  // what the kernels choose from, by the own positions' number
     int32_t own_splits;      // splits of own positions that a sequence has room for
     // Unnormalised partial outputs of the prefix, [slots * rows of a tile] rows of D floats:
     // 32 rows together, eight channels of each in turn ([row / 32][D / 8][32][8]), so

@@ -24,14 +24,17 @@
 //   mma         one lane issues both products; with two tiles one's products run
 //               while the other's softmax does
 // The (tile, 128 positions) units are cut over the CTAs (at most one per SM), each taking its
-// share in a row: within one tile, or evenly over all tiles where that leaves the longest
-// share shorter by more than a change of tile costs.  A CTA leaves one partial per tile it
-// touches; CTA i's of tile t is in slot t + i, which no other pair has.
+// share in a row, within one tile or (all of them) evenly over all tiles.  A CTA leaves one
+// partial per tile it touches; CTA i's of tile t is in slot t + i, which no other pair has.
 //
 // The own positions' kernel starts when all CTAs have started and fills the SMs that have
-// none, then those that are done; merge_kernel joins a row's partials of both.  (Before, with
-// the own positions first and one CTA per SM: 10007 positions x 23 sequences 36.9 us, now
-// 26.7; 8192 x 64 62.0, now 58.8.)
+// none, then those that are done; merge_kernel joins a row's partials of both.  An SM that
+// reads own positions alone waits for memory, one that multiplies alone hardly reads any,
+// so the two side by side are quicker than one after the other, and how many CTAs the prefix
+// gets depends on how many own positions there are: see best_cut.  Measured, own positions
+// first and one CTA per SM -> side by side, all SMs to the prefix -> the cut chosen: 10007
+// positions x 23 sequences 36.9 -> 26.7 -> 26.3 us; 8192 x 64 62.0 -> 58.8 -> 47.2 (96 CTAs
+// of 152 SMs); 32768 x 256 198.4 -> 193.9 -> 170.6 (96).
 //
 // Every wait has a limit, after which the kernel reports KVC8_DEV_TIMEOUT and leaves.
 #include "kvc8_codes.cuh"
@@ -52,7 +55,9 @@ constexpr float kLazy = 8.0f, kLift = 7.0f;
 constexpr int kLeastValuePower = -60;  // so that the sum of such weights times 2^-e is finite
 constexpr long long kWaitCycles = 4000000000ll;  // about two seconds
 constexpr int kMergeThreads = 256;
-constexpr int kTileChange = 3;  // steps that a CTA's change of tile costs, about
+// What else costs time, in steps, about: a CTA's start and end, its change of tile, the own
+// positions' kernel after the prefix's.
+constexpr int kStart = 4, kTileChange = 3, kOwnLeast = 3;
 
 // ---- PTX ------------------------------------------------------------------------
 
@@ -198,33 +203,61 @@ constexpr uint32_t instr_desc(int n, bool b_mn) {
 
 // ---- the work's split -------------------------------------------------------------
 
-// a / b for 0 <= a, 0 < b: in 32 bits where that does.
-__device__ __forceinline__ int64_t divide(int64_t a, int64_t b) {
-    if (((a | b) >> 32) == 0) return (int64_t)((uint32_t)a / (uint32_t)b);
-    return a / b;
-}
-
 // Units (tile, step of 128 positions), numbered tile by tile, are cut into shares: of `n`
 // CTAs that share `units` of them each takes `per` in a row, the first `more` one more.
-// The CTAs are those of one tile, or all of them share all tiles.
+// The CTAs are those of one tile, or all of them share all tiles.  All units are fewer than
+// 2^31 (larger calls are refused).
 struct PrefixWork {
-    int64_t units, per, more;
-    int32_t steps, len, n;
-    __device__ __forceinline__ int64_t first_of(int cta) const { return cta * per + min((int64_t)cta, more); }
-    __device__ __forceinline__ int cta_of(int64_t unit) const {
-        const int64_t edge = more * (per + 1);
-        return (int)(unit < edge ? divide(unit, per + 1) : more + divide(unit - edge, per));
+    uint32_t units, per, more, n;
+    int32_t steps, len, per_tile;
+    __device__ __forceinline__ uint32_t first_of(uint32_t cta) const { return cta * per + min(cta, more); }
+    __device__ __forceinline__ uint32_t cta_of(uint32_t unit) const {
+        const uint32_t edge = more * (per + 1);
+        return unit < edge ? unit / (per + 1) : more + (unit - edge) / per;
     }
 };
 
-__device__ __forceinline__ PrefixWork prefix_work(const PrefixArgs &p) {
+// The sequences' own positions, in units of 64: this thread's part of what the block adds up
+// (modulo 2^32: it only steers the cut).
+__device__ __forceinline__ uint32_t own_part(const PrefixArgs &p) {
+    const int64_t cap = (int64_t)p.own.g.max_blocks_per_seq * p.own.g.block_size;
+    uint32_t n = 0;
+    for (int b = threadIdx.x; b < p.own.g.num_seqs; b += blockDim.x)
+        n += (uint32_t)(min((int64_t)max(0, __ldg(p.own.context_lengths + b)), cap) + 63) >> 6;
+    return n;
+}
+
+// The cut with which prefix and own positions are done first, in steps' times.  The own
+// positions take `own` steps of an SM: on the SMs without a CTA while the prefix lasts,
+// then on all, and then not less than kOwnLeast.  (No operation that the compiler may fuse in
+// one kernel and not in the other: both have to find the same.)
+__device__ __forceinline__ PrefixCut best_cut(const PrefixArgs &p, uint32_t own_units) {
+    const float own = __fmul_rn(__uint2float_rn(own_units), p.own_weight);
+    PrefixCut best = p.cut[0];
+    if (p.cuts == 1) return best;
+    float least = INFINITY;
+#pragma unroll 1
+    for (int i = 0; i < p.cuts; ++i) {
+        const float rest = __fadd_rn(own, -p.cut[i].beside);
+        const float t = __fadd_rn(p.cut[i].time, rest > 0.0f ? __fadd_rn(rest, p.own_least) : 0.0f);
+        if (t < least) {
+            least = t;
+            best = p.cut[i];
+        }
+    }
+    return best;
+}
+
+__device__ __forceinline__ PrefixWork prefix_work(const PrefixArgs &p, int32_t given, uint32_t own_units) {
     PrefixWork w;
+    const PrefixCut cut = best_cut(p, own_units);
+    w.per_tile = cut.per_tile;
     const int64_t cap = (int64_t)p.max_prefix_blocks * p.own.g.block_size;
-    w.len = (int32_t)max((int64_t)0, min((int64_t)__ldg(p.prefix_length), cap));
+    w.len = (int32_t)max((int64_t)0, min((int64_t)given, cap));
     w.steps = (int32_t)(((uint32_t)w.len + kCols - 1) / kCols);
-    w.n = p.per_tile > 0 ? p.per_tile : p.ctas;
-    w.units = p.per_tile > 0 ? w.steps : (int64_t)p.tiles_per_head * p.own.g.kv_heads * w.steps;
-    w.per = divide(w.units, w.n);
+    w.n = (uint32_t)(cut.per_tile > 0 ? cut.per_tile : cut.ctas);
+    w.units = (uint32_t)w.steps * (uint32_t)(cut.per_tile > 0 ? 1 : p.tiles_per_head * p.own.g.kv_heads);
+    w.per = w.units / w.n;
     w.more = w.units - w.per * w.n;
     return w;
 }
@@ -259,6 +292,7 @@ struct Barriers {
     uint64_t q_full[2], s_full[2], p_full[2], o_full[2], drained;
     uint32_t tmem;
     int32_t stop;
+    uint32_t own[16];  // own positions, counted by each warp
     uint2 valid[kMaskSlots];  // 8 bytes: valid positions of each group of 16
     // modes 0 and 2: what was taken out of each group of 16's scales, as powers of two:
     // the keys' 2^e, the values' e and 2^-e
@@ -274,7 +308,7 @@ struct Prefix {
     Barriers &bar;
     const uint32_t base;  // shared memory, 1 KB aligned
     const PrefixWork w;
-    const int64_t total;     // units of this CTA
+    const int total;         // units of this CTA
     const int tile0, step0;  // the first one's tile and step
     const int lane;
 
@@ -436,7 +470,7 @@ struct Prefix {
         next();
         Ids ids = find(step, dw);
         int n = 0;
-        for (int64_t u = 0; u < total; ++u, ++n) {
+        for (; n < total; ++n) {
             const int st = n % kStages;
             const uint32_t par = (uint32_t)(n / kStages) & 1u;
             if (!wait_warp(bar.k_free[st], par ^ 1u)) return;
@@ -461,7 +495,7 @@ struct Prefix {
             fence_async();
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_u32(&bar.k_full[st]));
-            const bool more = u + 1 < total;
+            const bool more = n + 1 < total;
             if (more) {  // the next step's codes, and the block ids of the one after
                 x = place(ids, tile / p.tiles_per_head);
                 load(x, a.k_cache, k);
@@ -513,7 +547,7 @@ struct Prefix {
 
     __device__ bool products_loop(uint32_t tmem_any, uint32_t leader) const {
         const uint32_t tmem = (uint32_t)uniform((int)tmem_any);
-        const int units = uniform((int)total), steps = uniform(w.steps);
+        const int units = uniform(total), steps = uniform(w.steps);
         int in_tile = uniform(step0);  // step of the tile
         uint32_t seg = 0;
         bool first = true, next_p = false, next_v = false;
@@ -589,9 +623,9 @@ struct Prefix {
         const bool flip = a.scale_log2 < 0.0f;  // the sign goes to the query
         int n = 0;
         uint32_t seg = 0;
-        int64_t left = total;
+        int left = total;
         for (int tile = tile0; left > 0; ++tile, ++seg) {
-            const int count = (int)min(left, (int64_t)(w.steps - (tile == tile0 ? step0 : 0)));
+            const int count = min(left, w.steps - (tile == tile0 ? step0 : 0));
             const int h = tile / p.tiles_per_head;
             const int r0 = (tile - h * p.tiles_per_head) * (NT * kRows) + x * kRows + (warp & 3) * 32;
             const int r = r0 + lane;
@@ -806,49 +840,71 @@ __global__ void __launch_bounds__(Layout<D, NT>::kThreads, 1) prefix_kernel(cons
     __shared__ Barriers bar;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     pdl_launch_dependents();
-    const PrefixWork w = prefix_work(p);
+    const int32_t given = __ldg(p.prefix_length);
+    const bool choose = p.cuts > 1;
+    PrefixWork w;
+    uint32_t own = 0;
+    if (choose)
+        own = own_part(p);
+    else
+        w = prefix_work(p, given, 0);
+    if (warp == L::kMmaWarp) {
+        if (lane == 0) {
+            for (int i = 0; i < kStages; ++i) {
+                mbar_init(smem_u32(&bar.k_full[i]), L::kDequantWarps);
+                mbar_init(smem_u32(&bar.v_full[i]), L::kDequantWarps);
+                mbar_init(smem_u32(&bar.k_free[i]), 1);
+                mbar_init(smem_u32(&bar.v_free[i]), 1);
+            }
+            for (int i = 0; i < 2; ++i) {
+                mbar_init(smem_u32(&bar.q_full[i]), 4);
+                mbar_init(smem_u32(&bar.p_full[i]), 4);
+                mbar_init(smem_u32(&bar.s_full[i]), 1);
+                mbar_init(smem_u32(&bar.o_full[i]), 1);
+            }
+            mbar_init(smem_u32(&bar.drained), 1);
+            bar.stop = 0;
+            asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+            fence_async();
+        }
+        __syncwarp();
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&bar.tmem)),
+                     "r"((uint32_t)L::kTmemCols)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    if (choose) {
+        own = __reduce_add_sync(0xFFFFFFFFu, own);
+        if (lane == 0) bar.own[warp] = own;
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = bar.tmem;
+    if (choose) {
+        own = 0;
+#pragma unroll
+        for (int i = 0; i < L::kThreads / 32; ++i) own += bar.own[i];
+        w = prefix_work(p, given, own);
+    }
     if (blockIdx.x == 0 && threadIdx.x == 0) {
-        const int32_t given = __ldg(p.prefix_length);
         if (given < 0) report(p.own.dev_error, KVC8_DEV_BAD_LENGTH);
         if (given > w.len && given >= 0) report(p.own.dev_error, KVC8_DEV_POS_BEYOND_TABLE);
     }
-    const int group = blockIdx.x / w.n, share = blockIdx.x - group * w.n;  // group: the tile, or 0
-    const int64_t first = w.first_of(share), total = w.first_of(share + 1) - first;
+    const uint32_t group = blockIdx.x / w.n, share = blockIdx.x - group * w.n;  // group: the tile, or 0
+    const uint32_t groups = w.per_tile > 0 ? (uint32_t)(p.tiles_per_head * p.own.g.kv_heads) : 1u;
+    const uint32_t first = w.first_of(share), total = group < groups ? w.first_of(share + 1) - first : 0u;
     if (total > 0) {
-        if (warp == L::kMmaWarp) {
-            if (lane == 0) {
-                for (int i = 0; i < kStages; ++i) {
-                    mbar_init(smem_u32(&bar.k_full[i]), L::kDequantWarps);
-                    mbar_init(smem_u32(&bar.v_full[i]), L::kDequantWarps);
-                    mbar_init(smem_u32(&bar.k_free[i]), 1);
-                    mbar_init(smem_u32(&bar.v_free[i]), 1);
-                }
-                for (int i = 0; i < 2; ++i) {
-                    mbar_init(smem_u32(&bar.q_full[i]), 4);
-                    mbar_init(smem_u32(&bar.p_full[i]), 4);
-                    mbar_init(smem_u32(&bar.s_full[i]), 1);
-                    mbar_init(smem_u32(&bar.o_full[i]), 1);
-                }
-                mbar_init(smem_u32(&bar.drained), 1);
-                bar.stop = 0;
-                asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-                fence_async();
-            }
-            __syncwarp();
-            asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&bar.tmem)),
-                         "r"((uint32_t)L::kTmemCols)
-                         : "memory");
-            asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
-        }
-        tc_fence_before();
-        __syncthreads();
-        tc_fence_after();
-        const uint32_t tmem = bar.tmem;
         const uint32_t base = (smem_u32(dyn) + 1023u) & ~1023u;
-        const int tile_in = (int)divide(first, w.steps);
-        const Prefix<MODE, D, NT> k{p,     bar,           base,
-                                    w,     total,         group + tile_in,
-                                    (int)(first - (int64_t)tile_in * w.steps), lane};
+        const uint32_t tile_in = first / (uint32_t)w.steps;
+        const Prefix<MODE, D, NT> k{p,
+                                    bar,
+                                    base,
+                                    w,
+                                    (int)total,
+                                    (int)(group + tile_in),
+                                    (int)(first - tile_in * (uint32_t)w.steps),
+                                    lane};
         if (warp >= L::kMmaWarp) {
             reg_give<L::kMmaRegs>();
             if (warp == L::kMmaWarp) k.products(tmem);
@@ -863,17 +919,18 @@ __global__ void __launch_bounds__(Layout<D, NT>::kThreads, 1) prefix_kernel(cons
         tc_fence_before();
         __syncthreads();
         tc_fence_after();
-        if (warp == L::kMmaWarp)
-            asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"((uint32_t)L::kTmemCols)
-                         : "memory");
     }
+    if (warp == L::kMmaWarp)
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"((uint32_t)L::kTmemCols)
+                     : "memory");
 }
 
 // Joins a query row's partials: the prefix's segments and its own positions' splits.
-// D / 8 lanes per query row, eight channels each, four partials' loads in flight; where
+// D / 8 lanes per query row, eight channels each, four partials' loads in flight (eight, with
+// half as many warps: 49.3 us instead of 47.2 for 8192 positions x 64 sequences); where
 // rows are few and partials many, `share` warps take a part of them each.
 template <int D>
-__global__ void __launch_bounds__(kMergeThreads) merge_kernel(const PrefixArgs p, int rows_per_tile, int share) {
+__global__ void __launch_bounds__(kMergeThreads, 4) merge_kernel(const PrefixArgs p, int rows_per_tile, int share) {
     constexpr int kLanes = D / 8, kWarpRows = 32 / kLanes;
     __shared__ float s_acc[kMergeThreads][9], s_top[kMergeThreads], s_sum[kMergeThreads];
     const AttnArgs &a = p.own;
@@ -884,14 +941,24 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const PrefixArgs p
     const int at = (blockIdx.x * (kMergeThreads / 32) + (threadIdx.x >> 5)) / share * kWarpRows + lane / kLanes;
     const int row = min(at, B * H * G - 1);
     const int b = row / (H * G), hj = row - b * (H * G), h = hj / G, j = hj - h * G;
-    const PrefixWork w = prefix_work(p);
+    const int32_t given = __ldg(p.prefix_length);
+    __shared__ uint32_t s_own[kMergeThreads / 32];
+    uint32_t own_total = 0;
+    if (p.cuts > 1) {
+        const uint32_t part = __reduce_add_sync(0xFFFFFFFFu, own_part(p));
+        if (lane == 0) s_own[threadIdx.x >> 5] = part;
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < kMergeThreads / 32; ++i) own_total += s_own[i];
+    }
+    const PrefixWork w = prefix_work(p, given, own_total);
     const int r = b * G + j, tile = h * p.tiles_per_head + r / rows_per_tile;
     int parts = 0;
     int64_t slot = 0;  // row of the first segment's partial; segments are a tile's rows apart
     if (w.steps > 0) {
-        const int64_t first = p.per_tile > 0 ? 0 : (int64_t)tile * w.steps;
-        const int before = p.per_tile > 0 ? tile * p.per_tile : 0;
-        const int c0 = before + w.cta_of(first), c1 = before + w.cta_of(first + w.steps - 1);
+        const uint32_t first = w.per_tile > 0 ? 0u : (uint32_t)(tile * w.steps);
+        const int before = tile * w.per_tile;
+        const int c0 = before + (int)w.cta_of(first), c1 = before + (int)w.cta_of(first + w.steps - 1);
         parts = c1 - c0 + 1;
         slot = ((int64_t)tile + c0) * rows_per_tile + r % rows_per_tile;
     }
@@ -908,6 +975,19 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const PrefixArgs p
         stride *= share;
         const int rounds = (__reduce_max_sync(0xFFFFFFFFu, count) + kLanes - 1) / kLanes;
         for (int i0 = 0; i0 < rounds * kLanes; i0 += kLanes) {
+            float4 v[4][2];  // four partials, requested before their weights are known
+            auto request = [&](int k0) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    v[k][0] = v[k][1] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                    if (i0 + k0 + k < count) {
+                        const float4 *src = reinterpret_cast<const float4 *>(o + (i0 + k0 + k) * stride * D);
+                        v[k][0] = src[0];
+                        v[k][1] = src[1];
+                    }
+                }
+            };
+            request(0);
             const bool in = i0 + gl < count;
             const float m = in ? pm[(i0 + gl) * stride] : -INFINITY, l = in ? pl[(i0 + gl) * stride] : 0.0f;
             float n = m;
@@ -922,16 +1002,7 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const PrefixArgs p
             for (int e = 0; e < 8; ++e) acc[e] *= g;
             const int most = __reduce_max_sync(0xFFFFFFFFu, min(kLanes, count - i0));
             for (int k0 = 0; k0 < most; k0 += 4) {
-                float4 v[4][2];
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    v[k][0] = v[k][1] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                    if (i0 + k0 + k < count) {
-                        const float4 *src = reinterpret_cast<const float4 *>(o + (i0 + k0 + k) * stride * D);
-                        v[k][0] = src[0];
-                        v[k][1] = src[1];
-                    }
-                }
+                if (k0 > 0) request(k0);
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
                     const float fk = __shfl_sync(0xFFFFFFFFu, f, k0 + k, kLanes);
@@ -1002,6 +1073,52 @@ Space space(const kvc8_geom &g, int group) {
     return s;
 }
 
+// The cuts to choose from: CTAs that stay within a tile, as many as there is room for and
+// down to about half as many, and CTAs that share all work.  None has more CTAs than its
+// longest share needs.  Returns the most CTAs of one.
+int prefix_cuts(PrefixArgs &p, int64_t tiles, int64_t steps) {
+    const int64_t units = tiles * steps, sms = p.sms;
+    auto up = [](int64_t a, int64_t b) { return (a + b - 1) / b; };
+    constexpr int kInTile = 5;
+    int most = 0;
+    p.cuts = 0;
+    for (int i = 0; i < kPrefixCuts; ++i) {
+        const int64_t room = sms / tiles;
+        const int64_t each = i < kInTile ? room - i * up(room, 2 * kInTile) : 0;
+        PrefixCut c;
+        int64_t longest;
+        if (each > 0) {
+            longest = up(steps, each);
+            c.per_tile = (int32_t)up(steps, longest);
+            c.ctas = (int32_t)(tiles * c.per_tile);
+        } else {
+            longest = up(units, sms - sms * (i < kInTile ? i : i - kInTile) / 8);
+            c.per_tile = 0;
+            c.ctas = (int32_t)up(units, longest);
+            longest += kTileChange;
+        }
+        c.time = (float)(sms * (kStart + longest));
+        c.beside = (float)((sms - c.ctas) * (kStart + longest));
+        bool better = true;
+        for (int j = 0; j < p.cuts; ++j) better = better && (c.time < p.cut[j].time || c.ctas < p.cut[j].ctas);
+        if (!better) continue;
+        p.cut[p.cuts++] = c;
+        if (c.ctas > most) most = c.ctas;
+    }
+    // As many own positions as there is room for fit beside the quickest: nothing to choose.
+    // (Reading the lengths and choosing takes 1.5 us.)
+    int quick = 0;
+    for (int i = 1; i < p.cuts; ++i)
+        if (p.cut[i].time < p.cut[quick].time) quick = i;
+    const int64_t own_most = (int64_t)p.own.g.num_seqs * ((p.own.g.max_blocks_per_seq * (int64_t)p.own.g.block_size + 63) / 64);
+    if ((float)own_most * p.own_weight <= p.cut[quick].beside) {
+        p.cut[0] = p.cut[quick];
+        p.cuts = 1;
+        most = p.cut[0].ctas;
+    }
+    return most;
+}
+
 template <int MODE, int D, int NT>
 cudaError_t launch_variant(PrefixArgs p, cudaStream_t stream) {
     using L = Layout<D, NT>;
@@ -1025,20 +1142,13 @@ cudaError_t launch_variant(PrefixArgs p, cudaStream_t stream) {
     p.tiles_per_head = (p.rows + NT * kRows - 1) / (NT * kRows);
     const int64_t steps = ((int64_t)p.max_prefix_blocks * p.own.g.block_size + kCols - 1) / kCols;
     const int64_t tiles = (int64_t)p.tiles_per_head * p.own.g.kv_heads, units = tiles * steps;
-    // No more CTAs than the longest share needs: the SMs left over run own positions
-    // meanwhile.  CTAs that stay within a tile may take up to kTileChange steps more.
-    const int64_t sms = sm_count() < kMaxCtas ? sm_count() : kMaxCtas;
-    const int64_t even = (units + sms - 1) / sms;
-    p.ctas = (int32_t)((units + even - 1) / even);
-    p.per_tile = 0;
-    if (tiles <= sms) {
-        const int64_t each = (steps + sms / tiles - 1) / (sms / tiles);
-        if (each <= even + kTileChange) {
-            p.per_tile = (int32_t)((steps + each - 1) / each);
-            p.ctas = (int32_t)(tiles * p.per_tile);
-        }
-    }
-    kern<<<(unsigned)p.ctas, L::kThreads, (size_t)L::kBytes, stream>>>(p);
+    p.sms = sm_count() < kMaxCtas ? sm_count() : kMaxCtas;
+    // own positions of a kv head that an SM passes in a step's time
+    constexpr float kOwnPerStep = NT == 1 ? 130.0f : 220.0f;
+    p.own_weight = 64.0f * (float)p.own.g.kv_heads / kOwnPerStep;
+    p.own_least = (float)(p.sms * kOwnLeast);
+    const int grid = prefix_cuts(p, tiles, steps);
+    kern<<<(unsigned)grid, L::kThreads, (size_t)L::kBytes, stream>>>(p);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     e = launch_own(p, stream);
@@ -1046,7 +1156,7 @@ cudaError_t launch_variant(PrefixArgs p, cudaStream_t stream) {
     // Partials a row has of the prefix, about: CTAs per tile.  Up to six a warp (of 644 rows
     // with 38 partials each the merge took 32 us with one warp per two rows).
     int share = 1;
-    while (share < kMergeThreads / 32 && p.ctas > 6 * share * tiles) share *= 2;
+    while (share < kMergeThreads / 32 && grid > 6 * share * tiles) share *= 2;
     const int64_t all = (int64_t)p.rows * p.own.g.kv_heads, per = kMergeThreads / (D / 8) / share;
     return launch_dependent(merge_kernel<D>, dim3((unsigned)((all + per - 1) / per)), kMergeThreads, (size_t)0, stream, p,
                             NT * kRows, share);

@@ -146,6 +146,16 @@ def test_long_prefix_many_parts(mode):
     x.check()
 
 
+@pytest.mark.parametrize("lens", [[0] * 40, [0] * 39 + [2500], [2500, 0, 7, 64] * 10, [2500] * 40])
+@pytest.mark.parametrize("G", [3, 8])
+def test_tables_with_room_for_more(lens, G):
+    """The same tables more or less full: the work is cut by what is in them."""
+    x = Batch(5000, lens, H=2, G=G, D=64, bs=32, mode=1, seed=30, spare_own=80 - max(lens) // 32)
+    x.run()
+    assert x.error() == 0
+    x.check()
+
+
 @pytest.mark.parametrize("mode", [0, 1, 2])
 def test_many_calls_of_many_sequences(mode):
     """Enough work items for every SM to take several, twice, with other data in between

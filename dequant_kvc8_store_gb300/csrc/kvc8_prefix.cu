@@ -270,6 +270,10 @@ struct Layout {
     static constexpr int kSoftmaxWarps = 4 * NT;
     static constexpr int kMmaWarp = kSoftmaxWarps + kDequantWarps;  // three idle warps behind it
     static constexpr int kThreads = 512;
+    // The products of a step's first half run while the second half's weights are made.  With
+    // two tiles one's products run beside the other's softmax anyway (60000 positions in mode 0,
+    // one tile: 66.0 us in halves, 69.2 whole; two tiles, 1024 rows x 32768: 172.3 and 171.0).
+    static constexpr bool kHalves = NT == 1;
     // registers per thread: a softmax thread holds a row's 128 scores
     static constexpr int kSoftmaxRegs = 184, kDequantRegs = NT == 1 ? 112 : 104, kMmaRegs = 40;
     static constexpr int kLaunchRegs = 128;
@@ -289,7 +293,7 @@ struct Layout {
 
 struct Barriers {
     uint64_t k_full[kStages], k_free[kStages], v_full[kStages], v_free[kStages];
-    uint64_t q_full[2], s_full[2], p_full[2], o_full[2], drained;
+    uint64_t q_full[2], s_full[2], p_half[2], p_full[2], o_full[2], drained;
     uint32_t tmem;
     int32_t stop;
     uint32_t own[16];  // own positions, counted by each warp
@@ -527,12 +531,15 @@ struct Prefix {
             tc_mma_ss(tmem + x * kCols, q + at, k + at, instr_desc(kCols, false), i > 0, leader);
         }
     }
+    // One half of the step's positions.
     template <typename Peek>
-    __device__ __forceinline__ void pv(int x, int st, uint32_t tmem, bool acc, uint32_t leader, Peek &&peek) const {
+    __device__ __forceinline__ void pv(int x, int half, int st, uint32_t tmem, bool acc, uint32_t leader,
+                                       Peek &&peek) const {
         const uint64_t v = operand_desc(base + L::kV, kCols * 128) + (uint64_t)(st * (L::kTileBytes >> 4));
 #pragma unroll
-        for (int i = 0; i < kCols / 16; ++i) {
-            if (i == kCols / 16 - 3) peek();
+        for (int j = 0; j < kCols / 32; ++j) {
+            const int i = half * (kCols / 32) + j;
+            if (j == 1) peek();
             tc_mma_ts(tmem + NT * kCols + x * D, tmem + x * kCols + 8 * i, v + (uint64_t)(i * (2048 >> 4)),
                       instr_desc(D, true), acc || i > 0, leader);
         }
@@ -544,6 +551,9 @@ struct Prefix {
     // The loop's own quantities come from lane 0, so that the compiler keeps them, and
     // with them stages, addresses and descriptors, in uniform registers.
     __device__ __forceinline__ static int uniform(int x) { return __shfl_sync(0xFFFFFFFFu, x, 0); }
+
+    // The weights that a step's products wait for first.
+    __device__ __forceinline__ uint64_t &first_p(int x) const { return L::kHalves ? bar.p_half[x] : bar.p_full[x]; }
 
     __device__ bool products_loop(uint32_t tmem_any, uint32_t leader) const {
         const uint32_t tmem = (uint32_t)uniform((int)tmem_any);
@@ -572,10 +582,16 @@ struct Prefix {
             }
 #pragma unroll
             for (int x = 0; x < NT; ++x) {
-                if (!p_in[x] && !wait_warp(bar.p_full[x], (uint32_t)st)) return false;
+                if (!p_in[x] && !wait_warp(first_p(x), (uint32_t)st)) return false;
                 if (x == 0 && !v_in && !wait_warp(bar.v_full[st], par)) return false;
                 tc_fence_after();
-                pv(x, st, tmem, !first, leader, [&]() {
+                bool p_rest = !L::kHalves;
+                pv(x, 0, st, tmem, !first, leader, [&]() {
+                    if (L::kHalves) p_rest = ready(bar.p_full[x], (uint32_t)st);
+                });
+                if (!p_rest && !wait_warp(bar.p_full[x], (uint32_t)st)) return false;
+                if (L::kHalves) tc_fence_after();
+                pv(x, 1, st, tmem, true, leader, [&]() {
                     if (x == 0 && more) k_in = ready(bar.k_full[st1], par1);
                 });
                 if (x == NT - 1) tc_commit(smem_u32(&bar.v_free[st]), leader);
@@ -584,10 +600,10 @@ struct Prefix {
                     tc_fence_after();
                     qk(x, st1, tmem, leader, [&]() {
                         if (x + 1 < NT) {
-                            p_in[x + 1] = ready(bar.p_full[x + 1], (uint32_t)st);
+                            p_in[x + 1] = ready(first_p(x + 1), (uint32_t)st);
                         } else {
                             next_v = ready(bar.v_full[st1], par1);
-                            next_p = NT > 1 && ready(bar.p_full[0], (uint32_t)st1);
+                            next_p = NT > 1 && ready(first_p(0), (uint32_t)st1);
                         }
                     });
                     tc_commit(smem_u32(&bar.s_full[x]), leader);
@@ -641,10 +657,16 @@ struct Prefix {
             for (int t = 0; t < count; ++t, ++n) {
                 if (!wait_warp(bar.s_full[x], (uint32_t)n & 1u)) return;
                 tc_fence_after();
-                if (busy) step(s_at, o_at, scale, t > 0, n % kMaskSlots, m, l);
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(smem_u32(&bar.p_full[x]));
+                auto done = [&](uint64_t &b) {
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(smem_u32(&b));
+                };
+                if (busy)
+                    step(s_at, o_at, scale, t > 0, n % kMaskSlots, m, l, [&]() { done(bar.p_half[x]); });
+                else if (L::kHalves)
+                    done(bar.p_half[x]);
+                done(bar.p_full[x]);
             }
             if (!wait_warp(bar.o_full[x], seg & 1u)) return;
             tc_fence_after();
@@ -781,8 +803,9 @@ struct Prefix {
     // with the tile's values is the weight times the value; m bounds score + e, lazily.
     // fp16 holds such weights (at most 2^15) eight times finer than bf16, and what falls
     // below 2^-21 of the largest to 2^-32 of it.
+    template <typename Half>
     __device__ __forceinline__ void step(uint32_t s_at, uint32_t o_at, float scale, bool have_o, int slot,
-                                         float &m, float &l) const {
+                                         float &m, float &l, Half &&half) const {
         const bool whole = bar.valid[slot].x == 0x10101010u && bar.valid[slot].y == 0x10101010u;
         float s[4][32];
 #pragma unroll
@@ -828,6 +851,10 @@ struct Prefix {
                 const float part = sum[i].x + sum[i].y;
                 l = MODE == 1 ? l + part : fmaf(part, bar.v_inv[slot][2 * q + i], l);
             }
+            if (L::kHalves && q == 1) {
+                tc_wait_st();
+                half();
+            }
         }
         tc_wait_st();
     }
@@ -858,6 +885,7 @@ __global__ void __launch_bounds__(Layout<D, NT>::kThreads, 1) prefix_kernel(cons
             }
             for (int i = 0; i < 2; ++i) {
                 mbar_init(smem_u32(&bar.q_full[i]), 4);
+                mbar_init(smem_u32(&bar.p_half[i]), 4);
                 mbar_init(smem_u32(&bar.p_full[i]), 4);
                 mbar_init(smem_u32(&bar.s_full[i]), 1);
                 mbar_init(smem_u32(&bar.o_full[i]), 1);

@@ -36,6 +36,11 @@
 // positions x 23 sequences 36.9 -> 26.7 -> 26.3 us; 8192 x 64 62.0 -> 58.8 -> 47.2 (96 CTAs
 // of 152 SMs); 32768 x 256 198.4 -> 193.9 -> 170.6 (96).
 //
+// What bounds a step (two tiles, D = 128): 2048 cycles of tensor cores, and on the pipe of
+// shared memory 1540 cycles of operand reads, 680 of dequantised tiles stored and 560 of other
+// accesses; it takes about 3900.  32768 positions x 1024 rows x 8 kv heads, 137 GFLOP: 120 us
+// on all SMs, 166 on 96.
+//
 // Every wait has a limit, after which the kernel reports KVC8_DEV_TIMEOUT and leaves.
 #include "kvc8_codes.cuh"
 #include "kvc8_internal.cuh"

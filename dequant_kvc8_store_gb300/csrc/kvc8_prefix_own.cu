@@ -17,6 +17,9 @@
 // factor multiply the score, its value scale the weight, four products each a sub-tile;
 // per-channel scales are in the fp16 query and in the output.  The running maximum moves
 // only when the weights grow by more than 2^8, so most sub-tiles reduce and rescale nothing.
+// Measured (2048 items of 1 to 1024 positions, 300 MB): 70 us alone, 4.3 TB/s, issue 36%, the
+// warps waiting for loads 40% of the time.  Splits of 256, 512 or 1024 positions (217, 202
+// and 199 us for the call that took 199 with 2048), a cp.async ring and L2 prefetch did not help.
 #include "kvc8_codes.cuh"
 #include "kvc8_internal.cuh"
 

@@ -29,6 +29,12 @@
 // between y r (1 - 2^-21) and y r (1 + 2^-21).  Where both ends round to the same integer,
 // so does the quotient; else (a value within 2^-20 of a half-integer, mostly an exact tie of
 // a value row, 2 in 10^4) the lane divides.
+//
+// Measured (GB300, 32 query and 8 kv heads of 128): rows alone, 410 MB in 65 us (0.93 of the
+// copy rate); into bf16 pages, 480 MB in 77 us; into int8 pages with dynamic scales, 827 MB in
+// 146 us; with static channel scales (24 query heads), 186 MB in 39 us, where a reciprocal and
+// a limit for each channel take the issue slots.  HBM bounds the first three; five CTAs of
+// four warps per SM (96 registers) were faster than four or six.
 #include "kvc8_internal.cuh"
 
 namespace kvc8 {

@@ -269,7 +269,7 @@ __device__ __forceinline__ PrefixWork prefix_work(const PrefixArgs &p, int32_t g
 
 // ---- the kernel ---------------------------------------------------------------------
 
-template <int D, int NT>
+template <int MODE, int D, int NT>
 struct Layout {
     static constexpr int kDequantWarps = NT == 1 ? 8 : 4;
     static constexpr int kSoftmaxWarps = 4 * NT;
@@ -279,8 +279,12 @@ struct Layout {
     // two tiles one's products run beside the other's softmax anyway (60000 positions in mode 0,
     // one tile: 66.0 us in halves, 69.2 whole; two tiles, 1024 rows x 32768: 172.3 and 171.0).
     static constexpr bool kHalves = NT == 1;
-    // registers per thread: a softmax thread holds a row's 128 scores
-    static constexpr int kSoftmaxRegs = 184, kDequantRegs = NT == 1 ? 112 : 104, kMmaRegs = 40;
+    // Registers per thread: a softmax thread holds a row's 128 scores; a dequantising one two
+    // tiles' codes in flight, and with scales per row or block those too.  (Two tiles, 32768
+    // positions x 1024 rows: dynamic scales 221 us with 176 and 120, 235 with 184 and 104; channel
+    // scales 172.4 and 171.8.)
+    static constexpr bool kScales = MODE != 1 && NT == 2;
+    static constexpr int kSoftmaxRegs = kScales ? 176 : 184, kDequantRegs = NT == 1 ? 112 : kScales ? 120 : 104, kMmaRegs = 40;
     static constexpr int kLaunchRegs = 128;
     static_assert(32 * (kSoftmaxWarps * kSoftmaxRegs + kDequantWarps * kDequantRegs + 4 * kMmaRegs) <=
                       kThreads * kLaunchRegs,
@@ -312,7 +316,7 @@ struct Barriers {
 
 template <int MODE, int D, int NT>
 struct Prefix {
-    using L = Layout<D, NT>;
+    using L = Layout<MODE, D, NT>;
     const PrefixArgs &p;
     Barriers &bar;
     const uint32_t base;  // shared memory, 1 KB aligned
@@ -879,8 +883,8 @@ struct Prefix {
 };
 
 template <int MODE, int D, int NT>
-__global__ void __launch_bounds__(Layout<D, NT>::kThreads, 1) prefix_kernel(const PrefixArgs p) {
-    using L = Layout<D, NT>;
+__global__ void __launch_bounds__(Layout<MODE, D, NT>::kThreads, 1) prefix_kernel(const PrefixArgs p) {
+    using L = Layout<MODE, D, NT>;
     extern __shared__ uint8_t dyn[];
     __shared__ Barriers bar;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -1171,7 +1175,7 @@ int prefix_cuts(PrefixArgs &p, int64_t tiles, int64_t steps) {
 
 template <int MODE, int D, int NT>
 cudaError_t launch_variant(PrefixArgs p, cudaStream_t stream) {
-    using L = Layout<D, NT>;
+    using L = Layout<MODE, D, NT>;
     auto kern = prefix_kernel<MODE, D, NT>;
     static std::atomic<uint64_t> prepared{0};  // a bit per device
     int dev = 0;

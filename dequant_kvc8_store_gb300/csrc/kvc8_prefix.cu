@@ -34,7 +34,7 @@
 // gets depends on how many own positions there are: see best_cut.  Measured, own positions
 // first and one CTA per SM -> side by side, all SMs to the prefix -> the cut chosen: 10007
 // positions x 23 sequences 36.9 -> 26.7 -> 26.3 us; 8192 x 64 62.0 -> 58.8 -> 47.2 (96 CTAs
-// of 152 SMs); 32768 x 256 198.4 -> 193.9 -> 170.6 (96).
+// of 152 SMs; 45.1 since); 32768 x 256 198.4 -> 193.9 -> 170.6 (96).
 //
 // What bounds a step (two tiles, D = 128): 2048 cycles of tensor cores, and on the pipe of
 // shared memory 1540 cycles of operand reads, 680 of dequantised tiles stored and 560 of other
@@ -422,15 +422,16 @@ struct Prefix {
     // fp16 pairs (s / 2^e, s / 2^e) of a position's two scales, e the exponent of the largest
     // of its group of 16, so that 127 times it is far inside fp16 whatever the scales' size.
     // Sizes are compared as integers; in mode 2 a group has one scale.  (Two reductions by the
-    // whole warp instead of four exchanges: 32768 positions x 1024 rows, mode 0, 241.1 -> 233.7
-    // us; for the one group of the other layout the exchanges were faster, 66.0 and 67.4.)
+    // whole warp instead of four exchanges: 32768 positions x 1024 rows, mode 0, 241 -> 235
+    // us; for the one group of the other layout the exchanges were faster, 65.7 and 67.4.)
     __device__ __forceinline__ static uint32_t group_top(float s, int lane) {
         uint32_t size = __float_as_uint(s) & 0x7FFFFFFFu;
         if (MODE == 2) return size;
         if (kGroups == 1) {
+            float top = fabsf(s);
 #pragma unroll
-            for (int o = 1; o < 16; o <<= 1) size = max(size, __shfl_xor_sync(0xFFFFFFFFu, size, o));
-            return size;
+            for (int o = 1; o < 16; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+            return __float_as_uint(top);
         }
         const uint32_t a = __reduce_max_sync(0xFFFFFFFFu, lane < 16 ? size : 0u);
         const uint32_t b = __reduce_max_sync(0xFFFFFFFFu, lane < 16 ? 0u : size);

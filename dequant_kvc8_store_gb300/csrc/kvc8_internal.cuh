@@ -333,6 +333,7 @@ struct PrefixArgs {
     float own_weight;        // steps of an SM that 64 own positions (of all kv heads) take
     float own_least;         // the least that the own positions after the prefix take
     int32_t cuts;            // of those below
+    int32_t *chosen;         // which, where there are several
     PrefixCut cut[kPrefixCuts];  // what the kernels choose from, by the own positions' number
     int32_t own_splits;      // splits of own positions that a sequence has room for
     // Unnormalised partial outputs of the prefix, [slots * rows of a tile] rows of D floats:

@@ -234,12 +234,11 @@ __device__ __forceinline__ uint32_t own_part(const PrefixArgs &p) {
 
 // The cut with which prefix and own positions are done first, in steps' times.  The own
 // positions take `own` steps of an SM: on the SMs without a CTA while the prefix lasts,
-// then on all, and then not less than kOwnLeast.  (No operation that the compiler may fuse in
-// one kernel and not in the other: both have to find the same.)
-__device__ __forceinline__ PrefixCut best_cut(const PrefixArgs &p, uint32_t own_units) {
+// then on all, and then not less than kOwnLeast.  Every CTA finds the same; the first leaves it
+// in the workspace for the merge.
+__device__ __forceinline__ int best_cut(const PrefixArgs &p, uint32_t own_units) {
     const float own = __fmul_rn(__uint2float_rn(own_units), p.own_weight);
-    PrefixCut best = p.cut[0];
-    if (p.cuts == 1) return best;
+    int best = 0;
     float least = INFINITY;
 #pragma unroll 1
     for (int i = 0; i < p.cuts; ++i) {
@@ -247,15 +246,14 @@ __device__ __forceinline__ PrefixCut best_cut(const PrefixArgs &p, uint32_t own_
         const float t = __fadd_rn(p.cut[i].time, rest > 0.0f ? __fadd_rn(rest, p.own_least) : 0.0f);
         if (t < least) {
             least = t;
-            best = p.cut[i];
+            best = i;
         }
     }
     return best;
 }
 
-__device__ __forceinline__ PrefixWork prefix_work(const PrefixArgs &p, int32_t given, uint32_t own_units) {
+__device__ __forceinline__ PrefixWork prefix_work(const PrefixArgs &p, int32_t given, const PrefixCut &cut) {
     PrefixWork w;
-    const PrefixCut cut = best_cut(p, own_units);
     w.per_tile = cut.per_tile;
     const int64_t cap = (int64_t)p.max_prefix_blocks * p.own.g.block_size;
     w.len = (int32_t)max((int64_t)0, min((int64_t)given, cap));
@@ -897,7 +895,7 @@ __global__ void __launch_bounds__(Layout<MODE, D, NT>::kThreads, 1) prefix_kerne
     if (choose)
         own = own_part(p);
     else
-        w = prefix_work(p, given, 0);
+        w = prefix_work(p, given, p.cut[0]);
     if (warp == L::kMmaWarp) {
         if (lane == 0) {
             for (int i = 0; i < kStages; ++i) {
@@ -936,7 +934,9 @@ __global__ void __launch_bounds__(Layout<MODE, D, NT>::kThreads, 1) prefix_kerne
         own = 0;
 #pragma unroll
         for (int i = 0; i < L::kThreads / 32; ++i) own += bar.own[i];
-        w = prefix_work(p, given, own);
+        const int best = best_cut(p, own);
+        if (blockIdx.x == 0 && threadIdx.x == 0) *p.chosen = best;
+        w = prefix_work(p, given, p.cut[best]);
     }
     if (blockIdx.x == 0 && threadIdx.x == 0) {
         if (given < 0) report(p.own.dev_error, KVC8_DEV_BAD_LENGTH);
@@ -993,27 +993,22 @@ __global__ void __launch_bounds__(kMergeThreads, 4) merge_kernel(const PrefixArg
     const int row = min(at, B * H * G - 1);
     const int b = row / (H * G), hj = row - b * (H * G), h = hj / G, j = hj - h * G;
     const int32_t given = __ldg(p.prefix_length);
-    __shared__ uint32_t s_own[kMergeThreads / 32];
-    uint32_t own_total = 0;
-    if (p.cuts > 1) {
-        const uint32_t part = __reduce_add_sync(0xFFFFFFFFu, own_part(p));
-        if (lane == 0) s_own[threadIdx.x >> 5] = part;
-        __syncthreads();
-#pragma unroll
-        for (int i = 0; i < kMergeThreads / 32; ++i) own_total += s_own[i];
-    }
-    const PrefixWork w = prefix_work(p, given, own_total);
     const int r = b * G + j, tile = h * p.tiles_per_head + r / rows_per_tile;
     int parts = 0;
     int64_t slot = 0;  // row of the first segment's partial; segments are a tile's rows apart
-    if (w.steps > 0) {
-        const uint32_t first = w.per_tile > 0 ? 0u : (uint32_t)(tile * w.steps);
-        const int before = tile * w.per_tile;
-        const int c0 = before + (int)w.cta_of(first), c1 = before + (int)w.cta_of(first + w.steps - 1);
-        parts = c1 - c0 + 1;
-        slot = ((int64_t)tile + c0) * rows_per_tile + r % rows_per_tile;
-    }
+    auto locate = [&](const PrefixCut &cut) {
+        const PrefixWork w = prefix_work(p, given, cut);
+        if (w.steps > 0) {
+            const uint32_t first = w.per_tile > 0 ? 0u : (uint32_t)(tile * w.steps);
+            const int before = tile * w.per_tile;
+            const int c0 = before + (int)w.cta_of(first), c1 = before + (int)w.cta_of(first + w.steps - 1);
+            parts = c1 - c0 + 1;
+            slot = ((int64_t)tile + c0) * rows_per_tile + r % rows_per_tile;
+        }
+    };
+    if (p.cuts == 1) locate(p.cut[0]);
     pdl_wait_prior_grid();
+    const int best = p.cuts > 1 ? *p.chosen : 0;  // used after the own positions' partials
     float M = -INFINITY, L = 0.0f, acc[8];  // L: this lane's share
 #pragma unroll
     for (int e = 0; e < 8; ++e) acc[e] = 0.0f;
@@ -1065,9 +1060,10 @@ __global__ void __launch_bounds__(kMergeThreads, 4) merge_kernel(const PrefixArg
     };
     const int64_t len = min((int64_t)ld_nc_s32(a.context_lengths + b), (int64_t)a.g.max_blocks_per_seq * a.g.block_size);
     const int own = len > 0 ? (int)((len + kAttnChunk - 1) / kAttnChunk) : 0;  // splits of its own positions
-    join(p.part_m + slot, p.part_l + slot, p.part_o + slot / 32 * 32 * D + gl * 256 + slot % 32 * 8, rows_per_tile, parts);
     const int64_t own0 = ((int64_t)b * p.own_splits * H + h) * G + j;
     join(a.part_m + own0, a.part_l + own0, a.part_o + own0 * D + gl * 8, (int64_t)H * G, own);
+    if (p.cuts > 1) locate(p.cut[best]);
+    join(p.part_m + slot, p.part_l + slot, p.part_o + slot / 32 * 32 * D + gl * 256 + slot % 32 * 8, rows_per_tile, parts);
     if (share > 1) {  // the same in every warp
         s_top[threadIdx.x] = M;
         s_sum[threadIdx.x] = L;
@@ -1113,7 +1109,7 @@ __global__ void __launch_bounds__(kMergeThreads, 4) merge_kernel(const PrefixArg
 int tiles_per_cta(int64_t rows) { return rows > kRows ? 2 : 1; }
 
 struct Space {
-    size_t own, o, m, bytes;  // own partials first, then the prefix's O, m and l
+    size_t own, o, m, chosen, bytes;  // own partials first, then the prefix's O, m and l
 };
 
 Space space(const kvc8_geom &g, int group) {
@@ -1124,7 +1120,8 @@ Space space(const kvc8_geom &g, int group) {
     s.own = own_workspace_bytes(g, group);
     s.o = s.own;
     s.m = s.o + align_up(slots * g.head_dim * sizeof(float), kAlign);
-    s.bytes = s.m + 2 * align_up(slots * sizeof(float), kAlign);
+    s.chosen = s.m + 2 * align_up(slots * sizeof(float), kAlign);
+    s.bytes = s.chosen + kAlign;
     return s;
 }
 
@@ -1234,7 +1231,8 @@ cudaError_t launch_shared_prefix(PrefixArgs p, void *workspace, cudaStream_t str
     char *ws = static_cast<char *>(workspace);
     p.part_o = reinterpret_cast<float *>(ws + s.o);
     p.part_m = reinterpret_cast<float *>(ws + s.m);
-    p.part_l = reinterpret_cast<float *>(ws + s.m + (s.bytes - s.m) / 2);
+    p.part_l = reinterpret_cast<float *>(ws + s.m + (s.chosen - s.m) / 2);
+    p.chosen = reinterpret_cast<int32_t *>(ws + s.chosen);
     place_own(p, workspace);
     if (p.own.g.quant_mode == 0) return launch_mode<0>(p, stream);
     if (p.own.g.quant_mode == 1) return launch_mode<1>(p, stream);

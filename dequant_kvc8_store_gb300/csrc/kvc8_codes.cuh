@@ -28,7 +28,8 @@ __device__ __forceinline__ uint32_t mul_fp16(uint32_t a, uint32_t b) {
     asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
     return r;
 }
-// The power of two at or below x > 0, kept where it and its reciprocal are normal.
+// The power of two at or below x > 0, from 2^-100 to 2^100, where it and its reciprocal are
+// normal (divided by it, a value of 2^116 or more passes the range of fp16).
 __device__ __forceinline__ int power_of(float x) {
     return min(100, max(-100, (int)(__float_as_uint(x) >> 23) - 127));
 }

@@ -57,7 +57,10 @@ constexpr int kMaxCtas = 152;   // SMs of a GB300
 // m moves when a score passes it by kLift + kLazy more: the fp16 weights use fp16's range
 // up to 2^15, and one of 2^-21 of the row's largest still has all its eleven bits.
 constexpr float kLazy = 8.0f, kLift = 7.0f;
-constexpr int kLeastValuePower = -60;  // so that the sum of such weights times 2^-e is finite
+// The least exponent taken out of value scales, so that the sum of such weights (up to 2^15)
+// times 2^-e over 2^31 positions is finite.  Scales below 2^-74 then lie under fp16's normal
+// range: they and their products with a code are off by 2^-85 each, a value by 2^-78.
+constexpr int kLeastValuePower = -60;
 constexpr long long kWaitCycles = 4000000000ll;  // about two seconds
 constexpr int kMergeThreads = 256;
 // What else costs time, in steps, about: a CTA's start and end, its change of tile, the own

@@ -536,9 +536,16 @@ size_t kvc8_shared_prefix_workspace_bytes(const kvc8_geom *g, int32_t num_q_head
  * are fp32, the output is rounded to bf16.  fp16 keeps its eleven bits over a range:
  * of the scales in 16 prefix positions those above 2^-14 of the largest, of a query's
  * values those above 2^-14 of its largest, of the weights those above 2^-21 of a
- * row's largest; smaller ones keep 2^-25, 2^-25 and 2^-32 of that largest.  A query with no position at all gives
- * zeros.  P, the lengths and the tables are read on the device, so a captured graph
- * may be replayed with other values.  Three launches, no host synchronisation.
+ * row's largest; smaller ones keep 2^-25, 2^-25 and 2^-32 of that largest.  The powers
+ * of two that bring the largest into that range are limited too.  With scales per row
+ * or block, value scales hold from 2^-74 to 2^60 (below, a prefix position's value is
+ * off by 2^-78 at most) and key scales from 2^-114 to 2^100; a query's largest value (with
+ * scales per channel, its largest product with the key's) from 2^-100 to 2^100.
+ * softmax_scale times such a key scale and such a largest value is below 2^127.
+ *
+ * A query with no position at all gives zeros.  P, the lengths and the tables are read on
+ * the device, so a captured graph may be replayed with other values.  Three launches, no
+ * host synchronisation.
  *
  *   prefix_table      int32 [max_prefix_blocks], physical blocks of the prefix
  *   max_prefix_blocks >= 1; P is at most max_prefix_blocks * block_size

@@ -128,8 +128,9 @@ class Problem:
         ones = q.abs().amax(-1, keepdim=True).expand_as(q)
         return z, live, size, dots(ones, kp.abs(), ko.abs()) * abs(self.scale)
 
-    def answers(self):
-        """want, tol [B][Hq][D], and the wrong answers {name: (out, applies [B][H])}."""
+    def answers(self, least=0.0):
+        """want, tol [B][Hq][D], and the wrong answers {name: (out, applies [B][H])}.  least: an
+        absolute error of each value."""
         B, H, G, D, P = len(self.lens), self.H, self.G, self.D, self.prefix
         want, tol, pre, own = (torch.zeros(B, H * G, D, dtype=torch.float64, device=self.device) for _ in range(4))
         most = max(self.lens, default=0)
@@ -158,7 +159,7 @@ class Problem:
             off = torch.expm1(delta)
             sums = (n + 64) / 8 * F32
             N = mix(w * ((1 + off) * (1 + wr) - 1 + sums), vp.abs(), vo.abs())
-            N = N + n * 2.0 ** -31 * max([float(v.abs().max()) for v in (vp, vo) if v.numel()], default=0.0)
+            N = N + n * 2.0 ** -31 * max([float(v.abs().max()) for v in (vp, vo) if v.numel()], default=0.0) + least
             E = (w * (off + sums)).sum(-1, keepdim=True)
             assert E.numel() == 0 or float(E.max()) < 0.2
             err = (N + want[:, j].abs() * E) / (1 - E)

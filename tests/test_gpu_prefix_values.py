@@ -109,3 +109,36 @@ def test_a_replayed_graph_follows_its_lengths(mode):
         assert bool(((x.out.double() - want).abs() <= tol).all()), prefix
         # (the weights were balanced for the first lengths: not every mistake shows at the others)
         x.tells(want, tol, {k: wrong[k] for k in ("zeros", "the next head's")})
+
+
+LIMITS = [  # modes, and powers of two on value scales, key scales and queries
+    ((0, 2), -66, 0, 0), ((0, 2), 65, 0, 0), ((0, 2), 0, -106, 0), ((0, 2), 0, 105, 0), ((0, 1, 2), 0, 0, -103),
+    ((0, 1, 2), 0, 0, 96), ((0, 2), -66, -50, -53), ((1,), -66, -90, 0), ((1,), 65, 90, 0)]
+
+
+@pytest.mark.parametrize("mode,values,keys,query",
+                         [(m, v, k, q) for modes, v, k, q in LIMITS for m in modes])
+def test_scales_and_queries_at_the_ends_of_their_range(mode, values, keys, query):
+    """Value scales from 2^-74 to 2^60, key scales from 2^-114 to 2^100, queries from 2^-100 to
+    2^100 (the softmax's scale takes the powers of the last two back)."""
+    x = Problem(300, [40, 0, 130], H=2, G=4, D=128, bs=32, mode=mode, seed=9)
+    x.vs *= 2.0 ** values
+    x.ks *= 2.0 ** keys
+    x.q = (x.q.float() * 2.0 ** query).to(torch.bfloat16)
+    x.scale *= 2.0 ** -(keys + query)
+    _run(x)
+
+
+@pytest.mark.parametrize("mode", [0, 2])
+@pytest.mark.parametrize("values", [-70, -76, -84, -100])
+def test_value_scales_below_their_range(mode, values):
+    """A prefix's value is then off by 2^-78 at most, its own positions' as above."""
+    x = Problem(300, [40, 0, 130], H=2, G=4, D=128, bs=32, mode=mode, seed=10)
+    x.vs *= 2.0 ** values
+    x.run()
+    assert x.error() == 0
+    want, tol, _ = x.answers(least=2.0 ** -78)
+    assert bool(((x.out.double() - want).abs() <= tol).all())
+    x.prefix, x.out = 0, torch.full_like(x.out, float("nan"))
+    x.d["plen"].fill_(0)
+    _run(x)

@@ -776,7 +776,7 @@ static kvc8_status check_prefix_geom(const kvc8_geom *g, int32_t num_q_heads,
 size_t kvc8_shared_prefix_workspace_bytes(const kvc8_geom *g, int32_t num_q_heads,
                                           int32_t max_prefix_blocks) {
     if (check_prefix_geom(g, num_q_heads, max_prefix_blocks) != KVC8_OK) return 0;
-    return shared_prefix_workspace_bytes(*g, num_q_heads / g->kv_heads, max_prefix_blocks);
+    return shared_prefix_workspace_bytes(*g, num_q_heads / g->kv_heads);
 }
 
 kvc8_status kvc8_shared_prefix_attention(const kvc8_geom *g, int32_t num_q_heads,
@@ -809,7 +809,7 @@ kvc8_status kvc8_shared_prefix_attention(const kvc8_geom *g, int32_t num_q_heads
         return KVC8_ERR_INVALID_ARG;
     const int group = num_q_heads / g->kv_heads;
     if (workspace == nullptr || !aligned(workspace, kAlign) ||
-        workspace_bytes < shared_prefix_workspace_bytes(*g, group, max_prefix_blocks))
+        workspace_bytes < shared_prefix_workspace_bytes(*g, group))
         return KVC8_ERR_WORKSPACE;
     PrefixArgs p = {};
     AttnArgs &a = p.own;

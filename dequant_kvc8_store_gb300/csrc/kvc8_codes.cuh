@@ -1,5 +1,5 @@
 // kvc8_codes.cuh -- int8 codes as exact 16-bit floating-point pairs, and the small
-// arithmetic that the shared-prefix attention's kernels have in common.
+// arithmetic that the shared-prefix attention's kernels (and the rotation's) have in common.
 #pragma once
 
 #include <cstdint>
@@ -48,9 +48,8 @@ __device__ __forceinline__ uint32_t fp16_of(uint32_t x) {
     asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(0x64806480u));
     return r;
 }
-// Two neighbouring codes of a word (select 0x4140: the first two, 0x4342: the others);
-// fp16 takes the word with every sign bit flipped.
-__device__ __forceinline__ uint32_t codes_bf16(uint32_t w, uint32_t select) { return bf16_of(__byte_perm(w, 0u, select)); }
+// Two neighbouring codes of a word with every sign bit flipped (select 0x4140: the first two,
+// 0x4342: the others).
 __device__ __forceinline__ uint32_t codes_fp16(uint32_t biased, uint32_t select) {
     return fp16_of(__byte_perm(biased, 0x64646464u, select));
 }

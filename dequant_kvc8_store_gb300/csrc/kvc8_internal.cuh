@@ -348,7 +348,7 @@ struct PrefixArgs {
 size_t own_workspace_bytes(const kvc8_geom &g, int group);
 void place_own(PrefixArgs &p, void *workspace);  // p.own's partials, p.own_splits
 cudaError_t launch_own(const PrefixArgs &p, cudaStream_t stream);
-size_t shared_prefix_workspace_bytes(const kvc8_geom &g, int group, int32_t max_prefix_blocks);
+size_t shared_prefix_workspace_bytes(const kvc8_geom &g, int group);
 cudaError_t launch_shared_prefix(PrefixArgs a, void *workspace, cudaStream_t stream);
 cudaError_t launch_rope(const RopeArgs &a, RopeSink sink, cudaStream_t stream);
 

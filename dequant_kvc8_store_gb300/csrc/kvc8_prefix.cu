@@ -1196,7 +1196,7 @@ cudaError_t launch_variant(PrefixArgs p, cudaStream_t stream) {
     p.rows = p.own.g.num_seqs * p.own.group;
     p.tiles_per_head = (p.rows + NT * kRows - 1) / (NT * kRows);
     const int64_t steps = ((int64_t)p.max_prefix_blocks * p.own.g.block_size + kCols - 1) / kCols;
-    const int64_t tiles = (int64_t)p.tiles_per_head * p.own.g.kv_heads, units = tiles * steps;
+    const int64_t tiles = (int64_t)p.tiles_per_head * p.own.g.kv_heads;
     p.sms = sm_count() < kMaxCtas ? sm_count() : kMaxCtas;
     // own positions of a kv head that an SM passes in a step's time
     constexpr float kOwnPerStep = NT == 1 ? 130.0f : 220.0f;
@@ -1227,7 +1227,7 @@ cudaError_t launch_mode(const PrefixArgs &p, cudaStream_t stream) {
 
 }  // namespace
 
-size_t shared_prefix_workspace_bytes(const kvc8_geom &g, int group, int32_t) { return space(g, group).bytes; }
+size_t shared_prefix_workspace_bytes(const kvc8_geom &g, int group) { return space(g, group).bytes; }
 
 cudaError_t launch_shared_prefix(PrefixArgs p, void *workspace, cudaStream_t stream) {
     const Space s = space(p.own.g, p.own.group);

@@ -35,6 +35,7 @@
 // 146 us; with static channel scales (24 query heads), 186 MB in 39 us, where a reciprocal and
 // a limit for each channel take the issue slots.  HBM bounds the first three; five CTAs of
 // four warps per SM (96 registers) were faster than four or six.
+#include "kvc8_codes.cuh"
 #include "kvc8_internal.cuh"
 
 namespace kvc8 {
@@ -46,12 +47,6 @@ constexpr int kMaxPairs = 128;
 
 __device__ __forceinline__ float bf16_lo(uint32_t x) { return __uint_as_float(x << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t x) { return __uint_as_float(x & 0xFFFF0000u); }
-
-__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
-    uint32_t r;
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-    return r;
-}
 
 // Where a token goes.
 struct Slot {

@@ -31,10 +31,13 @@
 // a value row, 2 in 10^4) the lane divides.
 //
 // Measured (GB300, 32 query and 8 kv heads of 128): rows alone, 410 MB in 65 us (0.93 of the
-// copy rate); into bf16 pages, 480 MB in 77 us; into int8 pages with dynamic scales, 827 MB in
-// 146 us; with static channel scales (24 query heads), 186 MB in 39 us, where a reciprocal and
-// a limit for each channel take the issue slots.  HBM bounds the first three; five CTAs of
-// four warps per SM (96 registers) were faster than four or six.
+// copy rate); into bf16 pages, 480 MB in 77 us; into int8 pages, 829 MB with dynamic scales in
+// 147 us (0.83), 827 MB with block scales in 144 (0.84) and with channel scales in 179 (0.68).
+// HBM bounds all but the last, which computes a reciprocal and a limit for every channel of
+// every row: with 24 query heads, 161 MB in 39 us (0.61), issue slots 49% and DRAM 39% busy,
+// so what its 20 warps per SM wait for bounds it.  256 tokens (64 query heads, 10 MB): 9.8 us,
+// a launch's latency.  Five CTAs of four warps per SM (96 registers) were faster than
+// four or six.
 #include "kvc8_codes.cuh"
 #include "kvc8_internal.cuh"
 

@@ -283,7 +283,9 @@ struct Layout {
     // Registers per thread: a softmax thread holds a row's 128 scores; a dequantising one two
     // tiles' codes in flight, and with scales per row or block those too.  (Two tiles, 32768
     // positions x 1024 rows: dynamic scales 221 us with 176 and 120, 235 with 184 and 104; channel
-    // scales 172.4 and 171.8.)
+    // scales 172.4 and 171.8.)  Spilled all the same (bytes a thread stored / loaded): two tiles
+    // 20 / 36, in mode 1 32 / 44 at D = 128 and none at 64; one tile none, but 24 / 68 in mode 1
+    // at D = 64.
     static constexpr bool kScales = MODE != 1 && NT == 2;
     static constexpr int kSoftmaxRegs = kScales ? 176 : 184, kDequantRegs = NT == 1 ? 112 : kScales ? 120 : 104, kMmaRegs = 40;
     static constexpr int kLaunchRegs = 128;

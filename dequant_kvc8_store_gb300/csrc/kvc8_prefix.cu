@@ -235,8 +235,8 @@ __device__ __forceinline__ uint32_t own_part(const PrefixArgs &p) {
     return n;
 }
 
-// The cut with which prefix and own positions are done first, in steps' times.  The own
-// positions take `own` steps of an SM: on the SMs without a CTA while the prefix lasts,
+// The cut with which prefix and own positions are done first, in steps' times, for a prefix that
+// fills its table (see prefix_cuts).  The own positions take `own` steps of an SM: on the SMs without a CTA while the prefix lasts,
 // then on all, and then not less than kOwnLeast.  Every CTA finds the same; the first leaves it
 // in the workspace for the merge.
 __device__ __forceinline__ int best_cut(const PrefixArgs &p, uint32_t own_units) {
@@ -1132,7 +1132,12 @@ Space space(const kvc8_geom &g, int group) {
 
 // The cuts to choose from: CTAs that stay within a tile, as many as there is room for and
 // down to about half as many, and CTAs that share all work.  None has more CTAs than its
-// longest share needs.  Returns the most CTAs of one.
+// longest share needs.  Returns the most CTAs of one.  The host knows the tables' room and not
+// the lengths in them, so a cut's cost is that of a prefix which fills its table.  Behind a
+// shorter one own positions seem to fit beside it more often than they do, and the prefix gets
+// more SMs than is best (same lengths, table exact -> twice -> eight times as long: 8192 positions x 64
+// sequences 45.3 -> 51.7 -> 56.3 us, 10007 x 23 24.9 -> 26.8 -> 35.1, 32768 x 256 172 -> 182 ->
+// 189); likewise with cuts == 1, from the room for own positions.  Results do not depend on it.
 int prefix_cuts(PrefixArgs &p, int64_t tiles, int64_t steps) {
     const int64_t units = tiles * steps, sms = p.sms;
     auto up = [](int64_t a, int64_t b) { return (a + b - 1) / b; };

@@ -15,9 +15,11 @@
 // a time.  S = Q K'^T and O += P V' are tcgen05.mma (M = 128, fp16, fp32 in tensor
 // memory); P replaces S in tensor memory and is the second product's A operand.
 // Warps by role:
-//   softmax     4 per tile, one thread per query row: S from tensor memory, online
-//               softmax, P back; the running maximum moves only when the weights
-//               grow by more than 2^8, so O is seldom rescaled
+//   softmax     4 per tile, one thread per query row: S from tensor memory, one-pass
+//               softmax (Milakov and Gimelshein, Online normalizer calculation for
+//               softmax, 2018), P back; any m cancels in the quotient, so the running
+//               maximum moves only when the weights grow by more than 2^8, and O is
+//               seldom rescaled
 //   dequantise  codes from global memory a tile ahead in registers, K' and V' as fp16
 //               into a two-stage ring in the 128-byte swizzle (K' K-major, V' as the
 //               MN-major B operand of the same rows)

@@ -15,8 +15,15 @@
 // subtraction a pair (bf16, for values that a row's scale follows, takes two logic
 // operations more).  The scales follow in fp32: a position's key scale and the head's
 // factor multiply the score, its value scale the weight, four products each a sub-tile;
-// per-channel scales are in the fp16 query and in the output.  The running maximum moves
-// only when the weights grow by more than 2^8, so most sub-tiles reduce and rescale nothing.
+// per-channel scales are in the fp16 query and in the output.  A weight alone fits fp16 (see
+// kLift), but its product with a row's or block's value scale has the scale's range, so it is
+// rounded to bf16, eight bits where fp16 has eleven: the output is off by 0.0020 of its norm
+// then, with per-channel scales by 0.0017, which is the output's own rounding to bf16.
+// (The prefix's rows have that range taken out sixteen at a time, in shared memory.)
+// Any m gives the same quotient of the sums of 2^(score - m) V and 2^(score - m) as long as
+// neither over- nor underflows, so the running maximum (Milakov and Gimelshein, Online
+// normalizer calculation for softmax, 2018) need not follow every larger score: it moves
+// only when the weights grow by more than 2^8, and most sub-tiles reduce and rescale nothing.
 // Measured (2048 items of 1 to 1024 positions, 300 MB): 70 us alone, 4.3 TB/s, issue 36%, the
 // warps waiting for loads 40% of the time.  Splits of 256, 512 or 1024 positions (217, 202
 // and 199 us for the call that took 199 with 2048), a cp.async ring and L2 prefetch did not help.

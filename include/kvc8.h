@@ -408,7 +408,9 @@ kvc8_status kvc8_gather_bf16(const kvc8_geom *g, const void *key_cache,
  *   y_d = x_d / sqrt(mean_d(x_d^2) + eps) * w_d      over all D channels.
  * Everything is computed in fp32 from the bf16 inputs and rounded once, to bf16
  * or to the page's codes.  The products may be fused, so the last bit of an
- * fp32 intermediate is not specified.
+ * fp32 intermediate is not specified.  Squares and their mean are fp32 as well: a row
+ * that is normed has values of size 2^58 at most, and mean(x^2) + eps of 2^-110 at least
+ * (so a row of zeros needs an eps).
  *
  * The frequencies f_i are kept as fractions of a turn: freqs[i] =
  * round(f_i / (2 pi) * 2^64).  The phase pos * freqs[i] is then an integer

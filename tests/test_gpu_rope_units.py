@@ -9,7 +9,7 @@ import oracle
 import dequant_kvc8_store_gb300 as kv
 from dequant_kvc8_store_gb300 import workloads as W
 from dequant_kvc8_store_gb300.device import Bf16Batch, DeviceBatch, bf16_bits
-from _rope_ref import BF16, U, bf16_f64, bf16_tensor
+from _rope_ref import BF16, U, bf16_f64, bf16_tensor, norm_rotate, to_bf16_bits
 from test_gpu_rope import Turn, _append, _check_rows, _rows, _tokens
 
 pytestmark = pytest.mark.gpu
@@ -152,3 +152,23 @@ def test_rows_of_more_tokens_than_a_warp_looks_up_at_once():
     kv.kvc8_qk_norm_rope(turn.rope, n, 32, 1, q, 32, 32, q, 32, 32, 1, k, 32, 32, k, 32, 32)
     _check_rows(bf16_bits(q), turn, "q", qb, pos)
     _check_rows(bf16_bits(k), turn, "k", kb, pos)
+
+
+@pytest.mark.parametrize("power,eps", [(56, 1e-6), (56, 0.0), (-51, 0.0), (-20, 1e-6), (-100, 2.0 ** -110)])
+@pytest.mark.parametrize("D", [16, 128, 256])
+def test_norm_at_the_ends_of_its_range(D, power, eps):
+    """Rows of values up to 2^58, and down to a mean of squares plus eps of 2^-110."""
+    rng = np.random.default_rng([130, D])
+    x = np.clip(rng.standard_normal((40, 3, D)), -4.0, 4.0)
+    x[:, :, 0] = 1.5  # a mean of squares of no less than 2.25 / D
+    bits = to_bf16_bits(x * 2.0 ** power)
+    turn = Turn(rng, D, 16, positions=np.arange(40))
+    turn.rope.struct.norm_eps = eps
+    q = bf16_tensor(bits).cuda()
+    out = torch.full_like(q, float("nan"))
+    kv.kvc8_qk_norm_rope(turn.rope, 40, D, 3, q, 3 * D, D, out, 3 * D, D, 0, None, 0, 0, None, 0, 0)
+    y, e = norm_rotate(bits, turn.wq, float(np.float32(eps)), np.arange(40), turn.freqs, 16, False, 1.0)
+    got = bf16_f64(bf16_bits(out))
+    # (squares below fp32's normal numbers: 2^-149 each of a mean of 2^-110, far below U)
+    bad = ~(np.abs(got - y) <= e + BF16 * (np.abs(y) + e) + 2.0 ** -133)
+    assert not bad.any(), (np.argwhere(bad)[:4], got[bad][:4], y[bad][:4])

@@ -28,6 +28,8 @@ DEV_POS_BEYOND_TABLE = 2
 DEV_OUT_ROW_RANGE = 3
 DEV_BAD_LENGTH = 4
 DEV_TIMEOUT = 5
+DEV_NO_FREE_BLOCK = 6
+DEV_BAD_INDEX = 7
 
 ROPE_PLAIN = 0
 ROPE_LINEAR = 1
@@ -152,6 +154,17 @@ def configure(lib: ctypes.CDLL) -> ctypes.CDLL:
     lib.kvc8_shared_prefix_attention.argtypes = [G, i32, P, i64, i64, P, P, P, P, P, i32, P, P, P,
                                                  ctypes.c_float, P, i64, i64, P, sz, P, P]
     lib.kvc8_shared_prefix_attention.restype = ctypes.c_int
+    lib.kvc8_assign_blocks.argtypes = [G, P, P, P, P, P, P, P, P, i64, P, P]
+    lib.kvc8_assign_blocks.restype = ctypes.c_int
+    lib.kvc8_tree_attention_workspace_bytes.argtypes = [G, i32, i64, i32]
+    lib.kvc8_tree_attention_workspace_bytes.restype = sz
+    lib.kvc8_tree_attention.argtypes = [G, i32, i64, i32, P, i64, i64, P, P, P, P, P, P, P, P, i32,
+                                        ctypes.c_float, P, i64, i64, P, sz, P, P]
+    lib.kvc8_tree_attention.restype = ctypes.c_int
+    lib.kvc8_compact_drafts.argtypes = [G, P, P, P, P, P, P, P, i32, P, P, P, P]
+    lib.kvc8_compact_drafts.restype = ctypes.c_int
+    lib.kvc8_compact_drafts_bf16.argtypes = [G, P, P, P, P, P, i32, P, P, P, P]
+    lib.kvc8_compact_drafts_bf16.restype = ctypes.c_int
     return lib
 
 
@@ -441,6 +454,60 @@ def kvc8_shared_prefix_attention(g: Geom, num_q_heads, query, q_seq_stride, q_he
         float(softmax_scale), _p(out), int(out_seq_stride), int(out_head_stride), _p(workspace),
         int(workspace_bytes), _p(dev_error), _stream(stream))
     _ok(st, "kvc8_shared_prefix_attention")
+
+
+ASSIGN_MAX_SEQS = 8192  # KVC8_ASSIGN_MAX_SEQS
+MAX_DRAFTS = 256  # KVC8_MAX_DRAFTS
+
+
+def kvc8_assign_blocks(g: Geom, held_lens, want_lens, free_blocks, free_count, free_count_out,
+                       block_table, lens_out, slot_map=None, slot_rows=0, dev_error=None,
+                       stream=None) -> None:
+    st = load().kvc8_assign_blocks(ctypes.byref(g), _p(held_lens), _p(want_lens), _p(free_blocks),
+                                   _p(free_count), _p(free_count_out), _p(block_table),
+                                   _p(lens_out), _p(slot_map), int(slot_rows), _p(dev_error),
+                                   _stream(stream))
+    _ok(st, "kvc8_assign_blocks")
+
+
+def kvc8_tree_attention_workspace_bytes(g: Geom, num_q_heads: int, num_tokens: int,
+                                        max_drafts: int) -> int:
+    return int(load().kvc8_tree_attention_workspace_bytes(ctypes.byref(g), int(num_q_heads),
+                                                          int(num_tokens), int(max_drafts)))
+
+
+def kvc8_tree_attention(g: Geom, num_q_heads, num_tokens, max_drafts, query, q_tok_stride,
+                        q_head_stride, key_cache, value_cache, key_scale, value_scale, block_table,
+                        cu_q_lens, context_kv_lens, tree_mask, mask_words, softmax_scale, out,
+                        out_tok_stride, out_head_stride, workspace, workspace_bytes,
+                        dev_error=None, stream=None) -> None:
+    st = load().kvc8_tree_attention(
+        ctypes.byref(g), int(num_q_heads), int(num_tokens), int(max_drafts), _p(query),
+        int(q_tok_stride), int(q_head_stride), _p(key_cache), _p(value_cache), _p(key_scale),
+        _p(value_scale), _p(block_table), _p(cu_q_lens), _p(context_kv_lens), _p(tree_mask),
+        int(mask_words), float(softmax_scale), _p(out), int(out_tok_stride), int(out_head_stride),
+        _p(workspace), int(workspace_bytes), _p(dev_error), _stream(stream))
+    _ok(st, "kvc8_tree_attention")
+
+
+def kvc8_compact_drafts(g: Geom, key_cache, value_cache, key_scale, value_scale, block_table,
+                        context_kv_lens, accepted, max_accepted, num_accepted, lens_out=None,
+                        dev_error=None, stream=None) -> None:
+    st = load().kvc8_compact_drafts(ctypes.byref(g), _p(key_cache), _p(value_cache), _p(key_scale),
+                                    _p(value_scale), _p(block_table), _p(context_kv_lens),
+                                    _p(accepted), int(max_accepted), _p(num_accepted),
+                                    _p(lens_out), _p(dev_error), _stream(stream))
+    _ok(st, "kvc8_compact_drafts")
+
+
+def kvc8_compact_drafts_bf16(g: Geom, key_cache, value_cache, block_table, context_kv_lens,
+                             accepted, max_accepted, num_accepted, lens_out=None, dev_error=None,
+                             stream=None) -> None:
+    st = load().kvc8_compact_drafts_bf16(ctypes.byref(g), _p(key_cache), _p(value_cache),
+                                         _p(block_table), _p(context_kv_lens), _p(accepted),
+                                         int(max_accepted), _p(num_accepted), _p(lens_out),
+                                         _p(dev_error), _stream(stream))
+    _ok(st, "kvc8_compact_drafts_bf16")
 
 
 def kvc8_get_error(dev_error, reset: bool = False, stream=None) -> int:

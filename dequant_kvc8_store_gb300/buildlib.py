@@ -22,7 +22,7 @@ OUT_DIR = os.path.join(PKG, "_build")
 LIB_PATH = os.path.join(OUT_DIR, "libkvc8.so")
 SOURCES = ["kvc8_api.cu", "kvc8_store.cu", "kvc8_gather.cu", "kvc8_noalloc.cu", "kvc8_bf16.cu",
            "kvc8_attention.cu", "kvc8_rope.cu", "kvc8_prefix.cu",
-           "kvc8_prefix_own.cu"]
+           "kvc8_prefix_own.cu", "kvc8_blocks.cu", "kvc8_tree.cu", "kvc8_compact.cu"]
 HEADERS = [os.path.join(CSRC, "kvc8_internal.cuh"), os.path.join(CSRC, "kvc8_codes.cuh"),
            os.path.join(INCLUDE, "kvc8.h")]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

@@ -1,6 +1,7 @@
 // kvc8_api.cu -- the extern "C" entry points of libkvc8 (declared in kvc8.h):
 // host-side argument checks, then the launches in kvc8_store.cu,
-// kvc8_gather.cu, kvc8_bf16.cu, kvc8_attention.cu, kvc8_rope.cu and kvc8_prefix.cu.  Nothing here allocates device memory or synchronises,
+// kvc8_gather.cu, kvc8_bf16.cu, kvc8_attention.cu, kvc8_rope.cu, kvc8_prefix.cu, kvc8_blocks.cu,
+// kvc8_tree.cu and kvc8_compact.cu.  Nothing here allocates device memory or synchronises,
 // except kvc8_get_error, whose purpose is to synchronise.
 #include <cmath>
 #include <cstdint>
@@ -92,7 +93,7 @@ const char *kvc8_status_str(kvc8_status s) {
     return "unknown status";
 }
 
-int32_t kvc8_version(void) { return 10100; }
+int32_t kvc8_version(void) { return 10200; }
 
 kvc8_status kvc8_store(const kvc8_geom *g, int64_t num_tokens, const void *key_states,
                        const void *value_states, int64_t x_tok_stride, int64_t x_head_stride,
@@ -833,6 +834,179 @@ kvc8_status kvc8_shared_prefix_attention(const kvc8_geom *g, int32_t num_q_heads
     p.max_prefix_blocks = max_prefix_blocks;
     p.prefix_length = prefix_length;
     return cuda_status(launch_shared_prefix(p, workspace, stream));
+}
+
+kvc8_status kvc8_assign_blocks(const kvc8_geom *g, const int32_t *held_lens,
+                               const int32_t *want_lens, int32_t *free_blocks,
+                               const int32_t *free_count, int32_t *free_count_out,
+                               int32_t *block_table, int32_t *lens_out, int64_t *slot_map,
+                               int64_t slot_rows, int32_t *dev_error, cudaStream_t stream) {
+    kvc8_status st = check_geom(g);
+    if (st != KVC8_OK) return st;
+    if (g->num_seqs > KVC8_ASSIGN_MAX_SEQS) return KVC8_ERR_UNSUPPORTED;
+    if (free_blocks == nullptr || free_count == nullptr || free_count_out == nullptr || slot_rows < 0)
+        return KVC8_ERR_INVALID_ARG;
+    if (g->num_seqs > 0 && (held_lens == nullptr || want_lens == nullptr || block_table == nullptr ||
+                            lens_out == nullptr))
+        return KVC8_ERR_INVALID_ARG;
+    if (!aligned(slot_map, 8)) return KVC8_ERR_INVALID_ARG;
+    AssignArgs a = {};
+    a.num_seqs = g->num_seqs;
+    a.block_size = g->block_size;
+    a.num_blocks = g->num_blocks;
+    a.max_blocks_per_seq = g->max_blocks_per_seq;
+    a.held = held_lens;
+    a.want = want_lens;
+    a.free_blocks = free_blocks;
+    a.free_count = free_count;
+    a.free_count_out = free_count_out;
+    a.block_table = block_table;
+    a.lens_out = lens_out;
+    a.slot_map = slot_map;
+    a.slot_rows = slot_map == nullptr ? 0 : slot_rows;
+    a.dev_error = dev_error;
+    return cuda_status(launch_assign(a, stream));
+}
+
+// What the tree attention supports: kvc8_paged_decode_attention's geometries, with
+// units of 128 query rows and 128 positions counted in 32 bits.
+static kvc8_status check_tree_geom(const kvc8_geom *g, int32_t num_q_heads, int64_t num_tokens,
+                                   int32_t max_drafts) {
+    kvc8_status st = check_geom(g);
+    if (st != KVC8_OK) return st;
+    if (num_q_heads < 1 || num_q_heads % g->kv_heads != 0 || num_tokens < 0 || max_drafts < 1)
+        return KVC8_ERR_INVALID_ARG;
+    const int group = num_q_heads / g->kv_heads;
+    if (group > 8 || (g->head_dim != 64 && g->head_dim != 128) || g->block_size % 16 != 0 ||
+        max_drafts > KVC8_MAX_DRAFTS || num_tokens > INT32_MAX)
+        return KVC8_ERR_UNSUPPORTED;
+    // positions are 32-bit, with room for the drafts and a step's overhang
+    const int64_t cap = (int64_t)g->max_blocks_per_seq * g->block_size;
+    if (cap > (int64_t)INT32_MAX - 4096) return KVC8_ERR_UNSUPPORTED;
+    const int64_t tiles = (int64_t)g->num_seqs * ((max_drafts * group + 127) / 128);  // < 2^36
+    const int64_t steps = (cap + 127) / 128;
+    if (tiles > (int64_t)INT32_MAX / steps / g->kv_heads) return KVC8_ERR_UNSUPPORTED;
+    return KVC8_OK;
+}
+
+size_t kvc8_tree_attention_workspace_bytes(const kvc8_geom *g, int32_t num_q_heads,
+                                           int64_t num_tokens, int32_t max_drafts) {
+    if (check_tree_geom(g, num_q_heads, num_tokens, max_drafts) != KVC8_OK) return 0;
+    return tree_workspace_bytes(*g);
+}
+
+kvc8_status kvc8_tree_attention(const kvc8_geom *g, int32_t num_q_heads, int64_t num_tokens,
+                                int32_t max_drafts, const void *query, int64_t q_tok_stride,
+                                int64_t q_head_stride, const int8_t *key_cache,
+                                const int8_t *value_cache, const float *key_scale,
+                                const float *value_scale, const int32_t *block_table,
+                                const int32_t *cu_q_lens, const int32_t *context_kv_lens,
+                                const uint64_t *tree_mask, int32_t mask_words,
+                                float softmax_scale, void *out, int64_t out_tok_stride,
+                                int64_t out_head_stride, void *workspace,
+                                size_t workspace_bytes, int32_t *dev_error,
+                                cudaStream_t stream) {
+    kvc8_status st = check_tree_geom(g, num_q_heads, num_tokens, max_drafts);
+    if (st != KVC8_OK) return st;
+    if (!std::isfinite(softmax_scale)) return KVC8_ERR_INVALID_ARG;
+    if (cu_q_lens == nullptr && num_tokens != g->num_seqs) return KVC8_ERR_INVALID_ARG;
+    if (tree_mask != nullptr && mask_words < (max_drafts + 63) / 64) return KVC8_ERR_INVALID_ARG;
+    if (num_tokens == 0 || g->num_seqs == 0) return num_tokens == 0 ? KVC8_OK : KVC8_ERR_INVALID_ARG;
+    if (query == nullptr || key_cache == nullptr || value_cache == nullptr ||
+        key_scale == nullptr || value_scale == nullptr || block_table == nullptr ||
+        context_kv_lens == nullptr || out == nullptr || out == query)
+        return KVC8_ERR_INVALID_ARG;
+    if (q_tok_stride < 0 || q_head_stride < 0 || q_tok_stride % 8 != 0 || q_head_stride % 8 != 0 ||
+        out_tok_stride < 0 || out_head_stride < 0)
+        return KVC8_ERR_INVALID_ARG;
+    if (!aligned(query, 16) || !aligned(key_cache, 16) || !aligned(value_cache, 16) ||
+        !aligned(key_scale, 16) || !aligned(value_scale, 16) || !aligned(out, 2) ||
+        !aligned(tree_mask, 8))
+        return KVC8_ERR_INVALID_ARG;
+    if (workspace == nullptr || !aligned(workspace, kAlign) || workspace_bytes < tree_workspace_bytes(*g))
+        return KVC8_ERR_WORKSPACE;
+    TreeArgs t = {};
+    AttnArgs &a = t.base;
+    a.g = *g;
+    a.group = num_q_heads / g->kv_heads;
+    a.q = static_cast<const uint16_t *>(query);
+    a.q_seq_stride = q_tok_stride;
+    a.q_head_stride = q_head_stride;
+    a.k_cache = key_cache;
+    a.v_cache = value_cache;
+    a.k_scale = key_scale;
+    a.v_scale = value_scale;
+    a.block_table = block_table;
+    a.context_lengths = context_kv_lens;
+    a.scale_log2 = (float)((double)softmax_scale * 1.4426950408889634);  // log2(e)
+    a.out = static_cast<uint16_t *>(out);
+    a.out_seq_stride = out_tok_stride;
+    a.out_head_stride = out_head_stride;
+    a.dev_error = dev_error;
+    t.num_tokens = num_tokens;
+    t.max_drafts = max_drafts;
+    t.cu_q_lens = cu_q_lens;
+    t.mask = tree_mask;
+    t.mask_words = mask_words;
+    return cuda_status(launch_tree(t, workspace, stream));
+}
+
+static kvc8_status compact(const kvc8_geom *g, int32_t value_bytes, void *key_cache,
+                           void *value_cache, float *key_scale, float *value_scale,
+                           const int32_t *block_table, const int32_t *context_kv_lens,
+                           const int32_t *accepted, int32_t max_accepted,
+                           const int32_t *num_accepted, int32_t *lens_out, int32_t *dev_error,
+                           cudaStream_t stream) {
+    if (max_accepted < 1) return KVC8_ERR_INVALID_ARG;
+    if (max_accepted > KVC8_MAX_DRAFTS) return KVC8_ERR_UNSUPPORTED;
+    if (g->num_seqs == 0) return KVC8_OK;
+    if (key_cache == nullptr || value_cache == nullptr || block_table == nullptr ||
+        context_kv_lens == nullptr || accepted == nullptr || num_accepted == nullptr)
+        return KVC8_ERR_INVALID_ARG;
+    if (!aligned(key_cache, 16) || !aligned(value_cache, 16)) return KVC8_ERR_INVALID_ARG;
+    CompactArgs a = {};
+    a.g = *g;
+    a.row_bytes = g->head_dim * value_bytes;
+    a.k_cache = static_cast<char *>(key_cache);
+    a.v_cache = static_cast<char *>(value_cache);
+    a.k_scale = key_scale;
+    a.v_scale = value_scale;
+    a.block_table = block_table;
+    a.context_kv_lens = context_kv_lens;
+    a.accepted = accepted;
+    a.max_accepted = max_accepted;
+    a.num_accepted = num_accepted;
+    a.lens_out = lens_out;
+    a.dev_error = dev_error;
+    return cuda_status(launch_compact(a, stream));
+}
+
+kvc8_status kvc8_compact_drafts(const kvc8_geom *g, int8_t *key_cache, int8_t *value_cache,
+                                float *key_scale, float *value_scale,
+                                const int32_t *block_table, const int32_t *context_kv_lens,
+                                const int32_t *accepted, int32_t max_accepted,
+                                const int32_t *num_accepted, int32_t *lens_out,
+                                int32_t *dev_error, cudaStream_t stream) {
+    kvc8_status st = check_geom(g);
+    if (st != KVC8_OK) return st;
+    if (g->num_seqs > 0 && (key_scale == nullptr || value_scale == nullptr || !aligned(key_scale, 16) ||
+                            !aligned(value_scale, 16)))
+        return KVC8_ERR_INVALID_ARG;
+    return compact(g, 1, key_cache, value_cache, key_scale, value_scale, block_table,
+                   context_kv_lens, accepted, max_accepted, num_accepted, lens_out, dev_error,
+                   stream);
+}
+
+kvc8_status kvc8_compact_drafts_bf16(const kvc8_geom *g, void *key_cache, void *value_cache,
+                                     const int32_t *block_table,
+                                     const int32_t *context_kv_lens, const int32_t *accepted,
+                                     int32_t max_accepted, const int32_t *num_accepted,
+                                     int32_t *lens_out, int32_t *dev_error,
+                                     cudaStream_t stream) {
+    kvc8_status st = check_geom_bf16(g);
+    if (st != KVC8_OK) return st;
+    return compact(g, 2, key_cache, value_cache, nullptr, nullptr, block_table, context_kv_lens,
+                   accepted, max_accepted, num_accepted, lens_out, dev_error, stream);
 }
 
 kvc8_status kvc8_get_error(int32_t *dev_error, int32_t *host_code, int32_t reset,

@@ -312,6 +312,53 @@ struct RopeArgs {
     int32_t *dev_error;
 };
 
+// Block tables from lengths (kvc8_blocks.cu).
+struct AssignArgs {
+    int32_t num_seqs, block_size, num_blocks, max_blocks_per_seq;
+    const int32_t *held;
+    const int32_t *want;
+    int32_t *free_blocks;
+    const int32_t *free_count;
+    int32_t *free_count_out;
+    int32_t *block_table;
+    int32_t *lens_out;
+    int64_t *slot_map;  // or NULL
+    int64_t slot_rows;
+    int32_t *dev_error;
+};
+cudaError_t launch_assign(const AssignArgs &a, cudaStream_t stream);
+
+// Attention of drafted tokens (kvc8_tree.cu): base.q and base.out are rows of tokens (their
+// seq strides are token strides), base.context_lengths the positions before the drafts.
+struct TreeArgs {
+    AttnArgs base;
+    int64_t num_tokens;
+    int32_t max_drafts;
+    const int32_t *cu_q_lens;  // or NULL: one draft each
+    const uint64_t *mask;      // or NULL: a chain
+    int32_t mask_words;
+};
+size_t tree_workspace_bytes(const kvc8_geom &g);
+cudaError_t launch_tree(TreeArgs a, void *workspace, cudaStream_t stream);
+
+// Kept drafts' rows moved behind the context (kvc8_compact.cu).
+struct CompactArgs {
+    kvc8_geom g;
+    int32_t row_bytes;  // of a head's row: D codes or D bf16 values
+    char *k_cache;
+    char *v_cache;
+    float *k_scale;  // NULL: bf16 pages
+    float *v_scale;
+    const int32_t *block_table;
+    const int32_t *context_kv_lens;
+    const int32_t *accepted;
+    int32_t max_accepted;
+    const int32_t *num_accepted;
+    int32_t *lens_out;  // or NULL
+    int32_t *dev_error;
+};
+cudaError_t launch_compact(const CompactArgs &a, cudaStream_t stream);
+
 // Decode attention over a shared prefix and each sequence's own pages (kvc8_prefix.cu).
 // One way to cut a prefix's work over CTAs.
 struct PrefixCut {

@@ -79,7 +79,9 @@ enum {
     KVC8_DEV_POS_BEYOND_TABLE = 2, /* position >= max_blocks_per_seq * block_size */
     KVC8_DEV_OUT_ROW_RANGE = 3,    /* gather output row outside [0, out_rows) */
     KVC8_DEV_BAD_LENGTH = 4,       /* negative length or decreasing cu_q_lens */
-    KVC8_DEV_TIMEOUT = 5           /* a bounded wait inside a kernel ran out: outputs are not valid */
+    KVC8_DEV_TIMEOUT = 5,          /* a bounded wait inside a kernel ran out: outputs are not valid */
+    KVC8_DEV_NO_FREE_BLOCK = 6,    /* kvc8_assign_blocks: a sequence found too few free blocks */
+    KVC8_DEV_BAD_INDEX = 7         /* kvc8_compact_drafts: indices not ascending from 0 or more */
 };
 
 /* Geometry of one paged cache and one batch.  quant_mode: 0 = dynamic scale
@@ -579,6 +581,166 @@ kvc8_status kvc8_shared_prefix_attention(const kvc8_geom *g, int32_t num_q_heads
                                          int64_t out_head_stride, void *workspace,
                                          size_t workspace_bytes, int32_t *dev_error,
                                          cudaStream_t stream);
+
+/*
+ * Drafted tokens (speculative decoding).  A step gives each sequence a few drafted
+ * tokens, a chain or a tree, has the model look at all of them at once, and keeps
+ * those along one path.  With T_b = cu_q_lens[b+1] - cu_q_lens[b] drafts behind
+ * context_kv_lens[b] cached positions a step is
+ *   kvc8_assign_blocks       pages for context + T_b positions
+ *   kvc8_store or            draft i's key and value to position context + i (its
+ *     kvc8_rope_store          rotation by its depth in the tree: kvc8_rope.positions)
+ *   kvc8_tree_attention      each draft over the context and its ancestors
+ *   kvc8_compact_drafts      the kept drafts' rows moved together behind the context
+ *   kvc8_assign_blocks       the pages behind them back to the free blocks
+ */
+
+/* Largest num_seqs of kvc8_assign_blocks, drafts of a sequence in
+ * kvc8_tree_attention and kept drafts in kvc8_compact_drafts. */
+#define KVC8_ASSIGN_MAX_SEQS 8192
+#define KVC8_MAX_DRAFTS 256
+
+/*
+ * kvc8_assign_blocks -- block tables and slots from lengths, on the device.
+ * Sequence b's row of block_table covers held_lens[b] positions and shall cover
+ * want_lens[b]: h_b = ceil(held / bs) blocks now, w_b = ceil(want / bs) then.  The
+ * free blocks are a stack, free_blocks[0 .. F), F = *free_count.
+ *   - The blocks that sequences give up (entries [w_b, h_b) of rows with w_b < h_b)
+ *     are pushed in the order of sequences and entries: R blocks at F, F + 1, ...
+ *   - The blocks that sequences need (entries [h_b, w_b)) are popped in the same
+ *     order: the k-th of the batch is free_blocks[F + R - 1 - k].
+ *   - Sequences are served in order, wholly or not at all: b is served if it needs
+ *     no block or if all that sequences 0 .. b need is at most F + R; the first that
+ *     is not is reported as KVC8_DEV_NO_FREE_BLOCK, and its row stays as it was.
+ *   - lens_out[b] = want_lens[b] if served, else held_lens[b].
+ *   - slot_map, if not NULL: block * bs + position mod bs of every new position
+ *     (held .. want of sequences that grow), -1 where b is not served.  Sequences
+ *     follow one another without gaps, in the order of kvc8_store's new tokens.
+ *   - *free_count_out = F + R less what was popped.  Entries given up stay in the
+ *     table, and popped ones in free_blocks behind the new count.
+ * One launch.
+ *
+ *   g               num_seqs <= KVC8_ASSIGN_MAX_SEQS (else KVC8_ERR_UNSUPPORTED);
+ *                   kv_heads, head_dim and quant_mode are checked, but not used
+ *   held_lens, want_lens  int32 [B]
+ *   free_blocks     int32 [num_blocks], read and written
+ *   free_count      int32 [1]
+ *   free_count_out  int32 [1]; may be free_count
+ *   block_table     int32 [B][MB], read and written
+ *   lens_out        int32 [B]; may be held_lens or want_lens
+ *   slot_map        int64 [slot_rows] or NULL; 8-byte aligned
+ * Sequences with a negative length (KVC8_DEV_BAD_LENGTH) or one beyond the table
+ * (KVC8_DEV_POS_BEYOND_TABLE) are not served, keep lens_out = held_lens, need and
+ * give nothing.  Slots at slot_rows or beyond are not written
+ * (KVC8_DEV_OUT_ROW_RANGE).  A count outside [0, num_blocks] counts as the nearer
+ * end, and blocks pushed beyond num_blocks are dropped (KVC8_DEV_BAD_LENGTH both).
+ * Ids outside the pool are moved as they are and reported
+ * (KVC8_DEV_BAD_BLOCK_ID).
+ */
+kvc8_status kvc8_assign_blocks(const kvc8_geom *g, const int32_t *held_lens,
+                               const int32_t *want_lens, int32_t *free_blocks,
+                               const int32_t *free_count, int32_t *free_count_out,
+                               int32_t *block_table, int32_t *lens_out, int64_t *slot_map,
+                               int64_t slot_rows, int32_t *dev_error, cudaStream_t stream);
+
+/* Bytes of device workspace kvc8_tree_attention needs (they depend on head_dim
+ * only).  Host function; 0 for arguments that the call refuses. */
+size_t kvc8_tree_attention_workspace_bytes(const kvc8_geom *g, int32_t num_q_heads,
+                                           int64_t num_tokens, int32_t max_drafts);
+
+/*
+ * kvc8_tree_attention -- the drafted tokens of each sequence attend over its
+ * context and over those drafts that a mask names, all in the int8 pages (the
+ * drafts' rows were stored at positions context_kv_lens[b] + i).  Query head j of
+ * draft t of sequence b, kv head h = j / (num_q_heads / H), gives
+ *   out = sum_p w_p V[p] / sum_p w_p,  w_p = exp(softmax_scale <q, K[p]>)
+ * over p < context_kv_lens[b] and over p = context_kv_lens[b] + i, 0 <= i < T_b,
+ * where bit i of the draft's mask is set; without any position it gives zeros.  A
+ * draft sees itself only where its own bit is set.  K, V are the values that the
+ * pages stand for, fp32(code) * scale.  Operands, accumulation, rounding and the
+ * range of scales and queries are those of kvc8_shared_prefix_attention's prefix.
+ *
+ * Lengths, cu_q_lens, masks and tables are read on the device, so a captured graph
+ * may be replayed with other values of them.  Two launches, no host
+ * synchronisation.
+ *
+ *   num_q_heads     H * group with 1 <= group <= 8
+ *   num_tokens      rows of query and out, >= cu_q_lens[B]; rows from cu_q_lens[B] on
+ *                   are left as they are
+ *   max_drafts      1 .. KVC8_MAX_DRAFTS, at least every T_b
+ *   query           bf16 [num_tokens][num_q_heads][D], element strides
+ *                   (q_tok_stride, q_head_stride, 1), multiples of 8, 16-byte aligned
+ *   caches, scales, block_table  as in kvc8_dequant_gather (all three modes)
+ *   cu_q_lens       int32 [B+1] as in kvc8_store, or NULL: one draft per sequence,
+ *                   and num_tokens must equal B
+ *   context_kv_lens int32 [B], positions before the drafts
+ *   tree_mask       uint64 [num_tokens][mask_words], bit i % 64 of word i / 64 for
+ *                   draft i of the token's own sequence (other bits are not
+ *                   looked at), 8-byte aligned; or NULL: a chain, where draft t sees
+ *                   drafts 0 .. t
+ *   mask_words      with a mask: at least max_drafts / 64, rounded up
+ *   softmax_scale   finite
+ *   out             bf16 [num_tokens][num_q_heads][D], strides (out_tok_stride,
+ *                   out_head_stride, 1); not the query
+ *   workspace       >= kvc8_tree_attention_workspace_bytes bytes, 256-byte aligned;
+ *                   calls that overlap on the GPU need separate workspaces
+ * Supported: head_dim 64 or 128, block_size a multiple of 16, and fewer than 2^31
+ * units of 128 query rows (drafts * group) of a kv head by 128 positions for full
+ * tables.  A sequence whose cu_q_lens decrease, leave [0, num_tokens] or exceed
+ * max_drafts is left out and its rows stay unwritten (KVC8_DEV_BAD_LENGTH).  A
+ * negative context counts as 0 (KVC8_DEV_BAD_LENGTH); positions beyond the table
+ * (KVC8_DEV_POS_BEYOND_TABLE) and those of blocks outside the pool
+ * (KVC8_DEV_BAD_BLOCK_ID) are left out.
+ */
+kvc8_status kvc8_tree_attention(const kvc8_geom *g, int32_t num_q_heads, int64_t num_tokens,
+                                int32_t max_drafts, const void *query, int64_t q_tok_stride,
+                                int64_t q_head_stride, const int8_t *key_cache,
+                                const int8_t *value_cache, const float *key_scale,
+                                const float *value_scale, const int32_t *block_table,
+                                const int32_t *cu_q_lens, const int32_t *context_kv_lens,
+                                const uint64_t *tree_mask, int32_t mask_words,
+                                float softmax_scale, void *out, int64_t out_tok_stride,
+                                int64_t out_head_stride, void *workspace,
+                                size_t workspace_bytes, int32_t *dev_error,
+                                cudaStream_t stream);
+
+/*
+ * kvc8_compact_drafts -- the kept drafts' rows move together behind the context:
+ * for k = 0 .. n_b - 1 in turn (n_b = num_accepted[b]) the keys and values of
+ * position context_kv_lens[b] + accepted[b][k], all heads, go to position
+ * context_kv_lens[b] + k, and lens_out[b] = context_kv_lens[b] + n_b.  Indices
+ * ascend strictly from 0 or more, as along a path from the root, so no row is
+ * overwritten before it has moved.  Codes move as they are, in mode 0 with their
+ * scales; in mode 2, where the two blocks' scales differ, a row is quantised anew
+ * for its new block: clamp(round_half_even(fp32(fp32(code) * s_from) / s_to), -127,
+ * 127), 0 where s_to = 0.  One launch.
+ *
+ *   caches, scales, block_table  as in kvc8_store (mode 0 scales are written)
+ *   accepted        int32 [B][max_accepted], the drafts kept, counted in their sequence
+ *   max_accepted    1 .. KVC8_MAX_DRAFTS
+ *   num_accepted    int32 [B], 0 .. max_accepted
+ *   lens_out        int32 [B] or NULL; may be context_kv_lens
+ * A sequence whose indices do not ascend (KVC8_DEV_BAD_INDEX), whose context or
+ * count is out of range (KVC8_DEV_BAD_LENGTH) or whose positions leave the table
+ * (KVC8_DEV_POS_BEYOND_TABLE) is left as it is, with lens_out =
+ * context_kv_lens; a row with a block outside the pool (KVC8_DEV_BAD_BLOCK_ID) does
+ * not move.
+ */
+kvc8_status kvc8_compact_drafts(const kvc8_geom *g, int8_t *key_cache, int8_t *value_cache,
+                                float *key_scale, float *value_scale,
+                                const int32_t *block_table, const int32_t *context_kv_lens,
+                                const int32_t *accepted, int32_t max_accepted,
+                                const int32_t *num_accepted, int32_t *lens_out,
+                                int32_t *dev_error, cudaStream_t stream);
+
+/* kvc8_compact_drafts_bf16 -- the same in kvc8_store_bf16's pages;
+ * g->quant_mode is ignored. */
+kvc8_status kvc8_compact_drafts_bf16(const kvc8_geom *g, void *key_cache, void *value_cache,
+                                     const int32_t *block_table,
+                                     const int32_t *context_kv_lens, const int32_t *accepted,
+                                     int32_t max_accepted, const int32_t *num_accepted,
+                                     int32_t *lens_out, int32_t *dev_error,
+                                     cudaStream_t stream);
 
 /* Largest num_seqs that kvc8_dequant_gather_noalloc accepts. */
 #define KVC8_NOALLOC_MAX_SEQS 4096

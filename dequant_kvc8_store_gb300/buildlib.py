@@ -24,6 +24,7 @@ SOURCES = ["kvc8_api.cu", "kvc8_store.cu", "kvc8_gather.cu", "kvc8_noalloc.cu", 
            "kvc8_attention.cu", "kvc8_rope.cu", "kvc8_prefix.cu",
            "kvc8_prefix_own.cu", "kvc8_blocks.cu", "kvc8_tree.cu", "kvc8_compact.cu"]
 HEADERS = [os.path.join(CSRC, "kvc8_internal.cuh"), os.path.join(CSRC, "kvc8_codes.cuh"),
+           os.path.join(CSRC, "kvc8_tcgen05.cuh"),
            os.path.join(INCLUDE, "kvc8.h")]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xptxas", "-v",

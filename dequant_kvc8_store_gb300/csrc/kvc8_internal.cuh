@@ -328,10 +328,23 @@ struct AssignArgs {
 };
 cudaError_t launch_assign(const AssignArgs &a, cudaStream_t stream);
 
-// Attention of drafted tokens (kvc8_tree.cu): base.q and base.out are rows of tokens (their
-// seq strides are token strides), base.context_lengths the positions before the drafts.
+// Attention of drafted tokens (kvc8_tree.cu).
+// Where a CTA's first part of the work lies, for the merge of what several CTAs share.
+struct TreeShare {
+    uint32_t units;  // of the whole call
+    uint32_t first;  // unit with which the part's (sequence, kv head, row tile) begins
+    int32_t steps;   // of it
+    int32_t token;   // its sequence's first row
+    int32_t rows;    // query rows of its sequence and head
+    int32_t row;     // the tile's first
+    int32_t head;
+    int32_t pad;
+};
+// base.q and base.out are rows of tokens (their seq strides are token strides),
+// base.context_lengths the positions before the drafts.
 struct TreeArgs {
     AttnArgs base;
+    TreeShare *shares;
     int64_t num_tokens;
     int32_t max_drafts;
     const int32_t *cu_q_lens;  // or NULL: one draft each

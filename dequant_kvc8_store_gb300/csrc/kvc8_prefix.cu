@@ -52,7 +52,6 @@ namespace {
 constexpr int kStages = 2;      // steps of K' and of V' in shared memory
 constexpr int kMaskSlots = 4;   // steps whose valid counts are kept
 constexpr int kMaxCtas = 152;   // SMs of a GB300
-constexpr long long kWaitCycles = 4000000000ll;  // about two seconds
 constexpr int kMergeThreads = 256;
 // What else costs time, in steps, about: a CTA's start and end, its change of tile, the own
 // positions' kernel after the prefix's.
@@ -179,18 +178,7 @@ struct Prefix {
 
     // false: the limit ran out here or elsewhere in the CTA
     __device__ __forceinline__ bool wait(uint64_t &b, uint32_t parity) const {
-        const uint32_t at = smem_u32(&b);
-        if (mbar_try(at, parity)) return true;
-        const long long t0 = clock64();
-        while (!mbar_try(at, parity)) {
-            if (*static_cast<volatile int32_t *>(&bar.stop) != 0) return false;
-            if (clock64() - t0 > kWaitCycles) {
-                *static_cast<volatile int32_t *>(&bar.stop) = 1;
-                report(p.own.dev_error, KVC8_DEV_TIMEOUT);
-                return false;
-            }
-        }
-        return true;
+        return wait_limited(b, parity, bar.stop, p.own.dev_error);
     }
 
     // The same for a whole warp, which leaves it converged.

@@ -142,6 +142,23 @@ __device__ __forceinline__ void tc_wait_ld(float (&r)[32]) {
                  :
                  : "memory");
 }
+// Waits have a limit: about two seconds.
+constexpr long long kWaitCycles = 4000000000ll;
+// false: the limit ran out here or, by `stop`, elsewhere in the CTA.
+__device__ __forceinline__ bool wait_limited(uint64_t &b, uint32_t parity, int32_t &stop, int32_t *dev_error) {
+    const uint32_t at = smem_u32(&b);
+    if (mbar_try(at, parity)) return true;
+    const long long t0 = clock64();
+    while (!mbar_try(at, parity)) {
+        if (*static_cast<volatile int32_t *>(&stop) != 0) return false;
+        if (clock64() - t0 > kWaitCycles) {
+            *static_cast<volatile int32_t *>(&stop) = 1;
+            report(dev_error, KVC8_DEV_TIMEOUT);
+            return false;
+        }
+    }
+    return true;
+}
 // This warpgroup's registers per thread from here on.
 template <int N>
 __device__ __forceinline__ void reg_give() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }

@@ -178,6 +178,28 @@ constexpr uint32_t instr_desc(int n, bool b_mn) {
            ((uint32_t)(kRows >> 4) << 24);
 }
 
+// ---- loads ahead ----------------------------------------------------------------------
+
+// Loads whose place in the program matters: a step's codes, scales and block ids are asked for a
+// step before they are used, and the compiler, free to, moves such a load down to its use.
+__device__ __forceinline__ uint4 ld_ahead_16(const void *p) {
+    uint4 v;
+    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "l"(p));
+    return v;
+}
+__device__ __forceinline__ float ld_ahead_f32(const float *p) {
+    float v;
+    asm volatile("ld.global.nc.f32 %0, [%1];" : "=f"(v) : "l"(p));
+    return v;
+}
+__device__ __forceinline__ int32_t ld_ahead_s32(const int32_t *p) {
+    int32_t v;
+    asm volatile("ld.global.nc.s32 %0, [%1];" : "=r"(v) : "l"(p));
+    return v;
+}
+
 // ---- scores ------------------------------------------------------------------------
 
 __device__ __forceinline__ float max3(float a, float b, float c) {

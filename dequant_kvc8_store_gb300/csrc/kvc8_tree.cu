@@ -84,22 +84,35 @@ struct Cut {
     }
 };
 
-// A walk over a CTA's share, tile by tile; the next sequence's lengths are on their way.
+// A walk over a CTA's share, tile by tile; the next sequence's lengths are on their way.  Each warp has
+// its own in shared memory: it is looked at once a tile, and in registers the whole of it would push out what
+// a step needs.
 struct Walk {
     Seq s;
     Raw ahead;
     int tile, step;  // tile: kv head * s.tiles + row tile; step: the first of it in the share
     __device__ __forceinline__ int head() const { return tile / s.tiles; }
     __device__ __forceinline__ int row0() const { return (tile - tile / s.tiles * s.tiles) * kRows; }
-    // Only where the share goes on: there is a next tile then.
-    __device__ __forceinline__ void next_tile(const TreeArgs &p) {
-        step = 0;
-        if (++tile < s.tiles * p.base.g.kv_heads) return;
-        tile = 0;
-        do {
-            s = make_seq(p, s.b + 1, ahead);
-            ahead = read_raw(p, s.b + 1);
-        } while (s.drafts == 0 && s.b + 1 < p.base.g.num_seqs);
+    // By a whole warp, and only where the share goes on: there is a next tile then.
+    __device__ __forceinline__ void next_tile(const TreeArgs &p, int lane) {
+        __syncwarp();
+        if (lane == 0) {
+            step = 0;
+            if (tile + 1 < s.tiles * p.base.g.kv_heads) {
+                ++tile;
+            } else {
+                tile = 0;
+                Seq x = s;
+                Raw r = ahead;
+                do {
+                    x = make_seq(p, x.b + 1, r);
+                    r = read_raw(p, x.b + 1);
+                } while (x.drafts == 0 && x.b + 1 < p.base.g.num_seqs);
+                s = x;
+                ahead = r;
+            }
+        }
+        __syncwarp();
     }
 };
 
@@ -138,6 +151,8 @@ struct Barriers {
     uint32_t sum[Layout<128>::kThreads / 32];
     int32_t start_b;
     uint32_t start_off;
+    int32_t total;  // units of this CTA
+    Walk walk[Layout<128>::kMmaWarp + 1], walk_out[4];  // of each warp; of the rows that go out
     float q_scale[kStages][kRows];  // log2 per unit of score, with the query's power of two
     float m[kStages][kRows], l[kStages][kRows];
     uint2 valid[kMaskSlots];  // 8 bytes: valid positions of each group of 16
@@ -158,10 +173,15 @@ struct Tree {
 
     const TreeArgs &p;
     Barriers &bar;
-    const uint32_t base;  // shared memory, 1 KB aligned
-    const int total;      // units of this CTA
-    const Walk &start;
-    const int lane;
+    const uint32_t base, tmem;  // shared memory, 1 KB aligned
+    const int total;            // units of this CTA
+    Walk &walk;                 // this warp's
+    const int lane, warp;
+
+    // (Read again here, by each role for itself, than kept in registers from the kernel's start.)
+    __device__ __forceinline__ Tree(const TreeArgs &args, Barriers &b, uint8_t *dyn)
+        : p(args), bar(b), base((smem_u32(dyn) + 1023u) & ~1023u), tmem(b.tmem), total(b.total),
+          walk(b.walk[threadIdx.x >> 5]), lane(threadIdx.x & 31), warp(threadIdx.x >> 5) {}
 
     __device__ __forceinline__ bool wait(uint64_t &b, uint32_t parity) const {
         return wait_limited(b, parity, bar.stop, p.base.dev_error);
@@ -185,15 +205,14 @@ struct Tree {
     };
 
     // The block id of a step's group, requested a step before it is used.
-    __device__ __forceinline__ Id find(const Walk &w, int step, int dw) const {
+    __device__ __forceinline__ Id find(const int32_t *table, int pos, int len, int head) const {
         Id x;
         const uint32_t bs = (uint32_t)p.base.g.block_size;
-        const int pos = step * kCols + dw * kRpw;
         const uint32_t lb = (uint32_t)pos / bs;
         x.at = pos - (int)(lb * bs);
-        x.valid = min(16, w.s.len - pos);
-        x.blk = pos < w.s.len ? ld_nc_s32(p.base.block_table + (int64_t)w.s.b * p.base.g.max_blocks_per_seq + lb) : 0;
-        x.head = w.head();
+        x.valid = min(16, len - pos);
+        x.blk = pos < len ? ld_ahead_s32(table + lb) : 0;
+        x.head = head;
         return x;
     }
     __device__ __forceinline__ Place place(const Id &x) const {
@@ -212,25 +231,35 @@ struct Tree {
             const int at = i * T::kRpl + T::row_in(lane);
             c.c[i] = make_uint4(0u, 0u, 0u, 0u);
             if (at < x.valid)
-                c.c[i] = ld_stream_16(cache + (x.row + at) * D + T::block_in(lane) * 64 + lane % 4 * 16);
+                c.c[i] = ld_ahead_16(cache + (x.row + at) * D + T::block_in(lane) * 64 + lane % 4 * 16);
         }
     }
     // Modes 0 and 2: the scale of position `lane` of the group.
     __device__ __forceinline__ float load_scale(const Place &x, const float *scale) const {
-        return lane < 16 && lane < x.valid ? ld_nc_f32(scale + (MODE == 0 ? x.row + lane : x.blk)) : 0.0f;
+        return lane < 16 && lane < x.valid ? ld_ahead_f32(scale + (MODE == 0 ? x.row + lane : x.blk)) : 0.0f;
     }
 
-    __device__ void dequantise(int dw) const {
+    __device__ void dequantise() const {
         const AttnArgs &a = p.base;
-        Walk w = start;
-        int step = w.step;
+        const int dw = warp - L::kDequantWarp;
+        // of the step whose block id is asked for next: its first position, the tile's positions and table
+        int pos = 0, len = 0, head = 0;
+        const int32_t *table = nullptr;
+        auto enter = [&]() {
+            len = walk.s.len;
+            head = walk.head();
+            table = a.block_table + (int64_t)walk.s.b * a.g.max_blocks_per_seq;
+            pos = walk.step * kCols + dw * kRpw;
+        };
         auto next = [&]() {
-            if (++step == w.s.steps) {
-                w.next_tile(p);
-                step = 0;
+            pos += kCols;
+            if (pos - dw * kRpw >= len) {
+                walk.next_tile(p, lane);
+                enter();
             }
         };
-        Place x = place(find(w, step, dw));
+        enter();
+        Place x = place(find(table, pos, len, head));
         Codes k, v;
         float sk = 0.0f, sv = 0.0f;
         auto scales = [&]() {
@@ -244,7 +273,7 @@ struct Tree {
         Id id{};
         if (total > 1) {
             next();
-            id = find(w, step, dw);
+            id = find(table, pos, len, head);
         }
         for (int n = 0; n < total; ++n) {
             const int st = n % kStages;
@@ -280,7 +309,7 @@ struct Tree {
                 scales();
                 if (n + 2 < total) {
                     next();
-                    id = find(w, step, dw);
+                    id = find(table, pos, len, head);
                 }
             }
             if (!wait_warp(bar.v_free[st], par ^ 1u)) return;
@@ -292,31 +321,30 @@ struct Tree {
     }
 
     // ---- products (a warp, one lane issuing) --------------------------------------------------
-    __device__ __forceinline__ void qk(int q, int st, uint32_t tmem, uint32_t leader) const {
+    __device__ __forceinline__ void qk(int q, int st, uint32_t tm, uint32_t leader) const {
         const uint64_t qd = operand_desc(base + L::kQ, 16) + (uint64_t)(q * (L::kTileBytes >> 4));
         const uint64_t kd = operand_desc(base + L::kK, 16) + (uint64_t)(st * (L::kTileBytes >> 4));
 #pragma unroll
         for (int i = 0; i < D / 16; ++i) {
             const uint64_t at = (uint64_t)(((i / 4) * (kRows * 128) + (i % 4) * 32) >> 4);
-            tc_mma_ss(tmem + st * kCols, qd + at, kd + at, instr_desc(kCols, false), i > 0, leader);
+            tc_mma_ss(tm + st * kCols, qd + at, kd + at, instr_desc(kCols, false), i > 0, leader);
         }
     }
-    __device__ __forceinline__ void pv(int o, int st, uint32_t tmem, bool acc, uint32_t leader) const {
+    __device__ __forceinline__ void pv(int o, int st, uint32_t tm, bool acc, uint32_t leader) const {
         const uint64_t v = operand_desc(base + L::kV, kCols * 128) + (uint64_t)(st * (L::kTileBytes >> 4));
 #pragma unroll
         for (int i = 0; i < kCols / 16; ++i)
-            tc_mma_ts(tmem + L::kO + o * D, tmem + st * kCols + 8 * i, v + (uint64_t)(i * (2048 >> 4)), instr_desc(D, true),
+            tc_mma_ts(tm + L::kO + o * D, tm + st * kCols + 8 * i, v + (uint64_t)(i * (2048 >> 4)), instr_desc(D, true),
                       acc || i > 0, leader);
     }
     // What steers the loop comes from lane 0, so that the compiler keeps it, and with it stages,
     // addresses and descriptors, in uniform registers.
     __device__ __forceinline__ static int uniform(int x) { return __shfl_sync(0xFFFFFFFFu, x, 0); }
 
-    __device__ bool products_loop(uint32_t tmem_any, uint32_t leader) const {
-        const uint32_t tmem = (uint32_t)uniform((int)tmem_any);
+    __device__ bool products_loop(uint32_t leader) const {
+        const uint32_t tm = (uint32_t)uniform((int)tmem);
         const int units = uniform(total);
-        Walk w = start;
-        int left = uniform(w.s.steps - w.step);  // steps of the tile from the next scores on
+        int left = uniform(walk.s.steps - walk.step);  // steps of the tile from the next scores on
         uint32_t q_seg = 0, seg = 0;             // tile of the next scores, of the next weighted values
         bool q_first = true;
         // Scores of unit n; returns whether it is its tile's last.
@@ -325,7 +353,7 @@ struct Tree {
             ok = (!q_first || wait_warp(bar.q_full[q], (q_seg >> 1) & 1u)) && wait_warp(bar.k_full[st], (uint32_t)(n >> 1) & 1u);
             if (!ok) return false;
             tc_fence_after();
-            qk(q, st, tmem, leader);
+            qk(q, st, tm, leader);
             tc_commit(smem_u32(&bar.s_full[st]), leader);
             const bool last = --left == 0 || n + 1 == units;
             q_first = last;
@@ -333,8 +361,8 @@ struct Tree {
                 tc_commit(smem_u32(&bar.q_free[q]), leader);
                 ++q_seg;
                 if (n + 1 < units) {
-                    w.next_tile(p);
-                    left = uniform(w.s.steps);
+                    walk.next_tile(p, lane);
+                    left = uniform(walk.s.steps);
                 }
             }
             return last;
@@ -352,7 +380,7 @@ struct Tree {
             if (!wait_warp(bar.v_full[st], (uint32_t)(n >> 1) & 1u)) return false;
             if (!wait_warp(bar.p_full[st], (uint32_t)(n >> 1) & 1u)) return false;
             tc_fence_after();
-            pv(o, st, tmem, !first, leader);
+            pv(o, st, tm, !first, leader);
             tc_commit(smem_u32(&bar.v_free[st]), leader);
             if (last) {
                 tc_commit(smem_u32(&bar.o_full[o]), leader);
@@ -363,9 +391,9 @@ struct Tree {
         }
         return true;
     }
-    __device__ void products(uint32_t tmem) const {
+    __device__ void products() const {
         const uint32_t leader = elect_lane();
-        products_loop(tmem, leader);
+        products_loop(leader);
         // what was issued is done before the tensor memory is freed
         tc_commit(smem_u32(&bar.drained), leader);
         const long long t0 = clock64();
@@ -434,7 +462,7 @@ struct Tree {
     }
 
     // A tile's O: to the output where the CTA has the whole tile, else a partial.
-    __device__ __forceinline__ void store_rows(const Walk &w, int rw, int buf, uint32_t tmem, bool whole, uint32_t seg) const {
+    __device__ __forceinline__ void store_rows(const Walk &w, int rw, int buf, bool whole, uint32_t seg) const {
         const AttnArgs &a = p.base;
         const int h = w.head(), row = rw * 32 + lane, r0 = w.row0() + rw * 32, rows = w.s.drafts * a.group;
         if (r0 < rows) {
@@ -485,8 +513,9 @@ struct Tree {
         arrive(bar.o_free[buf]);
     }
 
-    __device__ void rows(int rw, uint32_t tmem) const {
-        Walk in = start, out = start;
+    __device__ void rows() const {
+        const int rw = warp - L::kSoftmaxWarps;
+        Walk &in = walk, &out = bar.walk_out[rw];
         int in_left = total, out_left = total;
         uint32_t in_seg = 0;
         auto load_next = [&]() {
@@ -494,7 +523,7 @@ struct Tree {
             if (!wait_warp(bar.q_free[buf], ((in_seg >> 1) & 1u) ^ 1u)) return false;
             load_rows(in, rw, buf);
             in_left -= min(in_left, in.s.steps - in.step);
-            if (in_left > 0) in.next_tile(p);
+            if (in_left > 0) in.next_tile(p, lane);
             ++in_seg;
             return true;
         };
@@ -504,9 +533,9 @@ struct Tree {
             const int count = min(out_left, out.s.steps - out.step), buf = (int)(seg & 1u);
             if (!wait_warp(bar.ml_full[buf], (seg >> 1) & 1u) || !wait_warp(bar.o_full[buf], (seg >> 1) & 1u)) return;
             tc_fence_after();
-            store_rows(out, rw, buf, tmem, count == out.s.steps, seg);
+            store_rows(out, rw, buf, count == out.s.steps, seg);
             out_left -= count;
-            if (out_left > 0) out.next_tile(p);
+            if (out_left > 0) out.next_tile(p, lane);
         }
     }
 
@@ -517,33 +546,31 @@ struct Tree {
         return word < 2 * p.mask_words ? __ldg(mask + word) : 0u;
     }
 
-    __device__ void softmax(int warp, uint32_t tmem) const {
+    __device__ void softmax() const {
         const int row = warp * 32 + lane;
         const uint32_t lanes = (uint32_t)(warp * 32) << 16;
-        Walk w = start;
         int n = 0, left = total;
         for (uint32_t seg = 0; left > 0; ++seg) {
-            const int count = min(left, w.s.steps - w.step), buf = (int)(seg & 1u);
-            const int r0 = w.row0() + warp * 32, rows = w.s.drafts * p.base.group;
+            const int count = min(left, walk.s.steps - walk.step), buf = (int)(seg & 1u);
+            const int r0 = walk.row0() + warp * 32, rows = walk.s.drafts * p.base.group;
             const bool busy = r0 < rows;  // uniform in the warp: some row is a query's
-            const int t = min(r0 + lane, rows - 1) / p.base.group;
-            const uint32_t *mask =
-                p.mask == nullptr ? nullptr : reinterpret_cast<const uint32_t *>(p.mask + (int64_t)(w.s.token + t) * p.mask_words);
+            int d0 = walk.step * kCols - walk.s.ctx;  // the draft at a step's first position, if not negative
             const uint32_t o_at = tmem + lanes + L::kO + buf * D;
             float scale = 0.0f, m = -INFINITY, l = 0.0f;
-            for (int i = 0; i < count; ++i, ++n) {
-                const int p0 = (w.step + i) * kCols, st = n & 1;
-                const bool drafts = p0 + kCols > w.s.ctx;  // some position is a draft's
+            for (int i = 0; i < count; ++i, ++n, d0 += kCols) {
+                const int st = n & 1;
+                const bool drafts = d0 + kCols > 0;  // some position is a draft's
                 uint32_t sees[4] = {0xFFFFFFFFu, 0xFFFFFFFFu, 0xFFFFFFFFu, 0xFFFFFFFFu};
                 if (drafts && busy) {
-                    const int d0 = p0 - w.s.ctx;  // the draft at the step's first position, if not negative
-                    if (mask == nullptr) {
+                    const int t = min(r0 + lane, rows - 1) / p.base.group;
+                    if (p.mask == nullptr) {
 #pragma unroll
                         for (int q = 0; q < 4; ++q) {
                             const int upto = t - d0 + 1 - 32 * q;  // positions from the word's first on that are seen
                             sees[q] = upto >= 32 ? 0xFFFFFFFFu : upto <= 0 ? 0u : (1u << upto) - 1u;
                         }
                     } else {
+                        const uint32_t *mask = reinterpret_cast<const uint32_t *>(p.mask + (int64_t)(walk.s.token + t) * p.mask_words);
                         uint32_t lo = mask_word(mask, d0 >> 5);
 #pragma unroll
                         for (int q = 0; q < 4; ++q) {
@@ -569,7 +596,7 @@ struct Tree {
             bar.l[buf][row] = l;
             arrive(bar.ml_full[buf]);
             left -= count;
-            if (left > 0) w.next_tile(p);
+            if (left > 0) walk.next_tile(p, lane);
         }
     }
 
@@ -752,36 +779,41 @@ __global__ void __launch_bounds__(Layout<D>::kThreads, 1) tree_kernel(const Tree
             if (before > first) break;
         }
         __syncthreads();
-        Walk w;
-        w.s = make_seq(p, bar.start_b, read_raw(p, bar.start_b));
-        w.ahead = read_raw(p, bar.start_b + 1);
-        w.tile = (int)(bar.start_off / (uint32_t)w.s.steps);
-        w.step = (int)(bar.start_off - (uint32_t)w.tile * (uint32_t)w.s.steps);
-        if (threadIdx.x == 0) {
-            TreeShare r;
-            r.units = units;
-            r.first = first - (uint32_t)w.step;
-            r.steps = w.s.steps;
-            r.token = w.s.token;
-            r.rows = w.s.drafts * p.base.group;
-            r.row = w.row0();
-            r.head = w.head();
-            r.pad = 0;
-            p.shares[blockIdx.x] = r;
+        if (lane == 0) {
+            Walk w;
+            w.s = make_seq(p, bar.start_b, read_raw(p, bar.start_b));
+            w.ahead = read_raw(p, bar.start_b + 1);
+            w.tile = (int)(bar.start_off / (uint32_t)w.s.steps);
+            w.step = (int)(bar.start_off - (uint32_t)w.tile * (uint32_t)w.s.steps);
+            if (warp <= L::kMmaWarp) bar.walk[warp] = w;
+            if (warp < L::kRowWarps) bar.walk_out[warp] = w;
+            if (warp == L::kMmaWarp) {
+                bar.total = total;
+                TreeShare r;
+                r.units = units;
+                r.first = first - (uint32_t)w.step;
+                r.steps = w.s.steps;
+                r.token = w.s.token;
+                r.rows = w.s.drafts * p.base.group;
+                r.row = w.row0();
+                r.head = w.head();
+                r.pad = 0;
+                p.shares[blockIdx.x] = r;
+            }
         }
-        const Tree<MODE, D> k{p, bar, (smem_u32(dyn) + 1023u) & ~1023u, total, w, lane};
+        __syncthreads();
         if (warp >= L::kMmaWarp) {
             reg_give<L::kMmaRegs>();
-            if (warp == L::kMmaWarp) k.products(tmem);
+            if (warp == L::kMmaWarp) Tree<MODE, D>(p, bar, dyn).products();
         } else if (warp >= L::kDequantWarp) {
             static_assert(L::kDequantRegs == L::kLaunchRegs, "as launched");
-            k.dequantise(warp - L::kDequantWarp);
+            Tree<MODE, D>(p, bar, dyn).dequantise();
         } else if (warp >= L::kSoftmaxWarps) {
             reg_give<L::kRowRegs>();
-            k.rows(warp - L::kSoftmaxWarps, tmem);
+            Tree<MODE, D>(p, bar, dyn).rows();
         } else {
             reg_take<L::kSoftmaxRegs>();
-            k.softmax(warp, tmem);
+            Tree<MODE, D>(p, bar, dyn).softmax();
         }
         __syncwarp();
         tc_fence_before();

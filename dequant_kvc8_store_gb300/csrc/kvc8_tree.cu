@@ -196,70 +196,66 @@ struct Tree {
     }
 
     // ---- dequantise ------------------------------------------------------------
+    // Where a warp's group of 16 positions lies; of the step whose block id is asked for next.
     struct Place {
-        int64_t row, blk;  // cache row of the group's first position; block * heads + head
-        int valid;
+        int64_t page;       // block * heads + head
+        int32_t at, valid;  // first slot in the block; positions before the end
     };
-    struct Id {
-        int32_t blk, at, valid, head;
-    };
-
-    // The block id of a step's group, requested a step before it is used.
-    __device__ __forceinline__ Id find(const int32_t *table, int pos, int len, int head) const {
-        Id x;
-        const uint32_t bs = (uint32_t)p.base.g.block_size;
-        const uint32_t lb = (uint32_t)pos / bs;
-        x.at = pos - (int)(lb * bs);
-        x.valid = min(16, len - pos);
-        x.blk = pos < len ? ld_ahead_s32(table + lb) : 0;
-        x.head = head;
-        return x;
-    }
-    __device__ __forceinline__ Place place(const Id &x) const {
-        const kvc8_geom &g = p.base.g;
-        const bool in = x.blk >= 0 && x.blk < g.num_blocks;
+    __device__ __forceinline__ Place place(int32_t blk, int at, int valid, int head) const {
+        const bool in = blk >= 0 && blk < p.base.g.num_blocks;
         if (!in && lane == 0) report(p.base.dev_error, KVC8_DEV_BAD_BLOCK_ID);
-        Place o;
-        o.valid = in ? max(0, x.valid) : 0;
-        o.blk = (int64_t)(in ? x.blk : 0) * g.kv_heads + x.head;
-        o.row = o.blk * g.block_size + x.at;
-        return o;
+        return Place{(int64_t)(in ? blk : 0) * p.base.g.kv_heads + head, at, in ? max(0, min(16, valid)) : 0};
     }
     __device__ __forceinline__ void load(const Place &x, const int8_t *cache, Codes &c) const {
+        const int8_t *src = cache + (x.page * p.base.g.block_size + x.at + T::row_in(lane)) * D + T::block_in(lane) * 64 + lane % 4 * 16;
+        if (x.valid == 16) {
 #pragma unroll
-        for (int i = 0; i < T::kLoads; ++i) {
-            const int at = i * T::kRpl + T::row_in(lane);
-            c.c[i] = make_uint4(0u, 0u, 0u, 0u);
-            if (at < x.valid)
-                c.c[i] = ld_ahead_16(cache + (x.row + at) * D + T::block_in(lane) * 64 + lane % 4 * 16);
+            for (int i = 0; i < T::kLoads; ++i) c.c[i] = ld_ahead_16(src + i * T::kRpl * D);
+        } else {
+#pragma unroll
+            for (int i = 0; i < T::kLoads; ++i) {
+                c.c[i] = make_uint4(0u, 0u, 0u, 0u);
+                if (i * T::kRpl + T::row_in(lane) < x.valid) c.c[i] = ld_ahead_16(src + i * T::kRpl * D);
+            }
         }
     }
     // Modes 0 and 2: the scale of position `lane` of the group.
     __device__ __forceinline__ float load_scale(const Place &x, const float *scale) const {
-        return lane < 16 && lane < x.valid ? ld_ahead_f32(scale + (MODE == 0 ? x.row + lane : x.blk)) : 0.0f;
+        const int64_t at = MODE == 0 ? x.page * p.base.g.block_size + x.at + lane : x.page;
+        return lane < x.valid ? ld_ahead_f32(scale + at) : 0.0f;  // (16 at most)
     }
 
     __device__ void dequantise() const {
         const AttnArgs &a = p.base;
         const int dw = warp - L::kDequantWarp;
-        // of the step whose block id is asked for next: its first position, the tile's positions and table
-        int pos = 0, len = 0, head = 0;
-        const int32_t *table = nullptr;
+        // of the step whose block id is asked for next: positions left, slot and entry of the table; a
+        // step is `jump` blocks and `rest` slots further on
+        const int bs = a.g.block_size, jump = kCols / bs, rest = kCols - jump * bs;
+        int left = 0, at = 0, head = 0;
+        const int32_t *entry = nullptr;
         auto enter = [&]() {
-            len = walk.s.len;
+            const int pos = walk.step * kCols + dw * kRpw;
+            left = walk.s.len - pos;
             head = walk.head();
-            table = a.block_table + (int64_t)walk.s.b * a.g.max_blocks_per_seq;
-            pos = walk.step * kCols + dw * kRpw;
+            at = pos % bs;
+            entry = a.block_table + (int64_t)walk.s.b * a.g.max_blocks_per_seq + pos / bs;
         };
         auto next = [&]() {
-            pos += kCols;
-            if (pos - dw * kRpw >= len) {
+            left -= kCols;
+            at += rest;
+            entry += jump;
+            if (at >= bs) {
+                at -= bs;
+                ++entry;
+            }
+            if (left + dw * kRpw <= 0) {
                 walk.next_tile(p, lane);
                 enter();
             }
         };
+        auto id = [&]() { return left > 0 ? ld_ahead_s32(entry) : 0; };
         enter();
-        Place x = place(find(table, pos, len, head));
+        Place x = place(id(), at, left, head);
         Codes k, v;
         float sk = 0.0f, sv = 0.0f;
         auto scales = [&]() {
@@ -267,13 +263,13 @@ struct Tree {
             sk = load_scale(x, a.k_scale);
             sv = load_scale(x, a.v_scale);
         };
-        load(x, a.k_cache, k);
         scales();
+        load(x, a.k_cache, k);
         load(x, a.v_cache, v);
-        Id id{};
+        int32_t blk = 0;
         if (total > 1) {
             next();
-            id = find(table, pos, len, head);
+            blk = id();
         }
         for (int n = 0; n < total; ++n) {
             const int st = n % kStages;
@@ -304,12 +300,12 @@ struct Tree {
             arrive(bar.k_full[st]);
             const bool more = n + 1 < total;
             if (more) {  // the next step's codes, and the block id of the one after
-                x = place(id);
-                load(x, a.k_cache, k);
+                x = place(blk, at, left, head);
                 scales();
+                load(x, a.k_cache, k);
                 if (n + 2 < total) {
                     next();
-                    id = find(table, pos, len, head);
+                    blk = id();
                 }
             }
             if (!wait_warp(bar.v_free[st], par ^ 1u)) return;

@@ -180,18 +180,16 @@ constexpr uint32_t instr_desc(int n, bool b_mn) {
 
 // ---- loads ahead ----------------------------------------------------------------------
 
-// Loads whose place in the program matters: a step's codes, scales and block ids are asked for a
-// step before they are used, and the compiler, free to, moves such a load down to its use.
-__device__ __forceinline__ uint4 ld_ahead_16(const void *p) {
-    uint4 v;
-    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                 : "l"(p));
-    return v;
-}
+// Loads whose place in the program matters: a step's scales and block ids are asked for steps
+// before they are used, and the compiler, free to, moves such a load down to its use.
 __device__ __forceinline__ float ld_ahead_f32(const float *p) {
     float v;
     asm volatile("ld.global.nc.f32 %0, [%1];" : "=f"(v) : "l"(p));
+    return v;
+}
+__device__ __forceinline__ float4 ld_ahead_f32x4(const float *p) {
+    float4 v;
+    asm volatile("ld.global.nc.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "l"(p));
     return v;
 }
 __device__ __forceinline__ int32_t ld_ahead_s32(const int32_t *p) {
@@ -268,28 +266,35 @@ struct CodeTile {
     // 16-byte chunk n of a 128-byte row lies at n ^ (row mod 8): a lane's two places repeat
     // (D = 128: with one bit flipped) from load to load, and the eight lanes of an access,
     // on two neighbouring rows, hit different banks.
-    __device__ __forceinline__ static void store(const Codes &c, uint32_t scale, uint32_t tile, int dw, int lane) {
+    __device__ __forceinline__ static void store_load(const uint4 &c, int i, uint32_t scale, uint32_t at, uint32_t c0, uint32_t c1,
+                                                      int r) {
+        const uint32_t wd[4] = {c.x, c.y, c.z, c.w};
+        const uint32_t s = MODE == 1 ? 0u : __shfl_sync(0xFFFFFFFFu, scale, i * kRpl + r);
+        uint32_t o[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            o[e] = codes_fp16(wd[e >> 1] ^ 0x80808080u, (e & 1) ? 0x4342u : 0x4140u);
+            if (MODE != 1) o[e] = mul_fp16(o[e], s);
+        }
+        const uint32_t flip = (uint32_t)(i * kRpl % 8) << 4, row = at + (uint32_t)(i * kRpl * 128);
+        asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(row + (c0 ^ flip)), "r"(o[0]), "r"(o[1]),
+                     "r"(o[2]), "r"(o[3])
+                     : "memory");
+        asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(row + (c1 ^ flip)), "r"(o[4]), "r"(o[5]),
+                     "r"(o[6]), "r"(o[7])
+                     : "memory");
+    }
+    // load(i): the codes of the i-th load; UNROLL of them at once.
+    template <int UNROLL, typename Load>
+    __device__ __forceinline__ static void store_each(Load &&load, uint32_t scale, uint32_t tile, int dw, int lane) {
         const int n = (lane & 3) * 2, r = row_in(lane);
         const uint32_t at = tile + (uint32_t)(dw * RPW + r) * 128 + (uint32_t)block_in(lane) * (kCols * 128);
         const uint32_t c0 = (uint32_t)((n ^ r) << 4), c1 = (uint32_t)(((n + 1) ^ r) << 4);
-#pragma unroll
-        for (int i = 0; i < kLoads; ++i) {
-            const uint32_t wd[4] = {c.c[i].x, c.c[i].y, c.c[i].z, c.c[i].w};
-            const uint32_t s = MODE == 1 ? 0u : __shfl_sync(0xFFFFFFFFu, scale, i * kRpl + r);
-            uint32_t o[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                o[e] = codes_fp16(wd[e >> 1] ^ 0x80808080u, (e & 1) ? 0x4342u : 0x4140u);
-                if (MODE != 1) o[e] = mul_fp16(o[e], s);
-            }
-            const uint32_t flip = (uint32_t)(i * kRpl % 8) << 4, row = at + (uint32_t)(i * kRpl * 128);
-            asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(row + (c0 ^ flip)), "r"(o[0]), "r"(o[1]),
-                         "r"(o[2]), "r"(o[3])
-                         : "memory");
-            asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(row + (c1 ^ flip)), "r"(o[4]), "r"(o[5]),
-                         "r"(o[6]), "r"(o[7])
-                         : "memory");
-        }
+#pragma unroll UNROLL
+        for (int i = 0; i < kLoads; ++i) store_load(load(i), i, scale, at, c0, c1, r);
+    }
+    __device__ __forceinline__ static void store(const Codes &c, uint32_t scale, uint32_t tile, int dw, int lane) {
+        store_each<kLoads>([&](int i) { return c.c[i]; }, scale, tile, dw, lane);
     }
 };
 

@@ -7,18 +7,21 @@
 // tensor cores more.
 //
 // tree_kernel: one persistent CTA per SM, a tile of 128 query rows, 128 positions a step.  S = Q
-// K'^T and O += P V' are tcgen05.mma (M = 128, fp16, fp32 in tensor memory); P replaces S in
-// tensor memory and is the second product's A operand.  Warps by role:
-//   softmax     4, a thread per query row: S from tensor memory, one-pass softmax (Milakov and
-//               Gimelshein, Online normalizer calculation for softmax, 2018), P back; any m cancels
-//               in the quotient, so the running maximum moves only when the weights grow by more
-//               than 2^8, and O is seldom rescaled.  Warps without a row do nothing
-//   rows        4: the next tile's queries into shared memory, the last one's O out of tensor memory
-//   dequantise  8: codes from global memory a step ahead in registers, K' and V' as fp16 into a
-//               two-stage ring
+// K'^T and O += P V' are tcgen05.mma (M = 128, fp16, fp32 in tensor memory); Q lies in tensor memory,
+// and P replaces S there: both are A operands.  Warps by role:
+//   walk        1: what the CTA's next tiles are
+//   fetch       1: pages' codes by bulk copies into a ring in shared memory, as many steps ahead as fit
+//   dequantise  8: codes to K' and V' as fp16, two stages of each in shared memory
 //   mma         one lane issues both products
-// S and O are there twice: the scores of a step are made while the softmax works on the step before,
-// and a tile's first products run while the last one's O is written.
+//   softmax     8, two threads per query row, half of a step's positions each: S from tensor memory,
+//               one-pass softmax (Milakov and Gimelshein, Online normalizer calculation for softmax,
+//               2018), P back; any m cancels in the quotient, so the running maximum moves only when
+//               the weights grow by more than 2^8, and O is seldom rescaled.  Warps without a row do
+//               nothing
+//   rows        4: the next tile's queries into tensor memory, the last one's O out of it
+// S and Q are there twice: the scores of a step are made while the softmax works on the step before.  The roles'
+// loops are kept short: together they must fit the SM's instruction cache (with 95 KB of code, of which each
+// step ran through about 30, a step took 3100 cycles and the warps waited for instructions).
 //
 // The units (sequence, kv head, row tile, step) are numbered in that order and cut into equal shares,
 // a CTA's share in a row: ragged lengths need no plan, every CTA adds up the lengths itself.  What a
@@ -33,8 +36,10 @@ namespace {
 
 constexpr int kStages = 2;     // steps of K', of V', of S; tiles of Q and O
 constexpr int kMaskSlots = 4;  // steps whose valid counts are kept
+constexpr int kTiles = 4;      // tiles that are known ahead
 constexpr int kMaxCtas = 152;  // SMs of a GB300
 constexpr int kMergeThreads = 256;
+constexpr uint32_t kWaitTicks = 4000000000u;  // of the SM's clock: about two seconds
 
 // ---- the work -----------------------------------------------------------------------
 
@@ -84,77 +89,65 @@ struct Cut {
     }
 };
 
-// A walk over a CTA's share, tile by tile; the next sequence's lengths are on their way.  Each warp has
-// its own in shared memory: it is looked at once a tile, and in registers the whole of it would push out what
-// a step needs.
-struct Walk {
-    Seq s;
-    Raw ahead;
-    int tile, step;  // tile: kv head * s.tiles + row tile; step: the first of it in the share
-    __device__ __forceinline__ int head() const { return tile / s.tiles; }
-    __device__ __forceinline__ int row0() const { return (tile - tile / s.tiles * s.tiles) * kRows; }
-    // By a whole warp, and only where the share goes on: there is a next tile then.
-    __device__ __forceinline__ void next_tile(const TreeArgs &p, int lane) {
-        __syncwarp();
-        if (lane == 0) {
-            step = 0;
-            if (tile + 1 < s.tiles * p.base.g.kv_heads) {
-                ++tile;
-            } else {
-                tile = 0;
-                Seq x = s;
-                Raw r = ahead;
-                do {
-                    x = make_seq(p, x.b + 1, r);
-                    r = read_raw(p, x.b + 1);
-                } while (x.drafts == 0 && x.b + 1 < p.base.g.num_seqs);
-                s = x;
-                ahead = r;
-            }
-        }
-        __syncwarp();
-    }
+// A tile of a CTA's share, for the roles.
+struct Tile {
+    int32_t b, token, ctx, len;  // its sequence
+    int32_t rows, row0, head;    // query rows of the sequence, the tile's first, the kv head
+    int32_t step, count, steps;  // the share's first step of it and how many of all
 };
 
 // ---- the kernel ---------------------------------------------------------------------
 
 template <int D>
 struct Layout {
-    static constexpr int kSoftmaxWarps = 4, kRowWarps = 4, kDequantWarps = 8;
-    static constexpr int kDequantWarp = kSoftmaxWarps + kRowWarps;
-    static constexpr int kMmaWarp = kDequantWarp + kDequantWarps;  // three idle warps behind it
-    static constexpr int kThreads = 640;
-    // Registers per thread: a softmax thread holds a row's 128 scores, a dequantising one two tiles'
-    // codes in flight.
-    static constexpr int kSoftmaxRegs = 184, kRowRegs = 64, kDequantRegs = 96, kMmaRegs = 40;
-    static constexpr int kLaunchRegs = 96;
+    static constexpr int kSoftmaxWarps = 8, kRowWarps = 4, kDequantWarps = 8;
+    static constexpr int kRowWarp = kSoftmaxWarps, kDequantWarp = kRowWarp + kRowWarps;
+    static constexpr int kMmaWarp = kDequantWarp + kDequantWarps, kFetchWarp = kMmaWarp + 1, kWalkWarp = kMmaWarp + 2;
+    static constexpr int kThreads = 768;
+    // Registers per thread: a softmax thread holds 64 scores, one with a row of queries or outputs 64 pairs.
+    static constexpr int kSoftmaxRegs = 112, kRowRegs = 72, kDequantRegs = 64, kMmaRegs = 48;
+    static constexpr int kLaunchRegs = 80;
     static_assert(32 * (kSoftmaxWarps * kSoftmaxRegs + kRowWarps * kRowRegs + kDequantWarps * kDequantRegs +
                         4 * kMmaRegs) <= kThreads * kLaunchRegs,
                   "the warpgroups' registers are the block's");
-    static constexpr int kTileBytes = kRows * D * 2;  // a Q tile, K' or V' stage
-    static constexpr int kQ = 0;
-    static constexpr int kK = kStages * kTileBytes;
-    static constexpr int kV = 2 * kStages * kTileBytes;
-    static constexpr int kEnd = 3 * kStages * kTileBytes;
+    static constexpr int kTileBytes = kCols * D * 2;  // a K' or V' stage
+    static constexpr int kRawBytes = kCols * D;       // a slot of the ring: a step's codes of keys or of values
+    static constexpr int kRing = 80 * 1024 / kRawBytes;
+    static constexpr int kK = 0;
+    static constexpr int kV = kStages * kTileBytes;
+    static constexpr int kRaw = 2 * kStages * kTileBytes;
     // more than half of an SM's shared memory, so that a CTA has the SM's tensor memory to itself
-    static constexpr int kBytes = (kEnd > 120 * 1024 ? kEnd : 120 * 1024) + 1024;
-    static constexpr int kO = kStages * kCols;  // columns of tensor memory: S twice, then O
+    static constexpr int kBytes = kRaw + kRing * kRawBytes + 1024;
+    static_assert(kBytes > 116 * 1024, "one CTA per SM");
+    static constexpr int kO = kStages * kCols, kQ = kO + D;  // columns of tensor memory: S twice, O, Q twice
     static constexpr int kTmemCols = 512;
+    static_assert(kQ + kStages * D / 2 <= kTmemCols, "tensor memory");
 };
+constexpr int kMaxRing = Layout<64>::kRing;
 
 struct Barriers {
     // s_full: a step's scores, and its K' stage is free; v_free: its weighted values, and its V' stage
     uint64_t k_full[kStages], v_full[kStages], s_full[kStages], p_full[kStages], v_free[kStages];
-    uint64_t q_full[kStages], q_free[kStages], o_full[kStages], o_free[kStages], ml_full[kStages], drained;
+    uint64_t q_full[kStages], q_free[kStages], o_full, o_free, ml_full, drained;
+    uint64_t raw_full[kMaxRing], raw_free[kMaxRing];
+    uint64_t pair[4];  // the two softmax warps of 32 rows
+    uint64_t tile_full[kTiles], tile_free[kTiles];
     uint32_t tmem;
     int32_t stop;
     uint32_t sum[Layout<128>::kThreads / 32];
     int32_t start_b;
     uint32_t start_off;
-    int32_t total;  // units of this CTA
-    Walk walk[Layout<128>::kMmaWarp + 1], walk_out[4];  // of each warp; of the rows that go out
+    uint32_t units, first;  // of all CTAs, this one's
+    int32_t total;          // units of this CTA
+    int32_t pad[2];
+    Tile tile[kTiles];
     float q_scale[kStages][kRows];  // log2 per unit of score, with the query's power of two
-    float m[kStages][kRows], l[kStages][kRows];
+    float m[kRows], l[2][kRows];    // l: of each half of the positions
+    float top[2][2][kRows];         // a step's largest score of each half, of two steps
+    // of the steps in the ring, where their keys lie: valid positions of each group of 16, scales (mode 2: one a group)
+    uint2 raw_valid[kMaxRing];
+    alignas(16) float raw_ks[kMaxRing][kCols];
+    alignas(16) float raw_vs[kMaxRing][kCols];
     uint2 valid[kMaskSlots];  // 8 bytes: valid positions of each group of 16
     // modes 0 and 2: what was taken out of each group of 16's scales, as powers of two:
     // the keys' 2^e, the values' e and 2^-e
@@ -168,222 +161,320 @@ struct Tree {
     using L = Layout<D>;
     static constexpr int kRpw = kCols / L::kDequantWarps;  // positions of a warp: one group of 16
     using T = CodeTile<MODE, D, kRpw>;
-    using Codes = typename T::Codes;
     static_assert(T::kGroups == 1, "a warp's positions lie in one block");
 
     const TreeArgs &p;
     Barriers &bar;
     const uint32_t base, tmem;  // shared memory, 1 KB aligned
     const int total;            // units of this CTA
-    Walk &walk;                 // this warp's
     const int lane, warp;
 
     // (Read again here, by each role for itself, than kept in registers from the kernel's start.)
     __device__ __forceinline__ Tree(const TreeArgs &args, Barriers &b, uint8_t *dyn)
-        : p(args), bar(b), base((smem_u32(dyn) + 1023u) & ~1023u), tmem(b.tmem), total(b.total),
-          walk(b.walk[threadIdx.x >> 5]), lane(threadIdx.x & 31), warp(threadIdx.x >> 5) {}
+        : p(args), bar(b), base((smem_u32(dyn) + 1023u) & ~1023u), tmem(b.tmem), total(b.total), lane(threadIdx.x & 31),
+          warp(threadIdx.x >> 5) {}
 
+    // A whole warp waits and stays converged.  false: the limit ran out here or elsewhere in the CTA.
     __device__ __forceinline__ bool wait(uint64_t &b, uint32_t parity) const {
-        return wait_limited(b, parity, bar.stop, p.base.dev_error);
-    }
-    // The same for a whole warp, which leaves it converged.
-    __device__ __forceinline__ bool wait_warp(uint64_t &b, uint32_t parity) const {
-        return __all_sync(0xFFFFFFFFu, wait(b, parity));
+        const uint32_t at = smem_u32(&b);
+        bool ok = mbar_try(at, parity);
+        if (!ok) {
+            const uint32_t t0 = clock();
+            do {
+                ok = mbar_try(at, parity);
+            } while (!ok && *static_cast<volatile int32_t *>(&bar.stop) == 0 && (uint32_t)clock() - t0 < kWaitTicks);
+            if (!ok) *static_cast<volatile int32_t *>(&bar.stop) = 1;
+        }
+        return __all_sync(0xFFFFFFFFu, ok);
     }
     __device__ __forceinline__ void arrive(uint64_t &b) const {
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&b));
     }
 
-    // ---- dequantise ------------------------------------------------------------
-    // Where a warp's group of 16 positions lies; of the step whose block id is asked for next.
-    struct Place {
-        int64_t page;       // block * heads + head
-        int32_t at, valid;  // first slot in the block; positions before the end
-    };
-    __device__ __forceinline__ Place place(int32_t blk, int at, int valid, int head) const {
-        const bool in = blk >= 0 && blk < p.base.g.num_blocks;
-        if (!in && lane == 0) report(p.base.dev_error, KVC8_DEV_BAD_BLOCK_ID);
-        return Place{(int64_t)(in ? blk : 0) * p.base.g.kv_heads + head, at, in ? max(0, min(16, valid)) : 0};
-    }
-    __device__ __forceinline__ void load(const Place &x, const int8_t *cache, Codes &c) const {
-        const int8_t *src = cache + (x.page * p.base.g.block_size + x.at + T::row_in(lane)) * D + T::block_in(lane) * 64 + lane % 4 * 16;
-        if (x.valid == 16) {
-#pragma unroll
-            for (int i = 0; i < T::kLoads; ++i) c.c[i] = ld_ahead_16(src + i * T::kRpl * D);
-        } else {
-#pragma unroll
-            for (int i = 0; i < T::kLoads; ++i) {
-                c.c[i] = make_uint4(0u, 0u, 0u, 0u);
-                if (i * T::kRpl + T::row_in(lane) < x.valid) c.c[i] = ld_ahead_16(src + i * T::kRpl * D);
+    // ---- walk (a warp) ------------------------------------------------------------
+    __device__ void walk() const {
+        int b = bar.start_b;
+        Seq s = make_seq(p, b, read_raw(p, b));
+        Raw ahead = read_raw(p, b + 1);  // the next sequence's lengths are on their way
+        int tile = (int)(bar.start_off / (uint32_t)s.steps);  // kv head * s.tiles + row tile
+        int step = (int)(bar.start_off - (uint32_t)tile * (uint32_t)s.steps);
+        int left = total;
+        for (uint32_t seg = 0; left > 0; ++seg) {
+            Tile x;
+            x.b = s.b;
+            x.token = s.token;
+            x.ctx = s.ctx;
+            x.len = s.len;
+            x.rows = s.drafts * p.base.group;
+            x.head = tile / s.tiles;
+            x.row0 = (tile - x.head * s.tiles) * kRows;
+            x.step = step;
+            x.count = min(left, s.steps - step);
+            x.steps = s.steps;
+            if (!wait(bar.tile_free[seg % kTiles], ((seg / kTiles) & 1u) ^ 1u)) return;
+            if (lane == 0) bar.tile[seg % kTiles] = x;
+            arrive(bar.tile_full[seg % kTiles]);
+            if (seg == 0 && lane == 0) {
+                TreeShare r;
+                r.units = bar.units;
+                r.first = bar.first - (uint32_t)step;
+                r.steps = x.steps;
+                r.token = x.token;
+                r.rows = x.rows;
+                r.row = x.row0;
+                r.head = x.head;
+                r.pad = 0;
+                p.shares[blockIdx.x] = r;
+            }
+            left -= x.count;
+            step = 0;
+            if (++tile == s.tiles * p.base.g.kv_heads && left > 0) {
+                tile = 0;
+                do {
+                    s = make_seq(p, s.b + 1, ahead);
+                    ahead = read_raw(p, s.b + 1);
+                } while (s.drafts == 0 && s.b + 1 < p.base.g.num_seqs);
             }
         }
     }
-    // Modes 0 and 2: the scale of position `lane` of the group.
-    __device__ __forceinline__ float load_scale(const Place &x, const float *scale) const {
-        const int64_t at = MODE == 0 ? x.page * p.base.g.block_size + x.at + lane : x.page;
-        return lane < x.valid ? ld_ahead_f32(scale + at) : 0.0f;  // (16 at most)
+    // The share's tile number `seg`, and that a warp needs it no more.
+    __device__ __forceinline__ bool enter(uint32_t seg) const { return wait(bar.tile_full[seg % kTiles], (seg / kTiles) & 1u); }
+    __device__ __forceinline__ void leave(uint32_t seg) const { arrive(bar.tile_free[seg % kTiles]); }
+    __device__ __forceinline__ const Tile &tile(uint32_t seg) const { return bar.tile[seg % kTiles]; }
+
+    // ---- fetch (a warp) ----------------------------------------------------------
+    // Lanes 0-7 have a group of 16 positions each: a step's groups may lie in different blocks.  In the loop's
+    // turn n, step n is copied, step n + 1 is placed and its scales asked for, and the block ids of step n + 2 are.
+    __device__ __forceinline__ void copy(uint32_t dst, const int8_t *src, uint64_t &full) const {
+        asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+                     "l"(src), "r"((uint32_t)(16 * D)), "r"(smem_u32(&full))
+                     : "memory");
+    }
+    __device__ void fetch() const {
+        const AttnArgs &a = p.base;
+        const int grp = lane & 7, bs = a.g.block_size;
+        uint32_t seg = 0;
+        int count = 0;                // steps of the tile not asked for yet
+        int left = 0, at = 0, head = 0;  // of the step asked for: positions left, slot and entry of the table
+        const int32_t *entry = nullptr;
+        int32_t blk = 0;
+        int64_t row = 0;  // of the step placed: cache row of the group's first position, how many of it
+        int valid = 0;
+        float4 ks = make_float4(0.0f, 0.0f, 0.0f, 0.0f), vs = ks;  // mode 0: of positions 4 lane .. 4 lane + 3; mode 2: .x, of the group
+        int slot = 0;
+        uint32_t round = 0;
+        bool good = true;
+#pragma unroll 1
+        for (int n = -2; n < total && good; ++n) {
+            if (n >= 0) {
+#pragma unroll 1
+                for (int values = 0; values < 2 && good; ++values) {
+                    good = wait(bar.raw_free[slot], round ^ 1u);
+                    if (!good) break;
+                    if (values == 0) {
+                        if (lane < 8) reinterpret_cast<uint8_t *>(&bar.raw_valid[slot])[grp] = (uint8_t)valid;
+                        if (MODE == 0) {
+                            reinterpret_cast<float4 *>(bar.raw_ks[slot])[lane] = ks;
+                            reinterpret_cast<float4 *>(bar.raw_vs[slot])[lane] = vs;
+                        } else if (MODE == 2 && lane < 8) {
+                            bar.raw_ks[slot][grp] = ks.x;
+                            bar.raw_vs[slot][grp] = vs.x;
+                        }
+                    }
+                    const uint32_t groups = __popc(__ballot_sync(0xFFFFFFFFu, lane < 8 && valid > 0));
+                    if (lane == 0)
+                        asm volatile("mbarrier.arrive.expect_tx.release.cta.shared::cta.b64 _, [%0], %1;" ::"r"(
+                                         smem_u32(&bar.raw_full[slot])),
+                                     "r"(groups * 16u * D)
+                                     : "memory");
+                    __syncwarp();
+                    if (lane < 8 && valid > 0)
+                        copy(base + L::kRaw + slot * L::kRawBytes + grp * 16 * D, (values == 0 ? a.k_cache : a.v_cache) + row * D,
+                             bar.raw_full[slot]);
+                    if (++slot == L::kRing) {
+                        slot = 0;
+                        round ^= 1u;
+                    }
+                }
+            }
+            if (n >= -1 && n + 1 < total) {
+                const bool in = blk >= 0 && blk < a.g.num_blocks;
+                if (!in && lane < 8) report(a.dev_error, KVC8_DEV_BAD_BLOCK_ID);
+                valid = in ? max(0, min(16, left)) : 0;
+                const int64_t page = (int64_t)(in ? blk : 0) * a.g.kv_heads + head;
+                row = page * bs + at;
+                if (MODE == 0) {
+                    const int64_t r = __shfl_sync(0xFFFFFFFFu, row, lane / 4) + lane % 4 * 4;
+                    if (__shfl_sync(0xFFFFFFFFu, valid, lane / 4) > 0) {
+                        ks = ld_ahead_f32x4(a.k_scale + r);
+                        vs = ld_ahead_f32x4(a.v_scale + r);
+                    }
+                } else if (MODE == 2 && valid > 0) {
+                    ks.x = ld_ahead_f32(a.k_scale + page);
+                    vs.x = ld_ahead_f32(a.v_scale + page);
+                }
+            }
+            if (good && n + 2 < total) {
+                if (count == 0) {
+                    good = enter(seg);
+                    if (!good) break;
+                    const Tile &x = tile(seg);
+                    const int pos = x.step * kCols + grp * 16;
+                    left = x.len - pos;
+                    head = x.head;
+                    at = pos % bs;
+                    entry = a.block_table + (int64_t)x.b * a.g.max_blocks_per_seq + pos / bs;
+                    count = x.count;
+                    leave(seg++);
+                } else {
+                    left -= kCols;
+                    at += kCols % bs;
+                    entry += kCols / bs;
+                    if (at >= bs) {
+                        at -= bs;
+                        ++entry;
+                    }
+                }
+                --count;
+                blk = left > 0 ? ld_ahead_s32(entry) : 0;
+            }
+        }
+        // nothing is in flight when the CTA ends, not after a wait that ran out either (a slot never used has no
+        // phase to wait for: its barrier answers for the phase before its first)
+#pragma unroll 1
+        for (int i = 0; i < L::kRing; ++i) {
+            const uint32_t t0 = clock();
+            while (!mbar_try(smem_u32(&bar.raw_full[slot]), round ^ 1u))
+                if ((uint32_t)clock() - t0 > kWaitTicks) break;
+            if (++slot == L::kRing) {
+                slot = 0;
+                round ^= 1u;
+            }
+        }
     }
 
+    // ---- dequantise (a warp has a group of 16 positions) ------------------------------------------------
+    // Keys and values of a step in turn, by the same few instructions: what the roles on an SM run through must
+    // fit the instruction caches.
     __device__ void dequantise() const {
-        const AttnArgs &a = p.base;
         const int dw = warp - L::kDequantWarp;
-        // of the step whose block id is asked for next: positions left, slot and entry of the table; a
-        // step is `jump` blocks and `rest` slots further on
-        const int bs = a.g.block_size, jump = kCols / bs, rest = kCols - jump * bs;
-        int left = 0, at = 0, head = 0;
-        const int32_t *entry = nullptr;
-        auto enter = [&]() {
-            const int pos = walk.step * kCols + dw * kRpw;
-            left = walk.s.len - pos;
-            head = walk.head();
-            at = pos % bs;
-            entry = a.block_table + (int64_t)walk.s.b * a.g.max_blocks_per_seq + pos / bs;
-        };
-        auto next = [&]() {
-            left -= kCols;
-            at += rest;
-            entry += jump;
-            if (at >= bs) {
-                at -= bs;
-                ++entry;
-            }
-            if (left + dw * kRpw <= 0) {
-                walk.next_tile(p, lane);
-                enter();
-            }
-        };
-        auto id = [&]() { return left > 0 ? ld_ahead_s32(entry) : 0; };
-        enter();
-        Place x = place(id(), at, left, head);
-        Codes k, v;
-        float sk = 0.0f, sv = 0.0f;
-        auto scales = [&]() {
-            if (MODE == 1) return;
-            sk = load_scale(x, a.k_scale);
-            sv = load_scale(x, a.v_scale);
-        };
-        scales();
-        load(x, a.k_cache, k);
-        load(x, a.v_cache, v);
-        int32_t blk = 0;
-        if (total > 1) {
-            next();
-            blk = id();
-        }
-        for (int n = 0; n < total; ++n) {
-            const int st = n % kStages;
-            const uint32_t par = (uint32_t)(n / kStages) & 1u;
-            if (!wait_warp(bar.s_full[st], par ^ 1u)) return;
-            uint32_t sk_half = 0u, sv_half = 0u;
-            if (MODE != 1) {
-                // A scale that is no number must not reach the rows that do not see its position,
-                // nor the other scales' power: the value counts as zero, and the score as no number.
-                const bool odd = (__float_as_uint(sk) & 0x7F800000u) == 0x7F800000u ||
-                                 (__float_as_uint(sv) & 0x7F800000u) == 0x7F800000u;
-                sk = odd ? 0.0f : sk;
-                sv = odd ? 0.0f : sv;
-                int ek, ev;
-                const uint32_t top_k = T::group_top(sk, lane), top_v = T::group_top(sv, lane);
-                sk_half = T::normal_scale(sk, top_k, -100, ek);
-                sv_half = T::normal_scale(sv, top_v, kLeastValuePower, ev);
-                if (odd) sk_half = 0x7FFF7FFFu;
-                if (lane == 0) {
-                    bar.k_pow[n % kMaskSlots][dw] = __uint_as_float((uint32_t)(127 + ek) << 23);
-                    bar.v_exp[n % kMaskSlots][dw] = (float)ev;
-                    bar.v_inv[n % kMaskSlots][dw] = __uint_as_float((uint32_t)(127 - ev) << 23);
+        const uint32_t src = base + L::kRaw + (uint32_t)((dw * 16 + T::row_in(lane)) * D + T::block_in(lane) * 64 + lane % 4 * 16);
+        int slot = 0;
+        uint32_t round = 0, next_scale = 0u;
+#pragma unroll 1
+        for (int i = 0; i < 2 * total; ++i) {
+            const int n = i >> 1, values = i & 1, st = n % kStages;
+            if (!wait(bar.raw_full[slot], round)) return;
+            uint32_t scale = next_scale;
+            if (values == 0) {
+                const int valid = reinterpret_cast<const uint8_t *>(&bar.raw_valid[slot])[dw];
+                if (MODE != 1) {
+                    float sk = 0.0f, sv = 0.0f;  // positions behind the end may have any scale
+                    if (lane < valid) {
+                        sk = bar.raw_ks[slot][MODE == 0 ? dw * 16 + lane : dw];
+                        sv = bar.raw_vs[slot][MODE == 0 ? dw * 16 + lane : dw];
+                    }
+                    // A scale that is no number must not reach the rows that do not see its position,
+                    // nor the other scales' power: the value counts as zero, and the score as no number.
+                    const bool odd = (__float_as_uint(sk) & 0x7F800000u) == 0x7F800000u ||
+                                     (__float_as_uint(sv) & 0x7F800000u) == 0x7F800000u;
+                    sk = odd ? 0.0f : sk;
+                    sv = odd ? 0.0f : sv;
+                    int ek, ev;
+                    const uint32_t top_k = T::group_top(sk, lane), top_v = T::group_top(sv, lane);
+                    scale = T::normal_scale(sk, top_k, -100, ek);
+                    next_scale = T::normal_scale(sv, top_v, kLeastValuePower, ev);
+                    if (odd) scale = 0x7FFF7FFFu;
+                    // (every use of this slot of the step four before is over: its values are in V')
+                    if (lane == 0) {
+                        bar.k_pow[n % kMaskSlots][dw] = __uint_as_float((uint32_t)(127 + ek) << 23);
+                        bar.v_exp[n % kMaskSlots][dw] = (float)ev;
+                        bar.v_inv[n % kMaskSlots][dw] = __uint_as_float((uint32_t)(127 - ev) << 23);
+                    }
                 }
+                if (lane == 0) reinterpret_cast<uint8_t *>(&bar.valid[n % kMaskSlots])[dw] = (uint8_t)valid;
             }
-            T::store(k, sk_half, base + L::kK + st * L::kTileBytes, dw, lane);
-            if (lane == 0) reinterpret_cast<uint8_t *>(&bar.valid[n % kMaskSlots])[dw] = (uint8_t)x.valid;
+            if (!wait(values == 0 ? bar.s_full[st] : bar.v_free[st], ((uint32_t)(n / kStages) & 1u) ^ 1u)) return;
+            T::template store_each<2>(
+                [&](int k) {
+                    uint4 c;
+                    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                                 : "=r"(c.x), "=r"(c.y), "=r"(c.z), "=r"(c.w)
+                                 : "r"(src + slot * L::kRawBytes + k * T::kRpl * D)
+                                 : "memory");
+                    return c;
+                },
+                scale, base + (values == 0 ? L::kK : L::kV) + st * L::kTileBytes, dw, lane);
             fence_async();
-            arrive(bar.k_full[st]);
-            const bool more = n + 1 < total;
-            if (more) {  // the next step's codes, and the block id of the one after
-                x = place(blk, at, left, head);
-                scales();
-                load(x, a.k_cache, k);
-                if (n + 2 < total) {
-                    next();
-                    blk = id();
-                }
+            arrive(values == 0 ? bar.k_full[st] : bar.v_full[st]);
+            if (lane == 0) mbar_arrive(smem_u32(&bar.raw_free[slot]));
+            if (++slot == L::kRing) {
+                slot = 0;
+                round ^= 1u;
             }
-            if (!wait_warp(bar.v_free[st], par ^ 1u)) return;
-            T::store(v, sv_half, base + L::kV + st * L::kTileBytes, dw, lane);
-            fence_async();
-            arrive(bar.v_full[st]);
-            if (more) load(x, a.v_cache, v);
         }
     }
 
     // ---- products (a warp, one lane issuing) --------------------------------------------------
     __device__ __forceinline__ void qk(int q, int st, uint32_t tm, uint32_t leader) const {
-        const uint64_t qd = operand_desc(base + L::kQ, 16) + (uint64_t)(q * (L::kTileBytes >> 4));
         const uint64_t kd = operand_desc(base + L::kK, 16) + (uint64_t)(st * (L::kTileBytes >> 4));
 #pragma unroll
         for (int i = 0; i < D / 16; ++i) {
-            const uint64_t at = (uint64_t)(((i / 4) * (kRows * 128) + (i % 4) * 32) >> 4);
-            tc_mma_ss(tm + st * kCols, qd + at, kd + at, instr_desc(kCols, false), i > 0, leader);
+            const uint64_t at = (uint64_t)(((i / 4) * (kCols * 128) + (i % 4) * 32) >> 4);
+            tc_mma_ts(tm + st * kCols, tm + L::kQ + q * (D / 2) + 8 * i, kd + at, instr_desc(kCols, false), i > 0, leader);
         }
     }
-    __device__ __forceinline__ void pv(int o, int st, uint32_t tm, bool acc, uint32_t leader) const {
+    __device__ __forceinline__ void pv(int st, uint32_t tm, bool acc, uint32_t leader) const {
         const uint64_t v = operand_desc(base + L::kV, kCols * 128) + (uint64_t)(st * (L::kTileBytes >> 4));
 #pragma unroll
         for (int i = 0; i < kCols / 16; ++i)
-            tc_mma_ts(tm + L::kO + o * D, tm + st * kCols + 8 * i, v + (uint64_t)(i * (2048 >> 4)), instr_desc(D, true),
+            tc_mma_ts(tm + L::kO, tm + st * kCols + 8 * i, v + (uint64_t)(i * (2048 >> 4)), instr_desc(D, true),
                       acc || i > 0, leader);
     }
     // What steers the loop comes from lane 0, so that the compiler keeps it, and with it stages,
     // addresses and descriptors, in uniform registers.
     __device__ __forceinline__ static int uniform(int x) { return __shfl_sync(0xFFFFFFFFu, x, 0); }
 
+    // Turn n: the scores of step n + 1, then the weighted values of step n.
     __device__ bool products_loop(uint32_t leader) const {
         const uint32_t tm = (uint32_t)uniform((int)tmem);
         const int units = uniform(total);
-        int left = uniform(walk.s.steps - walk.step);  // steps of the tile from the next scores on
-        uint32_t q_seg = 0, seg = 0;             // tile of the next scores, of the next weighted values
-        bool q_first = true;
-        // Scores of unit n; returns whether it is its tile's last.
-        auto scores = [&](int n, bool &ok) {
-            const int st = n & 1, q = (int)(q_seg & 1u);
-            ok = (!q_first || wait_warp(bar.q_full[q], (q_seg >> 1) & 1u)) && wait_warp(bar.k_full[st], (uint32_t)(n >> 1) & 1u);
-            if (!ok) return false;
-            tc_fence_after();
-            qk(q, st, tm, leader);
-            tc_commit(smem_u32(&bar.s_full[st]), leader);
-            const bool last = --left == 0 || n + 1 == units;
-            q_first = last;
-            if (last) {
-                tc_commit(smem_u32(&bar.q_free[q]), leader);
-                ++q_seg;
-                if (n + 1 < units) {
-                    walk.next_tile(p, lane);
-                    left = uniform(walk.s.steps);
-                }
-            }
-            return last;
-        };
-        bool ok, first = true, last = scores(0, ok);
-        if (!ok) return false;
-        for (int n = 0; n < units; ++n) {
-            const int st = n & 1, o = (int)(seg & 1u);
-            bool next_last = false;
+        int left = 0;                       // steps of the tile whose scores are still to come
+        uint32_t q_seg = 0, seg = 0;        // the next tile of the scores, the tile of the weighted values
+        bool first = true, last = false, next_first = true, next_last = false;
+#pragma unroll 1
+        for (int n = -1; n < units; ++n) {
+            first = next_first, last = next_last;
             if (n + 1 < units) {
-                next_last = scores(n + 1, ok);
-                if (!ok) return false;
+                const int st = (n + 1) & 1;
+                next_first = left == 0;
+                if (next_first) {
+                    if (!enter(q_seg)) return false;
+                    left = uniform(tile(q_seg).count);
+                    leave(q_seg);
+                    if (!wait(bar.q_full[q_seg & 1u], (q_seg >> 1) & 1u)) return false;
+                    ++q_seg;
+                }
+                if (!wait(bar.k_full[st], (uint32_t)((n + 1) >> 1) & 1u)) return false;
+                tc_fence_after();
+                qk((int)((q_seg - 1) & 1u), st, tm, leader);
+                tc_commit(smem_u32(&bar.s_full[st]), leader);
+                next_last = --left == 0;
+                if (next_last) tc_commit(smem_u32(&bar.q_free[(q_seg - 1) & 1u]), leader);
             }
-            if (first && !wait_warp(bar.o_free[o], ((seg >> 1) & 1u) ^ 1u)) return false;
-            if (!wait_warp(bar.v_full[st], (uint32_t)(n >> 1) & 1u)) return false;
-            if (!wait_warp(bar.p_full[st], (uint32_t)(n >> 1) & 1u)) return false;
+            if (n < 0) continue;
+            const int st = n & 1;
+            if (first && !wait(bar.o_free, (seg & 1u) ^ 1u)) return false;
+            if (!wait(bar.v_full[st], (uint32_t)(n >> 1) & 1u)) return false;
+            if (!wait(bar.p_full[st], (uint32_t)(n >> 1) & 1u)) return false;
             tc_fence_after();
-            pv(o, st, tm, !first, leader);
+            pv(st, tm, !first, leader);
             tc_commit(smem_u32(&bar.v_free[st]), leader);
             if (last) {
-                tc_commit(smem_u32(&bar.o_full[o]), leader);
+                tc_commit(smem_u32(&bar.o_full), leader);
                 ++seg;
             }
-            first = last;
-            last = next_last;
         }
         return true;
     }
@@ -392,93 +483,91 @@ struct Tree {
         products_loop(leader);
         // what was issued is done before the tensor memory is freed
         tc_commit(smem_u32(&bar.drained), leader);
-        const long long t0 = clock64();
+        const uint32_t t0 = clock();
         while (!mbar_try(smem_u32(&bar.drained), 0))
-            if (clock64() - t0 > kWaitCycles) break;
+            if ((uint32_t)clock() - t0 > kWaitTicks) break;
     }
 
-    // ---- rows in, rows out (a warp has 32 rows of the tile) ------------------------------------------
+    // ---- rows in, rows out (a thread per row of the tile) ------------------------------------------
     // Query rows of a tile, in mode 1 times the channels' key scales: fp16 after a power of two that
     // brings a row's largest value to [1, 2) and goes into its factor.  Eleven bits hold a bf16 value
     // whole (mode 1: round the product eight times finer than bf16); below 2^-14 of the largest they
-    // thin out to 2^-25 of it.  D / 8 lanes a row, kAhead loads in flight.
-    __device__ __forceinline__ void load_rows(const Walk &w, int rw, int buf) const {
-        constexpr int kLanes = D / 8, kWarpRows = 32 / kLanes, kAhead = 4;
+    // thin out to 2^-25 of it.
+    __device__ __forceinline__ void load_rows(const Tile &w, int rw, int buf) const {
         const AttnArgs &a = p.base;
-        const int h = w.head(), r0 = w.row0() + rw * 32, rows = w.s.drafts * a.group;
-        const int c = lane % kLanes;
-        const bool flip = a.scale_log2 < 0.0f;  // the sign goes to the query
-        float ks[8];
-        if (MODE == 1) {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) ks[e] = __ldg(a.k_scale + (int64_t)h * D + 8 * c + e);
-        }
-#pragma unroll 1
-        for (int i0 = 0; i0 < 32 / kWarpRows; i0 += kAhead) {
-            if (r0 + i0 * kWarpRows >= (rows + 31) / 32 * 32) break;
-            uint4 v[kAhead];
-#pragma unroll
-            for (int i = 0; i < kAhead; ++i) {
-                const int r = r0 + (i0 + i) * kWarpRows + lane / kLanes;
-                v[i] = make_uint4(0u, 0u, 0u, 0u);
-                if (r < rows) {
-                    const int t = r / a.group, j = r - t * a.group;
-                    v[i] = __ldg(reinterpret_cast<const uint4 *>(a.q + (int64_t)(w.s.token + t) * a.q_seq_stride +
-                                                                 (int64_t)(h * a.group + j) * a.q_head_stride + 8 * c));
+        const int h = w.head, r0 = w.row0 + rw * 32, rows = w.rows;
+        if (r0 < rows) {  // uniform in the warp: some row is a query's
+            const int r = r0 + lane, t = r / a.group, j = r - t * a.group;
+            const uint16_t *q = a.q + (int64_t)(w.token + t) * a.q_seq_stride + (int64_t)(h * a.group + j) * a.q_head_stride;
+            const float *ks = a.k_scale + (MODE == 1 ? (int64_t)h * D : 0);
+            // chunk i of the row, eight channels
+            auto read = [&](int i) { return r < rows ? __ldg(reinterpret_cast<const uint4 *>(q) + i) : make_uint4(0u, 0u, 0u, 0u); };
+            auto value = [&](uint32_t wd, int d) {
+                float2 y = make_float2(__uint_as_float(wd << 16), __uint_as_float(wd & 0xFFFF0000u));
+                if (MODE == 1) {
+                    const float2 s = __ldg(reinterpret_cast<const float2 *>(ks + d));
+                    y = make_float2(y.x * s.x, y.y * s.y);
                 }
-            }
-#pragma unroll
-            for (int i = 0; i < kAhead; ++i) {
-                const int at = rw * 32 + (i0 + i) * kWarpRows + lane / kLanes;  // row of the tile
-                uint32_t wd[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
-                float y[8], top = 0.0f;
+                return y;
+            };
+            float top = 0.0f;
+#pragma unroll 4
+            for (int i = 0; i < D / 8; ++i) {
+                const uint4 x = read(i);
+                const uint32_t wd[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    y[2 * e] = __uint_as_float(wd[e] << 16);
-                    y[2 * e + 1] = __uint_as_float(wd[e] & 0xFFFF0000u);
-                    if (MODE == 1) y[2 * e] *= ks[2 * e], y[2 * e + 1] *= ks[2 * e + 1];
-                    top = fmaxf(top, fmaxf(fabsf(y[2 * e]), fabsf(y[2 * e + 1])));
+                    const float2 y = value(wd[e], 8 * i + 2 * e);
+                    top = fmaxf(top, fmaxf(fabsf(y.x), fabsf(y.y)));
+                }
+            }
+            const int ex = power_of(top);
+            // (the sign of the softmax's scale goes to the query)
+            const float turn = __uint_as_float(((uint32_t)(127 - ex) << 23) | (a.scale_log2 < 0.0f ? 0x80000000u : 0u));
+            const uint32_t q_at = tmem + ((uint32_t)(rw * 32) << 16) + L::kQ + buf * (D / 2);
+#pragma unroll 1
+            for (int i = 0; i < D / 8; i += 4) {  // the row again, from the caches: it does not fit the registers
+                uint32_t o[16];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const uint4 x = read(i + k);
+                    o[4 * k] = x.x, o[4 * k + 1] = x.y, o[4 * k + 2] = x.z, o[4 * k + 3] = x.w;
                 }
 #pragma unroll
-                for (int o = kLanes / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
-                const int ex = power_of(top);
-                const float turn = __uint_as_float(((uint32_t)(127 - ex) << 23) | (flip ? 0x80000000u : 0u));
-#pragma unroll
-                for (int e = 0; e < 4; ++e) wd[e] = pack_fp16(y[2 * e] * turn, y[2 * e + 1] * turn);
-                const uint32_t dst = base + L::kQ + buf * L::kTileBytes + (uint32_t)at * 128 +
-                                     (uint32_t)(c / 8) * (kRows * 128) + (uint32_t)(((c % 8) ^ (at & 7)) << 4);
-                asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(dst), "r"(wd[0]), "r"(wd[1]), "r"(wd[2]),
-                             "r"(wd[3])
-                             : "memory");
-                if (c == 0) bar.q_scale[buf][at] = fabsf(a.scale_log2) * __uint_as_float((uint32_t)(127 + ex) << 23);
+                for (int e = 0; e < 16; ++e) {
+                    const float2 y = value(o[e], 8 * i + 2 * e);
+                    o[e] = pack_fp16(y.x * turn, y.y * turn);
+                }
+                tc_st16(q_at + 4 * i, o);
             }
+            bar.q_scale[buf][rw * 32 + lane] = fabsf(a.scale_log2) * __uint_as_float((uint32_t)(127 + ex) << 23);
+            tc_wait_st();
         }
-        fence_async();
+        tc_fence_before();
         arrive(bar.q_full[buf]);
     }
 
     // A tile's O: to the output where the CTA has the whole tile, else a partial.
-    __device__ __forceinline__ void store_rows(const Walk &w, int rw, int buf, bool whole, uint32_t seg) const {
+    __device__ __forceinline__ void store_rows(const Tile &w, int rw, bool whole, uint32_t seg) const {
         const AttnArgs &a = p.base;
-        const int h = w.head(), row = rw * 32 + lane, r0 = w.row0() + rw * 32, rows = w.s.drafts * a.group;
+        const int h = w.head, row = rw * 32 + lane, r0 = w.row0 + rw * 32, rows = w.rows;
+        const uint32_t o_at = tmem + ((uint32_t)(rw * 32) << 16) + L::kO;
+        const float *vs = a.v_scale + (MODE == 1 ? (int64_t)h * D : 0);
         if (r0 < rows) {
-            const uint32_t o_at = tmem + ((uint32_t)(rw * 32) << 16) + L::kO + buf * D;
+            const float m = bar.m[row], l = bar.l[0][row] + bar.l[1][row];
+            const float inv = !whole ? 1.0f : l == 0.0f ? 0.0f : 1.0f / l;
             const int r = r0 + lane, t = r / a.group, j = r - t * a.group;
-            const float m = bar.m[buf][row], l = bar.l[buf][row];
-            const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-            uint16_t *dst = a.out + (int64_t)(w.s.token + t) * a.out_seq_stride + (int64_t)(h * a.group + j) * a.out_head_stride;
+            uint16_t *dst = a.out + (int64_t)(w.token + t) * a.out_seq_stride + (int64_t)(h * a.group + j) * a.out_head_stride;
             const int64_t slot = (int64_t)(2 * blockIdx.x + (seg > 0 ? 1 : 0)) * kRows + row;
             float *po = a.part_o + (slot - lane) * D + lane * 8;  // 32 rows' eighths in turn
-#pragma unroll
+#pragma unroll 1
             for (int c = 0; c < D; c += 16) {
                 float o[16];
                 tc_ld16(o, o_at + c);
-                if (MODE == 1) {
 #pragma unroll
-                    for (int i = 0; i < 16; i += 4) {
-                        const float4 sv = __ldg(reinterpret_cast<const float4 *>(a.v_scale + (int64_t)h * D + c + i));
-                        o[i] *= sv.x, o[i + 1] *= sv.y, o[i + 2] *= sv.z, o[i + 3] *= sv.w;
-                    }
+                for (int i = 0; i < 16; i += 4) {
+                    const float4 s = MODE == 1 ? __ldg(reinterpret_cast<const float4 *>(vs + c + i)) : make_float4(1.0f, 1.0f, 1.0f, 1.0f);
+                    o[i] *= s.x * inv, o[i + 1] *= s.y * inv, o[i + 2] *= s.z * inv, o[i + 3] *= s.w * inv;
                 }
                 if (!whole) {
 #pragma unroll
@@ -487,7 +576,7 @@ struct Tree {
                 } else if (r < rows) {
                     uint32_t y[8];
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) y[i] = pack_bf16(o[2 * i] * inv, o[2 * i + 1] * inv);
+                    for (int i = 0; i < 8; ++i) y[i] = pack_bf16(o[2 * i], o[2 * i + 1]);
                     if ((reinterpret_cast<uintptr_t>(dst) & 15) == 0) {
                         reinterpret_cast<uint4 *>(dst + c)[0] = make_uint4(y[0], y[1], y[2], y[3]);
                         reinterpret_cast<uint4 *>(dst + c)[1] = make_uint4(y[4], y[5], y[6], y[7]);
@@ -506,99 +595,103 @@ struct Tree {
             }
         }
         tc_fence_before();
-        arrive(bar.o_free[buf]);
+        arrive(bar.o_free);
     }
 
+    // Turn seg: the queries of tile seg + 1, then O of tile seg.
     __device__ void rows() const {
-        const int rw = warp - L::kSoftmaxWarps;
-        Walk &in = walk, &out = bar.walk_out[rw];
+        const int rw = warp - L::kRowWarp;
         int in_left = total, out_left = total;
-        uint32_t in_seg = 0;
-        auto load_next = [&]() {
-            const int buf = (int)(in_seg & 1u);
-            if (!wait_warp(bar.q_free[buf], ((in_seg >> 1) & 1u) ^ 1u)) return false;
-            load_rows(in, rw, buf);
-            in_left -= min(in_left, in.s.steps - in.step);
-            if (in_left > 0) in.next_tile(p, lane);
-            ++in_seg;
-            return true;
-        };
-        if (!load_next()) return;
-        for (uint32_t seg = 0; out_left > 0; ++seg) {
-            if (in_left > 0 && !load_next()) return;
-            const int count = min(out_left, out.s.steps - out.step), buf = (int)(seg & 1u);
-            if (!wait_warp(bar.ml_full[buf], (seg >> 1) & 1u) || !wait_warp(bar.o_full[buf], (seg >> 1) & 1u)) return;
+#pragma unroll 1
+        for (uint32_t in = 0; out_left > 0; ++in) {
+            if (in_left > 0) {
+                const int buf = (int)(in & 1u);
+                if (!enter(in) || !wait(bar.q_free[buf], ((in >> 1) & 1u) ^ 1u)) return;
+                tc_fence_after();
+                load_rows(tile(in), rw, buf);
+                in_left -= tile(in).count;
+            }
+            if (in == 0) continue;
+            const uint32_t seg = in - 1;
+            const Tile &x = tile(seg);
+            if (!wait(bar.ml_full, seg & 1u) || !wait(bar.o_full, seg & 1u)) return;
             tc_fence_after();
-            store_rows(out, rw, buf, count == out.s.steps, seg);
-            out_left -= count;
-            if (out_left > 0) out.next_tile(p, lane);
+            store_rows(x, rw, x.count == x.steps, seg);
+            out_left -= x.count;
+            leave(seg);
         }
     }
 
-    // ---- softmax (one thread per query row) -----------------------------------
-    // 32 bits of a row's mask from draft i on; drafts before the first are the context.
+    // ---- softmax (two threads per query row, 64 of a step's positions each) -----------------------------------
+    // 32 bits of a row's mask; drafts before the first are the context.
     __device__ __forceinline__ uint32_t mask_word(const uint32_t *mask, int word) const {
         if (word < 0) return 0xFFFFFFFFu;
         return word < 2 * p.mask_words ? __ldg(mask + word) : 0u;
     }
 
-    __device__ void softmax() const {
-        const int row = warp * 32 + lane;
-        const uint32_t lanes = (uint32_t)(warp * 32) << 16;
-        int n = 0, left = total;
-        for (uint32_t seg = 0; left > 0; ++seg) {
-            const int count = min(left, walk.s.steps - walk.step), buf = (int)(seg & 1u);
-            const int r0 = walk.row0() + warp * 32, rows = walk.s.drafts * p.base.group;
-            const bool busy = r0 < rows;  // uniform in the warp: some row is a query's
-            int d0 = walk.step * kCols - walk.s.ctx;  // the draft at a step's first position, if not negative
-            const uint32_t o_at = tmem + lanes + L::kO + buf * D;
-            float scale = 0.0f, m = -INFINITY, l = 0.0f;
-            for (int i = 0; i < count; ++i, ++n, d0 += kCols) {
-                const int st = n & 1;
-                const bool drafts = d0 + kCols > 0;  // some position is a draft's
-                uint32_t sees[4] = {0xFFFFFFFFu, 0xFFFFFFFFu, 0xFFFFFFFFu, 0xFFFFFFFFu};
-                if (drafts && busy) {
-                    const int t = min(r0 + lane, rows - 1) / p.base.group;
-                    if (p.mask == nullptr) {
+    // What of 64 positions a row sees; d0: the draft at the first, if not negative.
+    __device__ __forceinline__ void visible(uint32_t (&sees)[2], int d0, int t, int token) const {
+        if (p.mask == nullptr) {
 #pragma unroll
-                        for (int q = 0; q < 4; ++q) {
-                            const int upto = t - d0 + 1 - 32 * q;  // positions from the word's first on that are seen
-                            sees[q] = upto >= 32 ? 0xFFFFFFFFu : upto <= 0 ? 0u : (1u << upto) - 1u;
-                        }
-                    } else {
-                        const uint32_t *mask = reinterpret_cast<const uint32_t *>(p.mask + (int64_t)(walk.s.token + t) * p.mask_words);
-                        uint32_t lo = mask_word(mask, d0 >> 5);
-#pragma unroll
-                        for (int q = 0; q < 4; ++q) {
-                            const uint32_t hi = mask_word(mask, (d0 >> 5) + q + 1);
-                            sees[q] = __funnelshift_r(lo, hi, (uint32_t)d0 & 31u);
-                            lo = hi;
-                        }
-                    }
-                }
-                if (i == 0) {
-                    if (!wait_warp(bar.q_full[buf], (seg >> 1) & 1u)) return;
-                    scale = bar.q_scale[buf][row];
-                    arrive(bar.q_free[buf]);
-                }
-                if (!wait_warp(bar.s_full[st], (uint32_t)(n >> 1) & 1u)) return;
-                tc_fence_after();
-                if (busy && !step(tmem + lanes + st * kCols, o_at, scale, i > 0, n, drafts, sees, m, l)) return;
-                tc_fence_before();
-                arrive(bar.p_full[st]);
+            for (int q = 0; q < 2; ++q) {
+                const int upto = t - d0 + 1 - 32 * q;  // positions from the word's first on that are seen
+                sees[q] = upto >= 32 ? 0xFFFFFFFFu : upto <= 0 ? 0u : (1u << upto) - 1u;
             }
-            if (!wait_warp(bar.o_free[buf], ((seg >> 1) & 1u) ^ 1u)) return;
-            bar.m[buf][row] = m;
-            bar.l[buf][row] = l;
-            arrive(bar.ml_full[buf]);
-            left -= count;
-            if (left > 0) walk.next_tile(p, lane);
+        } else {
+            const uint32_t *mask = reinterpret_cast<const uint32_t *>(p.mask + (int64_t)(token + t) * p.mask_words);
+            uint32_t lo = mask_word(mask, d0 >> 5);
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                const uint32_t hi = mask_word(mask, (d0 >> 5) + q + 1);
+                sees[q] = __funnelshift_r(lo, hi, (uint32_t)d0 & 31u);
+                lo = hi;
+            }
         }
     }
 
-    // A group's factor of the scores and shift, read again where they are used (a thread
-    // has no registers to keep sixteen).  The factor is never 0, which times the -inf of a
-    // position left out would be no number; 2^-126 instead does not show.
+    __device__ void softmax() const {
+        const int quad = warp & 3, half = warp >> 2, row = quad * 32 + lane;
+        const uint32_t lanes = (uint32_t)(quad * 32) << 16;
+        int n = 0;
+        uint32_t met = 0;  // steps in which the row's two warps met
+#pragma unroll 1
+        for (uint32_t seg = 0; n < total; ++seg) {
+            if (!enter(seg)) return;
+            const Tile &x = tile(seg);
+            const int end = n + x.count, buf = (int)(seg & 1u), token = x.token;
+            const bool busy = x.row0 + quad * 32 < x.rows;  // uniform in the warp: some row is a query's
+            const int t = min(x.row0 + row, x.rows - 1) / p.base.group;
+            int d0 = x.step * kCols + half * 64 - x.ctx;  // the draft at the first position, if not negative
+            leave(seg);
+            if (!wait(bar.q_full[buf], (seg >> 1) & 1u)) return;
+            const float scale = bar.q_scale[buf][row];
+            arrive(bar.q_free[buf]);
+            float m = -INFINITY, l = 0.0f;
+            bool have_o = false;
+#pragma unroll 1
+            for (; n < end; ++n, d0 += kCols) {
+                const int st = n & 1;
+                uint32_t sees[2] = {0xFFFFFFFFu, 0xFFFFFFFFu};
+                if (d0 + 64 > 0 && busy) visible(sees, d0, t, token);  // some position is a draft's
+                if (!wait(bar.s_full[st], (uint32_t)(n >> 1) & 1u)) return;
+                tc_fence_after();
+                if (busy) {
+                    if (!step(tmem + lanes + st * kCols, tmem + lanes + L::kO, quad, half, scale, have_o, n, met & 1u, sees, m, l)) return;
+                    ++met;
+                }
+                have_o = true;
+                tc_fence_before();
+                arrive(bar.p_full[st]);
+            }
+            if (!wait(bar.o_free, (seg & 1u) ^ 1u)) return;
+            if (half == 0) bar.m[row] = m;
+            bar.l[half][row] = l;
+            arrive(bar.ml_full);
+        }
+    }
+
+    // A group's factor of the scores and shift, read again where they are used.  The factor is never 0,
+    // which times the -inf of a position left out would be no number; 2^-126 instead does not show.
     __device__ __forceinline__ float2 factor_shift(int slot, int grp, float scale) const {
         if (MODE == 1) return make_float2(fmaxf(scale, 0x1p-126f), 0.0f);
         float f, e;
@@ -607,24 +700,24 @@ struct Tree {
         return make_float2(fmaxf(scale * f, 0x1p-126f), e);
     }
 
-    // One step of a row: S -> P, the running maximum m and sum l.  A group's weights are
+    // One step of a row's half: S -> P, the running maximum m and the half's sum l.  A group's weights are
     // 2^(score + e - m), e the exponent taken out of its value scales, so that the product
-    // with the tile's values is the weight times the value; m bounds score + e, lazily.
-    // fp16 holds such weights (at most 2^15) eight times finer than bf16, and what falls
-    // below 2^-21 of the largest to 2^-32 of it.
-    __device__ __forceinline__ bool step(uint32_t s_at, uint32_t o_at, float scale, bool have_o, int n, bool drafts,
-                                         const uint32_t (&sees)[4], float &m, float &l) const {
+    // with the tile's values is the weight times the value; m bounds score + e, lazily, and is the
+    // same in both halves.  fp16 holds such weights (at most 2^15) eight times finer than bf16, and what
+    // falls below 2^-21 of the largest to 2^-32 of it.
+    __device__ __forceinline__ bool step(uint32_t s_at, uint32_t o_at, int quad, int half, float scale, bool have_o, int n,
+                                         uint32_t met, const uint32_t (&sees)[2], float &m, float &l) const {
         const int slot = n % kMaskSlots;
-        const uint2 valid = bar.valid[slot];
-        float s[4][32];
+        const uint32_t valid = half == 0 ? bar.valid[slot].x : bar.valid[slot].y;
+        float s[2][32];
 #pragma unroll
-        for (int q = 0; q < 4; ++q) tc_ld32(s[q], s_at + 32 * q);
+        for (int q = 0; q < 2; ++q) tc_ld32(s[q], s_at + half * 64 + 32 * q);
 #pragma unroll
-        for (int q = 0; q < 4; ++q) tc_wait_ld(s[q]);
-        if (drafts || valid.x != 0x10101010u || valid.y != 0x10101010u) {
+        for (int q = 0; q < 2; ++q) tc_wait_ld(s[q]);
+        if (__any_sync(0xFFFFFFFFu, (sees[0] & sees[1]) != 0xFFFFFFFFu) || valid != 0x10101010u) {
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const uint32_t counts = (q < 2 ? valid.x : valid.y) >> (q % 2 * 16);
+            for (int q = 0; q < 2; ++q) {
+                const uint32_t counts = valid >> (q * 16);
                 const uint32_t in = ((1u << (counts & 0xFFu)) - 1u) | (((1u << (counts >> 8 & 0xFFu)) - 1u) << 16);
                 const uint32_t keep = in & sees[q];
 #pragma unroll
@@ -634,36 +727,45 @@ struct Tree {
         }
         float mx = -INFINITY;
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
+        for (int q = 0; q < 2; ++q) {
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                const float2 fe = factor_shift(slot, 2 * q + i, scale);
+                const float2 fe = factor_shift(slot, 4 * half + 2 * q + i, scale);
                 mx = fmaxf(mx, fmaf(top16(s[q], 16 * i), fe.x, fe.y));
             }
         }
+        // The halves' larger one; after it both have read S, over which P is written.
+        const int row = quad * 32 + lane;
+        bar.top[met][half][row] = mx;
+        tc_fence_before();
+        arrive(bar.pair[quad]);
+        if (!wait(bar.pair[quad], met)) return false;
+        tc_fence_after();
+        mx = fmaxf(mx, bar.top[met][half ^ 1][row]);
         const bool moves = mx > m + (kLift + kLazy) || (m == -INFINITY && mx > m);
         if (__any_sync(0xFFFFFFFFu, moves)) {
             const float c = moves ? ex2(m - (mx - kLift)) : 1.0f;  // 0 where there was nothing yet
             if (moves) m = mx - kLift;
             l *= c;
-            if (have_o) {  // once the step before is in it
-                if (!wait_warp(bar.v_free[(n - 1) & 1], (uint32_t)((n - 1) >> 1) & 1u)) return false;
+            if (have_o) {  // once the step before is in it; half of the channels each
+                if (!wait(bar.v_free[(n - 1) & 1], (uint32_t)((n - 1) >> 1) & 1u)) return false;
                 tc_fence_after();
-#pragma unroll
-                for (int d = 0; d < D; d += 16) {
+#pragma unroll 1
+                for (int d = 0; d < D / 2; d += 16) {
                     float o[16];
-                    tc_ld16(o, o_at + d);
+                    tc_ld16(o, o_at + half * (D / 2) + d);
                     uint32_t y[16];
 #pragma unroll
                     for (int i = 0; i < 16; ++i) y[i] = __float_as_uint(o[i] * c);
-                    tc_st16(o_at + d, y);
+                    tc_st16(o_at + half * (D / 2) + d, y);
                 }
             }
         }
         const float neg = m == -INFINITY ? 0.0f : -m;
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            const float2 a = factor_shift(slot, 2 * q, scale), b = factor_shift(slot, 2 * q + 1, scale);
+        for (int q = 0; q < 2; ++q) {
+            const int grp = 4 * half + 2 * q;
+            const float2 a = factor_shift(slot, grp, scale), b = factor_shift(slot, grp + 1, scale);
             const float f[2] = {a.x, b.x}, g[2] = {a.y + neg, b.y + neg};
             float2 sum[2];
             uint32_t o[16];
@@ -675,11 +777,11 @@ struct Tree {
                 sum[i / 16] = i % 16 == 0 ? y : __fadd2_rn(sum[i / 16], y);
                 o[i / 2] = pack_fp16(y.x, y.y);
             }
-            tc_st16(s_at + 16 * q, o);
+            tc_st16(s_at + half * 32 + 16 * q, o);
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 const float part = sum[i].x + sum[i].y;
-                l = MODE == 1 ? l + part : fmaf(part, bar.v_inv[slot][2 * q + i], l);
+                l = MODE == 1 ? l + part : fmaf(part, bar.v_inv[slot][grp + i], l);
             }
         }
         tc_wait_st();
@@ -717,10 +819,19 @@ __global__ void __launch_bounds__(Layout<D>::kThreads, 1) tree_kernel(const Tree
                 mbar_init(smem_u32(&bar.p_full[i]), L::kSoftmaxWarps);
                 mbar_init(smem_u32(&bar.q_full[i]), L::kRowWarps);
                 mbar_init(smem_u32(&bar.q_free[i]), 1 + L::kSoftmaxWarps);
-                mbar_init(smem_u32(&bar.o_full[i]), 1);
-                mbar_init(smem_u32(&bar.o_free[i]), L::kRowWarps);
-                mbar_init(smem_u32(&bar.ml_full[i]), L::kSoftmaxWarps);
             }
+            for (int i = 0; i < L::kRing; ++i) {
+                mbar_init(smem_u32(&bar.raw_full[i]), 1);
+                mbar_init(smem_u32(&bar.raw_free[i]), L::kDequantWarps);
+            }
+            for (int i = 0; i < 4; ++i) mbar_init(smem_u32(&bar.pair[i]), 2);
+            for (int i = 0; i < kTiles; ++i) {
+                mbar_init(smem_u32(&bar.tile_full[i]), 1);
+                mbar_init(smem_u32(&bar.tile_free[i]), L::kSoftmaxWarps + L::kRowWarps + 2);
+            }
+            mbar_init(smem_u32(&bar.o_full), 1);
+            mbar_init(smem_u32(&bar.o_free), L::kRowWarps);
+            mbar_init(smem_u32(&bar.ml_full), L::kSoftmaxWarps);
             mbar_init(smem_u32(&bar.drained), 1);
             bar.stop = 0;
             asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -774,37 +885,21 @@ __global__ void __launch_bounds__(Layout<D>::kThreads, 1) tree_kernel(const Tree
             before += all;
             if (before > first) break;
         }
-        __syncthreads();
-        if (lane == 0) {
-            Walk w;
-            w.s = make_seq(p, bar.start_b, read_raw(p, bar.start_b));
-            w.ahead = read_raw(p, bar.start_b + 1);
-            w.tile = (int)(bar.start_off / (uint32_t)w.s.steps);
-            w.step = (int)(bar.start_off - (uint32_t)w.tile * (uint32_t)w.s.steps);
-            if (warp <= L::kMmaWarp) bar.walk[warp] = w;
-            if (warp < L::kRowWarps) bar.walk_out[warp] = w;
-            if (warp == L::kMmaWarp) {
-                bar.total = total;
-                TreeShare r;
-                r.units = units;
-                r.first = first - (uint32_t)w.step;
-                r.steps = w.s.steps;
-                r.token = w.s.token;
-                r.rows = w.s.drafts * p.base.group;
-                r.row = w.row0();
-                r.head = w.head();
-                r.pad = 0;
-                p.shares[blockIdx.x] = r;
-            }
+        if (threadIdx.x == 0) {
+            bar.units = units;
+            bar.first = first;
+            bar.total = total;
         }
         __syncthreads();
         if (warp >= L::kMmaWarp) {
             reg_give<L::kMmaRegs>();
             if (warp == L::kMmaWarp) Tree<MODE, D>(p, bar, dyn).products();
+            if (warp == L::kFetchWarp) Tree<MODE, D>(p, bar, dyn).fetch();
+            if (warp == L::kWalkWarp) Tree<MODE, D>(p, bar, dyn).walk();
         } else if (warp >= L::kDequantWarp) {
-            static_assert(L::kDequantRegs == L::kLaunchRegs, "as launched");
+            reg_give<L::kDequantRegs>();
             Tree<MODE, D>(p, bar, dyn).dequantise();
-        } else if (warp >= L::kSoftmaxWarps) {
+        } else if (warp >= L::kRowWarp) {
             reg_give<L::kRowRegs>();
             Tree<MODE, D>(p, bar, dyn).rows();
         } else {
@@ -820,6 +915,7 @@ __global__ void __launch_bounds__(Layout<D>::kThreads, 1) tree_kernel(const Tree
         r.units = units;
         p.shares[blockIdx.x] = r;
     }
+    if (threadIdx.x == 0 && bar.stop != 0) report(p.base.dev_error, KVC8_DEV_TIMEOUT);
     if (warp == L::kMmaWarp)
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"((uint32_t)L::kTmemCols)
                      : "memory");

@@ -11,7 +11,8 @@
 // and P replaces S there: both are A operands.  Warps by role:
 //   walk        1: what the CTA's next tiles are
 //   fetch       1: pages' codes by bulk copies into a ring in shared memory, as many steps ahead as fit
-//   dequantise  8: codes to K' and V' as fp16, two stages of each in shared memory
+//   dequantise  16, eight for the keys and eight for the values: codes to K' and V' as fp16, two stages of
+//               each in shared memory
 //   mma         one lane issues both products
 //   softmax     8, two threads per query row, half of a step's positions each: S from tensor memory,
 //               one-pass softmax (Milakov and Gimelshein, Online normalizer calculation for softmax,
@@ -100,13 +101,13 @@ struct Tile {
 
 template <int D>
 struct Layout {
-    static constexpr int kSoftmaxWarps = 8, kRowWarps = 4, kDequantWarps = 8;
+    static constexpr int kSoftmaxWarps = 8, kRowWarps = 4, kDequantWarps = 16;
     static constexpr int kRowWarp = kSoftmaxWarps, kDequantWarp = kRowWarp + kRowWarps;
     static constexpr int kMmaWarp = kDequantWarp + kDequantWarps, kFetchWarp = kMmaWarp + 1, kWalkWarp = kMmaWarp + 2;
-    static constexpr int kThreads = 768;
-    // Registers per thread: a softmax thread holds 64 scores, one with a row of queries or outputs 64 pairs.
-    static constexpr int kSoftmaxRegs = 112, kRowRegs = 72, kDequantRegs = 64, kMmaRegs = 48;
-    static constexpr int kLaunchRegs = 80;
+    static constexpr int kThreads = 1024;
+    // Registers per thread: a softmax thread holds 64 scores.
+    static constexpr int kSoftmaxRegs = 104, kRowRegs = 64, kDequantRegs = 48, kMmaRegs = 48;
+    static constexpr int kLaunchRegs = 64;
     static_assert(32 * (kSoftmaxWarps * kSoftmaxRegs + kRowWarps * kRowRegs + kDequantWarps * kDequantRegs +
                         4 * kMmaRegs) <= kThreads * kLaunchRegs,
                   "the warpgroups' registers are the block's");
@@ -144,7 +145,7 @@ struct Barriers {
     float q_scale[kStages][kRows];  // log2 per unit of score, with the query's power of two
     float m[kRows], l[2][kRows];    // l: of each half of the positions
     float top[2][2][kRows];         // a step's largest score of each half, of two steps
-    // of the steps in the ring, where their keys lie: valid positions of each group of 16, scales (mode 2: one a group)
+    // of what is in the ring: valid positions of each group of 16, the keys' and the values' scales (mode 2: one a group)
     uint2 raw_valid[kMaxRing];
     alignas(16) float raw_ks[kMaxRing][kCols];
     alignas(16) float raw_vs[kMaxRing][kCols];
@@ -159,7 +160,7 @@ struct Barriers {
 template <int MODE, int D>
 struct Tree {
     using L = Layout<D>;
-    static constexpr int kRpw = kCols / L::kDequantWarps;  // positions of a warp: one group of 16
+    static constexpr int kRpw = 16;  // positions of a dequantising warp: one group
     using T = CodeTile<MODE, D, kRpw>;
     static_assert(T::kGroups == 1, "a warp's positions lie in one block");
 
@@ -246,9 +247,9 @@ struct Tree {
     // ---- fetch (a warp) ----------------------------------------------------------
     // Lanes 0-7 have a group of 16 positions each: a step's groups may lie in different blocks.  In the loop's
     // turn n, step n is copied, step n + 1 is placed and its scales asked for, and the block ids of step n + 2 are.
-    __device__ __forceinline__ void copy(uint32_t dst, const int8_t *src, uint64_t &full) const {
+    __device__ __forceinline__ void copy(uint32_t dst, const int8_t *src, uint64_t &full, uint32_t bytes) const {
         asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
-                     "l"(src), "r"((uint32_t)(16 * D)), "r"(smem_u32(&full))
+                     "l"(src), "r"(bytes), "r"(smem_u32(&full))
                      : "memory");
     }
     __device__ void fetch() const {
@@ -272,15 +273,13 @@ struct Tree {
                 for (int values = 0; values < 2 && good; ++values) {
                     good = wait(bar.raw_free[slot], round ^ 1u);
                     if (!good) break;
-                    if (values == 0) {
-                        if (lane < 8) reinterpret_cast<uint8_t *>(&bar.raw_valid[slot])[grp] = (uint8_t)valid;
-                        if (MODE == 0) {
-                            reinterpret_cast<float4 *>(bar.raw_ks[slot])[lane] = ks;
-                            reinterpret_cast<float4 *>(bar.raw_vs[slot])[lane] = vs;
-                        } else if (MODE == 2 && lane < 8) {
-                            bar.raw_ks[slot][grp] = ks.x;
-                            bar.raw_vs[slot][grp] = vs.x;
-                        }
+                    if (lane < 8) reinterpret_cast<uint8_t *>(&bar.raw_valid[slot])[grp] = (uint8_t)valid;
+                    if (MODE == 0) {
+                        if (values == 0) reinterpret_cast<float4 *>(bar.raw_ks[slot])[lane] = ks;
+                        reinterpret_cast<float4 *>(bar.raw_vs[slot])[lane] = vs;
+                    } else if (MODE == 2 && lane < 8) {
+                        bar.raw_ks[slot][grp] = ks.x;
+                        bar.raw_vs[slot][grp] = vs.x;
                     }
                     const uint32_t groups = __popc(__ballot_sync(0xFFFFFFFFu, lane < 8 && valid > 0));
                     if (lane == 0)
@@ -289,9 +288,10 @@ struct Tree {
                                      "r"(groups * 16u * D)
                                      : "memory");
                     __syncwarp();
-                    if (lane < 8 && valid > 0)
+                    const bool one = bs % 128 == 0 && groups == 8;
+                    if (one ? lane == 0 : lane < 8 && valid > 0)
                         copy(base + L::kRaw + slot * L::kRawBytes + grp * 16 * D, (values == 0 ? a.k_cache : a.v_cache) + row * D,
-                             bar.raw_full[slot]);
+                             bar.raw_full[slot], one ? 128 * D : 16 * D);
                     if (++slot == L::kRing) {
                         slot = 0;
                         round ^= 1u;
@@ -355,48 +355,46 @@ struct Tree {
     }
 
     // ---- dequantise (a warp has a group of 16 positions) ------------------------------------------------
-    // Keys and values of a step in turn, by the same few instructions: what the roles on an SM run through must
-    // fit the instruction caches.
     __device__ void dequantise() const {
-        const int dw = warp - L::kDequantWarp;
+        const int dw = (warp - L::kDequantWarp) % 8, values = (warp - L::kDequantWarp) / 8;
         const uint32_t src = base + L::kRaw + (uint32_t)((dw * 16 + T::row_in(lane)) * D + T::block_in(lane) * 64 + lane % 4 * 16);
-        int slot = 0;
-        uint32_t round = 0, next_scale = 0u;
+        int slot = values;  // keys and values take turns in the ring
+        uint32_t round = 0;
 #pragma unroll 1
-        for (int i = 0; i < 2 * total; ++i) {
-            const int n = i >> 1, values = i & 1, st = n % kStages;
+        for (int n = 0; n < total; ++n) {
+            const int st = n % kStages;
             if (!wait(bar.raw_full[slot], round)) return;
-            uint32_t scale = next_scale;
-            if (values == 0) {
-                const int valid = reinterpret_cast<const uint8_t *>(&bar.raw_valid[slot])[dw];
-                if (MODE != 1) {
-                    float sk = 0.0f, sv = 0.0f;  // positions behind the end may have any scale
-                    if (lane < valid) {
-                        sk = bar.raw_ks[slot][MODE == 0 ? dw * 16 + lane : dw];
-                        sv = bar.raw_vs[slot][MODE == 0 ? dw * 16 + lane : dw];
-                    }
-                    // A scale that is no number must not reach the rows that do not see its position,
-                    // nor the other scales' power: the value counts as zero, and the score as no number.
-                    const bool odd = (__float_as_uint(sk) & 0x7F800000u) == 0x7F800000u ||
-                                     (__float_as_uint(sv) & 0x7F800000u) == 0x7F800000u;
-                    sk = odd ? 0.0f : sk;
-                    sv = odd ? 0.0f : sv;
-                    int ek, ev;
-                    const uint32_t top_k = T::group_top(sk, lane), top_v = T::group_top(sv, lane);
-                    scale = T::normal_scale(sk, top_k, -100, ek);
-                    next_scale = T::normal_scale(sv, top_v, kLeastValuePower, ev);
-                    if (odd) scale = 0x7FFF7FFFu;
-                    // (every use of this slot of the step four before is over: its values are in V')
-                    if (lane == 0) {
-                        bar.k_pow[n % kMaskSlots][dw] = __uint_as_float((uint32_t)(127 + ek) << 23);
-                        bar.v_exp[n % kMaskSlots][dw] = (float)ev;
-                        bar.v_inv[n % kMaskSlots][dw] = __uint_as_float((uint32_t)(127 - ev) << 23);
-                    }
+            const int valid = reinterpret_cast<const uint8_t *>(&bar.raw_valid[slot])[dw];
+            uint32_t scale = 0u;
+            int ek = 0, ev = 0;
+            if (MODE != 1) {
+                float sk = 0.0f, sv = 0.0f;  // positions behind the end may have any scale
+                if (lane < valid) {
+                    if (values == 0) sk = bar.raw_ks[slot][MODE == 0 ? dw * 16 + lane : dw];
+                    sv = bar.raw_vs[slot][MODE == 0 ? dw * 16 + lane : dw];
                 }
-                if (lane == 0) reinterpret_cast<uint8_t *>(&bar.valid[n % kMaskSlots])[dw] = (uint8_t)valid;
+                // A scale that is no number must not reach the rows that do not see its position,
+                // nor the other scales' power: the value counts as zero, and the score as no number.
+                const bool odd = (__float_as_uint(sk) & 0x7F800000u) == 0x7F800000u ||
+                                 (__float_as_uint(sv) & 0x7F800000u) == 0x7F800000u;
+                sk = odd ? 0.0f : sk;
+                sv = odd ? 0.0f : sv;
+                scale = T::normal_scale(sv, T::group_top(sv, lane), kLeastValuePower, ev);
+                if (values == 0) {
+                    scale = T::normal_scale(sk, T::group_top(sk, lane), -100, ek);
+                    if (odd) scale = 0x7FFF7FFFu;
+                }
             }
             if (!wait(values == 0 ? bar.s_full[st] : bar.v_free[st], ((uint32_t)(n / kStages) & 1u) ^ 1u)) return;
-            T::template store_each<2>(
+            if (values == 0 && lane == 0) {  // (the step that had this place, four before, is through)
+                if (MODE != 1) {
+                    bar.k_pow[n % kMaskSlots][dw] = __uint_as_float((uint32_t)(127 + ek) << 23);
+                    bar.v_exp[n % kMaskSlots][dw] = (float)ev;
+                    bar.v_inv[n % kMaskSlots][dw] = __uint_as_float((uint32_t)(127 - ev) << 23);
+                }
+                reinterpret_cast<uint8_t *>(&bar.valid[n % kMaskSlots])[dw] = (uint8_t)valid;
+            }
+            T::template store_each<4>(
                 [&](int k) {
                     uint4 c;
                     asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
@@ -409,8 +407,9 @@ struct Tree {
             fence_async();
             arrive(values == 0 ? bar.k_full[st] : bar.v_full[st]);
             if (lane == 0) mbar_arrive(smem_u32(&bar.raw_free[slot]));
-            if (++slot == L::kRing) {
-                slot = 0;
+            slot += 2;
+            if (slot >= L::kRing) {
+                slot -= L::kRing;
                 round ^= 1u;
             }
         }
@@ -812,8 +811,8 @@ __global__ void __launch_bounds__(Layout<D>::kThreads, 1) tree_kernel(const Tree
     if (warp == L::kMmaWarp) {
         if (lane == 0) {
             for (int i = 0; i < kStages; ++i) {
-                mbar_init(smem_u32(&bar.k_full[i]), L::kDequantWarps);
-                mbar_init(smem_u32(&bar.v_full[i]), L::kDequantWarps);
+                mbar_init(smem_u32(&bar.k_full[i]), L::kDequantWarps / 2);
+                mbar_init(smem_u32(&bar.v_full[i]), L::kDequantWarps / 2);
                 mbar_init(smem_u32(&bar.s_full[i]), 1);
                 mbar_init(smem_u32(&bar.v_free[i]), 1);
                 mbar_init(smem_u32(&bar.p_full[i]), L::kSoftmaxWarps);
@@ -822,7 +821,7 @@ __global__ void __launch_bounds__(Layout<D>::kThreads, 1) tree_kernel(const Tree
             }
             for (int i = 0; i < L::kRing; ++i) {
                 mbar_init(smem_u32(&bar.raw_full[i]), 1);
-                mbar_init(smem_u32(&bar.raw_free[i]), L::kDequantWarps);
+                mbar_init(smem_u32(&bar.raw_free[i]), L::kDequantWarps / 2);
             }
             for (int i = 0; i < 4; ++i) mbar_init(smem_u32(&bar.pair[i]), 2);
             for (int i = 0; i < kTiles; ++i) {
@@ -849,9 +848,8 @@ __global__ void __launch_bounds__(Layout<D>::kThreads, 1) tree_kernel(const Tree
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = bar.tmem;
-    uint32_t units = 0;
-#pragma unroll
-    for (int i = 0; i < L::kThreads / 32; ++i) units += bar.sum[i];
+    static_assert(L::kThreads == 1024, "a lane per warp");
+    const uint32_t units = __reduce_add_sync(0xFFFFFFFFu, bar.sum[lane]);
     const Cut cut(units, gridDim.x);
     const uint32_t first = cut.first_of(blockIdx.x);
     const int total = (int)(cut.first_of(blockIdx.x + 1) - first);
@@ -871,13 +869,8 @@ __global__ void __launch_bounds__(Layout<D>::kThreads, 1) tree_kernel(const Tree
             __syncthreads();
             if (lane == 31) bar.sum[warp] = sum;
             __syncthreads();
-            uint32_t all = 0;
-#pragma unroll
-            for (int i = 0; i < L::kThreads / 32; ++i) {
-                if (i < warp) sum += bar.sum[i];
-                all += bar.sum[i];
-            }
-            sum += before;
+            const uint32_t others = bar.sum[lane], all = __reduce_add_sync(0xFFFFFFFFu, others);
+            sum += before + __reduce_add_sync(0xFFFFFFFFu, lane < warp ? others : 0u);
             if (first < sum && first >= sum - u) {
                 bar.start_b = b;
                 bar.start_off = first - (sum - u);
@@ -900,7 +893,7 @@ __global__ void __launch_bounds__(Layout<D>::kThreads, 1) tree_kernel(const Tree
             reg_give<L::kDequantRegs>();
             Tree<MODE, D>(p, bar, dyn).dequantise();
         } else if (warp >= L::kRowWarp) {
-            reg_give<L::kRowRegs>();
+            static_assert(L::kRowRegs == L::kLaunchRegs, "as launched");
             Tree<MODE, D>(p, bar, dyn).rows();
         } else {
             reg_take<L::kSoftmaxRegs>();

@@ -431,48 +431,71 @@ struct Tree {
             tc_mma_ts(tm + L::kO, tm + st * kCols + 8 * i, v + (uint64_t)(i * (2048 >> 4)), instr_desc(D, true),
                       acc || i > 0, leader);
     }
+    __device__ __forceinline__ bool ready(uint64_t &b, uint32_t parity) const {
+        return __all_sync(0xFFFFFFFFu, mbar_test(smem_u32(&b), parity));
+    }
     // What steers the loop comes from lane 0, so that the compiler keeps it, and with it stages,
     // addresses and descriptors, in uniform registers.
     __device__ __forceinline__ static int uniform(int x) { return __shfl_sync(0xFFFFFFFFu, x, 0); }
 
-    // Turn n: the scores of step n + 1, then the weighted values of step n.
+    // The scores of a step are issued before the weighted values of the step before, so that the softmax has
+    // them early, unless they must wait and the values need not: a new tile's queries may be late.
     __device__ bool products_loop(uint32_t leader) const {
         const uint32_t tm = (uint32_t)uniform((int)tmem);
         const int units = uniform(total);
-        int left = 0;                       // steps of the tile whose scores are still to come
-        uint32_t q_seg = 0, seg = 0;        // the next tile of the scores, the tile of the weighted values
-        bool first = true, last = false, next_first = true, next_last = false;
+        int s = 0, v = 0;             // steps whose scores and whose weighted values are issued
+        int left = 0;                 // steps of the tile whose scores are still to come
+        uint32_t q_seg = 0, seg = 0;  // the next tile of the scores, the tile of the weighted values
+        bool first = true;            // step v is its tile's first
+        uint32_t lasts = 0;           // bit n & 1: step n is its tile's last
 #pragma unroll 1
-        for (int n = -1; n < units; ++n) {
-            first = next_first, last = next_last;
-            if (n + 1 < units) {
-                const int st = (n + 1) & 1;
-                next_first = left == 0;
-                if (next_first) {
+        while (v < units) {
+            bool scores = s < units && s < v + 2;
+            if (scores && s > v) {  // step v's values could go first: whichever can
+                const uint32_t t0 = clock();
+                while (true) {
+                    scores = ready(bar.k_full[s & 1], (uint32_t)(s >> 1) & 1u) &&
+                             (left > 0 || ready(bar.q_full[q_seg & 1u], (q_seg >> 1) & 1u));
+                    if (scores || ready(bar.p_full[v & 1], (uint32_t)(v >> 1) & 1u)) break;
+                    if (*static_cast<volatile int32_t *>(&bar.stop) != 0 || (uint32_t)clock() - t0 > kWaitTicks) {
+                        *static_cast<volatile int32_t *>(&bar.stop) = 1;
+                        return false;
+                    }
+                }
+            }
+            if (scores) {
+                const int st = s & 1;
+                if (left == 0) {
                     if (!enter(q_seg)) return false;
                     left = uniform(tile(q_seg).count);
                     leave(q_seg);
                     if (!wait(bar.q_full[q_seg & 1u], (q_seg >> 1) & 1u)) return false;
                     ++q_seg;
                 }
-                if (!wait(bar.k_full[st], (uint32_t)((n + 1) >> 1) & 1u)) return false;
+                if (!wait(bar.k_full[st], (uint32_t)(s >> 1) & 1u)) return false;
                 tc_fence_after();
                 qk((int)((q_seg - 1) & 1u), st, tm, leader);
                 tc_commit(smem_u32(&bar.s_full[st]), leader);
-                next_last = --left == 0;
-                if (next_last) tc_commit(smem_u32(&bar.q_free[(q_seg - 1) & 1u]), leader);
-            }
-            if (n < 0) continue;
-            const int st = n & 1;
-            if (first && !wait(bar.o_free, (seg & 1u) ^ 1u)) return false;
-            if (!wait(bar.v_full[st], (uint32_t)(n >> 1) & 1u)) return false;
-            if (!wait(bar.p_full[st], (uint32_t)(n >> 1) & 1u)) return false;
-            tc_fence_after();
-            pv(st, tm, !first, leader);
-            tc_commit(smem_u32(&bar.v_free[st]), leader);
-            if (last) {
-                tc_commit(smem_u32(&bar.o_full), leader);
-                ++seg;
+                lasts &= ~(1u << st);
+                if (--left == 0) {
+                    tc_commit(smem_u32(&bar.q_free[(q_seg - 1) & 1u]), leader);
+                    lasts |= 1u << st;
+                }
+                ++s;
+            } else {
+                const int st = v & 1;
+                if (first && !wait(bar.o_free, (seg & 1u) ^ 1u)) return false;
+                if (!wait(bar.v_full[st], (uint32_t)(v >> 1) & 1u)) return false;
+                if (!wait(bar.p_full[st], (uint32_t)(v >> 1) & 1u)) return false;
+                tc_fence_after();
+                pv(st, tm, !first, leader);
+                tc_commit(smem_u32(&bar.v_free[st]), leader);
+                first = (lasts >> st & 1u) != 0;
+                if (first) {
+                    tc_commit(smem_u32(&bar.o_full), leader);
+                    ++seg;
+                }
+                ++v;
             }
         }
         return true;
@@ -509,15 +532,21 @@ struct Tree {
                 }
                 return y;
             };
+            // eight chunks in flight: a row does not fit the registers, and is read twice
             float top = 0.0f;
-#pragma unroll 4
-            for (int i = 0; i < D / 8; ++i) {
-                const uint4 x = read(i);
-                const uint32_t wd[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll 1
+            for (int i = 0; i < D / 8; i += 8) {
+                uint4 x[8];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float2 y = value(wd[e], 8 * i + 2 * e);
-                    top = fmaxf(top, fmaxf(fabsf(y.x), fabsf(y.y)));
+                for (int k = 0; k < 8; ++k) x[k] = read(i + k);
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    const uint32_t wd[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float2 y = value(wd[e], 8 * (i + k) + 2 * e);
+                        top = fmaxf(top, fmaxf(fabsf(y.x), fabsf(y.y)));
+                    }
                 }
             }
             const int ex = power_of(top);
@@ -525,19 +554,23 @@ struct Tree {
             const float turn = __uint_as_float(((uint32_t)(127 - ex) << 23) | (a.scale_log2 < 0.0f ? 0x80000000u : 0u));
             const uint32_t q_at = tmem + ((uint32_t)(rw * 32) << 16) + L::kQ + buf * (D / 2);
 #pragma unroll 1
-            for (int i = 0; i < D / 8; i += 4) {  // the row again, from the caches: it does not fit the registers
-                uint32_t o[16];
+            for (int i = 0; i < D / 8; i += 8) {
+                uint32_t o[2][16];
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
+                for (int k = 0; k < 8; ++k) {
                     const uint4 x = read(i + k);
-                    o[4 * k] = x.x, o[4 * k + 1] = x.y, o[4 * k + 2] = x.z, o[4 * k + 3] = x.w;
+                    uint32_t *to = o[k / 4] + 4 * (k % 4);
+                    to[0] = x.x, to[1] = x.y, to[2] = x.z, to[3] = x.w;
                 }
 #pragma unroll
-                for (int e = 0; e < 16; ++e) {
-                    const float2 y = value(o[e], 8 * i + 2 * e);
-                    o[e] = pack_fp16(y.x * turn, y.y * turn);
+                for (int k = 0; k < 2; ++k) {
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) {
+                        const float2 y = value(o[k][e], 8 * i + 32 * k + 2 * e);
+                        o[k][e] = pack_fp16(y.x * turn, y.y * turn);
+                    }
+                    tc_st16(q_at + 4 * i + 16 * k, o[k]);
                 }
-                tc_st16(q_at + 4 * i, o);
             }
             bar.q_scale[buf][rw * 32 + lane] = fabsf(a.scale_log2) * __uint_as_float((uint32_t)(127 + ex) << 23);
             tc_wait_st();
@@ -560,28 +593,30 @@ struct Tree {
             const int64_t slot = (int64_t)(2 * blockIdx.x + (seg > 0 ? 1 : 0)) * kRows + row;
             float *po = a.part_o + (slot - lane) * D + lane * 8;  // 32 rows' eighths in turn
 #pragma unroll 1
-            for (int c = 0; c < D; c += 16) {
-                float o[16];
-                tc_ld16(o, o_at + c);
+            for (int c = 0; c < D; c += 32) {
+                float o[32];
+                tc_ld32(o, o_at + c);
+                tc_wait_ld(o);
 #pragma unroll
-                for (int i = 0; i < 16; i += 4) {
+                for (int i = 0; i < 32; i += 4) {
                     const float4 s = MODE == 1 ? __ldg(reinterpret_cast<const float4 *>(vs + c + i)) : make_float4(1.0f, 1.0f, 1.0f, 1.0f);
                     o[i] *= s.x * inv, o[i + 1] *= s.y * inv, o[i + 2] *= s.z * inv, o[i + 3] *= s.w * inv;
                 }
                 if (!whole) {
 #pragma unroll
-                    for (int i = 0; i < 16; i += 4)
+                    for (int i = 0; i < 32; i += 4)
                         *reinterpret_cast<float4 *>(po + (c + i) / 8 * 256 + i % 8) = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
                 } else if (r < rows) {
-                    uint32_t y[8];
+                    uint32_t y[16];
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) y[i] = pack_bf16(o[2 * i], o[2 * i + 1]);
+                    for (int i = 0; i < 16; ++i) y[i] = pack_bf16(o[2 * i], o[2 * i + 1]);
                     if ((reinterpret_cast<uintptr_t>(dst) & 15) == 0) {
-                        reinterpret_cast<uint4 *>(dst + c)[0] = make_uint4(y[0], y[1], y[2], y[3]);
-                        reinterpret_cast<uint4 *>(dst + c)[1] = make_uint4(y[4], y[5], y[6], y[7]);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            reinterpret_cast<uint4 *>(dst + c)[i] = make_uint4(y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]);
                     } else {  // the output may lie on any element
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) {
+                        for (int i = 0; i < 16; ++i) {
                             dst[c + 2 * i] = (uint16_t)(y[i] & 0xFFFFu);
                             dst[c + 2 * i + 1] = (uint16_t)(y[i] >> 16);
                         }

@@ -113,12 +113,12 @@ struct Layout {
                   "the warpgroups' registers are the block's");
     static constexpr int kTileBytes = kCols * D * 2;  // a K' or V' stage
     static constexpr int kRawBytes = kCols * D;       // a slot of the ring: a step's codes of keys or of values
-    static constexpr int kRing = 80 * 1024 / kRawBytes;
+    static constexpr int kRing = 32 * 1024 / kRawBytes;  // of keys, and as many of values
     static constexpr int kK = 0;
     static constexpr int kV = kStages * kTileBytes;
     static constexpr int kRaw = 2 * kStages * kTileBytes;
     // more than half of an SM's shared memory, so that a CTA has the SM's tensor memory to itself
-    static constexpr int kBytes = kRaw + kRing * kRawBytes + 1024;
+    static constexpr int kBytes = kRaw + 2 * kRing * kRawBytes + 1024;
     static_assert(kBytes > 116 * 1024, "one CTA per SM");
     static constexpr int kO = kStages * kCols, kQ = kO + D;  // columns of tensor memory: S twice, O, Q twice
     static constexpr int kTmemCols = 512;
@@ -130,7 +130,9 @@ struct Barriers {
     // s_full: a step's scores, and its K' stage is free; v_free: its weighted values, and its V' stage
     uint64_t k_full[kStages], v_full[kStages], s_full[kStages], p_full[kStages], v_free[kStages];
     uint64_t q_full[kStages], q_free[kStages], o_full, o_free, ml_full, drained;
-    uint64_t raw_full[kMaxRing], raw_free[kMaxRing];
+    // slots of the keys, then of the values: a warp that waits for a slot's next phase has waited for the last, so
+    // that the parity tells them apart
+    uint64_t raw_full[2 * kMaxRing], raw_free[2 * kMaxRing];
     uint64_t pair[4];  // the two softmax warps of 32 rows
     uint64_t tile_full[kTiles], tile_free[kTiles];
     uint32_t tmem;
@@ -145,10 +147,12 @@ struct Barriers {
     float q_scale[kStages][kRows];  // log2 per unit of score, with the query's power of two
     float m[kRows], l[2][kRows];    // l: of each half of the positions
     float top[2][2][kRows];         // a step's largest score of each half, of two steps
-    // of what is in the ring: valid positions of each group of 16, the keys' and the values' scales (mode 2: one a group)
-    uint2 raw_valid[kMaxRing];
+    // of what is in the ring: valid positions of each group of 16, the keys' (only with the keys) and the values'
+    // scales (mode 2: one a group)
+    uint32_t filled[2 * kMaxRing];  // how often
+    uint2 raw_valid[2 * kMaxRing];
     alignas(16) float raw_ks[kMaxRing][kCols];
-    alignas(16) float raw_vs[kMaxRing][kCols];
+    alignas(16) float raw_vs[2 * kMaxRing][kCols];
     uint2 valid[kMaskSlots];  // 8 bytes: valid positions of each group of 16
     // modes 0 and 2: what was taken out of each group of 16's scales, as powers of two:
     // the keys' 2^e, the values' e and 2^-e
@@ -271,31 +275,33 @@ struct Tree {
             if (n >= 0) {
 #pragma unroll 1
                 for (int values = 0; values < 2 && good; ++values) {
-                    good = wait(bar.raw_free[slot], round ^ 1u);
+                    const int at = values * L::kRing + slot;
+                    good = wait(bar.raw_free[at], round ^ 1u);
                     if (!good) break;
-                    if (lane < 8) reinterpret_cast<uint8_t *>(&bar.raw_valid[slot])[grp] = (uint8_t)valid;
+                    if (lane < 8) reinterpret_cast<uint8_t *>(&bar.raw_valid[at])[grp] = (uint8_t)valid;
                     if (MODE == 0) {
                         if (values == 0) reinterpret_cast<float4 *>(bar.raw_ks[slot])[lane] = ks;
-                        reinterpret_cast<float4 *>(bar.raw_vs[slot])[lane] = vs;
+                        reinterpret_cast<float4 *>(bar.raw_vs[at])[lane] = vs;
                     } else if (MODE == 2 && lane < 8) {
-                        bar.raw_ks[slot][grp] = ks.x;
-                        bar.raw_vs[slot][grp] = vs.x;
+                        if (values == 0) bar.raw_ks[slot][grp] = ks.x;
+                        bar.raw_vs[at][grp] = vs.x;
                     }
                     const uint32_t groups = __popc(__ballot_sync(0xFFFFFFFFu, lane < 8 && valid > 0));
                     if (lane == 0)
                         asm volatile("mbarrier.arrive.expect_tx.release.cta.shared::cta.b64 _, [%0], %1;" ::"r"(
-                                         smem_u32(&bar.raw_full[slot])),
+                                         smem_u32(&bar.raw_full[at])),
                                      "r"(groups * 16u * D)
                                      : "memory");
+                    if (lane == 0) ++bar.filled[at];
                     __syncwarp();
                     const bool one = bs % 128 == 0 && groups == 8;
                     if (one ? lane == 0 : lane < 8 && valid > 0)
-                        copy(base + L::kRaw + slot * L::kRawBytes + grp * 16 * D, (values == 0 ? a.k_cache : a.v_cache) + row * D,
-                             bar.raw_full[slot], one ? 128 * D : 16 * D);
-                    if (++slot == L::kRing) {
-                        slot = 0;
-                        round ^= 1u;
-                    }
+                        copy(base + L::kRaw + at * L::kRawBytes + grp * 16 * D, (values == 0 ? a.k_cache : a.v_cache) + row * D,
+                             bar.raw_full[at], one ? 128 * D : 16 * D);
+                }
+                if (++slot == L::kRing) {
+                    slot = 0;
+                    round ^= 1u;
                 }
             }
             if (n >= -1 && n + 1 < total) {
@@ -340,17 +346,13 @@ struct Tree {
                 blk = left > 0 ? ld_ahead_s32(entry) : 0;
             }
         }
-        // nothing is in flight when the CTA ends, not after a wait that ran out either (a slot never used has no
-        // phase to wait for: its barrier answers for the phase before its first)
+        // nothing is in flight when the CTA ends, not after a wait that ran out either
+        __syncwarp();
 #pragma unroll 1
-        for (int i = 0; i < L::kRing; ++i) {
+        for (int i = 0; i < 2 * L::kRing; ++i) {
             const uint32_t t0 = clock();
-            while (!mbar_try(smem_u32(&bar.raw_full[slot]), round ^ 1u))
+            while (bar.filled[i] != 0u && !mbar_try(smem_u32(&bar.raw_full[i]), (bar.filled[i] - 1u) & 1u))
                 if ((uint32_t)clock() - t0 > kWaitTicks) break;
-            if (++slot == L::kRing) {
-                slot = 0;
-                round ^= 1u;
-            }
         }
     }
 
@@ -358,7 +360,7 @@ struct Tree {
     __device__ void dequantise() const {
         const int dw = (warp - L::kDequantWarp) % 8, values = (warp - L::kDequantWarp) / 8;
         const uint32_t src = base + L::kRaw + (uint32_t)((dw * 16 + T::row_in(lane)) * D + T::block_in(lane) * 64 + lane % 4 * 16);
-        int slot = values;  // keys and values take turns in the ring
+        int slot = values * L::kRing;
         uint32_t round = 0;
 #pragma unroll 1
         for (int n = 0; n < total; ++n) {
@@ -407,9 +409,8 @@ struct Tree {
             fence_async();
             arrive(values == 0 ? bar.k_full[st] : bar.v_full[st]);
             if (lane == 0) mbar_arrive(smem_u32(&bar.raw_free[slot]));
-            slot += 2;
-            if (slot >= L::kRing) {
-                slot -= L::kRing;
+            if (++slot == (values + 1) * L::kRing) {
+                slot = values * L::kRing;
                 round ^= 1u;
             }
         }
@@ -854,7 +855,8 @@ __global__ void __launch_bounds__(Layout<D>::kThreads, 1) tree_kernel(const Tree
                 mbar_init(smem_u32(&bar.q_full[i]), L::kRowWarps);
                 mbar_init(smem_u32(&bar.q_free[i]), 1 + L::kSoftmaxWarps);
             }
-            for (int i = 0; i < L::kRing; ++i) {
+            for (int i = 0; i < 2 * L::kRing; ++i) {
+                bar.filled[i] = 0u;
                 mbar_init(smem_u32(&bar.raw_full[i]), 1);
                 mbar_init(smem_u32(&bar.raw_free[i]), L::kDequantWarps / 2);
             }

@@ -8,8 +8,13 @@
 // one cluster of CTAs does the call, each with the sums of all sequences in its shared memory
 // (they are a few bytes per sequence, and cheaper made eight times than exchanged), and its
 // barrier orders pushes and pops, and reads of the lengths and the count before what is written
-// in their place (so none of these is a read-only load).  A thread then takes one id or slot, finds its sequence by a binary search
-// in the sums, and reads and writes whole lines with its neighbours.
+// in their place (so none of these is a read-only load).  A thread then takes one id or slot,
+// finds its sequence by a binary search in the sums, and reads and writes whole lines with its
+// neighbours.
+//
+// Slots follow from the inputs alone: a popped id is looked up where it comes from, in the stack
+// below or in the row that gives it up.  So many of them are made by a kernel of their own on all
+// SMs, before the cluster changes anything.
 #include "kvc8_internal.cuh"
 
 namespace kvc8 {
@@ -21,6 +26,11 @@ constexpr int kCluster = 8;
 __device__ __forceinline__ uint32_t cluster_rank() {
     uint32_t r;
     asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ uint32_t cluster_size() {
+    uint32_t r;
+    asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
     return r;
 }
 __device__ __forceinline__ void cluster_barrier() {
@@ -55,154 +65,225 @@ __device__ __forceinline__ Change from_below(const Change &a, int by) {
     return r;
 }
 
-__global__ void __launch_bounds__(kThreads, 1) assign_kernel(const AssignArgs a) {
-    extern __shared__ int64_t dyn[];
-    const int B = a.num_seqs, MB = a.max_blocks_per_seq;
-    const uint32_t bs = (uint32_t)a.block_size;
-    int64_t *s_add = dyn;                                    // [B + 1] exclusive sums
-    int32_t *s_need = reinterpret_cast<int32_t *>(s_add + B + 1);  // [B + 1]
-    int32_t *s_give = s_need + B + 1;                              // [B + 1]
-    int32_t *s_held = s_give + B + 1;                              // [B]; -1: lengths out of range
+// What all sequences up to one need, give and add, in shared memory, and the stack before the pops.
+struct Sums {
+    int64_t *add;              // [B + 1] exclusive
+    int32_t *need, *give;      // [B + 1] exclusive
+    int32_t *held;             // [B]; -1: lengths out of range
+    int32_t F, R, have, need_all;
+    int64_t add_all;
+
+    __device__ __forceinline__ uint32_t blocks(int b, uint32_t bs) const { return ((uint32_t)held[b] + bs - 1) / bs; }
+    __device__ __forceinline__ bool served(int b) const { return need[b + 1] == need[b] || need[b + 1] <= have; }
+};
+
+// By the whole block; `reports`: this block reports what is out of range.
+__device__ __forceinline__ Sums add_up(const AssignArgs &a, int64_t *dyn, bool reports) {
     __shared__ Change s_warp[kThreads / 32];
+    const int B = a.num_seqs, T = blockDim.x;
+    const uint32_t bs = (uint32_t)a.block_size;
+    Sums s;
+    s.add = dyn;
+    s.need = reinterpret_cast<int32_t *>(s.add + B + 1);
+    s.give = s.need + B + 1;
+    s.held = s.give + B + 1;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const uint32_t rank = cluster_rank();
-    const int64_t cap = (int64_t)MB * a.block_size;
+    const int64_t cap = (int64_t)a.max_blocks_per_seq * a.block_size;
 
     const int32_t given = *a.free_count;
-    const int32_t F = min(max(given, 0), a.num_blocks);
-    if (given != F && rank == 0 && threadIdx.x == 0) report(a.dev_error, KVC8_DEV_BAD_LENGTH);
-
-    Change before{0, 0, 0};
-    for (int b0 = 0; b0 < B; b0 += kThreads) {
-        const int b = b0 + threadIdx.x;
+    s.F = min(max(given, 0), a.num_blocks);
+    if (given != s.F && reports && threadIdx.x == 0) report(a.dev_error, KVC8_DEV_BAD_LENGTH);
+    if (threadIdx.x == 0) {
+        s.need[0] = s.give[0] = 0;
+        s.add[0] = 0;
+    }
+    // this thread's sequences in a row: what they change together, then one scan, then each one's sums
+    const int per = (B + T - 1) / T, b0 = min(B, (int)threadIdx.x * per), b1 = min(B, b0 + per);
+    auto change = [&](int b, bool first) {
         Change c{0, 0, 0};
-        if (b < B) {
-            const int32_t held = a.held[b], want = a.want[b];
-            const bool good = held >= 0 && want >= 0 && held <= cap && want <= cap;
-            if (good) {
-                const int32_t hb = (int32_t)(((uint32_t)held + bs - 1) / bs), wb = (int32_t)(((uint32_t)want + bs - 1) / bs);
-                c.need = max(0, wb - hb);
-                c.give = max(0, hb - wb);
-            } else if (rank == 0) {
-                report(a.dev_error, held < 0 || want < 0 ? KVC8_DEV_BAD_LENGTH : KVC8_DEV_POS_BEYOND_TABLE);
-            }
-            if (held >= 0 && want > held) c.add = want - held;
-            s_held[b] = good ? held : -1;
+        const int32_t held = a.held[b], want = a.want[b];
+        const bool good = held >= 0 && want >= 0 && held <= cap && want <= cap;
+        if (good) {
+            const int32_t hb = (int32_t)(((uint32_t)held + bs - 1) / bs), wb = (int32_t)(((uint32_t)want + bs - 1) / bs);
+            c.need = max(0, wb - hb);
+            c.give = max(0, hb - wb);
+        } else if (reports && first) {
+            report(a.dev_error, held < 0 || want < 0 ? KVC8_DEV_BAD_LENGTH : KVC8_DEV_POS_BEYOND_TABLE);
         }
-        Change sum = c;  // inclusive over the warp, then the block
+        if (held >= 0 && want > held) c.add = want - held;
+        s.held[b] = good ? held : -1;
+        return c;
+    };
+    Change sum{0, 0, 0};
+    for (int b = b0; b < b1; ++b) sum = plus(sum, change(b, true));
+    Change upto = sum;  // inclusive over the warp, then the block
+#pragma unroll
+    for (int by = 1; by < 32; by <<= 1) {
+        const Change o = from_below(upto, by);
+        if (lane >= by) upto = plus(upto, o);
+    }
+    if (lane == 31) s_warp[warp] = upto;
+    __syncthreads();
+    Change before{0, 0, 0}, all{0, 0, 0};
+    {  // every warp adds up the warps' sums for itself
+        Change w = lane < T / 32 ? s_warp[lane] : Change{0, 0, 0};
 #pragma unroll
         for (int by = 1; by < 32; by <<= 1) {
-            const Change o = from_below(sum, by);
-            if (lane >= by) sum = plus(sum, o);
+            const Change o = from_below(w, by);
+            if (lane >= by) w = plus(w, o);
         }
-        if (lane == 31) s_warp[warp] = sum;
-        __syncthreads();
-        if (warp == 0) {
-            Change w = s_warp[lane];
-#pragma unroll
-            for (int by = 1; by < 32; by <<= 1) {
-                const Change o = from_below(w, by);
-                if (lane >= by) w = plus(w, o);
-            }
-            s_warp[lane] = w;
-        }
-        __syncthreads();
-        sum = plus(sum, before);
-        if (warp > 0) sum = plus(sum, s_warp[warp - 1]);
-        if (b < B) {
-            s_need[b + 1] = sum.need;
-            s_give[b + 1] = sum.give;
-            s_add[b + 1] = sum.add;
-        }
-        before = plus(before, s_warp[kThreads / 32 - 1]);
-        __syncthreads();
+        const int below = warp > 0 ? warp - 1 : 0;
+        before = Change{__shfl_sync(0xFFFFFFFFu, w.need, below), __shfl_sync(0xFFFFFFFFu, w.give, below),
+                        __shfl_sync(0xFFFFFFFFu, w.add, below)};
+        if (warp == 0) before = Change{0, 0, 0};
+        all = Change{__shfl_sync(0xFFFFFFFFu, w.need, 31), __shfl_sync(0xFFFFFFFFu, w.give, 31),
+                     __shfl_sync(0xFFFFFFFFu, w.add, 31)};
     }
-    if (threadIdx.x == 0) {
-        s_need[0] = s_give[0] = 0;
-        s_add[0] = 0;
+    upto = plus(upto, before);
+    Change at{upto.need - sum.need, upto.give - sum.give, upto.add - sum.add};
+    for (int b = b0; b < b1; ++b) {
+        at = plus(at, per == 1 ? sum : change(b, false));
+        s.need[b + 1] = at.need;
+        s.give[b + 1] = at.give;
+        s.add[b + 1] = at.add;
     }
+    before = all;
     __syncthreads();
+    s.R = before.give;
+    s.have = (int32_t)min((int64_t)s.F + s.R, (int64_t)a.num_blocks);
+    s.need_all = before.need;
+    s.add_all = before.add;
+    return s;
+}
 
-    const uint32_t first = rank * kThreads + threadIdx.x, stride = kCluster * kThreads;
+// kRun slots in a row to a thread: one search, and one lookup of an id where they lie in one block.
+constexpr int kRun = 4;
+__device__ __forceinline__ void write_slots(const AssignArgs &a, const Sums &s, int64_t first, int64_t stride) {
+    const int B = a.num_seqs;
+    const int64_t MB = a.max_blocks_per_seq, slots = min(s.add_all, a.slot_rows);
+    const uint32_t bs = (uint32_t)a.block_size;
+    for (int64_t t0 = first * kRun; t0 < slots; t0 += stride * kRun) {
+        int b = owner(s.add, B, t0), last_b = -1;
+        uint32_t last_lb = 0;
+        int32_t id = 0;
+#pragma unroll
+        for (int e = 0; e < kRun; ++e) {
+            const int64_t t = t0 + e;
+            if (t >= slots) break;
+            while (t >= s.add[b + 1]) ++b;
+            const int32_t held = s.held[b];
+            int64_t slot = -1;
+            if (held >= 0 && s.served(b)) {
+                const uint32_t p = (uint32_t)held + (uint32_t)(t - s.add[b]), lb = p / bs, hb = s.blocks(b, bs);
+                if (b != last_b || lb != last_lb) {
+                    if (lb < hb) {
+                        id = a.block_table[b * MB + lb];
+                    } else {  // popped: from the stack as it was, or from the row that gives it up
+                        const int32_t at = s.have - 1 - (s.need[b] + (int32_t)(lb - hb));
+                        if (at < s.F) {
+                            id = a.free_blocks[at];
+                        } else {
+                            const int g = owner(s.give, B, at - s.F);
+                            id = a.block_table[g * MB + (int32_t)s.blocks(g, bs) - s.give[g + 1] + (at - s.F)];
+                        }
+                    }
+                    last_b = b;
+                    last_lb = lb;
+                }
+                slot = (int64_t)id * bs + (p - lb * bs);
+            }
+            a.slot_map[t] = slot;
+        }
+    }
+}
+
+__global__ void __launch_bounds__(kThreads, 1) slots_kernel(const AssignArgs a) {
+    extern __shared__ int64_t dyn[];
+    const Sums s = add_up(a, dyn, false);
+    write_slots(a, s, (int64_t)blockIdx.x * blockDim.x + threadIdx.x, (int64_t)gridDim.x * blockDim.x);
+}
+
+__global__ void __launch_bounds__(kThreads, 1) assign_kernel(const AssignArgs a, int with_slots) {
+    extern __shared__ int64_t dyn[];
+    const int B = a.num_seqs;
+    const int64_t MB = a.max_blocks_per_seq;
+    const uint32_t bs = (uint32_t)a.block_size, rank = cluster_rank();
+    const Sums s = add_up(a, dyn, rank == 0);
+    const uint32_t first = rank * blockDim.x + threadIdx.x, stride = cluster_size() * blockDim.x;
     auto in_pool = [&](int32_t id) {
         if (id < 0 || id >= a.num_blocks) report(a.dev_error, KVC8_DEV_BAD_BLOCK_ID);
     };
     // given up: entry w_b + j of b's row
-    const uint32_t R = (uint32_t)before.give;
-    for (uint32_t x = first; x < R; x += stride) {
-        const int b = owner(s_give, B, (int32_t)x);
-        const int32_t hb = (int32_t)(((uint32_t)s_held[b] + bs - 1) / bs);
-        const int32_t entry = hb - s_give[b + 1] + (int32_t)x;  // w_b + (x - s_give[b])
-        const int32_t id = a.block_table[(int64_t)b * MB + entry];
+    for (uint32_t x = first; x < (uint32_t)s.R; x += stride) {
+        const int b = owner(s.give, B, (int32_t)x);
+        const int32_t entry = (int32_t)s.blocks(b, bs) - s.give[b + 1] + (int32_t)x;  // w_b + (x - give[b])
+        const int32_t id = a.block_table[b * MB + entry];
         in_pool(id);
-        if ((int64_t)F + x < a.num_blocks) a.free_blocks[F + x] = id;
+        if ((int64_t)s.F + x < a.num_blocks) a.free_blocks[s.F + x] = id;
         else report(a.dev_error, KVC8_DEV_BAD_LENGTH);
     }
     cluster_barrier();
-    const int32_t have = (int32_t)min((int64_t)F + R, (int64_t)a.num_blocks);
-
+    const int32_t have = s.have;
     // needed: entry h_b + j of b's row
-    for (uint32_t k = first; k < (uint32_t)min(before.need, have); k += stride) {
-        const int b = owner(s_need, B, (int32_t)k);
-        if (s_need[b + 1] > have) continue;
-        const int32_t hb = (int32_t)(((uint32_t)s_held[b] + bs - 1) / bs);
+    for (uint32_t k = first; k < (uint32_t)min(s.need_all, have); k += stride) {
+        const int b = owner(s.need, B, (int32_t)k);
+        if (s.need[b + 1] > have) continue;
         const int32_t id = a.free_blocks[have - 1 - (int32_t)k];
         in_pool(id);
-        a.block_table[(int64_t)b * MB + hb + ((int32_t)k - s_need[b])] = id;
+        a.block_table[b * MB + (int32_t)s.blocks(b, bs) + ((int32_t)k - s.need[b])] = id;
     }
     for (uint32_t b = first; b < (uint32_t)B; b += stride) {
-        const bool whole = s_need[b + 1] == s_need[b] || s_need[b + 1] <= have;
-        if (!whole && s_need[b] <= have) report(a.dev_error, KVC8_DEV_NO_FREE_BLOCK);
-        a.lens_out[b] = whole && s_held[b] >= 0 ? a.want[b] : a.held[b];
+        const bool whole = s.served(b);
+        if (!whole && s.need[b] <= have) report(a.dev_error, KVC8_DEV_NO_FREE_BLOCK);
+        a.lens_out[b] = whole && s.held[b] >= 0 ? a.want[b] : a.held[b];
     }
-    if (rank == 0 && warp == 0) {  // the last sequence that is served says how many were popped
-        int32_t taken = 0;
-        if (before.need <= have) {
-            taken = before.need;
-        } else if (B > 0) {
-            taken = s_need[owner(s_need, B + 1, have)];
-        }
-        if (lane == 0) *a.free_count_out = have - taken;
+    if (rank == 0 && threadIdx.x == 0) {
+        // the last sequence that is served says how many were popped
+        int32_t taken = s.need_all;
+        if (taken > have) taken = s.need[owner(s.need, B + 1, have)];
+        *a.free_count_out = have - taken;
+        if (a.slot_map != nullptr && s.add_all > a.slot_rows) report(a.dev_error, KVC8_DEV_OUT_ROW_RANGE);
     }
-    const int64_t slots = min(before.add, a.slot_rows);
-    if (before.add > a.slot_rows && a.slot_map != nullptr && rank == 0 && threadIdx.x == 0)
-        report(a.dev_error, KVC8_DEV_OUT_ROW_RANGE);
-    for (int64_t t = first; t < slots; t += stride) {
-        const int b = owner(s_add, B, t);
-        const int32_t held = s_held[b];
-        int64_t slot = -1;
-        if (held >= 0 && (s_need[b + 1] == s_need[b] || s_need[b + 1] <= have)) {
-            const uint32_t p = (uint32_t)held + (uint32_t)(t - s_add[b]), lb = p / bs, hb = ((uint32_t)held + bs - 1) / bs;
-            const int32_t id = lb < hb ? a.block_table[(int64_t)b * MB + lb]
-                                       : a.free_blocks[have - 1 - (s_need[b] + (int32_t)(lb - hb))];
-            slot = (int64_t)id * bs + (p - lb * bs);
-        }
-        a.slot_map[t] = slot;
-    }
+    if (with_slots != 0) write_slots(a, s, first, stride);
 }
 
 size_t shared_bytes(int B) { return sizeof(int64_t) * ((size_t)B + 1) + sizeof(int32_t) * (3 * (size_t)B + 2); }
 
 }  // namespace
 
+// Slots beyond which they are made on all SMs, and sequences, blocks or slots beyond which the call takes a
+// cluster and not one CTA.
+constexpr int64_t kManySlots = 1 << 17, kManySeqs = 1024;
+
 cudaError_t launch_assign(const AssignArgs &a, cudaStream_t stream) {
     const size_t smem = shared_bytes(a.num_seqs);
     if (smem > 48 * 1024) {
-        const cudaError_t e = cudaFuncSetAttribute(assign_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        cudaError_t e = cudaFuncSetAttribute(assign_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        if (e != cudaSuccess) return e;
+        e = cudaFuncSetAttribute(slots_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
         if (e != cudaSuccess) return e;
     }
+    const bool many_slots = a.slot_map != nullptr && a.slot_rows > kManySlots;
+    if (many_slots) {
+        const int64_t ctas = (a.slot_rows + kThreads * kRun - 1) / (kThreads * kRun), sms = sm_count();
+        slots_kernel<<<(unsigned)(ctas < sms ? ctas : sms), kThreads, smem, stream>>>(a);
+        const cudaError_t e = cudaGetLastError();
+        if (e != cudaSuccess) return e;
+    }
+    const int64_t slots = a.slot_map != nullptr ? a.slot_rows : 0;
+    const unsigned cluster = a.num_seqs <= kManySeqs && slots <= 4096 ? 1 : kCluster;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(kCluster);
-    cfg.blockDim = dim3(kThreads);
+    cfg.gridDim = dim3(cluster);
+    cfg.blockDim = dim3(a.num_seqs > 512 || slots > 2048 ? kThreads : 512);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = kCluster;
+    attr[0].val.clusterDim.x = cluster;
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, assign_kernel, a);
+    return cudaLaunchKernelEx(&cfg, assign_kernel, a, a.slot_map != nullptr && !many_slots ? 1 : 0);
 }
 
 }  // namespace kvc8

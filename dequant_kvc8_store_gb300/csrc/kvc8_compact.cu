@@ -2,11 +2,14 @@
 // context + accepted[k] to context + k, k ascending, in every head of both caches.
 //
 // A CTA per sequence.  It checks the whole list and finds each row's places first, then a
-// thread takes 16 bytes of a head's row (mode 0: also one of the rows' scales) through all
+// thread takes a unit of bytes of a head's row (mode 0: also one of the rows' scales) through all
 // moves in order: up to kBatch of its loads are in flight, and since accepted[k] >= k ascends
 // strictly, no row of a later batch is written by an earlier one.  Different threads' bytes
-// do not meet.  The work is a few rows per sequence, so latency bounds it: lengths, indices and
-// block ids are each one round trip, and all rows another.
+// do not meet.  A unit is 16 bytes, or four codes where they are quantised anew, a division each.
+// The work is a few rows per sequence, so latency bounds it: lengths and indices are one round
+// trip, block ids another, and a batch's rows a third.
+#include <type_traits>
+
 #include "kvc8_internal.cuh"
 
 namespace kvc8 {
@@ -14,9 +17,10 @@ namespace {
 
 constexpr int kBatch = 8;  // moves in flight
 constexpr int kMaxThreads = 512;
+static_assert(KVC8_MAX_DRAFTS <= kMaxThreads, "a thread to an index where threads are many");
 
-// Sixteen codes quantised anew for another block's scale.
-__device__ __forceinline__ uint32_t requantise(uint32_t w, float from, float to) {
+// Four codes quantised anew for another block's scale.
+__device__ __forceinline__ uint32_t requantised(uint32_t w, float from, float to) {
     uint32_t r = 0;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -28,7 +32,9 @@ __device__ __forceinline__ uint32_t requantise(uint32_t w, float from, float to)
     return r;
 }
 
+template <bool REQUANT>
 __global__ void __launch_bounds__(kMaxThreads) compact_kernel(const CompactArgs a) {
+    using Unit = typename std::conditional<REQUANT, uint32_t, uint4>::type;
     __shared__ int32_t s_from[KVC8_MAX_DRAFTS], s_to[KVC8_MAX_DRAFTS];  // block ids; -1: does not move
     __shared__ int32_t s_from_at[KVC8_MAX_DRAFTS], s_to_at[KVC8_MAX_DRAFTS];
     const int b = blockIdx.x, H = a.g.kv_heads;
@@ -36,13 +42,16 @@ __global__ void __launch_bounds__(kMaxThreads) compact_kernel(const CompactArgs 
     const int64_t cap = (int64_t)a.g.max_blocks_per_seq * a.g.block_size;
     const int32_t ctx = a.context_kv_lens[b], n = a.num_accepted[b];
     const int32_t *idx = a.accepted + (int64_t)b * a.max_accepted;
+    // asked for together with the lengths
+    const int mine = threadIdx.x;
+    const int32_t first = mine < a.max_accepted ? idx[mine] : 0, before = mine > 0 && mine < a.max_accepted ? idx[mine - 1] : -1;
 
     bool bad_index = false, beyond = false;
     const bool in_range = ctx >= 0 && n >= 0 && n <= a.max_accepted;
     if (in_range) {
-        for (int k = threadIdx.x; k < n; k += blockDim.x) {
-            const int32_t i = idx[k];
-            if (i < 0 || (k > 0 && i <= idx[k - 1])) {
+        for (int k = mine; k < n; k += blockDim.x) {
+            const int32_t i = k == mine ? first : idx[k];
+            if (i < 0 || (k > 0 && i <= (k == mine ? before : idx[k - 1]))) {
                 bad_index = true;
             } else if ((int64_t)ctx + i >= cap) {
                 beyond = true;
@@ -75,38 +84,35 @@ __global__ void __launch_bounds__(kMaxThreads) compact_kernel(const CompactArgs 
     }
     if (threadIdx.x == 0 && a.lens_out != nullptr) a.lens_out[b] = ctx + n;
 
-    const int chunks = a.row_bytes / 16, rows = 2 * H;  // rows: of the keys, then of the values
+    const int chunks = a.row_bytes / (int)sizeof(Unit), rows = 2 * H;  // rows: of the keys, then of the values
     for (int u = threadIdx.x; u < rows * chunks; u += blockDim.x) {
         const int r = u / chunks, c = u - r * chunks, h = r < H ? r : r - H;
-        char *cache = r < H ? a.k_cache : a.v_cache;
+        char *cache = (r < H ? a.k_cache : a.v_cache) + c * (int)sizeof(Unit);
         const float *scale = r < H ? a.k_scale : a.v_scale;
-        const bool requant = scale != nullptr && a.g.quant_mode == 2;
         for (int k0 = 0; k0 < n; k0 += kBatch) {
-            uint4 x[kBatch];
+            Unit x[kBatch];
+            float from[kBatch], to[kBatch];
 #pragma unroll
             for (int i = 0; i < kBatch; ++i) {
                 const int k = k0 + i;
                 if (k < n && s_from[k] >= 0) {
-                    const int64_t at = ((int64_t)s_from[k] * H + h) * bs + s_from_at[k];
-                    x[i] = *reinterpret_cast<const uint4 *>(cache + at * a.row_bytes + 16 * c);
+                    const int64_t at = (int64_t)s_from[k] * H + h;
+                    x[i] = *reinterpret_cast<const Unit *>(cache + (at * bs + s_from_at[k]) * a.row_bytes);
+                    if (REQUANT) {
+                        from[i] = ld_nc_f32(scale + at);
+                        to[i] = ld_nc_f32(scale + (int64_t)s_to[k] * H + h);
+                    }
                 }
             }
 #pragma unroll
             for (int i = 0; i < kBatch; ++i) {
                 const int k = k0 + i;
                 if (k < n && s_from[k] >= 0) {
-                    if (requant && s_from[k] != s_to[k]) {
-                        const float from = ld_nc_f32(scale + (int64_t)s_from[k] * H + h);
-                        const float to = ld_nc_f32(scale + (int64_t)s_to[k] * H + h);
-                        if (from != to) {
-                            x[i].x = requantise(x[i].x, from, to);
-                            x[i].y = requantise(x[i].y, from, to);
-                            x[i].z = requantise(x[i].z, from, to);
-                            x[i].w = requantise(x[i].w, from, to);
-                        }
+                    if constexpr (REQUANT) {
+                        if (from[i] != to[i]) x[i] = requantised(x[i], from[i], to[i]);
                     }
                     const int64_t at = ((int64_t)s_to[k] * H + h) * bs + s_to_at[k];
-                    *reinterpret_cast<uint4 *>(cache + at * a.row_bytes + 16 * c) = x[i];
+                    *reinterpret_cast<Unit *>(cache + at * a.row_bytes) = x[i];
                 }
             }
         }
@@ -126,9 +132,11 @@ __global__ void __launch_bounds__(kMaxThreads) compact_kernel(const CompactArgs 
 }  // namespace
 
 cudaError_t launch_compact(const CompactArgs &a, cudaStream_t stream) {
-    const int64_t units = (int64_t)2 * a.g.kv_heads * (a.row_bytes / 16);
+    const bool requant = a.k_scale != nullptr && a.g.quant_mode == 2;
+    const int64_t units = (int64_t)2 * a.g.kv_heads * (a.row_bytes / (requant ? 4 : 16));
     const int threads = units >= kMaxThreads ? kMaxThreads : (int)((units + 31) / 32 * 32);
-    compact_kernel<<<(unsigned)a.g.num_seqs, threads, 0, stream>>>(a);
+    if (requant) compact_kernel<true><<<(unsigned)a.g.num_seqs, threads, 0, stream>>>(a);
+    else compact_kernel<false><<<(unsigned)a.g.num_seqs, threads, 0, stream>>>(a);
     return cudaGetLastError();
 }
 

@@ -20,7 +20,7 @@
 namespace kvc8 {
 namespace {
 
-constexpr int kThreads = 1024;
+constexpr int kThreads = 1024, kFewThreads = 256;
 constexpr int kCluster = 8;
 
 __device__ __forceinline__ uint32_t cluster_rank() {
@@ -28,11 +28,7 @@ __device__ __forceinline__ uint32_t cluster_rank() {
     asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
     return r;
 }
-__device__ __forceinline__ uint32_t cluster_size() {
-    uint32_t r;
-    asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
-    return r;
-}
+
 __device__ __forceinline__ void cluster_barrier() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
@@ -124,21 +120,18 @@ __device__ __forceinline__ Sums add_up(const AssignArgs &a, int64_t *dyn, bool r
     }
     if (lane == 31) s_warp[warp] = upto;
     __syncthreads();
-    Change before{0, 0, 0}, all{0, 0, 0};
-    {  // every warp adds up the warps' sums for itself
+    if (warp == 0) {
         Change w = lane < T / 32 ? s_warp[lane] : Change{0, 0, 0};
 #pragma unroll
         for (int by = 1; by < 32; by <<= 1) {
             const Change o = from_below(w, by);
             if (lane >= by) w = plus(w, o);
         }
-        const int below = warp > 0 ? warp - 1 : 0;
-        before = Change{__shfl_sync(0xFFFFFFFFu, w.need, below), __shfl_sync(0xFFFFFFFFu, w.give, below),
-                        __shfl_sync(0xFFFFFFFFu, w.add, below)};
-        if (warp == 0) before = Change{0, 0, 0};
-        all = Change{__shfl_sync(0xFFFFFFFFu, w.need, 31), __shfl_sync(0xFFFFFFFFu, w.give, 31),
-                     __shfl_sync(0xFFFFFFFFu, w.add, 31)};
+        s_warp[lane] = w;
     }
+    __syncthreads();
+    Change before = warp > 0 ? s_warp[warp - 1] : Change{0, 0, 0};
+    const Change all = s_warp[kThreads / 32 - 1];
     upto = plus(upto, before);
     Change at{upto.need - sum.need, upto.give - sum.give, upto.add - sum.add};
     for (int b = b0; b < b1; ++b) {
@@ -147,29 +140,29 @@ __device__ __forceinline__ Sums add_up(const AssignArgs &a, int64_t *dyn, bool r
         s.give[b + 1] = at.give;
         s.add[b + 1] = at.add;
     }
-    before = all;
     __syncthreads();
-    s.R = before.give;
+    s.R = all.give;
     s.have = (int32_t)min((int64_t)s.F + s.R, (int64_t)a.num_blocks);
-    s.need_all = before.need;
-    s.add_all = before.add;
+    s.need_all = all.need;
+    s.add_all = all.add;
     return s;
 }
 
-// kRun slots in a row to a thread: one search, and one lookup of an id where they lie in one block.
+// Where there are more slots than threads, kRun in a row to a thread: one search, and one lookup of an id where they lie in
+// one block (one slot to a thread is quicker while threads last: the lookups of a run follow one another).
 constexpr int kRun = 4;
 __device__ __forceinline__ void write_slots(const AssignArgs &a, const Sums &s, int64_t first, int64_t stride) {
     const int B = a.num_seqs;
     const int64_t MB = a.max_blocks_per_seq, slots = min(s.add_all, a.slot_rows);
     const uint32_t bs = (uint32_t)a.block_size;
-    for (int64_t t0 = first * kRun; t0 < slots; t0 += stride * kRun) {
+    const int run = slots <= stride ? 1 : kRun;
+    for (int64_t t0 = first * run; t0 < slots; t0 += stride * run) {
         int b = owner(s.add, B, t0), last_b = -1;
         uint32_t last_lb = 0;
         int32_t id = 0;
-#pragma unroll
-        for (int e = 0; e < kRun; ++e) {
-            const int64_t t = t0 + e;
-            if (t >= slots) break;
+        const int64_t end = min(t0 + run, slots);
+#pragma unroll 1
+        for (int64_t t = t0; t < end; ++t) {
             while (t >= s.add[b + 1]) ++b;
             const int32_t held = s.held[b];
             int64_t slot = -1;
@@ -209,7 +202,7 @@ __global__ void __launch_bounds__(kThreads, 1) assign_kernel(const AssignArgs a,
     const int64_t MB = a.max_blocks_per_seq;
     const uint32_t bs = (uint32_t)a.block_size, rank = cluster_rank();
     const Sums s = add_up(a, dyn, rank == 0);
-    const uint32_t first = rank * blockDim.x + threadIdx.x, stride = cluster_size() * blockDim.x;
+    const uint32_t first = rank * blockDim.x + threadIdx.x, stride = kCluster * blockDim.x;
     auto in_pool = [&](int32_t id) {
         if (id < 0 || id >= a.num_blocks) report(a.dev_error, KVC8_DEV_BAD_BLOCK_ID);
     };
@@ -251,9 +244,9 @@ size_t shared_bytes(int B) { return sizeof(int64_t) * ((size_t)B + 1) + sizeof(i
 
 }  // namespace
 
-// Slots beyond which they are made on all SMs, and sequences, blocks or slots beyond which the call takes a
-// cluster and not one CTA.
-constexpr int64_t kManySlots = 1 << 17, kManySeqs = 1024;
+// Slots beyond which they are made on all SMs (36 696 slots: 9.5 us in the cluster, 12.3 with a kernel of their own;
+// 820 000: 127 in the cluster, 36).
+constexpr int64_t kManySlots = 1 << 17;
 
 cudaError_t launch_assign(const AssignArgs &a, cudaStream_t stream) {
     const size_t smem = shared_bytes(a.num_seqs);
@@ -270,16 +263,18 @@ cudaError_t launch_assign(const AssignArgs &a, cudaStream_t stream) {
         const cudaError_t e = cudaGetLastError();
         if (e != cudaSuccess) return e;
     }
+    // Small CTAs start and meet sooner (256 sequences, 1150 slots: 5.8 us with 256 threads, 6.2 with 1024, 8.2 in one CTA),
+    // as long as they have a thread to a sequence and to a slot (36 696 slots: 12.3 and 9.5 us).
     const int64_t slots = a.slot_map != nullptr ? a.slot_rows : 0;
-    const unsigned cluster = a.num_seqs <= kManySeqs && slots <= 4096 ? 1 : kCluster;
+    const int threads = a.num_seqs <= kFewThreads && slots <= kFewThreads * kCluster ? kFewThreads : kThreads;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(cluster);
-    cfg.blockDim = dim3(a.num_seqs > 512 || slots > 2048 ? kThreads : 512);
+    cfg.gridDim = dim3(kCluster);
+    cfg.blockDim = dim3((unsigned)threads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = cluster;
+    attr[0].val.clusterDim.x = kCluster;
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;

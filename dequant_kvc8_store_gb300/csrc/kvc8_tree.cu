@@ -133,7 +133,6 @@ struct Barriers {
     // slots of the keys, then of the values: a warp that waits for a slot's next phase has waited for the last, so
     // that the parity tells them apart
     uint64_t raw_full[2 * kMaxRing], raw_free[2 * kMaxRing];
-    uint64_t pair[4];  // the two softmax warps of 32 rows
     uint64_t tile_full[kTiles], tile_free[kTiles];
     uint32_t tmem;
     int32_t stop;
@@ -155,10 +154,9 @@ struct Barriers {
     alignas(16) float raw_vs[2 * kMaxRing][kCols];
     uint2 valid[kMaskSlots];  // 8 bytes: valid positions of each group of 16
     // modes 0 and 2: what was taken out of each group of 16's scales, as powers of two:
-    // the keys' 2^e, the values' e and 2^-e
+    // the keys' 2^e, the values' e
     alignas(16) float k_pow[kMaskSlots][kCols / 16];
     alignas(16) float v_exp[kMaskSlots][kCols / 16];
-    alignas(16) float v_inv[kMaskSlots][kCols / 16];
 };
 
 template <int MODE, int D>
@@ -392,7 +390,6 @@ struct Tree {
                 if (MODE != 1) {
                     bar.k_pow[n % kMaskSlots][dw] = __uint_as_float((uint32_t)(127 + ek) << 23);
                     bar.v_exp[n % kMaskSlots][dw] = (float)ev;
-                    bar.v_inv[n % kMaskSlots][dw] = __uint_as_float((uint32_t)(127 - ev) << 23);
                 }
                 reinterpret_cast<uint8_t *>(&bar.valid[n % kMaskSlots])[dw] = (uint8_t)valid;
             }
@@ -657,6 +654,14 @@ struct Tree {
         }
     }
 
+    // The two softmax warps of 32 rows meet, by a hardware barrier: no limit, but none is needed, as a warp that
+    // leaves early (see leave_pair) has come to it for the last time, and the other one finds `stop` set.
+    __device__ __forceinline__ bool meet(int quad) const {
+        asm volatile("bar.sync %0, 64;" ::"r"(1 + quad) : "memory");
+        return *static_cast<volatile int32_t *>(&bar.stop) == 0;
+    }
+    __device__ __forceinline__ void leave_pair(int quad) const { asm volatile("bar.arrive %0, 64;" ::"r"(1 + quad) : "memory"); }
+
     // ---- softmax (two threads per query row, 64 of a step's positions each) -----------------------------------
     // 32 bits of a row's mask; drafts before the first are the context.
     __device__ __forceinline__ uint32_t mask_word(const uint32_t *mask, int word) const {
@@ -685,20 +690,24 @@ struct Tree {
     }
 
     __device__ void softmax() const {
+        if (!softmax_loop()) leave_pair(warp & 3);
+    }
+    // false: a wait ran out (not found by meeting the other warp, which has left then)
+    __device__ __forceinline__ bool softmax_loop() const {
         const int quad = warp & 3, half = warp >> 2, row = quad * 32 + lane;
         const uint32_t lanes = (uint32_t)(quad * 32) << 16;
         int n = 0;
         uint32_t met = 0;  // steps in which the row's two warps met
 #pragma unroll 1
         for (uint32_t seg = 0; n < total; ++seg) {
-            if (!enter(seg)) return;
+            if (!enter(seg)) return false;
             const Tile &x = tile(seg);
             const int end = n + x.count, buf = (int)(seg & 1u), token = x.token;
             const bool busy = x.row0 + quad * 32 < x.rows;  // uniform in the warp: some row is a query's
             const int t = min(x.row0 + row, x.rows - 1) / p.base.group;
             int d0 = x.step * kCols + half * 64 - x.ctx;  // the draft at the first position, if not negative
             leave(seg);
-            if (!wait(bar.q_full[buf], (seg >> 1) & 1u)) return;
+            if (!wait(bar.q_full[buf], (seg >> 1) & 1u)) return false;
             const float scale = bar.q_scale[buf][row];
             arrive(bar.q_free[buf]);
             float m = -INFINITY, l = 0.0f;
@@ -708,31 +717,23 @@ struct Tree {
                 const int st = n & 1;
                 uint32_t sees[2] = {0xFFFFFFFFu, 0xFFFFFFFFu};
                 if (d0 + 64 > 0 && busy) visible(sees, d0, t, token);  // some position is a draft's
-                if (!wait(bar.s_full[st], (uint32_t)(n >> 1) & 1u)) return;
+                if (!wait(bar.s_full[st], (uint32_t)(n >> 1) & 1u)) return false;
                 tc_fence_after();
                 if (busy) {
-                    if (!step(tmem + lanes + st * kCols, tmem + lanes + L::kO, quad, half, scale, have_o, n, met & 1u, sees, m, l)) return;
+                    const int went = step(tmem + lanes + st * kCols, tmem + lanes + L::kO, quad, half, scale, have_o, n, met & 1u, sees, m, l);
+                    if (went <= 0) return went < 0;
                     ++met;
                 }
                 have_o = true;
                 tc_fence_before();
                 arrive(bar.p_full[st]);
             }
-            if (!wait(bar.o_free, (seg & 1u) ^ 1u)) return;
+            if (!wait(bar.o_free, (seg & 1u) ^ 1u)) return false;
             if (half == 0) bar.m[row] = m;
             bar.l[half][row] = l;
             arrive(bar.ml_full);
         }
-    }
-
-    // A group's factor of the scores and shift, read again where they are used.  The factor is never 0,
-    // which times the -inf of a position left out would be no number; 2^-126 instead does not show.
-    __device__ __forceinline__ float2 factor_shift(int slot, int grp, float scale) const {
-        if (MODE == 1) return make_float2(fmaxf(scale, 0x1p-126f), 0.0f);
-        float f, e;
-        asm volatile("ld.shared.f32 %0, [%1];" : "=f"(f) : "r"(smem_u32(&bar.k_pow[slot][grp])));
-        asm volatile("ld.shared.f32 %0, [%1];" : "=f"(e) : "r"(smem_u32(&bar.v_exp[slot][grp])));
-        return make_float2(fmaxf(scale * f, 0x1p-126f), e);
+        return true;
     }
 
     // One step of a row's half: S -> P, the running maximum m and the half's sum l.  A group's weights are
@@ -740,7 +741,8 @@ struct Tree {
     // with the tile's values is the weight times the value; m bounds score + e, lazily, and is the
     // same in both halves.  fp16 holds such weights (at most 2^15) eight times finer than bf16, and what
     // falls below 2^-21 of the largest to 2^-32 of it.
-    __device__ __forceinline__ bool step(uint32_t s_at, uint32_t o_at, int quad, int half, float scale, bool have_o, int n,
+    // 1: done, 0: a wait ran out, -1: the other warp has left.
+    __device__ __forceinline__ int step(uint32_t s_at, uint32_t o_at, int quad, int half, float scale, bool have_o, int n,
                                          uint32_t met, const uint32_t (&sees)[2], float &m, float &l) const {
         const int slot = n % kMaskSlots;
         const uint32_t valid = half == 0 ? bar.valid[slot].x : bar.valid[slot].y;
@@ -760,21 +762,26 @@ struct Tree {
                     if ((keep >> i & 1u) == 0u) s[q][i] = -INFINITY;
             }
         }
+        // Each group of 16's factor of the scores and shift.  The factor is never 0, which times the -inf of a position left
+        // out would be no number; 2^-126 instead does not show.
+        float f[4], g[4];
+        if (MODE == 1) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) f[i] = fmaxf(scale, 0x1p-126f), g[i] = 0.0f;
+        } else {
+            const float4 k = reinterpret_cast<const float4 *>(bar.k_pow[slot])[half], e = reinterpret_cast<const float4 *>(bar.v_exp[slot])[half];
+            const float ks[4] = {k.x, k.y, k.z, k.w}, es[4] = {e.x, e.y, e.z, e.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) f[i] = fmaxf(scale * ks[i], 0x1p-126f), g[i] = es[i];
+        }
         float mx = -INFINITY;
 #pragma unroll
-        for (int q = 0; q < 2; ++q) {
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const float2 fe = factor_shift(slot, 4 * half + 2 * q + i, scale);
-                mx = fmaxf(mx, fmaf(top16(s[q], 16 * i), fe.x, fe.y));
-            }
-        }
+        for (int i = 0; i < 4; ++i) mx = fmaxf(mx, fmaf(top16(s[i / 2], i % 2 * 16), f[i], g[i]));
         // The halves' larger one; after it both have read S, over which P is written.
         const int row = quad * 32 + lane;
         bar.top[met][half][row] = mx;
         tc_fence_before();
-        arrive(bar.pair[quad]);
-        if (!wait(bar.pair[quad], met)) return false;
+        if (!meet(quad)) return -1;
         tc_fence_after();
         mx = fmaxf(mx, bar.top[met][half ^ 1][row]);
         const bool moves = mx > m + (kLift + kLazy) || (m == -INFINITY && mx > m);
@@ -783,7 +790,7 @@ struct Tree {
             if (moves) m = mx - kLift;
             l *= c;
             if (have_o) {  // once the step before is in it; half of the channels each
-                if (!wait(bar.v_free[(n - 1) & 1], (uint32_t)((n - 1) >> 1) & 1u)) return false;
+                if (!wait(bar.v_free[(n - 1) & 1], (uint32_t)((n - 1) >> 1) & 1u)) return 0;
                 tc_fence_after();
 #pragma unroll 1
                 for (int d = 0; d < D / 2; d += 16) {
@@ -799,15 +806,12 @@ struct Tree {
         const float neg = m == -INFINITY ? 0.0f : -m;
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
-            const int grp = 4 * half + 2 * q;
-            const float2 a = factor_shift(slot, grp, scale), b = factor_shift(slot, grp + 1, scale);
-            const float f[2] = {a.x, b.x}, g[2] = {a.y + neg, b.y + neg};
             float2 sum[2];
             uint32_t o[16];
 #pragma unroll
             for (int i = 0; i < 32; i += 2) {
-                float2 y = __ffma2_rn(make_float2(s[q][i], s[q][i + 1]), make_float2(f[i / 16], f[i / 16]),
-                                      make_float2(g[i / 16], g[i / 16]));
+                const float fi = f[2 * q + i / 16], gi = g[2 * q + i / 16] + neg;
+                float2 y = __ffma2_rn(make_float2(s[q][i], s[q][i + 1]), make_float2(fi, fi), make_float2(gi, gi));
                 y = make_float2(ex2(y.x), ex2(y.y));
                 sum[i / 16] = i % 16 == 0 ? y : __fadd2_rn(sum[i / 16], y);
                 o[i / 2] = pack_fp16(y.x, y.y);
@@ -816,11 +820,12 @@ struct Tree {
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 const float part = sum[i].x + sum[i].y;
-                l = MODE == 1 ? l + part : fmaf(part, bar.v_inv[slot][grp + i], l);
+                // (times 2^-e)
+                l = MODE == 1 ? l + part : fmaf(part, __uint_as_float((uint32_t)(127 - (int)g[2 * q + i]) << 23), l);
             }
         }
         tc_wait_st();
-        return true;
+        return 1;
     }
 };
 
@@ -860,7 +865,6 @@ __global__ void __launch_bounds__(Layout<D>::kThreads, 1) tree_kernel(const Tree
                 mbar_init(smem_u32(&bar.raw_full[i]), 1);
                 mbar_init(smem_u32(&bar.raw_free[i]), L::kDequantWarps / 2);
             }
-            for (int i = 0; i < 4; ++i) mbar_init(smem_u32(&bar.pair[i]), 2);
             for (int i = 0; i < kTiles; ++i) {
                 mbar_init(smem_u32(&bar.tile_full[i]), 1);
                 mbar_init(smem_u32(&bar.tile_free[i]), L::kSoftmaxWarps + L::kRowWarps + 2);

@@ -10,7 +10,8 @@
 // K'^T and O += P V' are tcgen05.mma (M = 128, fp16, fp32 in tensor memory); Q lies in tensor memory,
 // and P replaces S there: both are A operands.  Warps by role:
 //   walk        1: what the CTA's next tiles are
-//   fetch       1: pages' codes by bulk copies into a ring in shared memory, as many steps ahead as fit
+//   fetch       2, for the keys and for the values: pages' codes by bulk copies into rings in shared memory, two steps
+//               ahead
 //   dequantise  16, eight for the keys and eight for the values: codes to K' and V' as fp16, two stages of
 //               each in shared memory
 //   mma         one lane issues both products
@@ -103,7 +104,7 @@ template <int D>
 struct Layout {
     static constexpr int kSoftmaxWarps = 8, kRowWarps = 4, kDequantWarps = 16;
     static constexpr int kRowWarp = kSoftmaxWarps, kDequantWarp = kRowWarp + kRowWarps;
-    static constexpr int kMmaWarp = kDequantWarp + kDequantWarps, kFetchWarp = kMmaWarp + 1, kWalkWarp = kMmaWarp + 2;
+    static constexpr int kMmaWarp = kDequantWarp + kDequantWarps, kFetchWarp = kMmaWarp + 1, kWalkWarp = kMmaWarp + 2;  // kFetchWarp + 2: the values'
     static constexpr int kThreads = 1024;
     // Registers per thread: a softmax thread holds 64 scores.
     static constexpr int kSoftmaxRegs = 104, kRowRegs = 64, kDequantRegs = 48, kMmaRegs = 48;
@@ -256,7 +257,8 @@ struct Tree {
     }
     __device__ void fetch() const {
         const AttnArgs &a = p.base;
-        const int grp = lane & 7, bs = a.g.block_size;
+        const int grp = lane & 7, bs = a.g.block_size, values = (warp - L::kFetchWarp) / 2;
+        const int8_t *cache = values == 0 ? a.k_cache : a.v_cache;
         uint32_t seg = 0;
         int count = 0;                // steps of the tile not asked for yet
         int left = 0, at = 0, head = 0;  // of the step asked for: positions left, slot and entry of the table
@@ -271,32 +273,29 @@ struct Tree {
 #pragma unroll 1
         for (int n = -2; n < total && good; ++n) {
             if (n >= 0) {
-#pragma unroll 1
-                for (int values = 0; values < 2 && good; ++values) {
-                    const int at = values * L::kRing + slot;
-                    good = wait(bar.raw_free[at], round ^ 1u);
-                    if (!good) break;
-                    if (lane < 8) reinterpret_cast<uint8_t *>(&bar.raw_valid[at])[grp] = (uint8_t)valid;
-                    if (MODE == 0) {
-                        if (values == 0) reinterpret_cast<float4 *>(bar.raw_ks[slot])[lane] = ks;
-                        reinterpret_cast<float4 *>(bar.raw_vs[at])[lane] = vs;
-                    } else if (MODE == 2 && lane < 8) {
-                        if (values == 0) bar.raw_ks[slot][grp] = ks.x;
-                        bar.raw_vs[at][grp] = vs.x;
-                    }
-                    const uint32_t groups = __popc(__ballot_sync(0xFFFFFFFFu, lane < 8 && valid > 0));
-                    if (lane == 0)
-                        asm volatile("mbarrier.arrive.expect_tx.release.cta.shared::cta.b64 _, [%0], %1;" ::"r"(
-                                         smem_u32(&bar.raw_full[at])),
-                                     "r"(groups * 16u * D)
-                                     : "memory");
-                    if (lane == 0) ++bar.filled[at];
-                    __syncwarp();
-                    const bool one = bs % 128 == 0 && groups == 8;
-                    if (one ? lane == 0 : lane < 8 && valid > 0)
-                        copy(base + L::kRaw + at * L::kRawBytes + grp * 16 * D, (values == 0 ? a.k_cache : a.v_cache) + row * D,
-                             bar.raw_full[at], one ? 128 * D : 16 * D);
+                const int to = values * L::kRing + slot;
+                good = wait(bar.raw_free[to], round ^ 1u);
+                if (!good) break;
+                if (lane < 8) reinterpret_cast<uint8_t *>(&bar.raw_valid[to])[grp] = (uint8_t)valid;
+                if (MODE == 0) {
+                    if (values == 0) reinterpret_cast<float4 *>(bar.raw_ks[slot])[lane] = ks;
+                    reinterpret_cast<float4 *>(bar.raw_vs[to])[lane] = vs;
+                } else if (MODE == 2 && lane < 8) {
+                    if (values == 0) bar.raw_ks[slot][grp] = ks.x;
+                    bar.raw_vs[to][grp] = vs.x;
                 }
+                const uint32_t groups = __popc(__ballot_sync(0xFFFFFFFFu, lane < 8 && valid > 0));
+                __syncwarp();
+                if (lane == 0) {
+                    asm volatile("mbarrier.arrive.expect_tx.release.cta.shared::cta.b64 _, [%0], %1;" ::"r"(smem_u32(&bar.raw_full[to])),
+                                 "r"(groups * 16u * D)
+                                 : "memory");
+                    ++bar.filled[to];
+                }
+                __syncwarp();
+                const bool one = bs % 128 == 0 && groups == 8;  // one block holds the step
+                if (one ? lane == 0 : lane < 8 && valid > 0)
+                    copy(base + L::kRaw + to * L::kRawBytes + grp * 16 * D, cache + row * D, bar.raw_full[to], one ? 128 * D : 16 * D);
                 if (++slot == L::kRing) {
                     slot = 0;
                     round ^= 1u;
@@ -304,18 +303,18 @@ struct Tree {
             }
             if (n >= -1 && n + 1 < total) {
                 const bool in = blk >= 0 && blk < a.g.num_blocks;
-                if (!in && lane < 8) report(a.dev_error, KVC8_DEV_BAD_BLOCK_ID);
+                if (!in && lane < 8 && values == 0) report(a.dev_error, KVC8_DEV_BAD_BLOCK_ID);
                 valid = in ? max(0, min(16, left)) : 0;
                 const int64_t page = (int64_t)(in ? blk : 0) * a.g.kv_heads + head;
                 row = page * bs + at;
                 if (MODE == 0) {
                     const int64_t r = __shfl_sync(0xFFFFFFFFu, row, lane / 4) + lane % 4 * 4;
                     if (__shfl_sync(0xFFFFFFFFu, valid, lane / 4) > 0) {
-                        ks = ld_ahead_f32x4(a.k_scale + r);
+                        if (values == 0) ks = ld_ahead_f32x4(a.k_scale + r);
                         vs = ld_ahead_f32x4(a.v_scale + r);
                     }
                 } else if (MODE == 2 && valid > 0) {
-                    ks.x = ld_ahead_f32(a.k_scale + page);
+                    if (values == 0) ks.x = ld_ahead_f32(a.k_scale + page);
                     vs.x = ld_ahead_f32(a.v_scale + page);
                 }
             }
@@ -347,7 +346,7 @@ struct Tree {
         // nothing is in flight when the CTA ends, not after a wait that ran out either
         __syncwarp();
 #pragma unroll 1
-        for (int i = 0; i < 2 * L::kRing; ++i) {
+        for (int i = values * L::kRing; i < (values + 1) * L::kRing; ++i) {
             const uint32_t t0 = clock();
             while (bar.filled[i] != 0u && !mbar_try(smem_u32(&bar.raw_full[i]), (bar.filled[i] - 1u) & 1u))
                 if ((uint32_t)clock() - t0 > kWaitTicks) break;
@@ -867,7 +866,7 @@ __global__ void __launch_bounds__(Layout<D>::kThreads, 1) tree_kernel(const Tree
             }
             for (int i = 0; i < kTiles; ++i) {
                 mbar_init(smem_u32(&bar.tile_full[i]), 1);
-                mbar_init(smem_u32(&bar.tile_free[i]), L::kSoftmaxWarps + L::kRowWarps + 2);
+                mbar_init(smem_u32(&bar.tile_free[i]), L::kSoftmaxWarps + L::kRowWarps + 3);
             }
             mbar_init(smem_u32(&bar.o_full), 1);
             mbar_init(smem_u32(&bar.o_free), L::kRowWarps);
@@ -928,7 +927,7 @@ __global__ void __launch_bounds__(Layout<D>::kThreads, 1) tree_kernel(const Tree
         if (warp >= L::kMmaWarp) {
             reg_give<L::kMmaRegs>();
             if (warp == L::kMmaWarp) Tree<MODE, D>(p, bar, dyn).products();
-            if (warp == L::kFetchWarp) Tree<MODE, D>(p, bar, dyn).fetch();
+            if (warp == L::kFetchWarp || warp == L::kFetchWarp + 2) Tree<MODE, D>(p, bar, dyn).fetch();
             if (warp == L::kWalkWarp) Tree<MODE, D>(p, bar, dyn).walk();
         } else if (warp >= L::kDequantWarp) {
             reg_give<L::kDequantRegs>();

@@ -142,7 +142,6 @@ struct Barriers {
     uint32_t start_off;
     uint32_t units, first;  // of all CTAs, this one's
     int32_t total;          // units of this CTA
-    int32_t pad[2];
     Tile tile[kTiles];
     float q_scale[kStages][kRows];  // log2 per unit of score, with the query's power of two
     float m[kRows], l[2][kRows];    // l: of each half of the positions
@@ -653,8 +652,9 @@ struct Tree {
         }
     }
 
-    // The two softmax warps of 32 rows meet, by a hardware barrier: no limit, but none is needed, as a warp that
-    // leaves early (see leave_pair) has come to it for the last time, and the other one finds `stop` set.
+    // The two softmax warps of 32 rows meet, by a hardware barrier: no limit, but none is needed.  A warp leaves
+    // early only once `stop` is set, and then comes to the barrier one last time (leave_pair), whatever the other
+    // one has read: if that one still waits here or comes later, it goes on, finds `stop` set and leaves too.
     __device__ __forceinline__ bool meet(int quad) const {
         asm volatile("bar.sync %0, 64;" ::"r"(1 + quad) : "memory");
         return *static_cast<volatile int32_t *>(&bar.stop) == 0;
@@ -691,7 +691,7 @@ struct Tree {
     __device__ void softmax() const {
         if (!softmax_loop()) leave_pair(warp & 3);
     }
-    // false: a wait ran out (not found by meeting the other warp, which has left then)
+    // false: a wait ran out
     __device__ __forceinline__ bool softmax_loop() const {
         const int quad = warp & 3, half = warp >> 2, row = quad * 32 + lane;
         const uint32_t lanes = (uint32_t)(quad * 32) << 16;
@@ -719,8 +719,8 @@ struct Tree {
                 if (!wait(bar.s_full[st], (uint32_t)(n >> 1) & 1u)) return false;
                 tc_fence_after();
                 if (busy) {
-                    const int went = step(tmem + lanes + st * kCols, tmem + lanes + L::kO, quad, half, scale, have_o, n, met & 1u, sees, m, l);
-                    if (went <= 0) return went < 0;
+                    if (!step(tmem + lanes + st * kCols, tmem + lanes + L::kO, quad, half, scale, have_o, n, met & 1u, sees, m, l))
+                        return false;
                     ++met;
                 }
                 have_o = true;
@@ -740,8 +740,8 @@ struct Tree {
     // with the tile's values is the weight times the value; m bounds score + e, lazily, and is the
     // same in both halves.  fp16 holds such weights (at most 2^15) eight times finer than bf16, and what
     // falls below 2^-21 of the largest to 2^-32 of it.
-    // 1: done, 0: a wait ran out, -1: the other warp has left.
-    __device__ __forceinline__ int step(uint32_t s_at, uint32_t o_at, int quad, int half, float scale, bool have_o, int n,
+    // false: a wait ran out.
+    __device__ __forceinline__ bool step(uint32_t s_at, uint32_t o_at, int quad, int half, float scale, bool have_o, int n,
                                          uint32_t met, const uint32_t (&sees)[2], float &m, float &l) const {
         const int slot = n % kMaskSlots;
         const uint32_t valid = half == 0 ? bar.valid[slot].x : bar.valid[slot].y;
@@ -780,7 +780,7 @@ struct Tree {
         const int row = quad * 32 + lane;
         bar.top[met][half][row] = mx;
         tc_fence_before();
-        if (!meet(quad)) return -1;
+        if (!meet(quad)) return false;
         tc_fence_after();
         mx = fmaxf(mx, bar.top[met][half ^ 1][row]);
         const bool moves = mx > m + (kLift + kLazy) || (m == -INFINITY && mx > m);
@@ -789,7 +789,7 @@ struct Tree {
             if (moves) m = mx - kLift;
             l *= c;
             if (have_o) {  // once the step before is in it; half of the channels each
-                if (!wait(bar.v_free[(n - 1) & 1], (uint32_t)((n - 1) >> 1) & 1u)) return 0;
+                if (!wait(bar.v_free[(n - 1) & 1], (uint32_t)((n - 1) >> 1) & 1u)) return false;
                 tc_fence_after();
 #pragma unroll 1
                 for (int d = 0; d < D / 2; d += 16) {
@@ -824,7 +824,7 @@ struct Tree {
             }
         }
         tc_wait_st();
-        return 1;
+        return true;
     }
 };
 

@@ -880,9 +880,10 @@ static kvc8_status check_tree_geom(const kvc8_geom *g, int32_t num_q_heads, int6
     if (group > 8 || (g->head_dim != 64 && g->head_dim != 128) || g->block_size % 16 != 0 ||
         max_drafts > KVC8_MAX_DRAFTS || num_tokens > INT32_MAX)
         return KVC8_ERR_UNSUPPORTED;
-    // positions are 32-bit, with room for the drafts and a step's overhang
+    // A tile of query rows may have all its steps in one CTA, at about 1.4 us each: 2^26 positions take 0.7 s, which
+    // keeps clear of the two seconds that its waits are allowed.
     const int64_t cap = (int64_t)g->max_blocks_per_seq * g->block_size;
-    if (cap > (int64_t)INT32_MAX - 4096) return KVC8_ERR_UNSUPPORTED;
+    if (cap > (int64_t)1 << 26) return KVC8_ERR_UNSUPPORTED;
     const int64_t tiles = (int64_t)g->num_seqs * ((max_drafts * group + 127) / 128);  // < 2^36
     const int64_t steps = (cap + 127) / 128;
     if (tiles > (int64_t)INT32_MAX / steps / g->kv_heads) return KVC8_ERR_UNSUPPORTED;

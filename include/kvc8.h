@@ -618,7 +618,7 @@ kvc8_status kvc8_shared_prefix_attention(const kvc8_geom *g, int32_t num_q_heads
  *     follow one another without gaps, in the order of kvc8_store's new tokens.
  *   - *free_count_out = F + R less what was popped.  Entries given up stay in the
  *     table, and popped ones in free_blocks behind the new count.
- * One launch.
+ * One launch, two with more than 131072 slot_rows.
  *
  *   g               num_seqs <= KVC8_ASSIGN_MAX_SEQS (else KVC8_ERR_UNSUPPORTED);
  *                   kv_heads, head_dim and quant_mode are checked, but not used
@@ -684,9 +684,9 @@ size_t kvc8_tree_attention_workspace_bytes(const kvc8_geom *g, int32_t num_q_hea
  *                   out_head_stride, 1); not the query
  *   workspace       >= kvc8_tree_attention_workspace_bytes bytes, 256-byte aligned;
  *                   calls that overlap on the GPU need separate workspaces
- * Supported: head_dim 64 or 128, block_size a multiple of 16, and fewer than 2^31
- * units of 128 query rows (drafts * group) of a kv head by 128 positions for full
- * tables.  A sequence whose cu_q_lens decrease, leave [0, num_tokens] or exceed
+ * Supported: head_dim 64 or 128, block_size a multiple of 16, tables of at most 2^26
+ * positions, and fewer than 2^31 units of 128 query rows (drafts * group) of a kv
+ * head by 128 positions for full tables.  A sequence whose cu_q_lens decrease, leave [0, num_tokens] or exceed
  * max_drafts is left out and its rows stay unwritten (KVC8_DEV_BAD_LENGTH).  A
  * negative context counts as 0 (KVC8_DEV_BAD_LENGTH); positions beyond the table
  * (KVC8_DEV_POS_BEYOND_TABLE) and those of blocks outside the pool

@@ -102,3 +102,11 @@ def test_names():
     assert (B.DEV_NO_FREE_BLOCK, B.DEV_BAD_INDEX) == (6, 7) and kv.kvc8_version() >= 10200
     text = open(B.HEADER).read()
     assert f"#define KVC8_ASSIGN_MAX_SEQS {B.ASSIGN_MAX_SEQS}" in text and f"#define KVC8_MAX_DRAFTS {B.MAX_DRAFTS}" in text
+
+
+def test_tree_refuses_tables_of_more_than_2_26_positions():
+    # a tile of query rows may have all its steps in one CTA: its waits must end within their limit
+    g = lambda blocks: geom(num_seqs=1, kv_heads=1, max_blocks_per_seq=blocks, block_size=16)  # noqa: E731
+    size = lambda blocks: kv.kvc8_tree_attention_workspace_bytes(g(blocks), 4, 1, 4)  # noqa: E731
+    assert size(1 << 22) > 0 and size((1 << 22) + 1) == 0
+    assert tree(g((1 << 22) + 1), heads=4, n=1) == kv.ERR_UNSUPPORTED

@@ -270,3 +270,49 @@ class DecodeAttention:
                                       d.block_table, d.context_lengths, self.scale, o,
                                       o.stride(0), o.stride(1), self.workspace, self.ws_bytes,
                                       d.dev_error, stream)
+
+
+class TreeAttention:
+    """kvc8_tree_attention of a DeviceBatch's new tokens, taken as drafts that were stored
+    (one query of each, num_q_heads = group * kv_heads, seeded N(0, 1) bf16); output
+    bf16 [N][num_q_heads][D].
+
+    masks: host uint64 [N][words], the drafts that each draft sees; None: a chain."""
+
+    def __init__(self, d: DeviceBatch, group: int, masks=None, seed: int = 0, softmax_scale=None):
+        self.d = d
+        w = d.w
+        self.num_q_heads = w.kv_heads * group
+        rng = np.random.default_rng([seed, 79])
+        x = rng.standard_normal((w.num_tokens, self.num_q_heads, w.head_dim)).astype(np.float32)
+        self.q_bits = (x.view(np.uint32) >> 16).astype(np.uint16)
+        self.query = _bf16(self.q_bits).to(d.device)
+        self.out = torch.empty_like(self.query)
+        self.scale = float(softmax_scale if softmax_scale is not None else w.head_dim ** -0.5)
+        lens = [1] if w.cu_q_lens is None else np.diff(w.cu_q_lens)
+        self.max_drafts = int(max([1, *lens]))
+        self.masks, self.words = None, 0
+        if masks is not None:
+            masks = np.ascontiguousarray(masks, np.uint64)
+            self.words = masks.shape[1]
+            self.masks = torch.from_numpy(masks.view(np.int64)).to(d.device)
+        self.ws_bytes = B.kvc8_tree_attention_workspace_bytes(d.g, self.num_q_heads, w.num_tokens, self.max_drafts)
+        self.workspace = torch.empty(max(self.ws_bytes, 256), dtype=torch.uint8, device=d.device)
+
+    def __call__(self, stream=None):
+        d, q, o = self.d, self.query, self.out
+        B.kvc8_tree_attention(d.g, self.num_q_heads, q.shape[0], self.max_drafts, q, q.stride(0), q.stride(1),
+                              d.k_cache, d.v_cache, d.k_scale, d.v_scale, d.block_table, d.cu_q_lens,
+                              d.context_kv_lens, self.masks, self.words, self.scale, o, o.stride(0), o.stride(1),
+                              self.workspace, self.ws_bytes, d.dev_error, stream)
+
+    def keep(self, accepted, num_accepted, stream=None):
+        """kvc8_compact_drafts: the drafts of `accepted` (host int32 [B][most], the first
+        num_accepted[b] of a row) move behind the context; returns the new lengths (device)."""
+        d = self.d
+        accepted = torch.from_numpy(np.ascontiguousarray(accepted, np.int32)).to(d.device)
+        num = torch.from_numpy(np.asarray(num_accepted, np.int32)).to(d.device)
+        lens = torch.empty_like(d.context_kv_lens)
+        B.kvc8_compact_drafts(d.g, d.k_cache, d.v_cache, d.k_scale, d.v_scale, d.block_table, d.context_kv_lens,
+                              accepted, accepted.shape[1], num, lens, d.dev_error, stream)
+        return lens

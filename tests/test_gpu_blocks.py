@@ -189,3 +189,27 @@ def test_a_replayed_graph_follows_its_lengths_on_another_stream():
         torch.cuda.synchronize()
         y.d, y.g = x.d, x.g
         y.check()
+
+
+@pytest.mark.parametrize("alias", ["held", "want", None])
+def test_slots_of_a_launch_of_their_own_with_outputs_in_place_and_replayed(alias):
+    rng = np.random.default_rng(11)
+    x = Problem(*lengths(rng, 4096, 90, 150, 0.2), 16, seed=12)
+    x.place()
+    want = x.want_all()
+    assert x.d["slots"].numel() > 1 << 17
+    if alias is not None:
+        x.d["lens"], x.d["out"] = x.d[alias], x.d["count"]
+    first = {k: x.d[k].clone() for k in ("held", "want", "free", "count", "table")}
+    x.call()
+    x.check(want)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):  # the inputs again, the call, twice
+        for _ in range(2):
+            for k, v in first.items():
+                x.d[k].copy_(v)
+            x.call()
+    x.d["slots"].fill_(-99)
+    graph.replay()
+    torch.cuda.synchronize()
+    x.check(want)

@@ -8,9 +8,9 @@
 // do not meet.  A unit is 16 bytes, or four codes where they are quantised anew, a division each.
 // The work is a few rows per sequence, so latency bounds it: lengths and indices are one round
 // trip, block ids another, and a batch's rows a third.  bf16 pages, 256 sequences of 64 drafts
-// (16.5 MB): 7.3 us, 2.3 TB/s; the call by itself on int8 pages, 64 sequences of 24: under 6 us.
-// 33 sequences of 9 to 61 drafts with block scales: 34 us before four codes had a thread, 19
-// now, both with the gather that reads the pages back.
+// (16.5 MB): 7.2 us, 2.3 TB/s; int8 pages, 1 sequence of 12 drafts: 5.2 us, 64 of 24: 6.2 us.
+// 33 sequences of 9 to 61 drafts with block scales, a division for each code that changes blocks:
+// 12.3 us (with a gather that reads the pages back 19; 34 before four codes had a thread).
 #include <type_traits>
 
 #include "kvc8_internal.cuh"

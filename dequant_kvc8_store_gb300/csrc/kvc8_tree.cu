@@ -3,15 +3,20 @@
 //   out = sum_p w_p V'[p] / sum_p w_p,  w_p = exp(scale <q, K'[p]>),  K', V' = fp32(code) * scale
 //
 // A sequence's T drafts times G query heads are T G query rows against the same positions: 4 T G D
-// flops for 2 D bytes of codes a position and head, so HBM bounds up to about 150 rows and the
-// tensor cores more.
+// flops for 2 D bytes of codes a position and head, so HBM would bound up to about 150 rows and the
+// tensor cores more.  What bounds it in fact is a step's chain: its scores, their maximum, 64 exponentials a
+// thread, the weighted values, with the dequantising warps' instructions between (8 heads, D = 128, whole calls):
+//   256 sequences of up to 8192 positions, 16 rows, channel scales   663 us, 3.4 TB/s (a step 2500 cycles)
+//   64 of 8192, 16 and 64 rows, dynamic scales                       268 and 290 us, 4.1 and 3.9 TB/s
+//   2 of 131072, 256 rows, dynamic scales                            311 us, 878 TFLOP/s (2650 cycles, 71% of issue slots)
+//   1 of 500, 16 rows (2 heads, D = 64)                              12.4 us: two launches, round trips
 //
 // tree_kernel: one persistent CTA per SM, a tile of 128 query rows, 128 positions a step.  S = Q
 // K'^T and O += P V' are tcgen05.mma (M = 128, fp16, fp32 in tensor memory); Q lies in tensor memory,
 // and P replaces S there: both are A operands.  Warps by role:
 //   walk        1: what the CTA's next tiles are
-//   fetch       2, for the keys and for the values: pages' codes by bulk copies into rings in shared memory, two steps
-//               ahead
+//   fetch       2, for the keys and for the values: pages' codes by bulk copies into rings of two steps in shared
+//               memory (2 x 131072: 351 us with one warp for both, 311 with two; three steps of keys were no faster)
 //   dequantise  16, eight for the keys and eight for the values: codes to K' and V' as fp16, two stages of
 //               each in shared memory
 //   mma         one lane issues both products
@@ -21,9 +26,10 @@
 //               the weights grow by more than 2^8, and O is seldom rescaled.  Warps without a row do
 //               nothing
 //   rows        4: the next tile's queries into tensor memory, the last one's O out of it
+// With at most 64 rows idle softmax warps dequantise as well (given_up, below).
 // S and Q are there twice: the scores of a step are made while the softmax works on the step before.  The roles'
 // loops are kept short: together they must fit the SM's instruction cache (with 95 KB of code, of which each
-// step ran through about 30, a step took 3100 cycles and the warps waited for instructions).
+// step ran through about 30, a step took 3100 cycles and the warps waited for instructions; it is 75 now).
 //
 // The units (sequence, kv head, row tile, step) are numbered in that order and cut into equal shares,
 // a CTA's share in a row: ragged lengths need no plan, every CTA adds up the lengths itself.  What a
@@ -159,7 +165,7 @@ struct Barriers {
     alignas(16) float v_exp[kMaskSlots][kCols / 16];
 };
 
-template <int MODE, int D>
+template <int MODE, int D, int QUADS>
 struct Tree {
     using L = Layout<D>;
     static constexpr int kRpw = 16;  // positions of a dequantising warp: one group
@@ -353,8 +359,21 @@ struct Tree {
     }
 
     // ---- dequantise (a warp has a group of 16 positions) ------------------------------------------------
-    __device__ void dequantise() const {
-        const int dw = (warp - L::kDequantWarp) % 8, values = (warp - L::kDequantWarp) / 8;
+    // A tile's rows lie in QUADS quarters of tensor memory's lanes, and the softmax warps of a quarter are those with
+    // its number as their remainder by 4, which also share a scheduler of the SM.  Where quarters are empty, their idle
+    // softmax warps take places of dequantising warps from the schedulers that have softmax to do: three of one scheduler's
+    // four (1 quarter), two of each one's four (2 quarters).  64 x 8192 positions, D = 128: 8 rows to a head,
+    // dynamic and channel scales, 306 -> 267 and 283 -> 254 us.  Fewer loads unrolled are quicker with two copies
+    // of this loop in the instruction cache (285 and 260 us with four), and slower with one (2 x 131072, 256 rows: 320 and 312).
+    __device__ __forceinline__ static bool given_up(int place) {
+        return QUADS == 1 ? place > 0 && place % 4 == 0 : QUADS == 2 && place % 4 < 2 && place % 8 >= 4;
+    }
+    // The place that softmax warp w takes, or -1.
+    __device__ __forceinline__ static int taken(int w) {
+        return QUADS == 1 ? (w < 4 ? 4 * w : -1) : QUADS == 2 ? 4 + (w & 1) + 8 * (w >> 2) : -1;
+    }
+    __device__ void dequantise(int place) const {
+        const int dw = place % 8, values = place / 8;
         const uint32_t src = base + L::kRaw + (uint32_t)((dw * 16 + T::row_in(lane)) * D + T::block_in(lane) * 64 + lane % 4 * 16);
         int slot = values * L::kRing;
         uint32_t round = 0;
@@ -391,7 +410,7 @@ struct Tree {
                 }
                 reinterpret_cast<uint8_t *>(&bar.valid[n % kMaskSlots])[dw] = (uint8_t)valid;
             }
-            T::template store_each<4>(
+            T::template store_each<QUADS == 4 ? 4 : 2>(
                 [&](int k) {
                     uint4 c;
                     asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
@@ -828,9 +847,11 @@ struct Tree {
     }
 };
 
-template <int MODE, int D>
+template <int MODE, int D, int QUADS>
 __global__ void __launch_bounds__(Layout<D>::kThreads, 1) tree_kernel(const TreeArgs p) {
     using L = Layout<D>;
+    using Roles = Tree<MODE, D, QUADS>;
+    constexpr int kSoftmaxWarps = 2 * QUADS;  // that have a row
     extern __shared__ uint8_t dyn[];
     __shared__ Barriers bar;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -855,9 +876,9 @@ __global__ void __launch_bounds__(Layout<D>::kThreads, 1) tree_kernel(const Tree
                 mbar_init(smem_u32(&bar.v_full[i]), L::kDequantWarps / 2);
                 mbar_init(smem_u32(&bar.s_full[i]), 1);
                 mbar_init(smem_u32(&bar.v_free[i]), 1);
-                mbar_init(smem_u32(&bar.p_full[i]), L::kSoftmaxWarps);
+                mbar_init(smem_u32(&bar.p_full[i]), kSoftmaxWarps);
                 mbar_init(smem_u32(&bar.q_full[i]), L::kRowWarps);
-                mbar_init(smem_u32(&bar.q_free[i]), 1 + L::kSoftmaxWarps);
+                mbar_init(smem_u32(&bar.q_free[i]), 1 + kSoftmaxWarps);
             }
             for (int i = 0; i < 2 * L::kRing; ++i) {
                 bar.filled[i] = 0u;
@@ -866,11 +887,11 @@ __global__ void __launch_bounds__(Layout<D>::kThreads, 1) tree_kernel(const Tree
             }
             for (int i = 0; i < kTiles; ++i) {
                 mbar_init(smem_u32(&bar.tile_full[i]), 1);
-                mbar_init(smem_u32(&bar.tile_free[i]), L::kSoftmaxWarps + L::kRowWarps + 3);
+                mbar_init(smem_u32(&bar.tile_free[i]), kSoftmaxWarps + L::kRowWarps + 3);
             }
             mbar_init(smem_u32(&bar.o_full), 1);
             mbar_init(smem_u32(&bar.o_free), L::kRowWarps);
-            mbar_init(smem_u32(&bar.ml_full), L::kSoftmaxWarps);
+            mbar_init(smem_u32(&bar.ml_full), kSoftmaxWarps);
             mbar_init(smem_u32(&bar.drained), 1);
             bar.stop = 0;
             asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -926,18 +947,20 @@ __global__ void __launch_bounds__(Layout<D>::kThreads, 1) tree_kernel(const Tree
         __syncthreads();
         if (warp >= L::kMmaWarp) {
             reg_give<L::kMmaRegs>();
-            if (warp == L::kMmaWarp) Tree<MODE, D>(p, bar, dyn).products();
-            if (warp == L::kFetchWarp || warp == L::kFetchWarp + 2) Tree<MODE, D>(p, bar, dyn).fetch();
-            if (warp == L::kWalkWarp) Tree<MODE, D>(p, bar, dyn).walk();
+            if (warp == L::kMmaWarp) Roles(p, bar, dyn).products();
+            if (warp == L::kFetchWarp || warp == L::kFetchWarp + 2) Roles(p, bar, dyn).fetch();
+            if (warp == L::kWalkWarp) Roles(p, bar, dyn).walk();
         } else if (warp >= L::kDequantWarp) {
             reg_give<L::kDequantRegs>();
-            Tree<MODE, D>(p, bar, dyn).dequantise();
+            const int place = warp - L::kDequantWarp;
+            if (!Roles::given_up(place)) Roles(p, bar, dyn).dequantise(place);
         } else if (warp >= L::kRowWarp) {
             static_assert(L::kRowRegs == L::kLaunchRegs, "as launched");
-            Tree<MODE, D>(p, bar, dyn).rows();
+            Roles(p, bar, dyn).rows();
         } else {
             reg_take<L::kSoftmaxRegs>();
-            Tree<MODE, D>(p, bar, dyn).softmax();
+            if (warp % 4 < QUADS) Roles(p, bar, dyn).softmax();
+            else if (Roles::taken(warp) >= 0) Roles(p, bar, dyn).dequantise(Roles::taken(warp));
         }
         __syncwarp();
         tc_fence_before();
@@ -1054,10 +1077,10 @@ Space space(const kvc8_geom &g) {
     return s;
 }
 
-template <int MODE, int D>
+template <int MODE, int D, int QUADS>
 cudaError_t launch_variant(const TreeArgs &p, cudaStream_t stream) {
     using L = Layout<D>;
-    auto kern = tree_kernel<MODE, D>;
+    auto kern = tree_kernel<MODE, D, QUADS>;
     static std::atomic<uint64_t> prepared{0};  // a bit per device
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -1090,9 +1113,18 @@ cudaError_t launch_variant(const TreeArgs &p, cudaStream_t stream) {
                             (size_t)0, stream, p, grid, share);
 }
 
+// By the most rows that a head can have.
+template <int MODE, int D>
+cudaError_t launch_rows(const TreeArgs &p, cudaStream_t stream) {
+    const int rows = p.max_drafts * p.base.group;
+    if (rows <= kRows / 4) return launch_variant<MODE, D, 1>(p, stream);
+    if (rows <= kRows / 2) return launch_variant<MODE, D, 2>(p, stream);
+    return launch_variant<MODE, D, 4>(p, stream);
+}
+
 template <int MODE>
 cudaError_t launch_mode(const TreeArgs &p, cudaStream_t stream) {
-    return p.base.g.head_dim == 64 ? launch_variant<MODE, 64>(p, stream) : launch_variant<MODE, 128>(p, stream);
+    return p.base.g.head_dim == 64 ? launch_rows<MODE, 64>(p, stream) : launch_rows<MODE, 128>(p, stream);
 }
 
 }  // namespace

@@ -375,3 +375,17 @@ def test_a_step_of_drafts_from_pages_to_pages():
         for got, x in zip(rows, (0, 1)):
             want = torch.stack([r[x] for seq in kept for r in seq])
             assert bool(((got.double() - want).abs() <= want.abs() * (2.0 ** -8 + 2.0 ** -22)).all())
+
+
+@pytest.mark.parametrize("mode", [0, 1, 2])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("T,G", [(31, 1), (32, 1), (33, 1), (4, 8), (11, 3), (63, 1), (64, 1), (65, 1), (8, 8), (13, 5), (128, 1), (129, 1)])
+def test_rows_at_the_edges_of_a_tile_s_quarters(T, G, D, mode):
+    # full and shorter trees, contexts of none, of less and of more than a step, and long enough for several CTAs
+    run(TreeProblem([0, 1000, 77, 301, 5000], [T, T, 1, max(1, T // 2), T], G=G, D=D, mode=mode, seed=T))
+
+
+@pytest.mark.parametrize("T,G", [(4, 8), (16, 4)])
+def test_many_short_tiles_of_few_rows(T, G):
+    rng = np.random.default_rng(3)
+    run(TreeProblem(rng.integers(0, 40, 150).tolist(), rng.integers(0, T + 1, 149).tolist() + [T], G=G, D=128, seed=4))

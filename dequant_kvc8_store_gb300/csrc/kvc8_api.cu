@@ -912,6 +912,7 @@ kvc8_status kvc8_tree_attention(const kvc8_geom *g, int32_t num_q_heads, int64_t
     if (!std::isfinite(softmax_scale)) return KVC8_ERR_INVALID_ARG;
     if (cu_q_lens == nullptr && num_tokens != g->num_seqs) return KVC8_ERR_INVALID_ARG;
     if (tree_mask != nullptr && mask_words < (max_drafts + 63) / 64) return KVC8_ERR_INVALID_ARG;
+    if (tree_mask != nullptr && mask_words > 1 << 20) return KVC8_ERR_UNSUPPORTED;  // bits are counted in 32 bits
     if (num_tokens == 0 || g->num_seqs == 0) return num_tokens == 0 ? KVC8_OK : KVC8_ERR_INVALID_ARG;
     if (query == nullptr || key_cache == nullptr || value_cache == nullptr ||
         key_scale == nullptr || value_scale == nullptr || block_table == nullptr ||

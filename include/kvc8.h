@@ -678,7 +678,8 @@ size_t kvc8_tree_attention_workspace_bytes(const kvc8_geom *g, int32_t num_q_hea
  *                   draft i of the token's own sequence (other bits are not
  *                   looked at), 8-byte aligned; or NULL: a chain, where draft t sees
  *                   drafts 0 .. t
- *   mask_words      with a mask: at least max_drafts / 64, rounded up
+ *   mask_words      with a mask: at least max_drafts / 64, rounded up, at most 2^20
+ *                   (else KVC8_ERR_UNSUPPORTED)
  *   softmax_scale   finite
  *   out             bf16 [num_tokens][num_q_heads][D], strides (out_tok_stride,
  *                   out_head_stride, 1); not the query

@@ -110,3 +110,10 @@ def test_tree_refuses_tables_of_more_than_2_26_positions():
     size = lambda blocks: kv.kvc8_tree_attention_workspace_bytes(g(blocks), 4, 1, 4)  # noqa: E731
     assert size(1 << 22) > 0 and size((1 << 22) + 1) == 0
     assert tree(g((1 << 22) + 1), heads=4, n=1) == kv.ERR_UNSUPPORTED
+
+
+def test_tree_refuses_mask_rows_whose_bits_no_32_bit_count_holds():
+    # (no tokens: checks alone)
+    assert tree(geom(), n=0, words=1 << 20) == kv.OK
+    assert tree(geom(), n=0, words=(1 << 20) + 1) == tree(geom(), words=1 << 30) == kv.ERR_UNSUPPORTED
+    assert tree(geom(), n=0, words=1 << 30, mask=None) == kv.OK  # not looked at

@@ -392,12 +392,14 @@ struct Tree {
                 }
                 // A scale that is no number must not reach the rows that do not see its position,
                 // nor the other scales' power: the value counts as zero, and the score as no number.
-                const bool odd = (__float_as_uint(sk) & 0x7F800000u) == 0x7F800000u ||
-                                 (__float_as_uint(sv) & 0x7F800000u) == 0x7F800000u;
-                sk = odd ? 0.0f : sk;
-                sv = odd ? 0.0f : sv;
+                // The value scales' power is found twice, by the keys' warps, who hand it to the softmax, and by
+                // the values', who divide by it and see no key scale: so it goes by the value scales alone.
+                const bool odd_v = (__float_as_uint(sv) & 0x7F800000u) == 0x7F800000u;
+                sv = odd_v ? 0.0f : sv;
                 scale = T::normal_scale(sv, T::group_top(sv, lane), kLeastValuePower, ev);
                 if (values == 0) {
+                    const bool odd = odd_v || (__float_as_uint(sk) & 0x7F800000u) == 0x7F800000u;
+                    sk = odd ? 0.0f : sk;
                     scale = T::normal_scale(sk, T::group_top(sk, lane), -100, ek);
                     if (odd) scale = 0x7FFF7FFFu;
                 }

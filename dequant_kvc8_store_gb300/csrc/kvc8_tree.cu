@@ -474,7 +474,8 @@ struct Tree {
                     scores = ready(bar.k_full[s & 1], (uint32_t)(s >> 1) & 1u) &&
                              (left > 0 || ready(bar.q_full[q_seg & 1u], (q_seg >> 1) & 1u));
                     if (scores || ready(bar.p_full[v & 1], (uint32_t)(v >> 1) & 1u)) break;
-                    if (*static_cast<volatile int32_t *>(&bar.stop) != 0 || (uint32_t)clock() - t0 > kWaitTicks) {
+                    const bool over = *static_cast<volatile int32_t *>(&bar.stop) != 0 || (uint32_t)clock() - t0 > kWaitTicks;
+                    if (__any_sync(0xFFFFFFFFu, over)) {  // all lanes go together, whatever each has read
                         *static_cast<volatile int32_t *>(&bar.stop) = 1;
                         return false;
                     }
@@ -676,9 +677,10 @@ struct Tree {
     // The two softmax warps of 32 rows meet, by a hardware barrier: no limit, but none is needed.  A warp leaves
     // early only once `stop` is set, and then comes to the barrier one last time (leave_pair), whatever the other
     // one has read: if that one still waits here or comes later, it goes on, finds `stop` set and leaves too.
+    // What a warp's lanes have read they settle among themselves, so that they go the same way.
     __device__ __forceinline__ bool meet(int quad) const {
         asm volatile("bar.sync %0, 64;" ::"r"(1 + quad) : "memory");
-        return *static_cast<volatile int32_t *>(&bar.stop) == 0;
+        return __all_sync(0xFFFFFFFFu, *static_cast<volatile int32_t *>(&bar.stop) == 0);
     }
     __device__ __forceinline__ void leave_pair(int quad) const { asm volatile("bar.arrive %0, 64;" ::"r"(1 + quad) : "memory"); }
 

@@ -255,12 +255,26 @@ size_t shared_bytes(int B) { return sizeof(int64_t) * ((size_t)B + 1) + sizeof(i
 // 820 000: 127 in the cluster, 28.7).
 constexpr int64_t kManySlots = 1 << 17;
 
+// Lets both kernels have the shared memory of the largest batch, once per device: the limit is the function's, not
+// the launch's, so a limit of a batch's own size could be lowered by another host thread before its launch.
+static cudaError_t prepare_launches() {
+    static std::atomic<uint64_t> prepared{0};  // a bit per device
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = dev >= 0 && dev < kMaxDevices ? 1ull << dev : 0;
+    if ((prepared.load(std::memory_order_relaxed) & bit) != 0) return cudaSuccess;
+    const int most = (int)shared_bytes(KVC8_ASSIGN_MAX_SEQS);
+    e = cudaFuncSetAttribute(assign_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(slots_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
+    if (e == cudaSuccess) prepared.fetch_or(bit, std::memory_order_relaxed);
+    return e;
+}
+
 cudaError_t launch_assign(const AssignArgs &a, cudaStream_t stream) {
     const size_t smem = shared_bytes(a.num_seqs);
     if (smem > 48 * 1024) {
-        cudaError_t e = cudaFuncSetAttribute(assign_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-        if (e != cudaSuccess) return e;
-        e = cudaFuncSetAttribute(slots_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        const cudaError_t e = prepare_launches();
         if (e != cudaSuccess) return e;
     }
     const bool many_slots = a.slot_map != nullptr && a.slot_rows > kManySlots;

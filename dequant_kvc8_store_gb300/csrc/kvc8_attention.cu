@@ -467,7 +467,8 @@ cudaError_t launch_attention_variant(const AttnArgs &a, cudaStream_t stream) {
     static OccupancySlots slots;
     cudaError_t e = cudaSuccess;
     if (smem > 48 * 1024) {
-        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        static std::atomic<uint64_t> prepared{0};
+        e = allow_shared_memory(prepared, kern);
         if (e != cudaSuccess) return e;
     }
     int occ = 0;

@@ -488,7 +488,8 @@ cudaError_t launch_gather_variant(const GatherArgs &a, const AppendArgs &p, bool
     static OccupancySlots slots;
     cudaError_t e = cudaSuccess;
     if (smem > 48 * 1024) {
-        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        static std::atomic<uint64_t> prepared{0};
+        e = allow_shared_memory(prepared, kern);
         if (e != cudaSuccess) return e;
     }
     int occ = 0;

@@ -482,6 +482,25 @@ cudaError_t occupancy(OccupancySlots &slots, Kernel kern, int threads, size_t sm
     return cudaSuccess;
 }
 
+// Lets `kern` have as much dynamic shared memory as a CTA can, once per device (one `prepared` per kernel variant, a
+// bit per device).  The limit is the function's, not the launch's: with a call's own size, another host thread's
+// smaller call could lower it before this call's launch.
+template <typename Kernel>
+cudaError_t allow_shared_memory(std::atomic<uint64_t> &prepared, Kernel kern) {
+    int dev = 0, most = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = dev >= 0 && dev < kMaxDevices ? 1ull << dev : 0;
+    if ((prepared.load(std::memory_order_relaxed) & bit) != 0) return cudaSuccess;
+    cudaFuncAttributes attr;
+    e = cudaFuncGetAttributes(&attr, kern);
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&most, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev);
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, most - (int)attr.sharedSizeBytes);
+    if (e == cudaSuccess) prepared.fetch_or(bit, std::memory_order_relaxed);
+    return e;
+}
+
 // Host-side argument checks shared by the entry points (kvc8_api.cu).
 kvc8_status check_geom(const kvc8_geom *g);
 kvc8_status check_gather_args(const kvc8_geom *g, const int8_t *kc, const int8_t *vc,

@@ -620,6 +620,10 @@ struct Tree {
                     const float4 s = MODE == 1 ? __ldg(reinterpret_cast<const float4 *>(vs + c + i)) : make_float4(1.0f, 1.0f, 1.0f, 1.0f);
                     o[i] *= s.x * inv, o[i + 1] *= s.y * inv, o[i + 2] *= s.z * inv, o[i + 3] *= s.w * inv;
                 }
+                if (MODE == 1 && l == 0.0f) {  // no position: zeros, also where a channel's scale is infinite or no number
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) o[i] = 0.0f;
+                }
                 if (!whole) {
 #pragma unroll
                     for (int i = 0; i < 32; i += 4)

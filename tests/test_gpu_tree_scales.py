@@ -64,3 +64,18 @@ def test_one_bad_scale_of_a_draft_that_nobody_sees(which, bad):
     assert x.error() == 0
     want, tol, _ = clean.answers()
     assert bool(((x.out.double() - want).abs() <= tol).all())
+
+
+@pytest.mark.parametrize("which", ["ks", "vs"])
+@pytest.mark.parametrize("bad", BAD)
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("ctx,new,H", [([0], [5], 2), ([0], [256], 1), ([40, 0, 0], [3, 30, 200], 2)])
+def test_rows_without_a_position_are_zero_whatever_the_channels_scales(ctx, new, H, D, bad, which):
+    """Tiles that one CTA has whole, and tiles that are joined from several."""
+    x = TreeProblem(ctx, new, H=H, G=4, D=D, mode=1, kind="none", sharp=False, seed=23)
+    getattr(x, which)[:, 7] = bad
+    x.run()
+    n = new[0] if ctx[0] else 0
+    assert x.error() == 0 and bool((x.out[n:] == 0).all())
+    if n and np.isnan(bad):  # the others are what such scales make of them
+        assert bool(torch.isnan(x.out[:n, :, 7]).all())

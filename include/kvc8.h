@@ -659,6 +659,12 @@ size_t kvc8_tree_attention_workspace_bytes(const kvc8_geom *g, int32_t num_q_hea
  * draft sees itself only where its own bit is set.  K, V are the values that the
  * pages stand for, fp32(code) * scale.  Operands, accumulation, rounding and the
  * range of scales and queries are those of kvc8_shared_prefix_attention's prefix.
+ * Masks and that range: with scales per row, of 16 positions those count that some
+ * draft of the sequence may see, also for the drafts that do not see them, so the
+ * scales of context and seen drafts lie within 2^14 of one another for full
+ * precision; a draft that no draft sees (padding that was never stored) may have
+ * any scales, as positions behind the last draft may.  A scale that is NaN or
+ * infinite reaches the drafts that see its position and no others.
  *
  * Lengths, cu_q_lens, masks and tables are read on the device, so a captured graph
  * may be replayed with other values of them.  Two launches, no host

@@ -79,3 +79,26 @@ def test_rows_without_a_position_are_zero_whatever_the_channels_scales(ctx, new,
     assert x.error() == 0 and bool((x.out[n:] == 0).all())
     if n and np.isnan(bad):  # the others are what such scales make of them
         assert bool(torch.isnan(x.out[:n, :, 7]).all())
+
+
+@pytest.mark.parametrize("size", [2.0 ** 16, 2.0 ** 40, 1e38])
+@pytest.mark.parametrize("which", ["ks", "vs"])
+@pytest.mark.parametrize("ctx,new,G,D", [([40, 0, 250], [5, 17, 70], 4, 64), ([40, 0, 250], [5, 17, 70], 4, 128),
+                                         ([1000, 3], [256, 130], 8, 64), ([77, 128], [200, 4], 1, 128)])
+def test_large_scales_of_drafts_that_nobody_sees(ctx, new, G, D, which, size):
+    """Padding that was never stored: its scales are whatever the page held."""
+    make = lambda: TreeProblem(ctx, new, H=2, G=G, D=D, mode=0, kind="any", sharp=False, seed=24)  # noqa: E731
+    x, clean = make(), make()
+    hidden = [2, 3, 64, 66, 127, 128, 199]
+    for i in hidden:
+        if i < 64 * clean.words:
+            clean.mask[:, i // 64] &= ~np.uint64(1 << (i % 64))
+    x.mask = clean.mask
+    for b in range(len(ctx)):
+        for i in hidden:
+            if i < new[b]:
+                getattr(x, which)[at(x, b, ctx[b] + i)] = size
+    x.run()
+    assert x.error() == 0
+    want, tol, _ = clean.answers()
+    assert bool(((x.out.double() - want).abs() <= tol).all())

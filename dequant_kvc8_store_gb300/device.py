@@ -16,6 +16,15 @@ def _bf16(bits: np.ndarray) -> torch.Tensor:
     return torch.from_numpy(np.ascontiguousarray(bits).view(np.int16)).view(torch.bfloat16)
 
 
+def _torch_stream(stream, device):
+    """The stream of a call (None: torch's current one; a Stream; or its address) for torch."""
+    if stream is None:
+        return torch.cuda.current_stream(device)
+    if isinstance(stream, int):
+        return torch.cuda.ExternalStream(stream, device) if stream else torch.cuda.default_stream(device)
+    return stream
+
+
 def bf16_bits(t: torch.Tensor) -> np.ndarray:
     return t.detach().cpu().contiguous().view(torch.int16).numpy().view(np.uint16)
 
@@ -308,11 +317,14 @@ class TreeAttention:
 
     def keep(self, accepted, num_accepted, stream=None):
         """kvc8_compact_drafts: the drafts of `accepted` (host int32 [B][most], the first
-        num_accepted[b] of a row) move behind the context; returns the new lengths (device)."""
+        num_accepted[b] of a row) move behind the context; returns the new lengths (device, of
+        `stream`)."""
         d = self.d
-        accepted = torch.from_numpy(np.ascontiguousarray(accepted, np.int32)).to(d.device)
-        num = torch.from_numpy(np.asarray(num_accepted, np.int32)).to(d.device)
-        lens = torch.empty_like(d.context_kv_lens)
-        B.kvc8_compact_drafts(d.g, d.k_cache, d.v_cache, d.k_scale, d.v_scale, d.block_table, d.context_kv_lens,
-                              accepted, accepted.shape[1], num, lens, d.dev_error, stream)
+        # What the call reads and returns is made on its stream, which gives its memory back in its order.
+        with torch.cuda.stream(_torch_stream(stream, d.device)):
+            accepted = torch.from_numpy(np.ascontiguousarray(accepted, np.int32)).to(d.device)
+            num = torch.from_numpy(np.asarray(num_accepted, np.int32)).to(d.device)
+            lens = torch.empty_like(d.context_kv_lens)
+            B.kvc8_compact_drafts(d.g, d.k_cache, d.v_cache, d.k_scale, d.v_scale, d.block_table, d.context_kv_lens,
+                                  accepted, accepted.shape[1], num, lens, d.dev_error, stream)
         return lens

@@ -16,8 +16,8 @@
 // below or in the row that gives it up.  So many of them are made by a kernel of their own on all
 // SMs, before the cluster changes anything; meanwhile the cluster makes its sums.
 //
-// Latency bounds all of it: a decode step's 12 KB (256 sequences, 1150 slots) take 5.8 us, of which
-// the launch and one round trip for the lengths are most; 16 prompts of 36 696 slots (0.29 MB) 9.5 us;
+// Latency bounds all of it: a decode step's 12 KB (256 sequences, 1150 slots) take 5.9 us, of which
+// the launch and one round trip for the lengths are most; 16 prompts of 36 696 slots (0.29 MB) 8.3 us;
 // 4096 sequences with 820 000 slots (6.7 MB, 1 us at the copy rate) 28.7 us (36.3 without the overlap of
 // the two launches, 127 before slots had a kernel of their own).
 #include "kvc8_internal.cuh"
@@ -251,9 +251,14 @@ size_t shared_bytes(int B) { return sizeof(int64_t) * ((size_t)B + 1) + sizeof(i
 
 }  // namespace
 
-// Slots beyond which they are made on all SMs (36 696 slots: 9.5 us in the cluster, 12.3 with a kernel of their own;
-// 820 000: 127 in the cluster, 28.7).
-constexpr int64_t kManySlots = 1 << 17;
+// Slots beyond which they are made on all SMs.  us a call in a graph, in the cluster / with a kernel of their own:
+//   sequences   4096 slots     16 384        32 768        36 864       131 072       819 200
+//          16   4.4 /  6.9    6.3 /  7.1    6.5 /  7.1    8.5 /  7.1   13.4 /  7.1   61.6 / 12.7
+//         256   5.0 /  7.4    6.9 /  7.5    7.0 /  7.6    9.4 /  7.6   14.4 /  7.6   67.1 / 14.7
+//        4096   9.1 / 12.3   10.8 / 11.3                 13.9 / 11.5   18.9 / 11.4   76.7 / 21.5
+// The count is the device's, so the room for slots decides: with much room and few slots the second launch is for
+// nothing (256 sequences, 1024 slots, room for a million: 5.2 us, 4.2 with room for 1024).
+constexpr int64_t kManySlots = 1 << 15;
 
 // Lets both kernels have the shared memory of the largest batch, once per device: the limit is the function's, not
 // the launch's, so a limit of a batch's own size could be lowered by another host thread before its launch.
@@ -285,7 +290,7 @@ cudaError_t launch_assign(const AssignArgs &a, cudaStream_t stream) {
         if (e != cudaSuccess) return e;
     }
     // Small CTAs start and meet sooner (256 sequences, 1150 slots: 5.8 us with 256 threads, 6.2 with 1024, 8.2 in one CTA),
-    // as long as they have a thread to a sequence and to a slot (36 696 slots: 12.3 and 9.5 us).
+    // as long as they have a thread to a sequence and to a slot (16 sequences, 32 768 slots, in a graph: 8.5 and 6.5 us).
     const int64_t slots = a.slot_map != nullptr ? a.slot_rows : 0;
     const int threads = a.num_seqs <= kFewThreads && slots <= kFewThreads * kCluster ? kFewThreads : kThreads;
     cudaLaunchConfig_t cfg = {};

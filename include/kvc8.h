@@ -618,7 +618,7 @@ kvc8_status kvc8_shared_prefix_attention(const kvc8_geom *g, int32_t num_q_heads
  *     follow one another without gaps, in the order of kvc8_store's new tokens.
  *   - *free_count_out = F + R less what was popped.  Entries given up stay in the
  *     table, and popped ones in free_blocks behind the new count.
- * One launch, two with more than 131072 slot_rows.
+ * One launch, two with more than 32768 slot_rows.
  *
  *   g               num_seqs <= KVC8_ASSIGN_MAX_SEQS (else KVC8_ERR_UNSUPPORTED);
  *                   kv_heads, head_dim and quant_mode are checked, but not used

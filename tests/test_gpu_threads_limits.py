@@ -42,7 +42,7 @@ def at_once(*calls, times=400):
     assert not errors, errors
 
 
-@pytest.mark.parametrize("new", [60, 3])  # with a launch of the slots' own (more than 131072), and without
+@pytest.mark.parametrize("new", [60, 3])  # with a launch of the slots' own, and without
 def test_block_assignment(new):
     kv.load()
     rng = np.random.default_rng(31)

@@ -303,6 +303,8 @@ class TreeAttention:
         self.masks, self.words = None, 0
         if masks is not None:
             masks = np.ascontiguousarray(masks, np.uint64)
+            if masks.ndim != 2 or masks.shape[0] != w.num_tokens:
+                raise ValueError(f"masks of shape {masks.shape} for {w.num_tokens} drafts")
             self.words = masks.shape[1]
             self.masks = torch.from_numpy(masks.view(np.int64)).to(d.device)
         self.ws_bytes = B.kvc8_tree_attention_workspace_bytes(d.g, self.num_q_heads, w.num_tokens, self.max_drafts)
@@ -320,10 +322,12 @@ class TreeAttention:
         num_accepted[b] of a row) move behind the context; returns the new lengths (device, of
         `stream`)."""
         d = self.d
+        accepted, num = np.ascontiguousarray(accepted, np.int32), np.ascontiguousarray(num_accepted, np.int32)
+        if accepted.ndim != 2 or num.ndim != 1 or not accepted.shape[0] == num.shape[0] == d.w.num_seqs:
+            raise ValueError(f"accepted {accepted.shape} and num_accepted {num.shape} for {d.w.num_seqs} sequences")
         # What the call reads and returns is made on its stream, which gives its memory back in its order.
         with torch.cuda.stream(_torch_stream(stream, d.device)):
-            accepted = torch.from_numpy(np.ascontiguousarray(accepted, np.int32)).to(d.device)
-            num = torch.from_numpy(np.asarray(num_accepted, np.int32)).to(d.device)
+            accepted, num = (torch.from_numpy(x).to(d.device) for x in (accepted, num))
             lens = torch.empty_like(d.context_kv_lens)
             B.kvc8_compact_drafts(d.g, d.k_cache, d.v_cache, d.k_scale, d.v_scale, d.block_table, d.context_kv_lens,
                                   accepted, accepted.shape[1], num, lens, d.dev_error, stream)

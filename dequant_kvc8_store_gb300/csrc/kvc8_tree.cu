@@ -284,6 +284,7 @@ struct Tree {
         uint32_t seg = 0;
         int count = 0;                // steps of the tile not asked for yet
         int left = 0, at = 0, head = 0;  // of the step asked for: positions left, slot and entry of the table
+        int drafts = INT32_MIN;          // mode 0, with masks: positions of its tile behind the context
         const int32_t *entry = nullptr;
         int32_t blk = 0;
         int64_t row = 0;  // of the step placed: cache row of the group's first position
@@ -330,14 +331,12 @@ struct Tree {
                 if (MODE == 0) {
                     // The scales of drafts that no row of the tile sees, which may be anything, take no part in the
                     // power that 16 scales have in common.  (The tile's place is not taken by another before its rows
-                    // are stored, long after this.  64 x 8192, 16 query rows: 268 -> 274 us, with the masks gone through
+                    // are stored, long after this.  64 x 8192, 16 query rows: 268 -> 272 us, with the masks gone through
                     // here instead of by the walk warp 321.)
-                    const Tile &x = tile(seg - 1);
-                    const int d = x.len - left - x.ctx;  // the draft at the group's first position, if not negative
-                    if (d > -16 && p.mask != nullptr) {
-                        const int at = min(d, KVC8_MAX_DRAFTS - 1) + 32;
-                        const uint32_t *seen = bar.seen[(seg - 1) % kTiles] + at / 32;
-                        valid &= __funnelshift_r(seen[0], seen[1], (uint32_t)at & 31u);
+                    if (drafts > left - 16) {
+                        const int bit = min(drafts - left, KVC8_MAX_DRAFTS - 1) + 32;  // of the group's first position
+                        const uint32_t *seen = bar.seen[(seg - 1) % kTiles] + bit / 32;
+                        valid &= __funnelshift_r(seen[0], seen[1], (uint32_t)bit & 31u);
                     }
                 }
                 const int64_t page = (int64_t)(in ? blk : 0) * a.g.kv_heads + head;
@@ -360,6 +359,7 @@ struct Tree {
                     const Tile &x = tile(seg);
                     const int pos = x.step * kCols + grp * 16;
                     left = x.len - pos;
+                    if (MODE == 0) drafts = p.mask != nullptr ? x.len - x.ctx : INT32_MIN;
                     head = x.head;
                     at = pos % bs;
                     entry = a.block_table + (int64_t)x.b * a.g.max_blocks_per_seq + pos / bs;

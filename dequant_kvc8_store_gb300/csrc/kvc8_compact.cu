@@ -11,6 +11,12 @@
 // (16.5 MB): 7.2 us, 2.3 TB/s; int8 pages, 1 sequence of 12 drafts: 5.2 us, 64 of 24: 6.2 us.
 // 33 sequences of 9 to 61 drafts with block scales, a division for each code that changes blocks:
 // 12.3 us (with a gather that reads the pages back 19; 34 before four codes had a thread).
+//
+// The time goes by the longest path, eight moves a round trip and as many rounds as a sequence's rows
+// have units for its threads: 16, 64 and 256 kept drafts of one sequence (8 heads, D = 128, in a graph)
+// take 6.3, 17.6 and 64 us with a row's scales, 4.0, 10.7 and 37 with the channels', 7.6, 21 and 134 with
+// a block's, and 4.5, 11.4 and 40 in bf16; 64 such sequences 68, 40, 142 and 51.  A path is as long as a
+// draft tree is deep, so several CTAs to a sequence were not tried.
 #include <type_traits>
 
 #include "kvc8_internal.cuh"

@@ -6,15 +6,15 @@
 // flops for 2 D bytes of codes a position and head, so HBM would bound up to about 150 rows and the
 // tensor cores more.  What bounds it in fact is a step's chain: its scores, their maximum, 64 exponentials a
 // thread, the weighted values, with the dequantising warps' instructions between (8 heads, D = 128, whole calls):
-//   256 sequences of up to 8192 positions, 16 rows, channel scales   663 us, 3.4 TB/s (a step 2500 cycles)
-//   64 of 8192, 16 and 64 rows, dynamic scales                       268 and 290 us, 4.1 and 3.9 TB/s
-//   2 of 131072, 256 rows, dynamic scales                            311 us, 878 TFLOP/s (2650 cycles, 71% of issue slots)
-//   1 of 500, 16 rows (2 heads, D = 64)                              12.4 us: two launches, round trips
+//   256 sequences of up to 8192 positions, 16 rows, channel scales   674 us, 3.3 TB/s (a step 2500 cycles)
+//   64 of 8192, 16 and 64 rows, dynamic scales                       272 and 303 us, 4.1 and 3.7 TB/s
+//   2 of 131072, 256 rows, dynamic scales                            323 us, 845 TFLOP/s (2700 cycles, 70% of issue slots)
+//   1 of 500, 16 rows (2 heads, D = 64)                              12.3 us: two launches, round trips
 //
 // tree_kernel: one persistent CTA per SM, a tile of 128 query rows, 128 positions a step.  S = Q
 // K'^T and O += P V' are tcgen05.mma (M = 128, fp16, fp32 in tensor memory); Q lies in tensor memory,
 // and P replaces S there: both are A operands.  Warps by role:
-//   walk        1: what the CTA's next tiles are
+//   walk        1: what the CTA's next tiles are, and which drafts some row of them sees
 //   fetch       2, for the keys and for the values: pages' codes by bulk copies into rings of two steps in shared
 //               memory (2 x 131072: 351 us with one warp for both, 311 with two; three steps of keys were no faster)
 //   dequantise  16, eight for the keys and eight for the values: codes to K' and V' as fp16, two stages of
@@ -29,14 +29,15 @@
 // With at most 64 rows idle softmax warps dequantise as well (given_up, below).
 // S and Q are there twice: the scores of a step are made while the softmax works on the step before.  The roles'
 // loops are kept short: together they must fit the SM's instruction cache (with 95 KB of code, of which each
-// step ran through about 30, a step took 3100 cycles and the warps waited for instructions; it is 75 now).
+// step ran through about 30, a step took 3100 cycles and the warps waited for instructions; it is 68 to 79 now).
 //
 // The units (sequence, kv head, row tile, step) are numbered in that order and cut into equal shares,
 // a CTA's share in a row: ragged lengths need no plan, every CTA adds up the lengths itself.  What a
 // CTA has of a tile that it does not hold whole it leaves as a partial (m, l, O), two at most: of the
 // first tile of its share and of the last.  merge_kernel joins them.
 //
-// Every wait has a limit, after which the kernel reports KVC8_DEV_TIMEOUT and leaves.
+// Every wait on an mbarrier has a limit, after which the kernel reports KVC8_DEV_TIMEOUT and leaves.  The barrier at
+// which a row's two softmax warps meet needs none: a warp that leaves early comes to it once more.
 #include "kvc8_tcgen05.cuh"
 
 namespace kvc8 {

@@ -667,8 +667,8 @@ size_t kvc8_tree_attention_workspace_bytes(const kvc8_geom *g, int32_t num_q_hea
  * infinite reaches the drafts that see its position and no others.
  *
  * Lengths, cu_q_lens, masks and tables are read on the device, so a captured graph
- * may be replayed with other values of them.  Two launches, no host
- * synchronisation.
+ * may be replayed with other values of them.  Two launches, one where the tables
+ * have room for a single unit (below) only; no host synchronisation.
  *
  *   num_q_heads     H * group with 1 <= group <= 8
  *   num_tokens      rows of query and out, >= cu_q_lens[B]; rows from cu_q_lens[B] on

@@ -17,7 +17,8 @@
 // SMs, before the cluster changes anything; meanwhile the cluster makes its sums.
 //
 // Latency bounds all of it: a decode step's 12 KB (256 sequences, 1150 slots) take 5.9 us, of which
-// the launch and one round trip for the lengths are most; 16 prompts of 36 696 slots (0.29 MB) 8.3 us;
+// the launch and one round trip for the lengths are most; 16 prompts of 36 696 slots (0.29 MB) 8.2 to
+// 9.3 us (7.2 in a graph);
 // 4096 sequences with 820 000 slots (6.7 MB, 1 us at the copy rate) 28.7 us (36.3 without the overlap of
 // the two launches, 127 before slots had a kernel of their own).
 #include "kvc8_internal.cuh"

@@ -102,3 +102,20 @@ def test_large_scales_of_drafts_that_nobody_sees(ctx, new, G, D, which, size):
     assert x.error() == 0
     want, tol, _ = clean.answers()
     assert bool(((x.out.double() - want).abs() <= tol).all())
+
+
+@pytest.mark.parametrize("which", ["ks", "vs"])
+@pytest.mark.parametrize("bad", BAD)
+@pytest.mark.parametrize("D", [64, 128])
+def test_a_bad_scale_of_a_block_that_the_earlier_drafts_do_not_see(D, bad, which):
+    make = lambda: TreeProblem([32, 5], [40, 3], H=2, G=4, D=D, bs=16, mode=2, kind="chain", sharp=False, seed=25)  # noqa: E731
+    x, clean = make(), make()
+    getattr(x, which)[int(x.tab[0, 3])] = bad  # positions 48 to 63: drafts 16 to 31
+    x.run()
+    assert x.error() == 0
+    want, tol, _ = clean.answers()
+    sees = torch.zeros(x.N, dtype=torch.bool, device="cuda")
+    sees[16:40] = True
+    good = ((x.out.double() - want).abs() <= tol).flatten(1).all(1)
+    assert bool((good | sees).all()), (~good & ~sees).nonzero().flatten().tolist()
+    assert bool(torch.isnan(x.out[sees]).all())

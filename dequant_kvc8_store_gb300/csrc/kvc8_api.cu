@@ -37,8 +37,6 @@ constexpr int64_t kFusedAppendMaxRows = 16384;
 
 bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
-kvc8_status cuda_status(cudaError_t e) { return e == cudaSuccess ? KVC8_OK : KVC8_ERR_CUDA; }
-
 kvc8_status check_workspace(const kvc8_geom *g, const void *ws, size_t bytes) {
     if (ws == nullptr || !aligned(ws, kAlign)) return KVC8_ERR_WORKSPACE;
     if (bytes < plan_bytes(g->num_seqs)) return KVC8_ERR_WORKSPACE;
@@ -176,7 +174,7 @@ kvc8_status kvc8_dequant_gather(const kvc8_geom *g, const int8_t *key_cache,
     if (st != KVC8_OK) return st;
     cudaError_t e = launch_plan(*g, context_lengths, context_seq_offset, nullptr, workspace,
                                 dev_error, stream);
-    if (e != cudaSuccess) return KVC8_ERR_CUDA;
+    if ((st = cuda_status(e)) != KVC8_OK) return st;
     GatherArgs a;
     a.g = *g;
     a.k_cache = key_cache;
@@ -227,7 +225,7 @@ kvc8_status kvc8_dequant_gather_planned(const kvc8_geom *g, const int8_t *key_ca
     a.out_head_stride = out_head_stride;
     a.plan = workspace;
     a.dev_error = dev_error;
-    if (reset_plan_counter(workspace, stream) != cudaSuccess) return KVC8_ERR_CUDA;
+    if ((st = cuda_status(reset_plan_counter(workspace, stream))) != KVC8_OK) return st;
     return cuda_status(launch_gather(a, /*use_pdl=*/false, stream));
 }
 
@@ -338,17 +336,17 @@ kvc8_status kvc8_append_gather(const kvc8_geom *g, int64_t num_tokens, const voi
         s.context_kv_lens = context_kv_lens;
         s.dev_error = dev_error;
         s.bs_magic = g->block_size >= 2 ? ~0ull / (unsigned long long)g->block_size + 1ull : 0ull;
-        if (launch_store(s, stream) != cudaSuccess) return KVC8_ERR_CUDA;
+        if ((st = cuda_status(launch_store(s, stream))) != KVC8_OK) return st;
         int32_t *spans = reinterpret_cast<int32_t *>(static_cast<char *>(workspace) + span_at);
-        if (launch_plan_span(*g, context_kv_lens, cu_q_lens, context_seq_offset, workspace, spans,
-                             dev_error, stream) != cudaSuccess)
-            return KVC8_ERR_CUDA;
+        st = cuda_status(launch_plan_span(*g, context_kv_lens, cu_q_lens, context_seq_offset, workspace, spans,
+                                          dev_error, stream));
+        if (st != KVC8_OK) return st;
         a.context_lengths = spans;
         return cuda_status(launch_gather(a, /*use_pdl=*/true, stream));
     }
-    if (launch_plan_append(*g, context_kv_lens, cu_q_lens, context_seq_offset, nullptr,
-                           workspace, dev_error, stream) != cudaSuccess)
-        return KVC8_ERR_CUDA;
+    st = cuda_status(launch_plan_append(*g, context_kv_lens, cu_q_lens, context_seq_offset, nullptr,
+                                        workspace, dev_error, stream));
+    if (st != KVC8_OK) return st;
     return cuda_status(launch_append_gather(a, p, /*use_pdl=*/true, stream));
 }
 
@@ -386,7 +384,7 @@ kvc8_status kvc8_append_gather_planned(const kvc8_geom *g, int64_t num_tokens,
                                  out_rows, out_tok_stride, out_head_stride, workspace,
                                  workspace_bytes, dev_error, &a, &p);
     if (st != KVC8_OK) return st;
-    if (reset_plan_counter(workspace, stream) != cudaSuccess) return KVC8_ERR_CUDA;
+    if ((st = cuda_status(reset_plan_counter(workspace, stream))) != KVC8_OK) return st;
     return cuda_status(launch_append_gather(a, p, /*use_pdl=*/false, stream));
 }
 
@@ -514,9 +512,9 @@ kvc8_status kvc8_gather_bf16(const kvc8_geom *g, const void *key_cache, const vo
     q.quant_mode = 0;
     st = check_workspace(&q, workspace, workspace_bytes);
     if (st != KVC8_OK) return st;
-    if (launch_plan(q, context_lengths, context_seq_offset, nullptr, workspace, dev_error,
-                    stream) != cudaSuccess)
-        return KVC8_ERR_CUDA;
+    st = cuda_status(launch_plan(q, context_lengths, context_seq_offset, nullptr, workspace, dev_error,
+                                 stream));
+    if (st != KVC8_OK) return st;
     GatherBf16Args a;
     a.g = q;
     a.k_cache = static_cast<const uint16_t *>(key_cache);
@@ -1015,14 +1013,13 @@ kvc8_status kvc8_get_error(int32_t *dev_error, int32_t *host_code, int32_t reset
                            cudaStream_t stream) {
     if (dev_error == nullptr || host_code == nullptr) return KVC8_ERR_INVALID_ARG;
     int32_t v = 0;
-    if (cudaMemcpyAsync(&v, dev_error, sizeof v, cudaMemcpyDeviceToHost, stream) != cudaSuccess)
-        return KVC8_ERR_CUDA;
-    if (cudaStreamSynchronize(stream) != cudaSuccess) return KVC8_ERR_CUDA;
+    kvc8_status st = cuda_status(cudaMemcpyAsync(&v, dev_error, sizeof v, cudaMemcpyDeviceToHost, stream));
+    if (st != KVC8_OK) return st;
+    if ((st = cuda_status(cudaStreamSynchronize(stream))) != KVC8_OK) return st;
     *host_code = v;
     if (reset) {
-        if (cudaMemsetAsync(dev_error, 0, sizeof(int32_t), stream) != cudaSuccess)
-            return KVC8_ERR_CUDA;
-        if (cudaStreamSynchronize(stream) != cudaSuccess) return KVC8_ERR_CUDA;
+        if ((st = cuda_status(cudaMemsetAsync(dev_error, 0, sizeof(int32_t), stream))) != KVC8_OK) return st;
+        if ((st = cuda_status(cudaStreamSynchronize(stream))) != KVC8_OK) return st;
     }
     return v == 0 ? KVC8_OK : KVC8_ERR_DEVICE_BOUNDS;
 }

@@ -501,6 +501,14 @@ cudaError_t allow_shared_memory(std::atomic<uint64_t> &prepared, Kernel kern) {
     return e;
 }
 
+// A failure is reported by the call that it belongs to: left as the thread's last error, the next call would find it
+// behind its own launch and report it again.
+inline kvc8_status cuda_status(cudaError_t e) {
+    if (e == cudaSuccess) return KVC8_OK;
+    (void)cudaGetLastError();
+    return KVC8_ERR_CUDA;
+}
+
 // Host-side argument checks shared by the entry points (kvc8_api.cu).
 kvc8_status check_geom(const kvc8_geom *g);
 kvc8_status check_gather_args(const kvc8_geom *g, const int8_t *kc, const int8_t *vc,

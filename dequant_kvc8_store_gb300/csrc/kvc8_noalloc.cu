@@ -70,15 +70,14 @@ extern "C" kvc8_status kvc8_dequant_gather_noalloc(
     // The set-up comes before the early return, so that a call with
     // num_seqs = 0 at start-up prepares the device without doing any work.
     void *scratch = nullptr;
-    if (scratch_for_current_device(&scratch) != cudaSuccess) return KVC8_ERR_CUDA;
+    if ((st = cuda_status(scratch_for_current_device(&scratch))) != KVC8_OK) return st;
     if (g->num_seqs == 0) return KVC8_OK;
     st = check_gather_args(g, key_cache, value_cache, key_scale, value_scale, block_table,
                            context_lengths, key_out, value_out, out_rows, out_tok_stride,
                            out_head_stride);
     if (st != KVC8_OK) return st;
-    if (launch_plan(*g, context_lengths, context_seq_offset, nullptr, scratch, dev_error,
-                    stream) != cudaSuccess)
-        return KVC8_ERR_CUDA;
+    st = cuda_status(launch_plan(*g, context_lengths, context_seq_offset, nullptr, scratch, dev_error, stream));
+    if (st != KVC8_OK) return st;
     GatherArgs a;
     a.g = *g;
     a.k_cache = key_cache;
@@ -94,5 +93,5 @@ extern "C" kvc8_status kvc8_dequant_gather_noalloc(
     a.out_head_stride = out_head_stride;
     a.plan = scratch;
     a.dev_error = dev_error;
-    return launch_gather(a, /*use_pdl=*/true, stream) == cudaSuccess ? KVC8_OK : KVC8_ERR_CUDA;
+    return cuda_status(launch_gather(a, /*use_pdl=*/true, stream));
 }
